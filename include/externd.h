@@ -355,6 +355,113 @@ int externd_gemv_n(const float* R, int64_t m, int64_t n, const uint32_t* v_codes
 int externd_deflate(float* R, int64_t m, int64_t n, const uint32_t* u_codes,
                     const uint32_t* v_codes, float d, void* stream);
 
+/* ---- 4-bit weights with group scales ----
+ *
+ * The storage that the ternary factors are weighed against, and its products
+ * with a few tokens.  A group is `group` neighbouring entries of a row (32, 64
+ * or 128; the last group of a row may be shorter) with a bf16 scale s and,
+ * asymmetric, a bf16 minimum m:
+ *   symmetric:  s = bf16(max|w| / 7), code c = clamp(rint(w / s), -8, 7) + 8, value s (c - 8);
+ *   asymmetric: s = bf16((max w - min w) / 15), m = bf16(min w),
+ *               c = clamp(rint((w - m) / s), 0, 15), value s c + m.
+ * Steps are fp32, rint takes ties to even, and a group of scale 0 has c = 8
+ * (symmetric) or 0.  A group with a non-finite entry, or whose scale overflows,
+ * gets a NaN scale: all its values are NaN.
+ *
+ * Layout: tiles of 16 rows by chunks of 128 columns, tile-major,
+ * ceil(rows/16) x ceil(cols/128) of them:
+ *   codes:  256 uint32 words per tile of a chunk.  Word 4 l + i, l = r + 16 p
+ *           (r < 16, p < 4, i < 4), holds row r's codes of columns
+ *           32 i + 8 p + j, j = 0..7: j = 2 e in bits 4 e .. 4 e + 3, j = 2 e + 1
+ *           in bits 16 + 4 e .. 19 + 4 e.
+ *   scales, mins: bf16, 16 x (128 / group) per tile of a chunk, row r's groups
+ *           at r * (128 / group).
+ * Padding entries may hold any code; padding scales and minima must be
+ * finite.  codes must be 16-byte aligned, scales and mins 8-byte. */
+enum externd_dtype { EXTERND_F32 = 0, EXTERND_BF16 = 1, EXTERND_F16 = 2 };
+enum externd_activation {
+  EXTERND_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+  EXTERND_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
+  EXTERND_ACT_GELU_TANH = 2  /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+};
+
+typedef struct externd_q4 {
+  const uint32_t* codes;   /* device */
+  const uint16_t* scales;  /* device */
+  const uint16_t* mins;    /* device, NULL: symmetric */
+  int64_t rows, cols;
+  int32_t group;           /* 32, 64 or 128 */
+  int32_t reserved;
+} externd_q4;
+
+/* Elements of codes (uint32) and of scales or mins (bf16) in the layout above;
+ * -1 for a bad shape or group. */
+int64_t externd_q4_code_words(int64_t rows, int64_t cols);
+int64_t externd_q4_table_len(int64_t rows, int64_t cols, int32_t group);
+
+/* Quantize W (rows x cols of dtype, rows ldw >= cols entries apart).  mins
+ * NULL: symmetric.  Padding is written too. */
+int externd_q4_quantize(const void* W, int64_t rows, int64_t cols, int64_t ldw, int32_t dtype, int32_t group,
+                        void* stream, uint32_t* codes, uint16_t* scales, uint16_t* mins);
+
+/* Bring codes made elsewhere into the layout: codes_in one byte each (rows x
+ * cols, low four bits), scales_in and mins_in bf16, rows x ceil(cols/group).
+ * mins_in and mins are both NULL or both given. */
+int externd_q4_pack(const uint8_t* codes_in, const uint16_t* scales_in, const uint16_t* mins_in, int64_t rows,
+                    int64_t cols, int32_t group, void* stream, uint32_t* codes, uint16_t* scales, uint16_t* mins);
+
+/* The values (rows x cols of dtype, packed), each rounded once. */
+int externd_q4_reconstruct(const externd_q4* w, int32_t dtype, void* stream, void* out);
+
+/* y[t] = W x[t] for `tokens` rows of x (cols entries of dtype, ldx >= cols
+ * entries apart); y is tokens x rows of dtype, packed.  Sums are fp32, in an
+ * order that does not depend on timing; fp32 x is split into three bf16 parts
+ * that add up to it exactly.  A non-finite entry of x makes its token's outputs
+ * NaN; so does a finite one above 2^120.  tokens may be 0, at most 2^20.
+ * workspace: NULL, and where x needs a staged copy (fp32, or rows that are not
+ * all 16-byte aligned) externd_q4_workspace_bytes bytes are allocated and freed
+ * stream-ordered; or a caller device buffer, 256-byte aligned, of at least
+ * that many bytes, used instead.  Calls that overlap on one workspace race. */
+int externd_q4_apply(const externd_q4* w, const void* x, int64_t tokens, int64_t ldx, int32_t dtype, void* stream,
+                     void* y, void* workspace, size_t workspace_bytes);
+
+/* h[t] = act(Wg x[t]) * (Wu x[t]), both projections in one kernel; wg and wu
+ * have one shape, group size and kind.  Everything else as externd_q4_apply. */
+int externd_q4_gated(const externd_q4* wg, const externd_q4* wu, const void* x, int64_t tokens, int64_t ldx,
+                     int32_t dtype, int32_t act, void* stream, void* h, void* workspace, size_t workspace_bytes);
+
+/* Workspace bytes that covers externd_q4_apply and externd_q4_gated for any
+ * alignment of x; 0 for a bad shape or dtype. */
+size_t externd_q4_workspace_bytes(int64_t cols, int64_t tokens, int32_t dtype);
+
+/* ---- gated feed-forward block, dense 16-bit weights ----
+ *
+ * h = act(x Wg^T) * (x Wu^T): x tokens x cols (rows ldx entries apart), Wg and Wu
+ * rows x cols (rows ldw entries apart), h tokens x rows, packed; dtype
+ * EXTERND_BF16 or EXTERND_F16 (fp32 is EXTERND_EUNSUPPORTED: its matrix rate is
+ * a sixteenth).  Sums and the activation are fp32 and h is rounded once.  g and u
+ * (both or neither): tokens x rows fp32, the projections, kept for the
+ * backward pass.  Strides are in entries, at least cols.  tokens may be 0.
+ * workspace: as for externd_q4_apply, of externd_gated_forward_workspace_bytes
+ * bytes (which may be 0). */
+int externd_gated_forward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wg, const void* wu,
+                          int64_t rows, int64_t ldw, int32_t dtype, int32_t act, void* stream, void* h, float* g,
+                          float* u, void* workspace, size_t workspace_bytes);
+size_t externd_gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows);
+
+/* Gradients of the block from dh (tokens x rows, rows lddh entries apart) and
+ * the g and u that the forward pass kept:
+ *   dg = dh u act'(g), du = dh act(g)   (rounded once to dtype)
+ *   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x   (fp32 sums, rounded once).
+ * dx (tokens x cols) may be NULL; dwg and dwu (rows x cols) are both given or
+ * both NULL.  Outputs are packed.  With tokens = 0, dwg and dwu are zero.
+ * workspace: as above, of externd_gated_backward_workspace_bytes bytes. */
+int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wg, const void* wu,
+                           int64_t rows, int64_t ldw, const float* g, const float* u, const void* dh, int64_t lddh,
+                           int32_t dtype, int32_t act, void* stream, void* dx, void* dwg, void* dwu, void* workspace,
+                           size_t workspace_bytes);
+size_t externd_gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows);
+
 /* Status text and the last error message of the calling thread. */
 const char* externd_status_string(int status);
 const char* externd_last_error(void);

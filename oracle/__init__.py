@@ -15,6 +15,9 @@ greedy sequential decomposition and the plain block ALS (loaded by
 oracle/c_oracle.py, compiled by build() in __graft_entry__.py), pinned the
 same way in tests/test_oracle_c.py.
 
+oracle/q4.py and oracle/gated.py are the plain forms of the 4-bit group weights
+and of the gated feed-forward block (imported by name).
+
 Pins (tests/test_oracle_*.py) tie it to what the pages and mathematics fix:
 hand-worked T_tau vectors, the Gaussian zero-fraction closed form, the
 closed-form optimal projection against brute force, exact residual decrease,

@@ -18,6 +18,8 @@ __all__ = [
     "workspace_bytes",
     "rank_for_energy", "mu_for_energy", "project",
     "ternarize", "gemv_t", "gemv_n", "deflate", "Decomposition", "ExterndError",
+    "Q4", "q4_quantize", "q4_pack", "q4_reconstruct", "q4_apply", "q4_gated", "q4_workspace_bytes",
+    "gated", "gated_forward", "gated_backward", "gated_forward_workspace_bytes", "gated_backward_workspace_bytes",
     "STAT", "MODE_AUTO", "MODE_STREAMING", "MODE_RESIDENT", "MODE_PERSISTENT", "library_path",
 ]
 
@@ -67,6 +69,11 @@ class _Opts(ctypes.Structure):
     ]
 
 
+class _Q4(ctypes.Structure):
+    _fields_ = [("codes", _p), ("scales", _p), ("mins", _p), ("rows", _i64), ("cols", _i64),
+                ("group", _i32), ("reserved", _i32)]
+
+
 def _sig(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -96,6 +103,23 @@ _project = _sig("externd_project", ctypes.c_int, [_p, _i64, _p, _p, _p])
 _gemv_t = _sig("externd_gemv_t", ctypes.c_int, [_p, _i64, _i64, _p, _p, _p])
 _gemv_n = _sig("externd_gemv_n", ctypes.c_int, [_p, _i64, _i64, _p, _p, _p])
 _deflate = _sig("externd_deflate", ctypes.c_int, [_p, _i64, _i64, _p, _p, _f32, _p])
+_pq4 = ctypes.POINTER(_Q4)
+_size = ctypes.c_size_t
+_q4_quantize = _sig("externd_q4_quantize", ctypes.c_int, [_p, _i64, _i64, _i64, _i32, _i32, _p, _p, _p, _p])
+_q4_pack = _sig("externd_q4_pack", ctypes.c_int, [_p, _p, _p, _i64, _i64, _i32, _p, _p, _p, _p])
+_q4_reconstruct = _sig("externd_q4_reconstruct", ctypes.c_int, [_pq4, _i32, _p, _p])
+_q4_apply = _sig("externd_q4_apply", ctypes.c_int, [_pq4, _p, _i64, _i64, _i32, _p, _p, _p, _size])
+_q4_gated = _sig("externd_q4_gated", ctypes.c_int, [_pq4, _pq4, _p, _i64, _i64, _i32, _i32, _p, _p, _p, _size])
+_q4_ws = _sig("externd_q4_workspace_bytes", _size, [_i64, _i64, _i32])
+_q4_code_words = _sig("externd_q4_code_words", _i64, [_i64, _i64])
+_q4_table_len = _sig("externd_q4_table_len", _i64, [_i64, _i64, _i32])
+_gated_forward = _sig("externd_gated_forward", ctypes.c_int,
+                      [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _i32, _i32, _p, _p, _p, _p, _p, _size])
+_gated_forward_ws = _sig("externd_gated_forward_workspace_bytes", _size, [_i64, _i64, _i64])
+_gated_backward = _sig("externd_gated_backward", ctypes.c_int,
+                       [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _p, _i64, _i32, _i32, _p, _p, _p, _p, _p,
+                        _size])
+_gated_backward_ws = _sig("externd_gated_backward_workspace_bytes", _size, [_i64, _i64, _i64])
 _status_string = _sig("externd_status_string", ctypes.c_char_p, [ctypes.c_int])
 _last_error = _sig("externd_last_error", ctypes.c_char_p, [])
 
@@ -106,6 +130,10 @@ ABI_SYMBOLS = ("externd_decompose", "externd_decompose_noalloc", "externd_energy
                "externd_rank_for_energy",
                "externd_ternarize", "externd_project",
                "externd_gemv_t", "externd_gemv_n", "externd_deflate",
+               "externd_q4_code_words", "externd_q4_table_len", "externd_q4_quantize", "externd_q4_pack",
+               "externd_q4_reconstruct", "externd_q4_apply", "externd_q4_gated", "externd_q4_workspace_bytes",
+               "externd_gated_forward", "externd_gated_forward_workspace_bytes",
+               "externd_gated_backward", "externd_gated_backward_workspace_bytes",
                "externd_status_string", "externd_last_error")
 
 
@@ -448,3 +476,298 @@ def deflate(R, u_codes, v_codes, d):
     m, n = R.shape
     _check(_deflate(_ptr(R), m, n, _ptr(u_codes), _ptr(v_codes), float(d), _stream()))
     return R
+
+
+# ---- 4-bit weights with group scales, and the gated feed-forward block ----
+
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _op_device(*tensors):
+    """Index of the device that all tensors are on; it has to be the current one, whose stream the call uses."""
+    index = tensors[0].device.index
+    for t in tensors:
+        if not t.is_cuda:
+            raise TypeError("tensors must be CUDA (HIP) tensors")
+        if t.device.index != index:
+            raise ValueError("tensors are on different devices")
+    if index != torch.cuda.current_device():
+        raise ValueError("tensors are not on the current device")
+    return index
+
+
+def _act_code(act):
+    code = _ACT.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(_ACT)}, got {act!r}")
+    return code
+
+
+def _dtype_code(dtype, name):
+    code = _DTYPE.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _rows_of(x, cols, name):
+    """x with `cols` entries in its last dimension as (2-D tensor of unit column stride, row stride)."""
+    if x.dim() == 0 or x.shape[-1] != cols:
+        raise ValueError(f"{name} must have {cols} entries in its last dimension, got shape {tuple(x.shape)}")
+    if x.dim() != 2:
+        x = x.reshape(-1, cols)
+    tokens, ld = x.shape[0], x.stride(0)
+    if x.stride(1) != 1 and cols != 1 or ld < cols and tokens > 1:   # transposed, expanded or overlapping rows
+        x = x.contiguous()
+        ld = cols
+    return x, max(ld, cols)
+
+
+def _scratch(workspace):
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _out_or_new(out, shape, dtype, device, name="out"):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(out, dtype, name)
+    if tuple(out.shape) != tuple(shape) or out.device != device:
+        raise ValueError(f"{name} must have shape {tuple(shape)} on {device}")
+    return out
+
+
+class Q4:
+    """A weight matrix in 4 bits with group scales, in the library's layout.
+
+    codes: int32 words, scales and mins (None: symmetric): bfloat16, laid out as
+    include/externd.h says (tiles of 16 rows by chunks of 128 columns).
+    q4_quantize and q4_pack make them.  Its shape is (rows, cols)."""
+
+    __slots__ = ("codes", "scales", "mins", "rows", "cols", "group", "_c")
+
+    def __init__(self, codes, scales, mins, rows, cols, group):
+        words, table = _q4_code_words(rows, cols), _q4_table_len(rows, cols, group)
+        if words < 0 or table < 0:
+            raise ValueError("bad shape or group (32, 64 or 128)")
+        for t, dtype, n, name in ((codes, torch.int32, words, "codes"), (scales, torch.bfloat16, table, "scales"),
+                                  (mins, torch.bfloat16, table, "mins")):
+            if t is None and name == "mins":
+                continue
+            _need(t, dtype, name)
+            if t.numel() != n:
+                raise ValueError(f"{name} must hold {n} elements, got {t.numel()}")
+            if t.device != codes.device:
+                raise ValueError(f"{name} is on another device than codes")
+        self.codes, self.scales, self.mins = codes, scales, mins
+        self.rows, self.cols, self.group = rows, cols, group
+        self._c = _Q4(codes.data_ptr(), scales.data_ptr(), None if mins is None else mins.data_ptr(), rows, cols,
+                      group, 0)
+
+    @property
+    def shape(self):
+        return self.rows, self.cols
+
+    @property
+    def symmetric(self):
+        return self.mins is None
+
+    def __repr__(self):
+        return f"Q4({self.rows}x{self.cols}, group={self.group}, {'symmetric' if self.symmetric else 'with minima'})"
+
+
+def _q4_new(rows, cols, group, symmetric, device):
+    words, table = _q4_code_words(rows, cols), _q4_table_len(rows, cols, group)
+    if words < 0 or table < 0:
+        raise ValueError("bad shape or group (32, 64 or 128)")
+    codes = torch.empty((words,), dtype=torch.int32, device=device)
+    scales = torch.empty((table,), dtype=torch.bfloat16, device=device)
+    mins = None if symmetric else torch.empty((table,), dtype=torch.bfloat16, device=device)
+    return Q4(codes, scales, mins, rows, cols, group)
+
+
+def q4_quantize(W, group=32, symmetric=True):
+    """W (rows, cols; float32, bfloat16 or float16, unit column stride) to 4 bits: per group of
+    `group` entries of a row a bf16 scale and, unless symmetric, a bf16 minimum."""
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("W must be a 2-D tensor")
+    dtype = _dtype_code(W.dtype, "W")
+    _op_device(W)
+    W, ldw = _rows_of(W, W.shape[1], "W")
+    rows, cols = W.shape
+    q = _q4_new(rows, cols, group, symmetric, W.device)
+    _check(_q4_quantize(_ptr(W), rows, cols, ldw, dtype, group, _stream(), q._c.codes, q._c.scales, q._c.mins))
+    return q
+
+
+def q4_pack(codes, scales, mins=None, group=32):
+    """4-bit weights made elsewhere into the library's layout: codes uint8 (rows, cols) with values
+    0..15, scales and mins bfloat16 (rows, ceil(cols / group)).  Without mins a code c stands for
+    scale * (c - 8), with them for scale * c + min."""
+    _need(codes, torch.uint8, "codes")
+    if codes.dim() != 2:
+        raise ValueError("codes must be 2-D")
+    rows, cols = codes.shape
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    for t, name in ((scales, "scales"), (mins, "mins")):
+        if t is not None or name == "scales":
+            _need(t, torch.bfloat16, name)
+            if tuple(t.shape) != (rows, -(-cols // group)):
+                raise ValueError(f"{name} must have shape {(rows, -(-cols // group))}")
+    _op_device(*(t for t in (codes, scales, mins) if t is not None))
+    q = _q4_new(rows, cols, group, mins is None, codes.device)
+    _check(_q4_pack(_ptr(codes), _ptr(scales), _ptr(mins), rows, cols, group, _stream(), q._c.codes, q._c.scales,
+                    q._c.mins))
+    return q
+
+
+def q4_reconstruct(q, dtype=torch.float32):
+    """The values that q stands for, as a (rows, cols) tensor, each rounded once."""
+    code = _dtype_code(dtype, "dtype")
+    _op_device(q.codes)
+    out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
+    _check(_q4_reconstruct(q._c, code, _stream(), _ptr(out)))
+    return out
+
+
+def q4_workspace_bytes(cols, tokens, dtype):
+    """Device workspace that covers q4_apply and q4_gated on `tokens` rows of `cols` entries (0: invalid)."""
+    return int(_q4_ws(cols, tokens, _dtype_code(dtype, "dtype")))
+
+
+def q4_apply(q, x, out=None, workspace=None):
+    """y = x W^T with 4-bit W: x (..., cols) float32, bfloat16 or float16, y (..., rows) of its type.
+    Rows of x may be strided.  Where x needs a staged copy (float32, or rows that are not 16-byte
+    aligned) the library allocates it stream-ordered unless workspace (at least
+    q4_workspace_bytes(...) bytes, 256-byte aligned) is given.  Not differentiable."""
+    dtype = _dtype_code(x.dtype, "x")
+    _op_device(x, q.codes)
+    y = _out_or_new(out, x.shape[:-1] + (q.rows,), x.dtype, x.device)
+    x, ldx = _rows_of(x, q.cols, "x")
+    ws, wsb = _scratch(workspace)
+    _check(_q4_apply(q._c, x.data_ptr(), x.shape[0], ldx, dtype, _stream(), y.data_ptr(), ws, wsb))
+    return y
+
+
+def q4_gated(qg, qu, x, act="silu", out=None, workspace=None):
+    """h = act(x Wg^T) * (x Wu^T) with both matrices in 4 bits (one shape, group and kind), in one
+    kernel; everything else as q4_apply.  act: "silu", "gelu" (erf) or "gelu_tanh"."""
+    dtype = _dtype_code(x.dtype, "x")
+    _op_device(x, qg.codes, qu.codes)
+    h = _out_or_new(out, x.shape[:-1] + (qg.rows,), x.dtype, x.device)
+    x, ldx = _rows_of(x, qg.cols, "x")
+    ws, wsb = _scratch(workspace)
+    _check(_q4_gated(qg._c, qu._c, x.data_ptr(), x.shape[0], ldx, dtype, _act_code(act), _stream(), h.data_ptr(), ws,
+                     wsb))
+    return h
+
+
+def _gated_weights(x, Wg, Wu):
+    """Checks both weight matrices against x; returns (Wg, Wu, their common row stride, dtype code)."""
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"x must be bfloat16 or float16, got {x.dtype}")
+    for w, name in ((Wg, "Wg"), (Wu, "Wu")):
+        if w.dtype != x.dtype:
+            raise TypeError(f"{name} must be {x.dtype} like x, got {w.dtype}")
+        if w.dim() != 2 or w.shape != Wg.shape:
+            raise ValueError("Wg and Wu must be 2-D of one shape")
+    cols = Wg.shape[1]
+    Wg, ldg = _rows_of(Wg, cols, "Wg")
+    Wu, ldu = _rows_of(Wu, cols, "Wu")
+    if ldg != ldu:
+        Wg, Wu = Wg.contiguous(), Wu.contiguous()
+        ldg = cols
+    return Wg, Wu, ldg, _DTYPE[x.dtype]
+
+
+def gated_forward_workspace_bytes(tokens, cols, rows):
+    """Device workspace gated_forward needs (may be 0)."""
+    return int(_gated_forward_ws(tokens, cols, rows))
+
+
+def gated_backward_workspace_bytes(tokens, cols, rows):
+    """Device workspace gated_backward needs (0: invalid)."""
+    return int(_gated_backward_ws(tokens, cols, rows))
+
+
+def gated_forward(x, Wg, Wu, act="silu", save=False, out=None, workspace=None):
+    """h = act(x Wg^T) * (x Wu^T), the gated feed-forward block's first half, in one kernel.
+
+    x (..., cols) and Wg, Wu (rows, cols) bfloat16 or float16; h (..., rows) of their type.  With
+    save, returns (h, g, u): g and u are the projections (tokens, rows) in float32, which
+    gated_backward takes.  Rows of x and of the weights may be strided (both weights alike).  act:
+    "silu", "gelu" (erf) or "gelu_tanh".  See gated() for the differentiable form."""
+    act = _act_code(act)
+    _op_device(x, Wg, Wu)
+    Wg, Wu, ldw, dtype = _gated_weights(x, Wg, Wu)
+    rows, cols = Wg.shape
+    h = _out_or_new(out, x.shape[:-1] + (rows,), x.dtype, x.device)
+    x, ldx = _rows_of(x, cols, "x")
+    tokens = x.shape[0]
+    g = u = None
+    if save:
+        g, u = torch.empty((2, tokens, rows), dtype=torch.float32, device=x.device)
+    ws, wsb = _scratch(workspace)
+    _check(_gated_forward(x.data_ptr(), tokens, cols, ldx, Wg.data_ptr(), Wu.data_ptr(), rows, ldw, dtype, act,
+                          _stream(), h.data_ptr(), None if g is None else g.data_ptr(),
+                          None if u is None else u.data_ptr(), ws, wsb))
+    return (h, g, u) if save else h
+
+
+def gated_backward(x, Wg, Wu, g, u, dh, act="silu", need_dx=True, need_dw=True, workspace=None):
+    """(dx, dWg, dWu) of the gated block from dh (..., rows) and the g, u that gated_forward(...,
+    save=True) returned; None for what need_dx / need_dw leave out."""
+    act = _act_code(act)
+    _op_device(x, Wg, Wu, g, u, dh)
+    Wg, Wu, ldw, dtype = _gated_weights(x, Wg, Wu)
+    rows, cols = Wg.shape
+    shape = x.shape
+    x, ldx = _rows_of(x, cols, "x")
+    tokens = x.shape[0]
+    if dh.dtype != x.dtype:
+        raise TypeError(f"dh must be {x.dtype} like x, got {dh.dtype}")
+    if dh.shape[:-1] != shape[:-1]:
+        raise ValueError("dh and x must have the same leading dimensions")
+    dh, lddh = _rows_of(dh, rows, "dh")
+    for t, name in ((g, "g"), (u, "u")):
+        _need(t, torch.float32, name)
+        if t.numel() != tokens * rows:
+            raise ValueError(f"{name} must have {tokens} x {rows} entries")
+    dx = torch.empty(shape, dtype=x.dtype, device=x.device) if need_dx else None
+    dwg = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if need_dw else None
+    dwu = torch.empty_like(dwg) if need_dw else None
+    ws, wsb = _scratch(workspace)
+    _check(_gated_backward(x.data_ptr(), tokens, cols, ldx, Wg.data_ptr(), Wu.data_ptr(), rows, ldw, g.data_ptr(),
+                           u.data_ptr(), dh.data_ptr(), lddh, dtype, act, _stream(), _ptr(dx), _ptr(dwg), _ptr(dwu),
+                           ws, wsb))
+    return dx, dwg, dwu
+
+
+class _Gated(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, Wg, Wu, act):
+        ctx.act = act
+        if not any(ctx.needs_input_grad[:3]):
+            return gated_forward(x, Wg, Wu, act)
+        h, g, u = gated_forward(x, Wg, Wu, act, save=True)
+        ctx.save_for_backward(x, Wg, Wu, g, u)
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        x, Wg, Wu, g, u = ctx.saved_tensors
+        need_dx, need_dg, need_du = ctx.needs_input_grad[:3]
+        dx, dwg, dwu = gated_backward(x, Wg, Wu, g, u, dh, ctx.act, need_dx, need_dg or need_du)
+        return dx, dwg if need_dg else None, dwu if need_du else None, None
+
+
+def gated(x, Wg, Wu, act="silu"):
+    """gated_forward as a differentiable torch operation (gradients of x, Wg and Wu; g and u are kept
+    in float32 only where a gradient is needed)."""
+    return _Gated.apply(x, Wg, Wu, act)

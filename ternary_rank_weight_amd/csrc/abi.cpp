@@ -115,6 +115,70 @@ int get_ws(Workspace& w, const externd_opts& o, size_t bytes, hipStream_t s) {
   return EXTERND_OK;
 }
 
+// The caller's workspace when given (checked), else a stream-ordered one;
+// nothing when none is needed.
+int op_ws(Workspace& w, void* workspace, size_t workspace_bytes, size_t need, hipStream_t s) {
+  if (need == 0) return EXTERND_OK;
+  if (!workspace) return alloc_ws(w, need, s);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < need)
+    return fail(EXTERND_EINVAL, "workspace must be 256-byte aligned and at least %zu bytes", need);
+  w.ptr = workspace;
+  return EXTERND_OK;
+}
+
+bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+size_t dtype_bytes(int dtype) { return dtype == EXTERND_F32 ? 4 : 2; }
+bool bad_dtype(int dtype) { return dtype != EXTERND_F32 && dtype != EXTERND_BF16 && dtype != EXTERND_F16; }
+bool bad_act(int act) { return act != EXTERND_ACT_SILU && act != EXTERND_ACT_GELU && act != EXTERND_ACT_GELU_TANH; }
+bool bad_group(int group) { return group != 32 && group != 64 && group != 128; }
+// Row strides: at least the row, and small enough that offsets fit 63 bits with room.
+bool bad_stride(int64_t ld, int64_t cols) { return ld < cols || ld > int64_t(1) << 40; }
+constexpr int64_t kMaxTokens = int64_t(1) << 20;   // of the 4-bit products
+
+int check_q4(const externd_q4* w, const char* name) {
+  if (!w) return fail(EXTERND_EINVAL, "null %s", name);
+  if (bad_size(w->rows, w->cols)) return fail(EXTERND_EINVAL, "%s: bad shape", name);
+  if (bad_group(w->group)) return fail(EXTERND_EINVAL, "%s: group must be 32, 64 or 128", name);
+  if (!w->codes || !w->scales) return fail(EXTERND_EINVAL, "%s: null codes or scales", name);
+  if (!aligned_to(w->codes, 16) || !aligned_to(w->scales, 8) || !aligned_to(w->mins, 8))
+    return fail(EXTERND_EINVAL, "%s: codes must be 16-byte and tables 8-byte aligned", name);
+  return EXTERND_OK;
+}
+
+// The common part of the 4-bit products.
+int q4_product(const externd_q4* w, int mats, const void* x, int64_t tokens, int64_t ldx, int dtype, int act,
+               void* stream, void* y, void* workspace, size_t workspace_bytes) {
+  if (bad_dtype(dtype)) return fail(EXTERND_EINVAL, "unknown dtype %d", dtype);
+  if (tokens < 0 || tokens > kMaxTokens) return fail(EXTERND_EINVAL, "tokens must be 0 to 2^20");
+  if (bad_stride(ldx, w->cols)) return fail(EXTERND_EINVAL, "ldx must be at least the columns");
+  if (tokens == 0) return EXTERND_OK;
+  if (!x || !y) return fail(EXTERND_EINVAL, "null x or output pointer");
+  if (!aligned_to(x, dtype_bytes(dtype)) || !aligned_to(y, dtype_bytes(dtype)))
+    return fail(EXTERND_EINVAL, "x and the output must be aligned to their type");
+  int st = check_device(nullptr);
+  if (st != EXTERND_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t need = externd::q4_stages_x(w->cols, ldx, dtype, x) ? externd::q4_stage_bytes(w->cols, tokens, dtype) : 0;
+  Workspace ws;
+  if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
+  hipError_t e = externd::run_q4_apply(w, mats, x, tokens, ldx, dtype, act, y, ws.ptr, s);
+  if (e != hipSuccess) return hip_fail(e, "4-bit product");
+  return EXTERND_OK;
+}
+
+// Checks that both passes of the gated block share.
+int check_gated(const externd::GatedArgs& a) {
+  if (bad_dtype(a.dtype)) return fail(EXTERND_EINVAL, "unknown dtype %d", a.dtype);
+  if (a.dtype == EXTERND_F32) return fail(EXTERND_EUNSUPPORTED, "the gated block takes bf16 or fp16");
+  if (bad_act(a.act)) return fail(EXTERND_EINVAL, "unknown activation %d", a.act);
+  if (bad_size(a.rows, a.cols)) return fail(EXTERND_EINVAL, "bad weight shape");
+  if (a.tokens < 0 || (a.tokens > 0 && (bad_size(a.tokens, a.cols) || bad_size(a.tokens, a.rows))))
+    return fail(EXTERND_EINVAL, "bad number of tokens");
+  if (bad_stride(a.ldx, a.cols) || bad_stride(a.ldw, a.cols))
+    return fail(EXTERND_EINVAL, "ldx and ldw must be at least the columns");
+  return EXTERND_OK;
+}
+
 }  // namespace
 
 namespace externd {
@@ -496,6 +560,153 @@ int externd_deflate(float* R, int64_t m, int64_t n, const uint32_t* u_codes,
   hipError_t e = externd::launch_fill_f32(dptr, 1, d, s);
   if (e == hipSuccess) e = externd::launch_deflate(R, m, n, u_codes, v_codes, dptr, s);
   if (e != hipSuccess) return hip_fail(e, "deflate");
+  return EXTERND_OK;
+}
+
+int64_t externd_q4_code_words(int64_t rows, int64_t cols) {
+  if (bad_size(rows, cols)) return -1;
+  return (rows + 15) / 16 * ((cols + 127) / 128) * 256;
+}
+
+int64_t externd_q4_table_len(int64_t rows, int64_t cols, int32_t group) {
+  if (bad_size(rows, cols) || bad_group(group)) return -1;
+  return (rows + 15) / 16 * ((cols + 127) / 128) * 16 * (128 / group);
+}
+
+size_t externd_q4_workspace_bytes(int64_t cols, int64_t tokens, int32_t dtype) {
+  if (bad_size(1, cols) || tokens < 0 || tokens > kMaxTokens || bad_dtype(dtype)) return 0;
+  return externd::q4_stage_bytes(cols, tokens, dtype);
+}
+
+int externd_q4_quantize(const void* W, int64_t rows, int64_t cols, int64_t ldw, int32_t dtype, int32_t group,
+                        void* stream, uint32_t* codes, uint16_t* scales, uint16_t* mins) {
+  if (!W) return fail(EXTERND_EINVAL, "null W");
+  if (bad_dtype(dtype)) return fail(EXTERND_EINVAL, "unknown dtype %d", dtype);
+  if (bad_size(rows, cols) || bad_stride(ldw, cols)) return fail(EXTERND_EINVAL, "bad shape or stride");
+  if (!aligned_to(W, dtype_bytes(dtype))) return fail(EXTERND_EINVAL, "W must be aligned to its type");
+  const externd_q4 w = {codes, scales, mins, rows, cols, group, 0};
+  int st = check_q4(&w, "output");
+  if (st != EXTERND_OK) return st;
+  if ((st = check_device(nullptr)) != EXTERND_OK) return st;
+  hipError_t e = externd::run_q4_quantize(W, rows, cols, ldw, dtype, group, codes, scales, mins,
+                                          static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "q4_quantize");
+  return EXTERND_OK;
+}
+
+int externd_q4_pack(const uint8_t* codes_in, const uint16_t* scales_in, const uint16_t* mins_in, int64_t rows,
+                    int64_t cols, int32_t group, void* stream, uint32_t* codes, uint16_t* scales, uint16_t* mins) {
+  if (!codes_in || !scales_in) return fail(EXTERND_EINVAL, "null input");
+  if ((mins_in == nullptr) != (mins == nullptr)) return fail(EXTERND_EINVAL, "mins_in and mins go together");
+  if (!aligned_to(scales_in, 2) || !aligned_to(mins_in, 2)) return fail(EXTERND_EINVAL, "misaligned input");
+  const externd_q4 w = {codes, scales, mins, rows, cols, group, 0};
+  int st = check_q4(&w, "output");
+  if (st != EXTERND_OK) return st;
+  if ((st = check_device(nullptr)) != EXTERND_OK) return st;
+  hipError_t e = externd::run_q4_pack(codes_in, scales_in, mins_in, rows, cols, group, codes, scales, mins,
+                                      static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "q4_pack");
+  return EXTERND_OK;
+}
+
+int externd_q4_reconstruct(const externd_q4* w, int32_t dtype, void* stream, void* out) {
+  int st = check_q4(w, "weights");
+  if (st != EXTERND_OK) return st;
+  if (bad_dtype(dtype)) return fail(EXTERND_EINVAL, "unknown dtype %d", dtype);
+  if (!out || !aligned_to(out, dtype_bytes(dtype))) return fail(EXTERND_EINVAL, "null or misaligned output");
+  if ((st = check_device(nullptr)) != EXTERND_OK) return st;
+  hipError_t e = externd::run_q4_reconstruct(*w, dtype, out, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "q4_reconstruct");
+  return EXTERND_OK;
+}
+
+int externd_q4_apply(const externd_q4* w, const void* x, int64_t tokens, int64_t ldx, int32_t dtype, void* stream,
+                     void* y, void* workspace, size_t workspace_bytes) {
+  int st = check_q4(w, "weights");
+  if (st != EXTERND_OK) return st;
+  return q4_product(w, 1, x, tokens, ldx, dtype, EXTERND_ACT_SILU, stream, y, workspace, workspace_bytes);
+}
+
+int externd_q4_gated(const externd_q4* wg, const externd_q4* wu, const void* x, int64_t tokens, int64_t ldx,
+                     int32_t dtype, int32_t act, void* stream, void* h, void* workspace, size_t workspace_bytes) {
+  int st = check_q4(wg, "gate weights");
+  if (st != EXTERND_OK) return st;
+  if ((st = check_q4(wu, "up weights")) != EXTERND_OK) return st;
+  if (wg->rows != wu->rows || wg->cols != wu->cols || wg->group != wu->group ||
+      (wg->mins == nullptr) != (wu->mins == nullptr))
+    return fail(EXTERND_EINVAL, "gate and up weights differ in shape, group or kind");
+  if (bad_act(act)) return fail(EXTERND_EINVAL, "unknown activation %d", act);
+  const externd_q4 both[2] = {*wg, *wu};
+  return q4_product(both, 2, x, tokens, ldx, dtype, act, stream, h, workspace, workspace_bytes);
+}
+
+size_t externd_gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows) {
+  if (bad_size(rows, cols) || tokens < 1 || bad_size(tokens, cols) || bad_size(tokens, rows)) return 0;
+  return externd::gated_forward_workspace_bytes(tokens, cols, rows);
+}
+
+int externd_gated_forward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wg, const void* wu,
+                          int64_t rows, int64_t ldw, int32_t dtype, int32_t act, void* stream, void* h, float* g,
+                          float* u, void* workspace, size_t workspace_bytes) {
+  externd::GatedArgs a = {};
+  a.x = x; a.wg = wg; a.wu = wu;
+  a.tokens = tokens; a.cols = cols; a.rows = rows;
+  a.ldx = ldx; a.ldw = ldw;
+  a.dtype = dtype; a.act = act;
+  a.h = h; a.g = g; a.u = u;
+  int st = check_gated(a);
+  if (st != EXTERND_OK) return st;
+  if ((g == nullptr) != (u == nullptr)) return fail(EXTERND_EINVAL, "g and u go together");
+  if (tokens == 0) return EXTERND_OK;
+  if (!x || !wg || !wu || !h) return fail(EXTERND_EINVAL, "null pointer");
+  if (!aligned_to(x, 2) || !aligned_to(wg, 2) || !aligned_to(wu, 2) || !aligned_to(h, 2) || !aligned_to(g, 4) ||
+      !aligned_to(u, 4))
+    return fail(EXTERND_EINVAL, "pointers must be aligned to their type");
+  if ((st = check_device(nullptr)) != EXTERND_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Workspace ws;
+  if ((st = op_ws(ws, workspace, workspace_bytes, externd::gated_forward_workspace_bytes(tokens, cols, rows), s)) !=
+      EXTERND_OK)
+    return st;
+  hipError_t e = externd::run_gated_forward(a, ws.ptr, s);
+  if (e != hipSuccess) return hip_fail(e, "gated forward");
+  return EXTERND_OK;
+}
+
+size_t externd_gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows) {
+  if (bad_size(rows, cols) || tokens < 1 || bad_size(tokens, cols) || bad_size(tokens, rows)) return 0;
+  return externd::gated_backward_workspace_bytes(tokens, cols, rows);
+}
+
+int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wg, const void* wu,
+                           int64_t rows, int64_t ldw, const float* g, const float* u, const void* dh, int64_t lddh,
+                           int32_t dtype, int32_t act, void* stream, void* dx, void* dwg, void* dwu, void* workspace,
+                           size_t workspace_bytes) {
+  externd::GatedArgs a = {};
+  a.x = x; a.wg = wg; a.wu = wu;
+  a.tokens = tokens; a.cols = cols; a.rows = rows;
+  a.ldx = ldx; a.ldw = ldw;
+  a.dtype = dtype; a.act = act;
+  a.g = const_cast<float*>(g); a.u = const_cast<float*>(u);
+  a.dh = dh; a.lddh = lddh;
+  a.dx = dx; a.dwg = dwg; a.dwu = dwu;
+  int st = check_gated(a);
+  if (st != EXTERND_OK) return st;
+  if (bad_stride(lddh, rows)) return fail(EXTERND_EINVAL, "lddh must be at least the rows of the weights");
+  if ((dwg == nullptr) != (dwu == nullptr)) return fail(EXTERND_EINVAL, "dwg and dwu go together");
+  if (!dx && !dwg) return EXTERND_OK;
+  if (tokens > 0 && (!x || !wg || !wu || !g || !u || !dh)) return fail(EXTERND_EINVAL, "null pointer");
+  if (tokens == 0 && !dwg) return EXTERND_OK;
+  if (!aligned_to(x, 2) || !aligned_to(wg, 2) || !aligned_to(wu, 2) || !aligned_to(dh, 2) || !aligned_to(dx, 2) ||
+      !aligned_to(dwg, 2) || !aligned_to(dwu, 2) || !aligned_to(g, 4) || !aligned_to(u, 4))
+    return fail(EXTERND_EINVAL, "pointers must be aligned to their type");
+  if ((st = check_device(nullptr)) != EXTERND_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Workspace ws;
+  const size_t need = tokens > 0 ? externd::gated_backward_workspace_bytes(tokens, cols, rows) : 0;
+  if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
+  hipError_t e = externd::run_gated_backward(a, ws.ptr, s);
+  if (e != hipSuccess) return hip_fail(e, "gated backward");
   return EXTERND_OK;
 }
 

@@ -1,0 +1,58 @@
+// The gated block's activations and their slopes, in fp32.
+//   silu      g / (1 + exp(-g))
+//   gelu      g (1 + erf(g / sqrt 2)) / 2
+//   gelu_tanh g (1 + tanh(z)) / 2 = g / (1 + exp(-2 z)),  z = sqrt(2 / pi) (g + 0.044715 g^3)
+// Each holds over the whole fp32 range: exp of a large argument is inf, and
+// the quotient by it 0.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "../../include/externd.h"
+
+namespace externd {
+
+__device__ __forceinline__ float sigmoid_f32(float z) { return 1.f / (1.f + expf(-z)); }
+
+// Twice the tanh form's z, and its slope in g.
+__device__ __forceinline__ float gelu_2z(float g) { return 1.5957691216057308f * g * (1.f + 0.044715f * g * g); }
+__device__ __forceinline__ float gelu_2z_slope(float g) { return 1.5957691216057308f * (1.f + 0.134145f * g * g); }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+  if constexpr (ACT == EXTERND_ACT_SILU) return g * sigmoid_f32(g);
+  else if constexpr (ACT == EXTERND_ACT_GELU) return 0.5f * g * erfcf(-0.7071067811865476f * g);
+  else return g * sigmoid_f32(gelu_2z(g));
+}
+
+// act(g) and act'(g).
+template <int ACT>
+__device__ __forceinline__ void act_both(float g, float& a, float& slope) {
+  if constexpr (ACT == EXTERND_ACT_SILU) {
+    const float p = sigmoid_f32(g);
+    a = g * p;
+    slope = p + a * (1.f - p);
+  } else if constexpr (ACT == EXTERND_ACT_GELU) {
+    const float phi = 0.5f * erfcf(-0.7071067811865476f * g);
+    a = g * phi;
+    slope = phi + g * 0.3989422804014327f * expf(-0.5f * g * g);
+  } else {
+    const float p = sigmoid_f32(gelu_2z(g));
+    a = g * p;
+    // 0 where p is 0 or 1: the cubic may overflow there
+    const float q = p * (1.f - p);
+    slope = p + (q == 0.f ? 0.f : g * q * gelu_2z_slope(g));
+  }
+}
+
+__device__ __forceinline__ float act_value(int act, float g) {
+  if (act == EXTERND_ACT_SILU) return act_value<EXTERND_ACT_SILU>(g);
+  if (act == EXTERND_ACT_GELU) return act_value<EXTERND_ACT_GELU>(g);
+  return act_value<EXTERND_ACT_GELU_TANH>(g);
+}
+__device__ __forceinline__ void act_both(int act, float g, float& a, float& slope) {
+  if (act == EXTERND_ACT_SILU) act_both<EXTERND_ACT_SILU>(g, a, slope);
+  else if (act == EXTERND_ACT_GELU) act_both<EXTERND_ACT_GELU>(g, a, slope);
+  else act_both<EXTERND_ACT_GELU_TANH>(g, a, slope);
+}
+
+}  // namespace externd

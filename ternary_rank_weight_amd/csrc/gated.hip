@@ -1,0 +1,446 @@
+// The gated feed-forward block: g = x Wg^T, u = x Wu^T, h = act(g) u in one
+// kernel, and its backward pass
+//   dg = dh u act'(g), du = dh act(g)           (one pass over T x F)
+//   dx = dg Wg + du Wu                          (one product over 2 F)
+//   dWg = dg^T x, dWu = du^T x                  (one launch)
+// for T tokens, K columns (the model's width) and F rows of each weight
+// matrix (the hidden width).
+//
+// All products are one tiled kernel on the bf16/fp16 matrix instructions with
+// fp32 sums, k_gated_gemm, in three forms that differ in where an operand's
+// entries lie along the contraction: neighbours in a row ("rows", forward), or
+// one per row ("cols": both operands of dW, the weights of dx), which is read
+// from LDS with the transposing 64-bit read.  Both weight matrices share a
+// forward tile, gate and up rows of the same hidden units, so that the
+// activation and the product are done on the accumulators and neither g nor u
+// goes to memory unless the caller keeps them for the backward pass.  They are
+// kept in fp32: dg and du are then the only roundings that the gradients see
+// besides their own (16-bit g and u would add two more of the same size).
+#include <algorithm>
+
+#include "activation.hpp"
+#include "device_common.hpp"
+#include "frag.hpp"
+#include "kernels.hpp"
+
+namespace externd {
+
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+enum { kFwd = 0, kDx = 1, kDw = 2 };
+constexpr int kBK = 64;   // contraction entries per step
+
+// One operand of a product: `outer` output rows (or columns) by `inner`
+// contraction entries.  Two sources: the forward's gate and up rows, dx's two
+// segments of the contraction, dW's two outputs.
+struct Operand {
+  const uint16_t* p[2];
+  int64_t ld;
+  int64_t outer;
+  int aligned;   // 16-byte loads to LDS apply (base, ld and, for cols, outer)
+};
+
+struct GemmArgs {
+  Operand a, b;         // a: output rows, b: output columns
+  int64_t inner;        // contraction length of one segment
+  int64_t steps;        // steps of the whole contraction (all segments)
+  int64_t split_steps;  // steps per split
+  int64_t mt, nt;       // tiles
+  uint16_t* out[2];     // forward: h; dx: dx; dw: dWg, dWu
+  int64_t ldo;          // columns of the outputs
+  float* save[2];       // forward: g, u (or null)
+  float* part;          // partial sums of a split contraction (or null)
+  int act;
+};
+
+// LDS image of an operand tile for one step: O outer entries x 64 contraction
+// entries in 16-byte slots.  Slots are permuted so that the 16 rows (or the
+// 4 k rows x 32 bytes per lane group) of a fragment read lie in different
+// banks; a slot's content is chosen by its source address, since loads to LDS
+// write lanes in order.
+template <bool COLS, int O>
+struct Tile {
+  static constexpr int kSlots = O * 8;
+  // contraction-major permutation: which 32-byte block of a k row holds block b
+  __device__ static int mix(int k) { return (k & 3) | (((k >> 3) & (O / 64 - 1)) << 2); }
+  // (outer, k) of a slot's first entry
+  __device__ static void place(int slot, int& o, int& k) {
+    if constexpr (!COLS) {
+      o = slot >> 3;
+      k = ((slot & 7) ^ (o & 7)) * 8;
+    } else {
+      constexpr int per = O / 8;
+      k = slot / per;
+      const int s = slot % per;
+      o = ((s >> 1) ^ mix(k)) * 16 + (s & 1) * 8;
+    }
+  }
+  // The fragment of outer entries o0 .. o0 + 15 and contraction entries 32 kk .. + 31.
+  __device__ static u32x4 frag(const uint16_t* lds, int o0, int kk, int lane) {
+    const int r = lane & 15, p = lane >> 4;
+    if constexpr (!COLS) {
+      const int o = o0 + r;
+      return *reinterpret_cast<const u32x4*>(lds + o * 64 + (((kk * 4 + p) ^ (o & 7)) * 8));
+    } else {
+      // two transposing reads of 4 k rows x 16 outer entries per lane group:
+      // lane r of a group supplies k row r / 4, entries 4 (r % 4) .. + 3, and
+      // receives entry r of the four rows
+      u32x4 v;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int k = kk * 32 + 8 * p + 4 * hf + (r >> 2);
+        const uint16_t* q = lds + k * O + (((o0 >> 4) ^ mix(k)) * 16) + 4 * (r & 3);
+        const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(__attribute__((address_space(3))) void*)(q));
+        const uint64_t b = __builtin_bit_cast(uint64_t, t);
+        v[2 * hf] = (uint32_t)b;
+        v[2 * hf + 1] = (uint32_t)(b >> 32);
+      }
+      return v;
+    }
+  }
+};
+
+// out tile = sum over k of A[m][k] B[n][k].  BM x BN outputs per workgroup of
+// WM x WN waves.  The products take b's fragment as first and a's as second
+// operand, so that a lane holds four neighbouring output columns of one row.
+template <bool BF, int MODE, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * kWave) void k_gated_gemm(GemmArgs g) {
+  constexpr int NTHR = WM * WN * kWave;
+  constexpr bool ACOLS = MODE == kDw, BCOLS = MODE != kFwd;
+  constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
+  using TA = Tile<ACOLS, BM>;
+  using TB = Tile<BCOLS, BN>;
+  constexpr int SA = TA::kSlots / NTHR, SB = TB::kSlots / NTHR;
+  __shared__ __align__(16) uint16_t la[2][BM * kBK];
+  __shared__ __align__(16) uint16_t lb[2][BN * kBK];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int wm = wave / WN, wn = wave % WN;
+
+  // tiles are numbered down groups of 8 tile rows, each XCD a run of them
+  int64_t id = blockIdx.x;
+  const int64_t total = (int64_t)g.mt * g.nt;
+  {
+    const int64_t x = id & 7, q = total / 8, rest = total % 8;
+    id = x * q + min(x, rest) + (id >> 3);
+  }
+  const int64_t group = 8 * g.nt, g0 = id / group * 8;
+  const int64_t gh = min<int64_t>(8, g.mt - g0);
+  const int64_t mt = g0 + (id % group) % gh, ntile = (id % group) / gh;
+
+  // which source and where
+  constexpr int BNO = MODE == kFwd ? BN / 2 : BN;   // output columns per tile
+  int64_t m0 = mt * BM;
+  const int64_t n0 = ntile * BNO;
+  int outsel = 0;
+  if constexpr (MODE == kDw) {   // tile rows: all of dWg, then all of dWu
+    const int64_t half = g.mt / 2;
+    outsel = mt >= half;
+    m0 = (mt - outsel * half) * BM;
+  }
+  const int64_t s_begin = (int64_t)blockIdx.y * g.split_steps;
+  const int64_t s_end = min(g.steps, s_begin + g.split_steps);
+  const int64_t seg_steps = MODE == kDx ? g.steps / 2 : g.steps;
+
+  f32x4 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // source of a slot at contraction offset k0
+  auto src_a = [&](int slot, int seg, int64_t k0, int64_t& left_o, int64_t& left_k) -> const uint16_t* {
+    int o, k;
+    TA::place(slot, o, k);
+    const uint16_t* base = g.a.p[MODE == kDx ? seg : outsel];
+    left_o = g.a.outer - (m0 + o);
+    left_k = g.inner - (k0 + k);
+    if constexpr (!ACOLS) return base + min(m0 + o, g.a.outer - 1) * g.a.ld + (k0 + k);
+    else return base + (k0 + k) * g.a.ld + (m0 + o);
+  };
+  auto src_b = [&](int slot, int seg, int64_t k0, int64_t& left_o, int64_t& left_k) -> const uint16_t* {
+    int o, k;
+    TB::place(slot, o, k);
+    if constexpr (MODE == kFwd) {   // the tile's first half gate rows, its second up rows
+      const int which = o >= BNO;
+      o -= which * BNO;
+      left_o = 8;
+      left_k = g.inner - (k0 + k);
+      return g.b.p[which] + min(n0 + o, g.b.outer - 1) * g.b.ld + (k0 + k);
+    } else {
+      const uint16_t* base = g.b.p[MODE == kDx ? seg : 0];
+      left_o = g.b.outer - (n0 + o);
+      left_k = g.inner - (k0 + k);
+      return base + (k0 + k) * g.b.ld + (n0 + o);
+    }
+  };
+  // eight entries of a slot through registers, zero past either end
+  auto fetch = [&](const uint16_t* p, bool cols, int64_t left_o, int64_t left_k) -> u32x4 {
+    const int64_t n = cols ? (left_k > 0 ? left_o : 0) : left_k;
+    if (n >= 8) return (reinterpret_cast<uintptr_t>(p) & 15) == 0 ? load8<true>(p) : load8<false>(p);
+    return n > 0 ? load8_part(p, n) : u32x4{0u, 0u, 0u, 0u};
+  };
+  u32x4 ra[SA], rb[SB];
+  auto load = [&](int64_t step) {
+    const int seg = MODE == kDx ? (int)(step / seg_steps) : 0;
+    const int64_t k0 = (step - seg * seg_steps) * kBK;
+#pragma unroll
+    for (int i = 0; i < SA; ++i) {
+      int64_t lo, lk;
+      const uint16_t* p = src_a(i * NTHR + tid, seg, k0, lo, lk);
+      ra[i] = fetch(p, ACOLS, lo, lk);
+    }
+#pragma unroll
+    for (int i = 0; i < SB; ++i) {
+      int64_t lo, lk;
+      const uint16_t* p = src_b(i * NTHR + tid, seg, k0, lo, lk);
+      rb[i] = fetch(p, BCOLS, lo, lk);
+    }
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < SA; ++i) *reinterpret_cast<u32x4*>(&la[buf][(i * NTHR + tid) * 8]) = ra[i];
+#pragma unroll
+    for (int i = 0; i < SB; ++i) *reinterpret_cast<u32x4*>(&lb[buf][(i * NTHR + tid) * 8]) = rb[i];
+  };
+  auto compute = [&](int buf) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      u32x4 fa[MI], fb[NI];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) fa[i] = TA::frag(la[buf], (wm * MI + i) * 16, kk, lane);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        int o;
+        if constexpr (MODE == kFwd) o = (j / (NI / 2)) * BNO + (wn * (NI / 2) + j % (NI / 2)) * 16;
+        else o = (wn * NI + j) * 16;
+        fb[j] = TB::frag(lb[buf], o, kk, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = mfma16<BF>(fb[j], fa[i], acc[i][j]);
+    }
+  };
+
+  if (s_begin < s_end) {
+    load(s_begin);
+    store(0);
+  }
+  __syncthreads();
+  for (int64_t s = s_begin; s < s_end; ++s) {
+    const int buf = (int)(s - s_begin) & 1;
+    if (s + 1 < s_end) load(s + 1);
+    compute(buf);
+    if (s + 1 < s_end) store(buf ^ 1);
+    __syncthreads();
+  }
+
+  // ---- outputs: lane holds row m, columns n .. n + 3 of each fragment ----
+  const int r = lane & 15, p = lane >> 4;
+  const int64_t mend = MODE == kDw ? g.a.outer : g.a.outer;
+  const int64_t nend = g.ldo;
+  auto put16 = [&](uint16_t* row, int64_t n, const float (&v)[4]) {
+    if (n + 4 <= nend && (reinterpret_cast<uintptr_t>(row + n) & 7) == 0) {
+      uint2 w;
+      w.x = f32_to_16<BF>(v[0]) | (f32_to_16<BF>(v[1]) << 16);
+      w.y = f32_to_16<BF>(v[2]) | (f32_to_16<BF>(v[3]) << 16);
+      *reinterpret_cast<uint2*>(row + n) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < nend) row[n + e] = (uint16_t)f32_to_16<BF>(v[e]);
+    }
+  };
+  auto put32 = [&](float* row, int64_t n, const float (&v)[4]) {
+    if (n + 4 <= nend && (reinterpret_cast<uintptr_t>(row + n) & 15) == 0) {
+      *reinterpret_cast<float4*>(row + n) = float4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < nend) row[n + e] = v[e];
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t m = m0 + (wm * MI + i) * 16 + r;
+    if (m >= mend) continue;
+    if constexpr (MODE == kFwd) {
+#pragma unroll
+      for (int j = 0; j < NI / 2; ++j) {
+        const int64_t n = n0 + (wn * (NI / 2) + j) * 16 + 4 * p;
+        if (n >= nend) continue;
+        float gv[4], uv[4], hv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          gv[e] = acc[i][j][e];
+          uv[e] = acc[i][j + NI / 2][e];
+          hv[e] = act_value(g.act, gv[e]) * uv[e];
+        }
+        put16(g.out[0] + m * g.ldo, n, hv);
+        if (g.save[0]) {
+          put32(g.save[0] + m * g.ldo, n, gv);
+          put32(g.save[1] + m * g.ldo, n, uv);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const int64_t n = n0 + (wn * NI + j) * 16 + 4 * p;
+        if (n >= nend) continue;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e];
+        if (g.part) put32(g.part + ((int64_t)blockIdx.y * mend + m) * g.ldo, n, v);
+        else put16(g.out[outsel] + m * g.ldo, n, v);
+      }
+    }
+  }
+}
+
+// dg and du, rounded to the operands' type, in rows of ldd entries (a
+// multiple of 8; zero past the hidden width).  Bound by HBM: reads 4 + 4 + 2 bytes,
+// writes 2 + 2 per hidden unit and token.
+template <bool BF>
+__global__ __launch_bounds__(256) void k_gated_slopes(const float* __restrict__ g, const float* __restrict__ u,
+                                                       const uint16_t* __restrict__ dh, int64_t tokens, int64_t hidden,
+                                                       int64_t lddh, int64_t ldd, int act, uint16_t* __restrict__ dg,
+                                                       uint16_t* __restrict__ du) {
+  const int64_t total = tokens * (ldd / 4);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / (ldd / 4), c = (i - t * (ldd / 4)) * 4;
+    uint32_t og[4], ou[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      og[e] = ou[e] = 0u;
+      if (c + e < hidden) {
+        const float gv = g[t * hidden + c + e], uv = u[t * hidden + c + e];
+        const float d = f32_from_16<BF>(dh[t * lddh + c + e]);
+        float a, slope;
+        act_both(act, gv, a, slope);
+        og[e] = f32_to_16<BF>(d * uv * slope);
+        ou[e] = f32_to_16<BF>(d * a);
+      }
+    }
+    *reinterpret_cast<uint2*>(dg + t * ldd + c) = uint2{og[0] | (og[1] << 16), og[2] | (og[3] << 16)};
+    *reinterpret_cast<uint2*>(du + t * ldd + c) = uint2{ou[0] | (ou[1] << 16), ou[2] | (ou[3] << 16)};
+  }
+}
+
+// Zero outputs (a weight gradient of no tokens).
+__global__ void k_fill_u16(uint16_t* __restrict__ p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+    p[i] = 0;
+}
+
+template <int MODE, int BM, int BN, int WM, int WN>
+hipError_t launch_gemm(GemmArgs g, bool bf, int64_t splits, hipStream_t s) {
+  const dim3 grid((unsigned)(g.mt * g.nt), (unsigned)splits), block(WM * WN * kWave);
+  if (bf) hipLaunchKernelGGL((k_gated_gemm<true, MODE, BM, BN, WM, WN>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((k_gated_gemm<false, MODE, BM, BN, WM, WN>), grid, block, 0, s, g);
+  return hipGetLastError();
+}
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t padded(int64_t hidden) { return up(hidden, 8) * 8; }
+
+}  // namespace
+
+size_t gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows) {
+  (void)cols;
+  return (size_t)(2 * tokens * padded(rows)) * 2 + 256;
+}
+
+size_t gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows) {
+  (void)tokens; (void)cols; (void)rows;
+  return 0;
+}
+
+hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s) {
+  (void)ws;
+  GemmArgs g = {};
+  g.a.p[0] = static_cast<const uint16_t*>(a.x);
+  g.a.ld = a.ldx;
+  g.a.outer = a.tokens;
+  g.b.p[0] = static_cast<const uint16_t*>(a.wg);
+  g.b.p[1] = static_cast<const uint16_t*>(a.wu);
+  g.b.ld = a.ldw;
+  g.b.outer = a.rows;
+  g.inner = a.cols;
+  g.steps = g.split_steps = up(a.cols, kBK);
+  g.mt = up(a.tokens, 128);
+  g.nt = up(a.rows, 64);
+  g.out[0] = static_cast<uint16_t*>(a.h);
+  g.ldo = a.rows;
+  g.save[0] = a.g;
+  g.save[1] = a.u;
+  g.act = a.act;
+  return launch_gemm<kFwd, 128, 128, 2, 2>(g, a.dtype == EXTERND_BF16, 1, s);
+}
+
+hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
+  const bool bf = a.dtype == EXTERND_BF16;
+  hipError_t e;
+  if (a.tokens == 0) {
+    for (void* w : {a.dwg, a.dwu}) {
+      if (!w) continue;
+      hipLaunchKernelGGL(k_fill_u16, dim3(1024), dim3(256), 0, s, static_cast<uint16_t*>(w), a.rows * a.cols);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+  const int64_t ldd = padded(a.rows);
+  uint16_t* dg = reinterpret_cast<uint16_t*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~(uintptr_t)255);
+  uint16_t* du = dg + a.tokens * ldd;
+  {
+    const dim3 grid((unsigned)std::min<int64_t>(up(a.tokens * (ldd / 4), 256), 16384));
+    if (bf)
+      hipLaunchKernelGGL(k_gated_slopes<true>, grid, dim3(256), 0, s, a.g, a.u, static_cast<const uint16_t*>(a.dh),
+                         a.tokens, a.rows, a.lddh, ldd, a.act, dg, du);
+    else
+      hipLaunchKernelGGL(k_gated_slopes<false>, grid, dim3(256), 0, s, a.g, a.u, static_cast<const uint16_t*>(a.dh),
+                         a.tokens, a.rows, a.lddh, ldd, a.act, dg, du);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.dx) {
+    GemmArgs g = {};
+    g.a.p[0] = dg;
+    g.a.p[1] = du;
+    g.a.ld = ldd;
+    g.a.outer = a.tokens;
+    g.b.p[0] = static_cast<const uint16_t*>(a.wg);
+    g.b.p[1] = static_cast<const uint16_t*>(a.wu);
+    g.b.ld = a.ldw;
+    g.b.outer = a.cols;
+    g.inner = a.rows;
+    g.steps = g.split_steps = 2 * up(a.rows, kBK);
+    g.mt = up(a.tokens, 128);
+    g.nt = up(a.cols, 128);
+    g.out[0] = static_cast<uint16_t*>(a.dx);
+    g.ldo = a.cols;
+    if ((e = launch_gemm<kDx, 128, 128, 2, 2>(g, bf, 1, s)) != hipSuccess) return e;
+  }
+  if (a.dwg) {
+    GemmArgs g = {};
+    g.a.p[0] = dg;
+    g.a.p[1] = du;
+    g.a.ld = ldd;
+    g.a.outer = a.rows;
+    g.b.p[0] = static_cast<const uint16_t*>(a.x);
+    g.b.ld = a.ldx;
+    g.b.outer = a.cols;
+    g.inner = a.tokens;
+    g.steps = g.split_steps = up(a.tokens, kBK);
+    g.mt = 2 * up(a.rows, 128);
+    g.nt = up(a.cols, 128);
+    g.out[0] = static_cast<uint16_t*>(a.dwg);
+    g.out[1] = static_cast<uint16_t*>(a.dwu);
+    g.ldo = a.cols;
+    if ((e = launch_gemm<kDw, 128, 128, 2, 2>(g, bf, 1, s)) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace externd

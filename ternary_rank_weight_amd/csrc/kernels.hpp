@@ -146,4 +146,35 @@ size_t apply_workspace_bytes(int64_t m, int64_t k);
 hipError_t run_apply(const uint32_t* B2, const uint32_t* C2, const float* D, int64_t m, int64_t n, int64_t k,
                      const float* x, float* y, void* ws, hipStream_t s);
 
+// 4-bit weights with group scales (q4.hip).  q4_stages_x: whether x goes
+// through a staged 16-bit copy (fp32, or rows that are not 16-byte aligned);
+// then ws holds q4_stage_bytes, else it is null.
+bool q4_stages_x(int64_t cols, int64_t ldx, int dtype, const void* x);
+size_t q4_stage_bytes(int64_t cols, int64_t tokens, int dtype);
+hipError_t run_q4_quantize(const void* W, int64_t rows, int64_t cols, int64_t ldw, int dtype, int group, void* codes,
+                           uint16_t* scales, uint16_t* mins, hipStream_t s);
+hipError_t run_q4_pack(const uint8_t* src, const uint16_t* ssrc, const uint16_t* msrc, int64_t rows, int64_t cols,
+                       int group, void* codes, uint16_t* scales, uint16_t* mins, hipStream_t s);
+hipError_t run_q4_reconstruct(const externd_q4& w, int dtype, void* out, hipStream_t s);
+// w: one matrix (mats = 1, y = W x) or two (mats = 2, y = act(Wg x) (Wu x)).
+hipError_t run_q4_apply(const externd_q4* w, int mats, const void* x, int64_t tokens, int64_t ldx, int dtype, int act,
+                        void* y, void* ws, hipStream_t s);
+
+// gated feed-forward block on dense 16-bit weights (gated.hip)
+struct GatedArgs {
+  const void *x, *wg, *wu;
+  int64_t tokens, cols, rows;   // rows: hidden width
+  int64_t ldx, ldw;
+  int dtype, act;
+  void* h;                      // forward output
+  float *g, *u;                 // forward: saved (or null); backward: inputs
+  const void* dh;
+  int64_t lddh;
+  void *dx, *dwg, *dwu;         // backward outputs: dx or null; both of dwg and dwu or null
+};
+size_t gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows);
+hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s);
+size_t gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows);
+hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s);
+
 }  // namespace externd

@@ -1,0 +1,591 @@
+// 4-bit weights with group scales: quantization, the values they stand for,
+// and their products with a few tokens.
+//
+// A group is `group` (32, 64 or 128) neighbouring entries of a row, with a
+// bf16 scale s and, asymmetric, a bf16 minimum m:
+//
+//   symmetric   s = bf16(max|w| / 7),         c = clamp(rint(w / s), -8, 7) + 8,   value s (c - 8)
+//   asymmetric  s = bf16((max w - min w) / 15), m = bf16(min w),
+//               c = clamp(rint((w - m) / s), 0, 15),                               value s c + m
+//
+// (all steps in fp32, rounded once to the stored type; a group of scale 0
+// has c - 8 = 0 or c = 0).  The scales are bf16 because it has fp32's range:
+// no weight matrix overflows or loses its small groups.  Its 8 bits cost
+// nothing in the codes, which are chosen for the rounded scale.
+//
+// Layout: tiles of 16 rows x chunks of 128 columns.  A wave reads one tile
+// of one chunk with one 16-byte load per lane, 1 KB of neighbouring bytes:
+// lane r + 16 p holds row r, and its word i (0..3) the codes of columns
+// 32 i + 8 p + j, which are exactly the entries that lane holds in the i-th
+// 16x16x32 product of the chunk.  So nothing is moved between lanes, and each
+// product stays inside one group.  Code j = 2 s sits at bits 4 s, code
+// j = 2 s + 1 at bits 16 + 4 s: one shift and one and-or give two operand entries.
+// The scales (and minima) of a tile of a chunk are 16 x 128 / group
+// neighbouring bf16 values.
+#include <algorithm>
+
+#include "activation.hpp"
+#include "device_common.hpp"
+#include "frag.hpp"
+#include "kernels.hpp"
+
+namespace externd {
+
+namespace {
+
+constexpr int kTile = 16, kChunk = 128;
+
+// ---- quantize, pack, reconstruct: one wave per (tile, chunk) ----
+
+struct Place {
+  int64_t tile, chunk, row, col;   // col: the lane's first column of word 0
+  int r, p;
+};
+__device__ inline Place place_of(int64_t job, int64_t chunks, int lane) {
+  Place q;
+  q.tile = job / chunks;
+  q.chunk = job - q.tile * chunks;
+  q.r = lane & 15;
+  q.p = lane >> 4;
+  q.row = kTile * q.tile + q.r;
+  q.col = kChunk * q.chunk + 8 * q.p;
+  return q;
+}
+
+// Eight codes as a word of the layout.
+__device__ inline uint32_t pack_word(const uint32_t (&c)[8]) {
+  uint32_t w = 0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w |= (c[j] & 15u) << (4 * (j >> 1) + 16 * (j & 1));
+  return w;
+}
+
+// Entries col .. col + 7 of a row as fp32 (0 past the end); n: entries left in the row.
+template <int DT>
+__device__ inline void load_weights(const void* W, int64_t at, int64_t n, float (&w)[8]) {
+  if constexpr (DT == EXTERND_F32) {
+    const float* p = static_cast<const float*>(W) + at;
+    if (n >= 8) {
+      const u32x4_a4 a = *reinterpret_cast<const u32x4_a4*>(p), b = *reinterpret_cast<const u32x4_a4*>(p + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { w[j] = __uint_as_float(a[j]); w[4 + j] = __uint_as_float(b[j]); }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = j < n ? p[j] : 0.f;
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(W) + at;
+    u32x4 v;
+    if (n >= 8) v = (reinterpret_cast<uintptr_t>(p) & 15) == 0 ? load8<true>(p) : load8<false>(p);
+    else v = load8_part(p, n);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = f32_from_16<DT == EXTERND_BF16>((v[j / 2] >> (16 * (j & 1))) & 0xffffu);
+  }
+}
+
+// Max of a value over the four lanes that share a row.
+__device__ inline float row_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, kWave));
+  return fmaxf(v, __shfl_xor(v, 32, kWave));
+}
+
+// Bound by HBM: one read of the matrix, one write of 4.5 to 5 bits per entry.
+template <int DT, int GPC, bool MINS>
+__global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ W, int64_t rows, int64_t cols,
+                                                      int64_t ldw, int64_t chunks, int64_t jobs,
+                                                      u32x4* __restrict__ codes, uint16_t* __restrict__ scales,
+                                                      uint16_t* __restrict__ mins) {
+  constexpr int SPG = 4 / GPC;   // words (of 32 columns) per group
+  const int lane = threadIdx.x & (kWave - 1);
+  for (int64_t job = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; job < jobs; job += 4 * (int64_t)gridDim.x) {
+    const Place q = place_of(job, chunks, lane);
+    float w[4][8];
+    int64_t left[4];
+  #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      left[i] = q.row < rows ? cols - q.col - 32 * i : 0;
+      load_weights<DT>(W, q.row * ldw + q.col + 32 * i, left[i], w[i]);
+    }
+    u32x4 out;
+  #pragma unroll
+    for (int g = 0; g < GPC; ++g) {
+      float top = 0.f, low = INFINITY, high = -INFINITY, bad = 0.f;
+  #pragma unroll
+      for (int i = g * SPG; i < (g + 1) * SPG; ++i)
+  #pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float v = w[i][j];
+          if (j < left[i]) {
+            if (!(fabsf(v) < INFINITY)) bad = 1.f;   // fmaxf drops a NaN: remember it
+            if constexpr (MINS) { low = fminf(low, v); high = fmaxf(high, v); }
+            else top = fmaxf(top, fabsf(v));
+          }
+        }
+      float s, m = 0.f;
+      if constexpr (MINS) {
+        high = row_max(high);
+        low = -row_max(-low);
+        const bool any = low <= high;   // a group past the row's end has scale and minimum 0
+        s = any ? bf16_to_f32(f32_to_bf16((high - low) / 15.f)) : 0.f;
+        m = any ? bf16_to_f32(f32_to_bf16(low)) : 0.f;
+      } else {
+        s = bf16_to_f32(f32_to_bf16(row_max(top) / 7.f));
+      }
+      if (row_max(bad) != 0.f || !(s < INFINITY) || !(fabsf(m) < INFINITY)) s = m = NAN;
+      const bool on = s > 0.f;
+  #pragma unroll
+      for (int i = g * SPG; i < (g + 1) * SPG; ++i) {
+        uint32_t c[8];
+  #pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (MINS) {
+            const float t = on ? rintf((w[i][j] - m) / s) : 0.f;
+            c[j] = j < left[i] ? (uint32_t)fminf(fmaxf(t, 0.f), 15.f) : 0u;
+          } else {
+            const float t = on ? rintf(w[i][j] / s) : 0.f;
+            c[j] = j < left[i] ? (uint32_t)(fminf(fmaxf(t, -8.f), 7.f) + 8.f) : 8u;
+          }
+        }
+        out[i] = pack_word(c);
+      }
+      if (q.p == 0) {
+        scales[(job * kTile + q.r) * GPC + g] = (uint16_t)f32_to_bf16(s);
+        if constexpr (MINS) mins[(job * kTile + q.r) * GPC + g] = (uint16_t)f32_to_bf16(m);
+      }
+    }
+    codes[job * kWave + lane] = out;
+  }
+}
+
+// Codes one byte each and tables row by row (rows x ceil(cols / group)) into
+// the layout; padding gets code 0, scale 0, minimum 0.
+__global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ src, const uint16_t* __restrict__ ssrc,
+                                                  const uint16_t* __restrict__ msrc, int64_t rows, int64_t cols,
+                                                  int gpc, int64_t chunks, int64_t jobs, u32x4* __restrict__ codes,
+                                                  uint16_t* __restrict__ scales, uint16_t* __restrict__ mins) {
+  const int lane = threadIdx.x & (kWave - 1);
+  for (int64_t job = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; job < jobs; job += 4 * (int64_t)gridDim.x) {
+    const Place q = place_of(job, chunks, lane);
+    u32x4 out;
+  #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t left = q.row < rows ? cols - q.col - 32 * i : 0;
+      uint32_t c[8];
+  #pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = j < left ? src[q.row * cols + q.col + 32 * i + j] : 0u;
+      out[i] = pack_word(c);
+    }
+    codes[job * kWave + lane] = out;
+    const int64_t groups = (cols + kChunk / gpc - 1) / (kChunk / gpc);
+    if (q.p < gpc) {   // lane (r, p) moves group p of row r
+      const int64_t g = q.chunk * gpc + q.p;
+      const bool ok = q.row < rows && g < groups;
+      scales[(job * kTile + q.r) * gpc + q.p] = ok ? ssrc[q.row * groups + g] : (uint16_t)0;
+      if (msrc) mins[(job * kTile + q.r) * gpc + q.p] = ok ? msrc[q.row * groups + g] : (uint16_t)0;
+    }
+  }
+}
+
+// The values, rounded once to the output's type.  Bound by HBM: the write.
+template <int DT>
+__global__ __launch_bounds__(256) void k_q4_reconstruct(const u32x4* __restrict__ codes,
+                                                         const uint16_t* __restrict__ scales,
+                                                         const uint16_t* __restrict__ mins, int64_t rows, int64_t cols,
+                                                         int gpc, int64_t chunks, int64_t jobs, void* __restrict__ out) {
+  const int lane = threadIdx.x & (kWave - 1);
+  for (int64_t job = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; job < jobs; job += 4 * (int64_t)gridDim.x) {
+    const Place q = place_of(job, chunks, lane);
+    if (q.row >= rows) continue;
+    const u32x4 cw = codes[job * kWave + lane];
+  #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t col = q.col + 32 * i, left = cols - col;
+      if (left <= 0) break;
+      const int64_t at = (job * kTile + q.r) * gpc + i * gpc / 4;
+      const float s = bf16_to_f32(scales[at]);
+      const float m = mins ? bf16_to_f32(mins[at]) : 0.f;
+      const float mid = mins ? 0.f : 8.f;
+      float v[8];
+  #pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t c = (cw[i] >> (4 * (j >> 1) + 16 * (j & 1))) & 15u;
+        v[j] = s * ((float)c - mid) + m;   // the product is exact: 8 by 4 bits
+      }
+      if constexpr (DT == EXTERND_F32) {
+        float* p = static_cast<float*>(out) + q.row * cols + col;
+        if (left >= 8) {
+          u32x4 a, b;
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) { a[j] = __float_as_uint(v[j]); b[j] = __float_as_uint(v[4 + j]); }
+          *reinterpret_cast<u32x4_a4*>(p) = a;
+          *reinterpret_cast<u32x4_a4*>(p + 4) = b;
+        } else {
+  #pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < left) p[j] = v[j];
+        }
+      } else {
+        constexpr bool BF = DT == EXTERND_BF16;
+        uint16_t* p = static_cast<uint16_t*>(out) + q.row * cols + col;
+        if (left >= 8 && (reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+          u32x4 a;
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) a[j] = f32_to_16<BF>(v[2 * j]) | (f32_to_16<BF>(v[2 * j + 1]) << 16);
+          *reinterpret_cast<u32x4_a4*>(p) = a;
+        } else {
+  #pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < left) p[j] = (uint16_t)f32_to_16<BF>(v[j]);
+        }
+      }
+    }
+  }
+}
+
+// ---- products ----
+
+// x for the products where it is not already 16-bit rows of 16-byte
+// alignment: rows of chunks * 128 entries, zero past the end.  fp32 x becomes
+// three bf16 rows per token that add up to it exactly (8 of its 24 bits each).
+template <int DT>
+__global__ __launch_bounds__(256) void k_q4_stage_x(const void* __restrict__ x, int64_t tokens, int64_t cols,
+                                                     int64_t ldx, int64_t lds, uint16_t* __restrict__ out) {
+  const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (col >= lds) return;
+  for (int64_t t = blockIdx.y; t < tokens; t += gridDim.y) {
+    if constexpr (DT == EXTERND_F32) {
+      const float v = col < cols ? static_cast<const float*>(x)[t * ldx + col] : 0.f;
+      const float hi = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+      const float r1 = v - hi;
+      const float mid = __uint_as_float(__float_as_uint(r1) & 0xffff0000u);
+      const float lo = r1 - mid;
+      uint16_t* o = out + 3 * t * lds + col;
+      o[0] = (uint16_t)(__float_as_uint(hi) >> 16);
+      o[lds] = (uint16_t)(__float_as_uint(mid) >> 16);
+      o[2 * lds] = (uint16_t)(__float_as_uint(lo) >> 16);
+    } else {
+      out[t * lds + col] = col < cols ? static_cast<const uint16_t*>(x)[t * ldx + col] : (uint16_t)0;
+    }
+  }
+}
+
+// Codes of one word as the operand 16 + c (exact in bf16 and fp16: the code
+// sits in the four mantissa bits below 16's units).
+template <bool BF>
+__device__ __forceinline__ u32x4 unpack_q4(uint32_t w) {
+  constexpr uint32_t mask = BF ? 0x00780078u : 0x03C003C0u, base = BF ? 0x41804180u : 0x4C004C00u;
+  u32x4 r;
+  if constexpr (BF) {
+    r.x = ((w << 3) & mask) | base;
+    r.y = ((w >> 1) & mask) | base;
+    r.z = ((w >> 5) & mask) | base;
+    r.w = ((w >> 9) & mask) | base;
+  } else {
+    r.x = ((w << 6) & mask) | base;
+    r.y = ((w << 2) & mask) | base;
+    r.z = ((w >> 2) & mask) | base;
+    r.w = ((w >> 6) & mask) | base;
+  }
+  return r;
+}
+
+struct Q4Args {
+  const u32x4* codes[2];
+  const uint16_t* scales[2];
+  const uint16_t* mins[2];
+  const uint16_t* x;    // 16-bit rows ("slots": a token, or one of its three parts)
+  void* y;
+  int64_t ldx, rows, cols, chunks, tokens;
+  int pieces;           // slots per token: 1, or 3 for fp32
+  int act;
+};
+
+// y = W x (MATS = 1) or act(Wg x) (Wu x) (MATS = 2) for tiles of 16 slots.
+//
+// A workgroup of WV waves takes RT row tiles and NT slot tiles; its waves take
+// every WV-th chunk, so neighbouring waves read neighbouring kilobytes, and
+// their sums are joined in LDS in wave order (the result does not depend on
+// timing).  Per chunk a wave makes four 16x16x32 products per row and slot
+// tile, with the slots as rows of the first operand and weight rows as columns
+// of the second: D[slot][weight row] then has one weight row per lane, and
+// the group's scale is one multiplication by the lane's own value.
+//
+// The operand is 16 + c, not c - 8 or c: its offset is taken off by a product of x
+// with the constant -24 (or -16), accumulated before the group's own, once
+// for all row tiles.  With minima that product, scaled by -m / 16, is also the
+// m sum(x) term.  Sums are fp32 throughout.
+template <bool BF, int GPC, bool MINS, int MATS, int RT, int NT, int WV>
+__global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type) {
+  constexpr int F = MATS * RT;      // row tiles held by a wave, of all matrices
+  constexpr int SPG = 4 / GPC;      // products per group
+  __shared__ float red[WV][F][256];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int r = lane & 15, p = lane >> 4;
+  const int64_t tiles = (a.rows + kTile - 1) / kTile;
+  const int64_t tile0 = (int64_t)blockIdx.x * RT;
+  const int per = a.pieces == 3 ? 15 : 16;         // slots of a slot tile
+  const int64_t slots = a.tokens * a.pieces;
+
+  const uint16_t* xp[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    // a slot past the end repeats the last one: its sums are not written
+    const int64_t s = min(((int64_t)blockIdx.y * NT + n) * per + r, slots - 1);
+    xp[n] = a.x + s * a.ldx + 8 * p;
+  }
+  const u32x4* cp[F];
+  const uint16_t* sp[F];
+  const uint16_t* mp[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int64_t tile = min(tile0 + f % RT, tiles - 1);   // as for slots
+    cp[f] = a.codes[f / RT] + tile * a.chunks * kWave + lane;
+    sp[f] = a.scales[f / RT] + (tile * a.chunks * kTile + r) * GPC;
+    if constexpr (MINS) mp[f] = a.mins[f / RT] + (tile * a.chunks * kTile + r) * GPC;
+  }
+  f32x4 acc[F][NT];
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[f][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  struct Stage {
+    u32x4 c[F];
+    uint64_t s[F], m[F];   // GPC bf16 values in the low bits
+  };
+  auto table = [](const uint16_t* q) -> uint64_t {
+    if constexpr (GPC == 4) return *reinterpret_cast<const uint64_t*>(q);
+    else if constexpr (GPC == 2) return *reinterpret_cast<const uint32_t*>(q);
+    else return *q;
+  };
+  auto fetch = [&](int64_t c, Stage& st) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      st.c[f] = __builtin_nontemporal_load(cp[f] + c * kWave);
+      st.s[f] = table(sp[f] + c * kTile * GPC);
+      if constexpr (MINS) st.m[f] = table(mp[f] + c * kTile * GPC);
+    }
+  };
+  constexpr uint32_t off2 = MINS ? (BF ? 0xC180C180u : 0xCC00CC00u) : (BF ? 0xC1C0C1C0u : 0xCE00CE00u);
+  const u32x4 off = {off2, off2, off2, off2};
+  auto work = [&](int64_t c, const Stage& st, bool tail) {
+#pragma unroll
+    for (int g = 0; g < GPC; ++g) {
+      u32x4 xf[SPG][NT];
+      f32x4 xo[NT];
+#pragma unroll
+      for (int i = 0; i < SPG; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int64_t k = kChunk * c + 32 * (g * SPG + i);
+          if (!tail) xf[i][n] = *reinterpret_cast<const u32x4*>(xp[n] + k);
+          else xf[i][n] = k + 8 * p < a.cols ? *reinterpret_cast<const u32x4*>(xp[n] + k) : u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        xo[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < SPG; ++i) xo[n] = mfma16<BF>(xf[i][n], off, xo[n]);
+      }
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        u32x4 wf[SPG];
+#pragma unroll
+        for (int i = 0; i < SPG; ++i) wf[i] = unpack_q4<BF>(st.c[f][g * SPG + i]);
+        const float s = bf16_to_f32((uint32_t)(st.s[f] >> (16 * g)) & 0xffffu);
+        const float m = MINS ? -0.0625f * bf16_to_f32((uint32_t)(st.m[f] >> (16 * g)) & 0xffffu) : 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          f32x4 d = xo[n];
+#pragma unroll
+          for (int i = 0; i < SPG; ++i) d = mfma16<BF>(xf[i][n], wf[i], d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[f][n][e] = fmaf(s, d[e], acc[f][n][e]);
+            if constexpr (MINS) acc[f][n][e] = fmaf(m, xo[n][e], acc[f][n][e]);
+          }
+        }
+      }
+    }
+  };
+  // the next chunk's codes are on their way while one is worked on
+  const int64_t full = a.cols / kChunk;   // chunks without a tail
+  Stage now, next;
+  int64_t c = wave;
+  if (c < a.chunks) fetch(c, now);
+  for (; c < full; c += WV) {
+    if (c + WV < a.chunks) fetch(c + WV, next);
+    work(c, now, false);
+    now = next;
+  }
+  if (c < a.chunks) work(c, now, true);
+
+  const int rows_here = (int)min<int64_t>(RT * kTile, a.rows - tile0 * kTile);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (n) __syncthreads();
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[wave][f][(4 * p + e) * kTile + r] = acc[f][n][e];
+    __syncthreads();
+    const int64_t tok0 = ((int64_t)blockIdx.y * NT + n) * (per / a.pieces);
+    for (int o = threadIdx.x; o < RT * 256; o += WV * kWave) {
+      const int f = o >> 8, tk = (o >> 4) & 15, row = o & 15;
+      if (tk >= per / a.pieces || tok0 + tk >= a.tokens || f * kTile + row >= rows_here) continue;
+      float v[MATS];
+#pragma unroll
+      for (int q = 0; q < MATS; ++q) {
+        float sum = 0.f;
+        for (int e = 0; e < a.pieces; ++e)
+#pragma unroll
+          for (int w = 0; w < WV; ++w) sum += red[w][q * RT + f][(tk * a.pieces + e) * kTile + row];
+        v[q] = sum;
+      }
+      float out = v[0];
+      if constexpr (MATS == 2) out = act_value(a.act, v[0]) * v[1];
+      const int64_t at = (tok0 + tk) * a.rows + (tile0 + f) * kTile + row;
+      if (out_type == EXTERND_F32) static_cast<float*>(a.y)[at] = out;
+      else static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_16<BF>(out);
+    }
+  }
+}
+
+template <bool BF, int GPC, bool MINS, int MATS, int RT, int NT, int WV>
+hipError_t launch_apply(const Q4Args& a, int out_type, hipStream_t s) {
+  const int64_t tiles = (a.rows + kTile - 1) / kTile;
+  const int64_t tpt = a.pieces == 3 ? 5 : 16;   // tokens of a slot tile
+  const int64_t gy = (a.tokens + tpt * NT - 1) / (tpt * NT);
+  const int64_t gx = (tiles + RT - 1) / RT;
+  hipLaunchKernelGGL((k_q4_apply<BF, GPC, MINS, MATS, RT, NT, WV>), dim3((unsigned)gx, (unsigned)gy),
+                     dim3(WV * kWave), 0, s, a, out_type);
+  return hipGetLastError();
+}
+
+template <bool BF, int GPC, bool MINS>
+hipError_t pick_apply(const Q4Args& a, int mats, int out_type, hipStream_t s) {
+  const int64_t slot_tiles = a.pieces == 3 ? (a.tokens + 4) / 5 : (a.tokens + 15) / 16;
+  const int64_t tiles = (a.rows + kTile - 1) / kTile;
+  if (mats == 2) {
+    if (slot_tiles == 1) return launch_apply<BF, GPC, MINS, 2, 1, 1, 8>(a, out_type, s);
+    if (slot_tiles == 2) return launch_apply<BF, GPC, MINS, 2, 1, 2, 8>(a, out_type, s);
+    return launch_apply<BF, GPC, MINS, 2, 2, 4, 4>(a, out_type, s);
+  }
+  if (slot_tiles == 1) {
+    if (tiles < 512) return launch_apply<BF, GPC, MINS, 1, 1, 1, 16>(a, out_type, s);
+    return launch_apply<BF, GPC, MINS, 1, 2, 1, 8>(a, out_type, s);
+  }
+  if (slot_tiles == 2) return launch_apply<BF, GPC, MINS, 1, 2, 2, 8>(a, out_type, s);
+  return launch_apply<BF, GPC, MINS, 1, 4, 4, 4>(a, out_type, s);
+}
+
+template <bool BF>
+hipError_t pick_group(const Q4Args& a, int gpc, int mats, int out_type, hipStream_t s) {
+  const bool mins = a.mins[0] != nullptr;
+  if (gpc == 4) return mins ? pick_apply<BF, 4, true>(a, mats, out_type, s) : pick_apply<BF, 4, false>(a, mats, out_type, s);
+  if (gpc == 2) return mins ? pick_apply<BF, 2, true>(a, mats, out_type, s) : pick_apply<BF, 2, false>(a, mats, out_type, s);
+  return mins ? pick_apply<BF, 1, true>(a, mats, out_type, s) : pick_apply<BF, 1, false>(a, mats, out_type, s);
+}
+
+int64_t chunks_of(int64_t cols) { return (cols + kChunk - 1) / kChunk; }
+int64_t jobs_of(int64_t rows, int64_t cols) { return (rows + kTile - 1) / kTile * chunks_of(cols); }
+// Workgroups of four waves, one job each until the grid's limit.
+dim3 jobs_grid(int64_t jobs) { return dim3((unsigned)std::min<int64_t>((jobs + 3) / 4, 1 << 22)); }
+
+}  // namespace
+
+bool q4_stages_x(int64_t cols, int64_t ldx, int dtype, const void* x) {
+  return dtype == EXTERND_F32 || cols % 8 != 0 || ldx % 8 != 0 || (reinterpret_cast<uintptr_t>(x) & 15) != 0;
+}
+
+size_t q4_stage_bytes(int64_t cols, int64_t tokens, int dtype) {
+  return (size_t)(chunks_of(cols) * kChunk * tokens * (dtype == EXTERND_F32 ? 3 : 1)) * 2;
+}
+
+hipError_t run_q4_apply(const externd_q4* w, int mats, const void* x, int64_t tokens, int64_t ldx, int dtype, int act,
+                        void* y, void* ws, hipStream_t s) {
+  Q4Args a;
+  for (int q = 0; q < 2; ++q) {
+    const externd_q4& m = w[q < mats ? q : 0];
+    a.codes[q] = reinterpret_cast<const u32x4*>(m.codes);
+    a.scales[q] = m.scales;
+    a.mins[q] = m.mins;
+  }
+  a.rows = w[0].rows;
+  a.cols = w[0].cols;
+  a.chunks = chunks_of(a.cols);
+  a.tokens = tokens;
+  a.pieces = dtype == EXTERND_F32 ? 3 : 1;
+  a.act = act;
+  a.y = y;
+  if (ws) {
+    const int64_t lds = a.chunks * kChunk;
+    uint16_t* o = static_cast<uint16_t*>(ws);
+    const dim3 grid((unsigned)((lds + 255) / 256), (unsigned)std::min<int64_t>(tokens, 32768));
+    if (dtype == EXTERND_F32)
+      hipLaunchKernelGGL(k_q4_stage_x<EXTERND_F32>, grid, dim3(256), 0, s, x, tokens, a.cols, ldx, lds, o);
+    else
+      hipLaunchKernelGGL(k_q4_stage_x<EXTERND_BF16>, grid, dim3(256), 0, s, x, tokens, a.cols, ldx, lds, o);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.x = o;
+    a.ldx = lds;
+    a.cols = lds;   // zero past the end: no tail
+  } else {
+    a.x = static_cast<const uint16_t*>(x);
+    a.ldx = ldx;
+  }
+  const int gpc = kChunk / w[0].group;
+  if (dtype == EXTERND_F16) return pick_group<false>(a, gpc, mats, EXTERND_F16, s);
+  return pick_group<true>(a, gpc, mats, dtype, s);
+}
+
+template <int DT>
+static hipError_t launch_quantize(const void* W, int64_t rows, int64_t cols, int64_t ldw, int group, void* codes,
+                                  uint16_t* scales, uint16_t* mins, hipStream_t s) {
+  const int64_t jobs = jobs_of(rows, cols), chunks = chunks_of(cols);
+  const dim3 grid = jobs_grid(jobs), block(256);
+  u32x4* c = static_cast<u32x4*>(codes);
+#define EXTERND_Q4_QUANT(GPC)                                                                                        \
+  if (mins)                                                                                                          \
+    hipLaunchKernelGGL((k_q4_quantize<DT, GPC, true>), grid, block, 0, s, W, rows, cols, ldw, chunks, jobs, c, scales, mins); \
+  else                                                                                                               \
+    hipLaunchKernelGGL((k_q4_quantize<DT, GPC, false>), grid, block, 0, s, W, rows, cols, ldw, chunks, jobs, c, scales, mins)
+  if (group == 32) { EXTERND_Q4_QUANT(4); }
+  else if (group == 64) { EXTERND_Q4_QUANT(2); }
+  else { EXTERND_Q4_QUANT(1); }
+#undef EXTERND_Q4_QUANT
+  return hipGetLastError();
+}
+
+hipError_t run_q4_quantize(const void* W, int64_t rows, int64_t cols, int64_t ldw, int dtype, int group, void* codes,
+                           uint16_t* scales, uint16_t* mins, hipStream_t s) {
+  if (dtype == EXTERND_F32) return launch_quantize<EXTERND_F32>(W, rows, cols, ldw, group, codes, scales, mins, s);
+  if (dtype == EXTERND_BF16) return launch_quantize<EXTERND_BF16>(W, rows, cols, ldw, group, codes, scales, mins, s);
+  return launch_quantize<EXTERND_F16>(W, rows, cols, ldw, group, codes, scales, mins, s);
+}
+
+hipError_t run_q4_pack(const uint8_t* src, const uint16_t* ssrc, const uint16_t* msrc, int64_t rows, int64_t cols,
+                       int group, void* codes, uint16_t* scales, uint16_t* mins, hipStream_t s) {
+  const int64_t jobs = jobs_of(rows, cols);
+  hipLaunchKernelGGL(k_q4_pack, jobs_grid(jobs), dim3(256), 0, s, src, ssrc, msrc, rows, cols,
+                     kChunk / group, chunks_of(cols), jobs, static_cast<u32x4*>(codes), scales, mins);
+  return hipGetLastError();
+}
+
+hipError_t run_q4_reconstruct(const externd_q4& w, int dtype, void* out, hipStream_t s) {
+  const int64_t jobs = jobs_of(w.rows, w.cols);
+  const dim3 grid = jobs_grid(jobs), block(256);
+  const u32x4* c = reinterpret_cast<const u32x4*>(w.codes);
+  const int gpc = kChunk / w.group;
+#define EXTERND_Q4_RECON(DT)                                                                                          \
+  hipLaunchKernelGGL(k_q4_reconstruct<DT>, grid, block, 0, s, c, w.scales, w.mins, w.rows, w.cols, gpc, chunks_of(w.cols), \
+                     jobs, out)
+  if (dtype == EXTERND_F32) EXTERND_Q4_RECON(EXTERND_F32);
+  else if (dtype == EXTERND_BF16) EXTERND_Q4_RECON(EXTERND_BF16);
+  else EXTERND_Q4_RECON(EXTERND_F16);
+#undef EXTERND_Q4_RECON
+  return hipGetLastError();
+}
+
+}  // namespace externd

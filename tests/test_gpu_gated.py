@@ -1,0 +1,265 @@
+"""GPU checks of the gated feed-forward block, forward and backward, against
+oracle/gated.py in fp64.
+
+Tolerances.  Operands are 16-bit, products exact in fp32, sums fp32: a sum of n
+terms of total magnitude S is off by at most (n + 64) 2^-24 S.  h, dx, dWg and dWu are
+rounded once to the operands' type (half ulp u: 2^-8 bf16, 2^-11 fp16), dg and
+du before the products by the same u, which moves a gradient by at most u times
+its terms' total magnitude.  Activation values and slopes are Lipschitz with
+constants below 1.13 and 0.9 and carry a few fp32 roundings of their own.
+fp16 adds its subnormal step."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import gated as og
+
+pytestmark = pytest.mark.gpu
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+TINY = {torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -25}
+E = 2.0 ** -24
+
+
+def _host(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _inputs(tokens, cols, rows, dtype, seed):
+    rng = np.random.default_rng(seed)
+    t = lambda a: torch.from_numpy(a.astype(np.float32)).to(dtype).cuda()
+    scale = 1.0 / np.sqrt(cols)
+    return (t(rng.standard_normal((tokens, cols))), t(scale * 1.5 * rng.standard_normal((rows, cols))),
+            t(scale * rng.standard_normal((rows, cols))), t(rng.standard_normal((tokens, rows))))
+
+
+def _projection_errors(x, wg, wu):
+    cols = x.shape[1]
+    return (cols + 64) * E * (np.abs(x) @ np.abs(wg).T), (cols + 64) * E * (np.abs(x) @ np.abs(wu).T)
+
+
+def _within(got, ref, tol, what):
+    err = np.abs(_host(got).reshape(ref.shape) - ref)
+    assert np.all(err <= tol), (what, float((err / tol).max()))
+
+
+def _check(lib, tokens, cols, rows, dtype, act, seed, tensors=None):
+    xt, wgt, wut, dht = tensors or _inputs(tokens, cols, rows, dtype, seed)
+    x, wg, wu, dh = map(_host, (xt, wgt, wut, dht))
+    h, g, u = lib.gated_forward(xt, wgt, wut, act, save=True)
+    assert torch.equal(lib.gated_forward(xt, wgt, wut, act), h)
+    ref, gv, uv = og.forward(x, wg, wu, act)
+    eg, eu = _projection_errors(x, wg, wu)
+    _within(g, gv, eg + 1e-30, "g")
+    _within(u, uv, eu + 1e-30, "u")
+    a, slope = og.act(act, gv)
+    ea, es = 1.13 * eg + 16 * E * np.abs(gv), 0.9 * eg + 32 * E * (1 + np.abs(gv))
+    un, tiny = U[dtype] * 1.02, TINY[dtype]
+    _within(h, ref, ea * (np.abs(uv) + eu) + np.abs(a) * eu + un * np.abs(ref) + tiny, "h")
+
+    dx, dwg, dwu = lib.gated_backward(xt, wgt, wut, g, u, dht, act)
+    dg, du = dh * uv * slope, dh * a
+    edg = np.abs(dh) * ((np.abs(uv) + eu) * es + eu * np.abs(slope)) + un * np.abs(dg) + tiny
+    edu = np.abs(dh) * ea + un * np.abs(du) + tiny
+    rdx, rdg, rdu = og.backward(x, wg, wu, dh, act)
+    mdx = (np.abs(dg) + edg) @ np.abs(wg) + (np.abs(du) + edu) @ np.abs(wu)
+    _within(dx, rdx, edg @ np.abs(wg) + edu @ np.abs(wu) + (2 * rows + 128) * E * mdx + un * np.abs(rdx) + tiny, "dx")
+    for got, want, d, ed, what in ((dwg, rdg, dg, edg, "dWg"), (dwu, rdu, du, edu, "dWu")):
+        m = (np.abs(d) + ed).T @ np.abs(x)
+        _within(got, want, ed.T @ np.abs(x) + (tokens + 64) * E * m + un * np.abs(want) + tiny, what)
+    return h, dx, dwg, dwu
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("tokens,cols,rows", [
+    (1, 1, 1), (1, 64, 128), (3, 8, 16), (2, 7, 5), (16, 128, 64), (17, 72, 40), (33, 200, 136), (64, 256, 512),
+    (65, 333, 129), (100, 1000, 24), (130, 63, 65), (257, 264, 300), (300, 520, 1032), (600, 77, 131)])
+def test_block(lib, dtype, tokens, cols, rows):
+    act = ("silu", "gelu", "gelu_tanh")[(tokens + cols) % 3]
+    _check(lib, tokens, cols, rows, dtype, act, tokens + rows)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations(lib, act):
+    _check(lib, 40, 96, 80, torch.bfloat16, act, 5)
+    _check(lib, 200, 96, 80, torch.float16, act, 6)
+
+
+def test_wide_projections_stay_finite(lib):
+    x, wg, wu, dh = _inputs(70, 64, 48, torch.bfloat16, 1)
+    x = x * 3000
+    for act in ("silu", "gelu", "gelu_tanh"):
+        h, g, u = lib.gated_forward(x, wg, wu, act, save=True)
+        grads = lib.gated_backward(x, wg, wu, g, u, dh, act)
+        assert all(torch.isfinite(t).all() for t in (h, *grads))
+        assert (g < -200).any() and (h[g < -200] == 0).all()
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 40, 150])
+def test_strides_and_alignment(lib, tokens):
+    dtype = torch.bfloat16
+    x, wg, wu, dh = _inputs(2 * tokens, 300, 150, dtype, tokens)
+    for lo, hi in ((0, 264), (8, 272), (1, 257), (3, 203)):
+        xs, gs, us, ds = x[::2, lo:hi], wg[10:110, lo:hi], wu[40:140, lo:hi], dh[1::2, 7:107]
+        got = _check(lib, tokens, hi - lo, 100, dtype, "silu", 0, (xs, gs, us, ds))
+        same = [t.contiguous() for t in (xs, gs, us, ds)]
+        want = _check(lib, tokens, hi - lo, 100, dtype, "silu", 0, same)
+        for a, b in zip(got, want):
+            assert torch.allclose(a.float(), b.float(), rtol=2 ** -6, atol=1e-2)
+
+
+def test_shared_packed_weights(lib):
+    # gate and up halves of one matrix, and leading batch dimensions
+    x, wg, wu, dh = _inputs(24, 160, 96, torch.float16, 3)
+    both = torch.cat([wg, wu])
+    h = lib.gated_forward(x.view(2, 3, 4, 160), both[:96], both[96:])
+    assert h.shape == (2, 3, 4, 96)
+    assert torch.equal(h.view(24, 96), lib.gated_forward(x, wg, wu))
+
+
+def test_empty_batch(lib):
+    x, wg, wu, dh = _inputs(4, 64, 32, torch.bfloat16, 0)
+    h, g, u = lib.gated_forward(x[:0], wg, wu, save=True)
+    assert h.shape == (0, 32) and g.shape == (0, 32)
+    dx, dwg, dwu = lib.gated_backward(x[:0], wg, wu, g, u, dh[:0])
+    assert dx.shape == (0, 64) and not dwg.any() and not dwu.any()
+
+
+def test_bad_token_stays_in_its_row(lib):
+    for tokens in (6, 200):
+        x, wg, wu, dh = _inputs(tokens, 136, 72, torch.bfloat16, 2)
+        h = lib.gated_forward(x, wg, wu)
+        bad = x.clone()
+        bad[3, 100] = float("nan")
+        bad[5, 0] = float("inf")
+        hb = lib.gated_forward(bad, wg, wu)
+        keep = [t for t in range(tokens) if t not in (3, 5)]
+        assert torch.equal(h[keep], hb[keep])
+        assert torch.isnan(hb[3]).all() and not torch.isfinite(hb[5]).any()
+
+
+def test_parts_of_the_gradient(lib):
+    x, wg, wu, dh = _inputs(50, 128, 64, torch.bfloat16, 4)
+    h, g, u = lib.gated_forward(x, wg, wu, save=True)
+    dx, dwg, dwu = lib.gated_backward(x, wg, wu, g, u, dh)
+    a = lib.gated_backward(x, wg, wu, g, u, dh, need_dw=False)
+    b = lib.gated_backward(x, wg, wu, g, u, dh, need_dx=False)
+    assert torch.equal(a[0], dx) and a[1] is None and a[2] is None
+    assert b[0] is None and torch.equal(b[1], dwg) and torch.equal(b[2], dwu)
+    again = lib.gated_backward(x, wg, wu, g, u, dh)
+    assert all(torch.equal(p, q) for p, q in zip(again, (dx, dwg, dwu)))
+
+
+def test_autograd(lib):
+    x, wg, wu, dh = _inputs(30, 64, 48, torch.bfloat16, 7)
+    h, g, u = lib.gated_forward(x, wg, wu, "gelu", save=True)
+    want = lib.gated_backward(x, wg, wu, g, u, dh, "gelu")
+    leaves = [t.clone().requires_grad_() for t in (x, wg, wu)]
+    out = lib.gated(*leaves, "gelu")
+    assert torch.equal(out, h)
+    out.backward(dh)
+    assert all(torch.equal(t.grad, w) for t, w in zip(leaves, want))
+    leaves = [x.clone().requires_grad_(), wg, wu]
+    lib.gated(*leaves).sum().backward()   # an expanded dh
+    ones = torch.ones_like(dh)
+    h, g, u = lib.gated_forward(x, wg, wu, save=True)
+    assert torch.equal(leaves[0].grad, lib.gated_backward(x, wg, wu, g, u, ones)[0])
+
+
+def test_gradient_against_differences(lib):
+    # sum(h dh) moves by <grad, step>: the kernel's own forward in fp16 outputs is
+    # too coarse, so the kept fp32 projections give h here
+    x, wg, wu, dh = _inputs(8, 64, 32, torch.float16, 9)
+    h, g, u = lib.gated_forward(x, wg, wu, save=True)
+    dx, dwg, dwu = lib.gated_backward(x, wg, wu, g, u, dh)
+
+    def loss(*ops):
+        _, gg, uu = lib.gated_forward(*ops, save=True)
+        return float((gg.double() * torch.sigmoid(gg.double()) * uu.double() * dh.double()).sum())
+    for k, grad in enumerate((dx, dwg, dwu)):
+        ops = [x, wg, wu]
+        step = torch.sign(torch.randn_like(grad.float())) * ops[k].float().abs().clamp(min=2 ** -6) * 2 ** -5
+        hi, lo = [list(ops) for _ in range(2)]
+        hi[k] = (ops[k].float() + step).to(ops[k].dtype)
+        lo[k] = (ops[k].float() - step).to(ops[k].dtype)
+        diff = loss(*hi) - loss(*lo)
+        want = float((grad.double() * (hi[k].double() - lo[k].double())).sum())
+        # third-order term of a 1/32 relative step, against the terms' root sum of squares
+        size = float((grad.double() * (hi[k].double() - lo[k].double())).norm())
+        assert abs(diff - want) <= 0.05 * size + 1e-3 * abs(want), k
+
+
+def test_workspace(lib):
+    x, wg, wu, dh = _inputs(70, 136, 72, torch.bfloat16, 8)
+    h, g, u = lib.gated_forward(x, wg, wu, save=True)
+    want = lib.gated_backward(x, wg, wu, g, u, dh)
+    need = lib.gated_backward_workspace_bytes(70, 136, 72)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = lib.gated_backward(x, wg, wu, g, u, dh, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(lib.ExterndError):
+        lib.gated_backward(x, wg, wu, g, u, dh, workspace=ws[:need // 2])
+    n = lib.gated_forward_workspace_bytes(70, 136, 72)
+    ws = torch.full((max(n, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    assert torch.equal(lib.gated_forward(x, wg, wu, workspace=ws), h)
+
+
+def test_side_stream(lib):
+    x, wg, wu, dh = _inputs(128, 256, 192, torch.bfloat16, 8)
+    h, g, u = lib.gated_forward(x, wg, wu, save=True)
+    want = lib.gated_backward(x, wg, wu, g, u, dh)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        late = torch.zeros_like(x)
+        late.copy_(x)
+        h2, g2, u2 = lib.gated_forward(late, wg, wu, save=True)
+        got = lib.gated_backward(late, wg, wu, g2, u2, dh)
+    s.synchronize()
+    assert torch.equal(h2, h) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("tokens", [2, 150])
+def test_in_a_graph(lib, tokens):
+    x, wg, wu, dh = _inputs(tokens, 256, 192, torch.bfloat16, 8)
+    lib.gated_backward(x, wg, wu, *lib.gated_forward(x, wg, wu, save=True)[1:], dh)
+    torch.cuda.synchronize()
+    ws = torch.empty((lib.gated_backward_workspace_bytes(tokens, 256, 192),), dtype=torch.uint8, device="cuda")
+    static = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h, g, u = lib.gated_forward(static, wg, wu, save=True)
+        grads = lib.gated_backward(static, wg, wu, g, u, dh, workspace=ws)
+    for k in range(4):
+        new = _inputs(tokens, 256, 192, torch.bfloat16, 20 + k)[0]
+        static.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        h2, g2, u2 = lib.gated_forward(new, wg, wu, save=True)
+        want = lib.gated_backward(new, wg, wu, g2, u2, dh)
+        assert torch.equal(h, h2) and all(torch.equal(a, b) for a, b in zip(grads, want))
+
+
+def test_refusals(lib):
+    x, wg, wu, dh = _inputs(4, 64, 32, torch.bfloat16, 0)
+    with pytest.raises(TypeError):
+        lib.gated_forward(x.float(), wg.float(), wu.float())
+    with pytest.raises(TypeError):
+        lib.gated_forward(x, wg, wu.half())
+    with pytest.raises(TypeError):
+        lib.gated_forward(x, wg, wu.cpu())
+    with pytest.raises(ValueError):
+        lib.gated_forward(x, wg, wu[:31])
+    with pytest.raises(ValueError):
+        lib.gated_forward(x[:, :60], wg, wu)
+    with pytest.raises(ValueError):
+        lib.gated_forward(x, wg, wu, "relu")
+    h, g, u = lib.gated_forward(x, wg, wu, save=True)
+    with pytest.raises(ValueError):
+        lib.gated_backward(x, wg, wu, g, u, dh[:3])
+    with pytest.raises(ValueError):
+        lib.gated_backward(x, wg, wu, g[:3].contiguous(), u, dh)
+    with pytest.raises(TypeError):
+        lib.gated_backward(x, wg, wu, g.half(), u, dh)
+    with pytest.raises(TypeError):
+        lib.gated_backward(x, wg, wu, g, u, dh.float())
