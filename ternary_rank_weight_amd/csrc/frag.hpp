@@ -73,4 +73,10 @@ __device__ __forceinline__ u32x4 load8_part(const uint16_t* p, int64_t n) {
   return r;
 }
 
+// 16 bytes per lane from memory straight to LDS, lane l's at dst + 16 l bytes (dst the same in all lanes).
+__device__ __forceinline__ void to_lds16(const void* src, uint16_t* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
 }  // namespace externd

@@ -17,6 +17,7 @@
 // kept in fp32: dg and du are then the only roundings that the gradients see
 // besides their own (16-bit g and u would add two more of the same size).
 #include <algorithm>
+#include <cstdlib>
 
 #include "activation.hpp"
 #include "device_common.hpp"
@@ -39,14 +40,13 @@ struct Operand {
   const uint16_t* p[2];
   int64_t ld;
   int64_t outer;
-  int aligned;   // 16-byte loads to LDS apply (base, ld and, for cols, outer)
 };
 
 struct GemmArgs {
   Operand a, b;         // a: output rows, b: output columns
   int64_t inner;        // contraction length of one segment
-  int64_t steps;        // steps of the whole contraction (all segments)
-  int64_t split_steps;  // steps per split
+  int64_t full;         // whole steps of one segment
+  int64_t split_steps;  // whole steps per split; the last split also takes the partial steps
   int64_t mt, nt;       // tiles
   uint16_t* out[2];     // forward: h; dx: dx; dw: dWg, dWu
   int64_t ldo;          // columns of the outputs
@@ -106,16 +106,20 @@ struct Tile {
 // out tile = sum over k of A[m][k] B[n][k].  BM x BN outputs per workgroup of
 // WM x WN waves.  The products take b's fragment as first and a's as second
 // operand, so that a lane holds four neighbouring output columns of one row.
-template <bool BF, int MODE, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * kWave) void k_gated_gemm(GemmArgs g) {
+//
+// DMA: both operands can be read in 16-byte pieces, and whole steps go from
+// memory to LDS without passing through registers.  Otherwise (and for the
+// last, partial step of a contraction) a step is read through registers.
+template <bool BF, int MODE, int BM, int BN, int WM, int WN, bool DMA>
+__global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
   constexpr int NTHR = WM * WN * kWave;
   constexpr bool ACOLS = MODE == kDw, BCOLS = MODE != kFwd;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   using TA = Tile<ACOLS, BM>;
   using TB = Tile<BCOLS, BN>;
   constexpr int SA = TA::kSlots / NTHR, SB = TB::kSlots / NTHR;
-  __shared__ __align__(16) uint16_t la[2][BM * kBK];
-  __shared__ __align__(16) uint16_t lb[2][BN * kBK];
+  __shared__ __align__(16) uint16_t la0[BM * kBK], lb0[BN * kBK];
+  __shared__ __align__(16) uint16_t la1[DMA ? BM * kBK : 8], lb1[DMA ? BN * kBK : 8];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int wm = wave / WN, wn = wave % WN;
 
@@ -140,9 +144,11 @@ __global__ __launch_bounds__(WM * WN * kWave) void k_gated_gemm(GemmArgs g) {
     outsel = mt >= half;
     m0 = (mt - outsel * half) * BM;
   }
+  // steps of this split: whole steps of all segments in order, then their partial steps
+  constexpr int SEGS = MODE == kDx ? 2 : 1;
   const int64_t s_begin = (int64_t)blockIdx.y * g.split_steps;
-  const int64_t s_end = min(g.steps, s_begin + g.split_steps);
-  const int64_t seg_steps = MODE == kDx ? g.steps / 2 : g.steps;
+  const int64_t s_end = min(SEGS * g.full, s_begin + g.split_steps);
+  const bool last = blockIdx.y == gridDim.y - 1;
 
   f32x4 acc[MI][NI];
 #pragma unroll
@@ -182,41 +188,33 @@ __global__ __launch_bounds__(WM * WN * kWave) void k_gated_gemm(GemmArgs g) {
     if (n >= 8) return (reinterpret_cast<uintptr_t>(p) & 15) == 0 ? load8<true>(p) : load8<false>(p);
     return n > 0 ? load8_part(p, n) : u32x4{0u, 0u, 0u, 0u};
   };
-  u32x4 ra[SA], rb[SB];
-  auto load = [&](int64_t step) {
-    const int seg = MODE == kDx ? (int)(step / seg_steps) : 0;
-    const int64_t k0 = (step - seg * seg_steps) * kBK;
-#pragma unroll
-    for (int i = 0; i < SA; ++i) {
+  // a partial step, slot by slot through registers
+  auto stage_part = [&](int seg, int64_t k0) {
+#pragma unroll 1
+    for (int slot = tid; slot < TA::kSlots; slot += NTHR) {
       int64_t lo, lk;
-      const uint16_t* p = src_a(i * NTHR + tid, seg, k0, lo, lk);
-      ra[i] = fetch(p, ACOLS, lo, lk);
+      const uint16_t* p = src_a(slot, seg, k0, lo, lk);
+      *reinterpret_cast<u32x4*>(la0 + slot * 8) = fetch(p, ACOLS, lo, lk);
     }
-#pragma unroll
-    for (int i = 0; i < SB; ++i) {
+#pragma unroll 1
+    for (int slot = tid; slot < TB::kSlots; slot += NTHR) {
       int64_t lo, lk;
-      const uint16_t* p = src_b(i * NTHR + tid, seg, k0, lo, lk);
-      rb[i] = fetch(p, BCOLS, lo, lk);
+      const uint16_t* p = src_b(slot, seg, k0, lo, lk);
+      *reinterpret_cast<u32x4*>(lb0 + slot * 8) = fetch(p, BCOLS, lo, lk);
     }
   };
-  auto store = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < SA; ++i) *reinterpret_cast<u32x4*>(&la[buf][(i * NTHR + tid) * 8]) = ra[i];
-#pragma unroll
-    for (int i = 0; i < SB; ++i) *reinterpret_cast<u32x4*>(&lb[buf][(i * NTHR + tid) * 8]) = rb[i];
-  };
-  auto compute = [&](int buf) {
+  auto compute = [&](const uint16_t* ca, const uint16_t* cb) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       u32x4 fa[MI], fb[NI];
 #pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = TA::frag(la[buf], (wm * MI + i) * 16, kk, lane);
+      for (int i = 0; i < MI; ++i) fa[i] = TA::frag(ca, (wm * MI + i) * 16, kk, lane);
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
         int o;
         if constexpr (MODE == kFwd) o = (j / (NI / 2)) * BNO + (wn * (NI / 2) + j % (NI / 2)) * 16;
         else o = (wn * NI + j) * 16;
-        fb[j] = TB::frag(lb[buf], o, kk, lane);
+        fb[j] = TB::frag(cb, o, kk, lane);
       }
 #pragma unroll
       for (int i = 0; i < MI; ++i)
@@ -225,17 +223,94 @@ __global__ __launch_bounds__(WM * WN * kWave) void k_gated_gemm(GemmArgs g) {
     }
   };
 
-  if (s_begin < s_end) {
+  if constexpr (DMA) {
+    // byte offsets of this thread's slots from the tile's first entry
+    uint32_t va[SA], vb[SB];
+    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+#pragma unroll
+    for (int i = 0; i < SA; ++i) {
+      int o, k;
+      TA::place(i * NTHR + tid, o, k);
+      if constexpr (!ACOLS) va[i] = (uint32_t)(min<int64_t>(o, g.a.outer - 1 - m0) * g.a.ld + k) * 2u;
+      else va[i] = (uint32_t)(k * g.a.ld + min<int64_t>(o, g.a.outer - 8 - m0)) * 2u;
+    }
+#pragma unroll
+    for (int i = 0; i < SB; ++i) {
+      int o, k;
+      TB::place(i * NTHR + tid, o, k);
+      if constexpr (MODE == kFwd) o -= (o >= BNO) * BNO;
+      if constexpr (!BCOLS) vb[i] = (uint32_t)(min<int64_t>(o, g.b.outer - 1 - n0) * g.b.ld + k) * 2u;
+      else vb[i] = (uint32_t)(k * g.b.ld + min<int64_t>(o, g.b.outer - 8 - n0)) * 2u;
+    }
+    auto stage = [&](int64_t step, uint16_t* da, uint16_t* db) {
+      const int seg = SEGS == 2 ? (int)(step >= g.full) : 0;
+      const int64_t k0 = (step - seg * g.full) * kBK;
+      const char* pa = reinterpret_cast<const char*>(g.a.p[MODE == kDx ? seg : outsel] +
+                                                     (ACOLS ? k0 * g.a.ld + m0 : m0 * g.a.ld + k0));
+#pragma unroll
+      for (int i = 0; i < SA; ++i) to_lds16(pa + va[i], da + (i * NTHR + uwave * kWave) * 8);
+#pragma unroll
+      for (int i = 0; i < SB; ++i) {
+        // a wave's 64 slots of the forward's b are 8 rows of one source
+        const int src = MODE == kFwd ? (i * NTHR + uwave * kWave) / 8 >= BNO : MODE == kDx ? seg : 0;
+        const char* pb = reinterpret_cast<const char*>(g.b.p[src] + (BCOLS ? k0 * g.b.ld + n0 : n0 * g.b.ld + k0));
+        to_lds16(pb + vb[i], db + (i * NTHR + uwave * kWave) * 8);
+      }
+    };
+    if (s_begin < s_end) {
+      stage(s_begin, la0, lb0);
+      __syncthreads();
+      for (int64_t s = s_begin; s < s_end; s += 2) {
+        if (s + 1 < s_end) stage(s + 1, la1, lb1);
+        compute(la0, lb0);
+        __syncthreads();
+        if (s + 1 >= s_end) break;
+        if (s + 2 < s_end) stage(s + 2, la0, lb0);
+        compute(la1, lb1);
+        __syncthreads();
+      }
+    }
+  } else if (s_begin < s_end) {
+    // the next step is in registers while one is worked on
+    u32x4 ra[SA], rb[SB];
+    auto load = [&](int64_t step) {
+      const int seg = SEGS == 2 ? (int)(step >= g.full) : 0;
+      const int64_t k0 = (step - seg * g.full) * kBK;
+      int64_t lo, lk;
+#pragma unroll
+      for (int i = 0; i < SA; ++i) {
+        const uint16_t* p = src_a(i * NTHR + tid, seg, k0, lo, lk);
+        ra[i] = fetch(p, ACOLS, lo, lk);
+      }
+#pragma unroll
+      for (int i = 0; i < SB; ++i) {
+        const uint16_t* p = src_b(i * NTHR + tid, seg, k0, lo, lk);
+        rb[i] = fetch(p, BCOLS, lo, lk);
+      }
+    };
+    auto store = [&](uint16_t* da, uint16_t* db) {
+#pragma unroll
+      for (int i = 0; i < SA; ++i) *reinterpret_cast<u32x4*>(da + (i * NTHR + tid) * 8) = ra[i];
+#pragma unroll
+      for (int i = 0; i < SB; ++i) *reinterpret_cast<u32x4*>(db + (i * NTHR + tid) * 8) = rb[i];
+    };
     load(s_begin);
-    store(0);
+    for (int64_t s = s_begin; s < s_end; ++s) {
+      store(la0, lb0);
+      __syncthreads();
+      if (s + 1 < s_end) load(s + 1);
+      compute(la0, lb0);
+      __syncthreads();
+    }
   }
-  __syncthreads();
-  for (int64_t s = s_begin; s < s_end; ++s) {
-    const int buf = (int)(s - s_begin) & 1;
-    if (s + 1 < s_end) load(s + 1);
-    compute(buf);
-    if (s + 1 < s_end) store(buf ^ 1);
-    __syncthreads();
+  if (last && g.full * kBK < g.inner) {
+#pragma unroll 1
+    for (int seg = 0; seg < SEGS; ++seg) {
+      stage_part(seg, g.full * kBK);
+      __syncthreads();
+      compute(la0, lb0);
+      __syncthreads();
+    }
   }
 
   // ---- outputs: lane holds row m, columns n .. n + 3 of each fragment ----
@@ -335,15 +410,33 @@ __global__ void k_fill_u16(uint16_t* __restrict__ p, int64_t n) {
     p[i] = 0;
 }
 
-template <int MODE, int BM, int BN, int WM, int WN>
-hipError_t launch_gemm(GemmArgs g, bool bf, int64_t splits, hipStream_t s) {
-  const dim3 grid((unsigned)(g.mt * g.nt), (unsigned)splits), block(WM * WN * kWave);
-  if (bf) hipLaunchKernelGGL((k_gated_gemm<true, MODE, BM, BN, WM, WN>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((k_gated_gemm<false, MODE, BM, BN, WM, WN>), grid, block, 0, s, g);
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int MODE, int BM, int BN, int WM, int WN, bool DMA>
+hipError_t launch_tile(GemmArgs g, bool bf, hipStream_t s) {
+  g.mt = MODE == kDw ? 2 * up(g.a.outer, BM) : up(g.a.outer, BM);
+  g.nt = up(g.b.outer, MODE == kFwd ? BN / 2 : BN);
+  const dim3 grid((unsigned)(g.mt * g.nt), (unsigned)std::max<int64_t>(1, up((MODE == kDx ? 2 : 1) * g.full, g.split_steps))), block(WM * WN * kWave);
+  if (bf) hipLaunchKernelGGL((k_gated_gemm<true, MODE, BM, BN, WM, WN, DMA>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((k_gated_gemm<false, MODE, BM, BN, WM, WN, DMA>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 
-int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool dma_ok(const Operand& o, const void* p, bool cols) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && o.ld % 8 == 0 && o.ld < (1 << 22) &&
+         (!cols || o.outer % 8 == 0);
+}
+
+template <int MODE>
+hipError_t launch_gemm(const GemmArgs& g, bool bf, hipStream_t s) {
+  const bool two_a = MODE != kFwd, two_b = MODE != kDw;
+  const bool dma = dma_ok(g.a, g.a.p[0], MODE == kDw) && dma_ok(g.b, g.b.p[0], MODE != kFwd) &&
+                   (!two_a || dma_ok(g.a, g.a.p[1], MODE == kDw)) && (!two_b || dma_ok(g.b, g.b.p[1], MODE != kFwd));
+  if (!dma) return launch_tile<MODE, 128, 128, 2, 2, false>(g, bf, s);
+  if (getenv("T128")) return launch_tile<MODE, 128, 128, 2, 2, true>(g, bf, s);
+  return launch_tile<MODE, 256, 256, 2, 4, true>(g, bf, s);
+}
+
 int64_t padded(int64_t hidden) { return up(hidden, 8) * 8; }
 
 }  // namespace
@@ -369,15 +462,14 @@ hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s) {
   g.b.ld = a.ldw;
   g.b.outer = a.rows;
   g.inner = a.cols;
-  g.steps = g.split_steps = up(a.cols, kBK);
-  g.mt = up(a.tokens, 128);
-  g.nt = up(a.rows, 64);
+  g.full = a.cols / kBK;
+  g.split_steps = std::max<int64_t>(1, g.full);
   g.out[0] = static_cast<uint16_t*>(a.h);
   g.ldo = a.rows;
   g.save[0] = a.g;
   g.save[1] = a.u;
   g.act = a.act;
-  return launch_gemm<kFwd, 128, 128, 2, 2>(g, a.dtype == EXTERND_BF16, 1, s);
+  return launch_gemm<kFwd>(g, a.dtype == EXTERND_BF16, s);
 }
 
 hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
@@ -415,12 +507,11 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
     g.b.ld = a.ldw;
     g.b.outer = a.cols;
     g.inner = a.rows;
-    g.steps = g.split_steps = 2 * up(a.rows, kBK);
-    g.mt = up(a.tokens, 128);
-    g.nt = up(a.cols, 128);
+    g.full = a.rows / kBK;
+    g.split_steps = std::max<int64_t>(1, 2 * g.full);
     g.out[0] = static_cast<uint16_t*>(a.dx);
     g.ldo = a.cols;
-    if ((e = launch_gemm<kDx, 128, 128, 2, 2>(g, bf, 1, s)) != hipSuccess) return e;
+    if ((e = launch_gemm<kDx>(g, bf, s)) != hipSuccess) return e;
   }
   if (a.dwg) {
     GemmArgs g = {};
@@ -432,13 +523,12 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
     g.b.ld = a.ldx;
     g.b.outer = a.cols;
     g.inner = a.tokens;
-    g.steps = g.split_steps = up(a.tokens, kBK);
-    g.mt = 2 * up(a.rows, 128);
-    g.nt = up(a.cols, 128);
+    g.full = a.tokens / kBK;
+    g.split_steps = std::max<int64_t>(1, g.full);
     g.out[0] = static_cast<uint16_t*>(a.dwg);
     g.out[1] = static_cast<uint16_t*>(a.dwu);
     g.ldo = a.cols;
-    if ((e = launch_gemm<kDw, 128, 128, 2, 2>(g, bf, 1, s)) != hipSuccess) return e;
+    if ((e = launch_gemm<kDw>(g, bf, s)) != hipSuccess) return e;
   }
   return hipSuccess;
 }
