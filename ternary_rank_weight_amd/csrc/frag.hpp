@@ -73,10 +73,36 @@ __device__ __forceinline__ u32x4 load8_part(const uint16_t* p, int64_t n) {
   return r;
 }
 
-// 16 bytes per lane from memory straight to LDS, lane l's at dst + 16 l bytes (dst the same in all lanes).
-__device__ __forceinline__ void to_lds16(const void* src, uint16_t* dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+// A pointer that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const void* uniform(const void* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo);
+}
+
+// 16 bytes per lane from base + offset (bytes, the lane's own) straight to LDS,
+// lane l's at dst + 16 l bytes; base and dst the same in all lanes.
+__device__ __forceinline__ void to_lds16(const void* base, uint32_t offset, uint16_t* dst) {
+  const __attribute__((address_space(1))) char* p = (const __attribute__((address_space(1))) char*)base;
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(p + offset),
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// Waits until at most VM of the wave's memory operations (loads to LDS among
+// them) and LGKM of its LDS operations are outstanding.
+template <int VM, int LGKM>
+__device__ __forceinline__ void wait_vm() {
+  // vmcnt in bits 3:0 and 15:14, lgkmcnt in 11:8; expcnt (6:4) at its largest: not waited for
+  __builtin_amdgcn_s_waitcnt(0x0070 | (VM & 15) | ((VM >> 4) << 14) | (LGKM << 8));
+  asm volatile("" ::: "memory");
+}
+
+// A workgroup barrier that waits for nothing else: the caller has waited for
+// what other waves will read.
+__device__ __forceinline__ void block_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 }  // namespace externd

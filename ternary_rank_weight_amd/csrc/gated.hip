@@ -18,6 +18,7 @@
 // besides their own (16-bit g and u would add two more of the same size).
 #include <algorithm>
 #include <cstdlib>
+#include <type_traits>
 
 #include "activation.hpp"
 #include "device_common.hpp"
@@ -31,7 +32,8 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 enum { kFwd = 0, kDx = 1, kDw = 2 };
-constexpr int kBK = 64;   // contraction entries per step
+constexpr int kBK = 32;   // contraction entries per step: one 16x16x32 product
+constexpr int kStages = 4;   // LDS images of steps: one read, one ready, two on their way
 
 // One operand of a product: `outer` output rows (or columns) by `inner`
 // contraction entries.  Two sources: the forward's gate and up rows, dx's two
@@ -55,21 +57,21 @@ struct GemmArgs {
   int act;
 };
 
-// LDS image of an operand tile for one step: O outer entries x 64 contraction
+// LDS image of an operand tile for one step: O outer entries x 32 contraction
 // entries in 16-byte slots.  Slots are permuted so that the 16 rows (or the
 // 4 k rows x 32 bytes per lane group) of a fragment read lie in different
 // banks; a slot's content is chosen by its source address, since loads to LDS
 // write lanes in order.
 template <bool COLS, int O>
 struct Tile {
-  static constexpr int kSlots = O * 8;
+  static constexpr int kSlots = O * 4;
   // contraction-major permutation: which 32-byte block of a k row holds block b
-  __device__ static int mix(int k) { return (k & 3) | (((k >> 3) & (O / 64 - 1)) << 2); }
+  __device__ static int mix(int k) { return k & 3; }
   // (outer, k) of a slot's first entry
   __device__ static void place(int slot, int& o, int& k) {
     if constexpr (!COLS) {
-      o = slot >> 3;
-      k = ((slot & 7) ^ (o & 7)) * 8;
+      o = slot >> 2;
+      k = ((slot & 3) ^ ((o >> 1) & 3)) * 8;
     } else {
       constexpr int per = O / 8;
       k = slot / per;
@@ -77,12 +79,12 @@ struct Tile {
       o = ((s >> 1) ^ mix(k)) * 16 + (s & 1) * 8;
     }
   }
-  // The fragment of outer entries o0 .. o0 + 15 and contraction entries 32 kk .. + 31.
-  __device__ static u32x4 frag(const uint16_t* lds, int o0, int kk, int lane) {
+  // The fragment of outer entries o0 .. o0 + 15.
+  __device__ static u32x4 frag(const uint16_t* lds, int o0, int lane) {
     const int r = lane & 15, p = lane >> 4;
     if constexpr (!COLS) {
       const int o = o0 + r;
-      return *reinterpret_cast<const u32x4*>(lds + o * 64 + (((kk * 4 + p) ^ (o & 7)) * 8));
+      return *reinterpret_cast<const u32x4*>(lds + o * 32 + ((p ^ ((o >> 1) & 3)) * 8));
     } else {
       // two transposing reads of 4 k rows x 16 outer entries per lane group:
       // lane r of a group supplies k row r / 4, entries 4 (r % 4) .. + 3, and
@@ -90,7 +92,7 @@ struct Tile {
       u32x4 v;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int k = kk * 32 + 8 * p + 4 * hf + (r >> 2);
+        const int k = 8 * p + 4 * hf + (r >> 2);
         const uint16_t* q = lds + k * O + (((o0 >> 4) ^ mix(k)) * 16) + 4 * (r & 3);
         const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) s16x4*)(__attribute__((address_space(3))) void*)(q));
@@ -118,8 +120,9 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
   using TA = Tile<ACOLS, BM>;
   using TB = Tile<BCOLS, BN>;
   constexpr int SA = TA::kSlots / NTHR, SB = TB::kSlots / NTHR;
-  __shared__ __align__(16) uint16_t la0[BM * kBK], lb0[BN * kBK];
-  __shared__ __align__(16) uint16_t la1[DMA ? BM * kBK : 8], lb1[DMA ? BN * kBK : 8];
+  constexpr int MA = DMA ? BM * kBK : 8, MB = DMA ? BN * kBK : 8;
+  __shared__ __align__(16) uint16_t la0[BM * kBK], la1[MA], la2[MA], la3[MA];
+  __shared__ __align__(16) uint16_t lb0[BN * kBK], lb1[MB], lb2[MB], lb3[MB];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int wm = wave / WN, wn = wave % WN;
 
@@ -203,26 +206,24 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
       *reinterpret_cast<u32x4*>(lb0 + slot * 8) = fetch(p, BCOLS, lo, lk);
     }
   };
-  auto compute = [&](const uint16_t* ca, const uint16_t* cb) {
+  auto read_a = [&](const uint16_t* img, int i) { return TA::frag(img, (wm * MI + i) * 16, lane); };
+  auto read_b = [&](const uint16_t* img, int j) {
+    int o;
+    if constexpr (MODE == kFwd) o = (j / (NI / 2)) * BNO + (wn * (NI / 2) + j % (NI / 2)) * 16;
+    else o = (wn * NI + j) * 16;
+    return TB::frag(img, o, lane);
+  };
+  auto multiply_all = [&]() {   // one step whose image is la0, lb0
+    u32x4 b[NI];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      u32x4 fa[MI], fb[NI];
+    for (int j = 0; j < NI; ++j) b[j] = read_b(lb0, j);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = TA::frag(ca, (wm * MI + i) * 16, kk, lane);
+    for (int i = 0; i < MI; ++i) {
+      const u32x4 a = read_a(la0, i);
 #pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        int o;
-        if constexpr (MODE == kFwd) o = (j / (NI / 2)) * BNO + (wn * (NI / 2) + j % (NI / 2)) * 16;
-        else o = (wn * NI + j) * 16;
-        fb[j] = TB::frag(cb, o, kk, lane);
-      }
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = mfma16<BF>(fb[j], fa[i], acc[i][j]);
+      for (int j = 0; j < NI; ++j) acc[i][j] = mfma16<BF>(b[j], a, acc[i][j]);
     }
   };
-
   if constexpr (DMA) {
     // byte offsets of this thread's slots from the tile's first entry
     uint32_t va[SA], vb[SB];
@@ -242,33 +243,100 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
       if constexpr (!BCOLS) vb[i] = (uint32_t)(min<int64_t>(o, g.b.outer - 1 - n0) * g.b.ld + k) * 2u;
       else vb[i] = (uint32_t)(k * g.b.ld + min<int64_t>(o, g.b.outer - 8 - n0)) * 2u;
     }
-    auto stage = [&](int64_t step, uint16_t* da, uint16_t* db) {
+    const uint16_t *const a0 = g.a.p[MODE == kDw ? outsel : 0], *const a1 = MODE == kDx ? g.a.p[1] : a0;
+    const uint16_t *const b0 = g.b.p[0], *const b1 = MODE != kDw ? g.b.p[1] : b0;
+    const int64_t lda = g.a.ld, ldb = g.b.ld;
+    // One of the SA + SB pieces that a wave moves per step.
+    auto stage = [&](int64_t step, int piece, uint16_t* da, uint16_t* db) {
       const int seg = SEGS == 2 ? (int)(step >= g.full) : 0;
       const int64_t k0 = (step - seg * g.full) * kBK;
-      const char* pa = reinterpret_cast<const char*>(g.a.p[MODE == kDx ? seg : outsel] +
-                                                     (ACOLS ? k0 * g.a.ld + m0 : m0 * g.a.ld + k0));
-#pragma unroll
-      for (int i = 0; i < SA; ++i) to_lds16(pa + va[i], da + (i * NTHR + uwave * kWave) * 8);
-#pragma unroll
-      for (int i = 0; i < SB; ++i) {
-        // a wave's 64 slots of the forward's b are 8 rows of one source
-        const int src = MODE == kFwd ? (i * NTHR + uwave * kWave) / 8 >= BNO : MODE == kDx ? seg : 0;
-        const char* pb = reinterpret_cast<const char*>(g.b.p[src] + (BCOLS ? k0 * g.b.ld + n0 : n0 * g.b.ld + k0));
-        to_lds16(pb + vb[i], db + (i * NTHR + uwave * kWave) * 8);
+      if (piece < SA) {
+        const uint16_t* pa = (seg ? a1 : a0) + (ACOLS ? k0 * lda + m0 : m0 * lda + k0);
+        to_lds16(uniform(pa), va[piece], da + (piece * NTHR + uwave * kWave) * 8);
+      } else {
+        const int i = piece - SA;
+        // a wave's 64 slots of the forward's b are 16 rows of one source
+        const int src = MODE == kFwd ? (i * NTHR + uwave * kWave) / 4 >= BNO : MODE == kDx ? seg : 0;
+        const uint16_t* pb = (src ? b1 : b0) + (BCOLS ? k0 * ldb + n0 : n0 * ldb + k0);
+        to_lds16(uniform(pb), vb[i], db + (i * NTHR + uwave * kWave) * 8);
       }
     };
-    if (s_begin < s_end) {
-      stage(s_begin, la0, lb0);
-      __syncthreads();
-      for (int64_t s = s_begin; s < s_end; s += 2) {
-        if (s + 1 < s_end) stage(s + 1, la1, lb1);
-        compute(la0, lb0);
-        __syncthreads();
-        if (s + 1 >= s_end) break;
-        if (s + 2 < s_end) stage(s + 2, la0, lb0);
-        compute(la1, lb1);
-        __syncthreads();
+    // Step s is multiplied row by row of fragments.  Its b fragments and first
+    // three a fragments are in registers when it begins; while fragment row i is
+    // multiplied, a fragment i + 3 and one of the next step's b are read, and a
+    // piece of step s + 3 sets out from memory.  The barrier at the beginning
+    // of s makes the image of s + 1 visible to all waves and frees that of s - 1:
+    // its last reads come before the last three a fragments, all that the wait leaves out.
+    constexpr int AOPS = ACOLS ? 2 : 1, BOPS = BCOLS ? 2 : 1;   // LDS reads per fragment
+    constexpr int PIECES = SA + SB;
+    const int64_t n = s_end - s_begin;
+    u32x4 fa[4], fb[2][NI];
+    auto iter = [&](auto par, auto steady, int64_t s, const uint16_t* ca, const uint16_t* na, const uint16_t* nb,
+                    uint16_t* sa, uint16_t* sb) {
+      constexpr int P = decltype(par)::value;
+      constexpr bool STEADY = decltype(steady)::value;
+      if (STEADY || s + 2 < n) wait_vm<PIECES, 3 * AOPS>();
+      else wait_vm<0, 3 * AOPS>();
+      block_barrier();
+      const bool more = STEADY || s + 3 < n;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        // (past the last step these read an image that is not used)
+        if (i + 3 < MI) fa[(i + 3) & 3] = read_a(ca, i + 3);
+        if (i < NI) fb[P ^ 1][i] = read_b(nb, i);
+        if (i + 3 >= MI) fa[(i + 3) & 3] = read_a(na, i + 3 - MI);
+        if (more) {
+#pragma unroll
+          for (int q = i * PIECES / MI; q < (i + 1) * PIECES / MI; ++q) stage(s_begin + s + 3, q, sa, sb);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = mfma16<BF>(fb[P][j], fa[i & 3], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    static_assert(NI <= MI && MI % 4 == 0, "fragment rotation");
+    if (n > 0) {
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q) stage(s_begin, q, la0, lb0);
+      if (n > 1) {
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) stage(s_begin + 1, q, la1, lb1);
+      }
+      if (n > 2) {
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) stage(s_begin + 2, q, la2, lb2);
+      }
+      if (n > 2) wait_vm<2 * PIECES, 0>();
+      else wait_vm<0, 0>();
+      block_barrier();
+#pragma unroll
+      for (int j = 0; j < NI; ++j) fb[0][j] = read_b(lb0, j);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) fa[i] = read_a(la0, i);
+      constexpr std::integral_constant<int, 0> p0;
+      constexpr std::integral_constant<int, 1> p1;
+      constexpr std::true_type steady;
+      constexpr std::false_type ending;
+      int64_t s = 0;
+#pragma unroll 1
+      for (; s + 6 < n; s += 4) {
+        iter(p0, steady, s, la0, la1, lb1, la3, lb3);
+        iter(p1, steady, s + 1, la1, la2, lb2, la0, lb0);
+        iter(p0, steady, s + 2, la2, la3, lb3, la1, lb1);
+        iter(p1, steady, s + 3, la3, la0, lb0, la2, lb2);
+      }
+#pragma unroll 1
+      for (; s < n; s += 4) {
+        iter(p0, ending, s, la0, la1, lb1, la3, lb3);
+        if (s + 1 >= n) break;
+        iter(p1, ending, s + 1, la1, la2, lb2, la0, lb0);
+        if (s + 2 >= n) break;
+        iter(p0, ending, s + 2, la2, la3, lb3, la1, lb1);
+        if (s + 3 >= n) break;
+        iter(p1, ending, s + 3, la3, la0, lb0, la2, lb2);
+      }
+      __syncthreads();
     }
   } else if (s_begin < s_end) {
     // the next step is in registers while one is worked on
@@ -299,7 +367,7 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
       store(la0, lb0);
       __syncthreads();
       if (s + 1 < s_end) load(s + 1);
-      compute(la0, lb0);
+      multiply_all();
       __syncthreads();
     }
   }
@@ -308,7 +376,7 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
     for (int seg = 0; seg < SEGS; ++seg) {
       stage_part(seg, g.full * kBK);
       __syncthreads();
-      compute(la0, lb0);
+      multiply_all();
       __syncthreads();
     }
   }
