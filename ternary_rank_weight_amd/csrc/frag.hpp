@@ -73,19 +73,15 @@ __device__ __forceinline__ u32x4 load8_part(const uint16_t* p, int64_t n) {
   return r;
 }
 
-// A pointer that is the same in all lanes, in scalar registers.
-__device__ __forceinline__ const void* uniform(const void* p) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo);
-}
-
 // 16 bytes per lane from base + offset (bytes, the lane's own) straight to LDS,
-// lane l's at dst + 16 l bytes; base and dst the same in all lanes.
-__device__ __forceinline__ void to_lds16(const void* base, uint32_t offset, uint16_t* dst) {
-  const __attribute__((address_space(1))) char* p = (const __attribute__((address_space(1))) char*)base;
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(p + offset),
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+// lane l's at dst + 16 l bytes; base and dst the same in all lanes.  (The
+// buffer form: after the global form the compiler waits for every LDS
+// operation where it would otherwise count them.)
+__device__ __forceinline__ void to_lds16(const void* base, uint32_t offset,
+                                         __attribute__((address_space(3))) uint16_t* dst) {
+  // stride 0, no range limit below 4 GB, raw 32-bit data
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, offset, 0, 0, 0);
 }
 
 // Waits until at most VM of the wave's memory operations (loads to LDS among

@@ -30,10 +30,12 @@ namespace externd {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) uint16_t* lds16;
 
 enum { kFwd = 0, kDx = 1, kDw = 2 };
-constexpr int kBK = 32;   // contraction entries per step: one 16x16x32 product
-constexpr int kStages = 4;   // LDS images of steps: one read, one ready, two on their way
+constexpr int kBK = 64;   // contraction entries per step: two 16x16x32 products, 128 bytes of a row
 
 // One operand of a product: `outer` output rows (or columns) by `inner`
 // contraction entries.  Two sources: the forward's gate and up rows, dx's two
@@ -57,21 +59,21 @@ struct GemmArgs {
   int act;
 };
 
-// LDS image of an operand tile for one step: O outer entries x 32 contraction
+// LDS image of an operand tile for one step: O outer entries x 64 contraction
 // entries in 16-byte slots.  Slots are permuted so that the 16 rows (or the
 // 4 k rows x 32 bytes per lane group) of a fragment read lie in different
 // banks; a slot's content is chosen by its source address, since loads to LDS
 // write lanes in order.
 template <bool COLS, int O>
 struct Tile {
-  static constexpr int kSlots = O * 4;
+  static constexpr int kSlots = O * 8;
   // contraction-major permutation: which 32-byte block of a k row holds block b
   __device__ static int mix(int k) { return k & 3; }
   // (outer, k) of a slot's first entry
   __device__ static void place(int slot, int& o, int& k) {
     if constexpr (!COLS) {
-      o = slot >> 2;
-      k = ((slot & 3) ^ ((o >> 1) & 3)) * 8;
+      o = slot >> 3;
+      k = ((slot & 7) ^ (o & 7)) * 8;
     } else {
       constexpr int per = O / 8;
       k = slot / per;
@@ -79,12 +81,26 @@ struct Tile {
       o = ((s >> 1) ^ mix(k)) * 16 + (s & 1) * 8;
     }
   }
-  // The fragment of outer entries o0 .. o0 + 15.
-  __device__ static u32x4 frag(const uint16_t* lds, int o0, int lane) {
-    const int r = lane & 15, p = lane >> 4;
+  // A lane's offsets (entries) into an image for the fragments of a wave whose
+  // first outer entry is w0 (a multiple of 64 for COLS): rows, by the half of the
+  // step; cols, by the fragment number modulo 4.  Kept as plain values so that
+  // a fragment's address is image + offset + constant.
+  struct Lane {
+    uint32_t at[COLS ? 4 : 2];
+    __device__ Lane(int w0, int lane) {
+      const int r = lane & 15, p = lane >> 4;
+#pragma unroll
+      for (int q = 0; q < (COLS ? 4 : 2); ++q) {
+        if constexpr (!COLS) at[q] = (w0 + r) * 64 + (((q * 4 + p) ^ (r & 7)) * 8);
+        else at[q] = (8 * p + (r >> 2)) * O + ((w0 >> 4) + (q ^ (r >> 2))) * 16 + 4 * (r & 3);
+        asm("" : "+v"(at[q]));
+      }
+    }
+  };
+  // The wave's fragment i (16 outer entries from 16 i on), contraction entries 32 kk .. + 31.
+  __device__ static u32x4 frag(lds16 img, const Lane& l, int i, int kk) {
     if constexpr (!COLS) {
-      const int o = o0 + r;
-      return *reinterpret_cast<const u32x4*>(lds + o * 32 + ((p ^ ((o >> 1) & 3)) * 8));
+      return *(const lds_u32x4*)(img + l.at[kk] + i * 16 * 64);
     } else {
       // two transposing reads of 4 k rows x 16 outer entries per lane group:
       // lane r of a group supplies k row r / 4, entries 4 (r % 4) .. + 3, and
@@ -92,18 +108,25 @@ struct Tile {
       u32x4 v;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int k = 8 * p + 4 * hf + (r >> 2);
-        const uint16_t* q = lds + k * O + (((o0 >> 4) ^ mix(k)) * 16) + 4 * (r & 3);
-        const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)(__attribute__((address_space(3))) void*)(q));
-        const uint64_t b = __builtin_bit_cast(uint64_t, t);
-        v[2 * hf] = (uint32_t)b;
-        v[2 * hf + 1] = (uint32_t)(b >> 32);
+        const uint64_t t = __builtin_bit_cast(
+            uint64_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                          (lds_s16x4*)(img + l.at[i & 3] + ((kk * 32 + 4 * hf) * O + (i >> 2) * 64))));
+        v[2 * hf] = (uint32_t)t;
+        v[2 * hf + 1] = (uint32_t)(t >> 32);
       }
       return v;
     }
   }
 };
+
+// f(0), f(1), ..., f(N - 1) with the index as a compile-time constant.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void for_constants(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    for_constants<N, I + 1>(f);
+  }
+}
 
 // out tile = sum over k of A[m][k] B[n][k].  BM x BN outputs per workgroup of
 // WM x WN waves.  The products take b's fragment as first and a's as second
@@ -120,32 +143,32 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
   using TA = Tile<ACOLS, BM>;
   using TB = Tile<BCOLS, BN>;
   constexpr int SA = TA::kSlots / NTHR, SB = TB::kSlots / NTHR;
-  constexpr int MA = DMA ? BM * kBK : 8, MB = DMA ? BN * kBK : 8;
-  __shared__ __align__(16) uint16_t la0[BM * kBK], la1[MA], la2[MA], la3[MA];
-  __shared__ __align__(16) uint16_t lb0[BN * kBK], lb1[MB], lb2[MB], lb3[MB];
+  // separate objects: the compiler then sees that a read of one image need not
+  // wait for the loads into another
+  constexpr int A1 = DMA ? BM * kBK : 8, B1 = DMA ? BN * kBK : 8;
+  __shared__ __align__(16) uint16_t sa0[BM * kBK], sa1[A1], sa2[A1];
+  __shared__ __align__(16) uint16_t sb0[BN * kBK], sb1[B1];
+  const lds16 la0 = (lds16)sa0, la1 = (lds16)sa1, la2 = (lds16)sa2, lb0 = (lds16)sb0, lb1 = (lds16)sb1;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int wm = wave / WN, wn = wave % WN;
 
   // tiles are numbered down groups of 8 tile rows, each XCD a run of them
-  int64_t id = blockIdx.x;
-  const int64_t total = (int64_t)g.mt * g.nt;
-  {
-    const int64_t x = id & 7, q = total / 8, rest = total % 8;
-    id = x * q + min(x, rest) + (id >> 3);
-  }
-  const int64_t group = 8 * g.nt, g0 = id / group * 8;
-  const int64_t gh = min<int64_t>(8, g.mt - g0);
-  const int64_t mt = g0 + (id % group) % gh, ntile = (id % group) / gh;
-
-  // which source and where
   constexpr int BNO = MODE == kFwd ? BN / 2 : BN;   // output columns per tile
-  int64_t m0 = mt * BM;
-  const int64_t n0 = ntile * BNO;
   int outsel = 0;
-  if constexpr (MODE == kDw) {   // tile rows: all of dWg, then all of dWu
-    const int64_t half = g.mt / 2;
-    outsel = mt >= half;
-    m0 = (mt - outsel * half) * BM;
+  int64_t m0, n0;
+  {
+    const uint32_t total = (uint32_t)(g.mt * g.nt), x = blockIdx.x & 7, rest = total % 8;
+    const uint32_t id = x * (total / 8) + min(x, rest) + (blockIdx.x >> 3);
+    const uint32_t group = 8 * (uint32_t)g.nt, g0 = id / group * 8, gh = min(8u, (uint32_t)g.mt - g0);
+    uint32_t mt = __builtin_amdgcn_readfirstlane(g0 + id % group % gh);
+    const uint32_t ntile = __builtin_amdgcn_readfirstlane(id % group / gh);
+    if constexpr (MODE == kDw) {   // tile rows: all of dWg, then all of dWu
+      const uint32_t half = (uint32_t)g.mt / 2;
+      outsel = mt >= half;
+      mt -= outsel * half;
+    }
+    m0 = (int64_t)mt * BM;
+    n0 = (int64_t)ntile * BNO;
   }
   // steps of this split: whole steps of all segments in order, then their partial steps
   constexpr int SEGS = MODE == kDx ? 2 : 1;
@@ -197,31 +220,35 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
     for (int slot = tid; slot < TA::kSlots; slot += NTHR) {
       int64_t lo, lk;
       const uint16_t* p = src_a(slot, seg, k0, lo, lk);
-      *reinterpret_cast<u32x4*>(la0 + slot * 8) = fetch(p, ACOLS, lo, lk);
+      *(lds_u32x4*)(la0 + slot * 8) = fetch(p, ACOLS, lo, lk);
     }
 #pragma unroll 1
     for (int slot = tid; slot < TB::kSlots; slot += NTHR) {
       int64_t lo, lk;
       const uint16_t* p = src_b(slot, seg, k0, lo, lk);
-      *reinterpret_cast<u32x4*>(lb0 + slot * 8) = fetch(p, BCOLS, lo, lk);
+      *(lds_u32x4*)(lb0 + slot * 8) = fetch(p, BCOLS, lo, lk);
     }
   };
-  auto read_a = [&](const uint16_t* img, int i) { return TA::frag(img, (wm * MI + i) * 16, lane); };
-  auto read_b = [&](const uint16_t* img, int j) {
-    int o;
-    if constexpr (MODE == kFwd) o = (j / (NI / 2)) * BNO + (wn * (NI / 2) + j % (NI / 2)) * 16;
-    else o = (wn * NI + j) * 16;
-    return TB::frag(img, o, lane);
+  // the forward's b: half of a wave's fragments in the gate rows, half in the up rows
+  const typename TA::Lane lane_a(wm * MI * 16, lane);
+  const typename TB::Lane lane_b(wn * (MODE == kFwd ? NI / 2 : NI) * 16, lane);
+  auto read_a = [&](lds16 img, int i, int kk) { return TA::frag(img, lane_a, i, kk); };
+  auto read_b = [&](lds16 img, int j, int kk) {
+    if constexpr (MODE == kFwd) return TB::frag(img, lane_b, j / (NI / 2) * (BNO / 16) + j % (NI / 2), kk);
+    else return TB::frag(img, lane_b, j, kk);
   };
-  auto multiply_all = [&]() {   // one step whose image is la0, lb0
-    u32x4 b[NI];
+  auto multiply_all = [&]() {   // one step whose image is the first
 #pragma unroll
-    for (int j = 0; j < NI; ++j) b[j] = read_b(lb0, j);
+    for (int kk = 0; kk < 2; ++kk) {
+      u32x4 b[NI];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const u32x4 a = read_a(la0, i);
+      for (int j = 0; j < NI; ++j) b[j] = read_b(lb0, j, kk);
 #pragma unroll
-      for (int j = 0; j < NI; ++j) acc[i][j] = mfma16<BF>(b[j], a, acc[i][j]);
+      for (int i = 0; i < MI; ++i) {
+        const u32x4 a = read_a(la0, i, kk);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = mfma16<BF>(b[j], a, acc[i][j]);
+      }
     }
   };
   if constexpr (DMA) {
@@ -243,99 +270,127 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
       if constexpr (!BCOLS) vb[i] = (uint32_t)(min<int64_t>(o, g.b.outer - 1 - n0) * g.b.ld + k) * 2u;
       else vb[i] = (uint32_t)(k * g.b.ld + min<int64_t>(o, g.b.outer - 8 - n0)) * 2u;
     }
-    const uint16_t *const a0 = g.a.p[MODE == kDw ? outsel : 0], *const a1 = MODE == kDx ? g.a.p[1] : a0;
-    const uint16_t *const b0 = g.b.p[0], *const b1 = MODE != kDw ? g.b.p[1] : b0;
-    const int64_t lda = g.a.ld, ldb = g.b.ld;
-    // One of the SA + SB pieces that a wave moves per step.
-    auto stage = [&](int64_t step, int piece, uint16_t* da, uint16_t* db) {
-      const int seg = SEGS == 2 ? (int)(step >= g.full) : 0;
-      const int64_t k0 = (step - seg * g.full) * kBK;
-      if (piece < SA) {
-        const uint16_t* pa = (seg ? a1 : a0) + (ACOLS ? k0 * lda + m0 : m0 * lda + k0);
-        to_lds16(uniform(pa), va[piece], da + (piece * NTHR + uwave * kWave) * 8);
-      } else {
-        const int i = piece - SA;
-        // a wave's 64 slots of the forward's b are 16 rows of one source
-        const int src = MODE == kFwd ? (i * NTHR + uwave * kWave) / 4 >= BNO : MODE == kDx ? seg : 0;
-        const uint16_t* pb = (src ? b1 : b0) + (BCOLS ? k0 * ldb + n0 : n0 * ldb + k0);
-        to_lds16(uniform(pb), vb[i], db + (i * NTHR + uwave * kWave) * 8);
+    // Where the next step of each operand is read; a wave moves SA or SB pieces of
+    // a step, 64 slots each.
+    const int64_t move_a = ACOLS ? kBK * g.a.ld : kBK, move_b = BCOLS ? kBK * g.b.ld : kBK;
+    const int seg0 = SEGS == 2 && s_begin >= g.full;
+    const int64_t first = (s_begin - seg0 * g.full);
+    const int64_t from_a = ACOLS ? m0 : m0 * g.a.ld, from_b = BCOLS ? n0 : n0 * g.b.ld;
+    const uint16_t* pa = g.a.p[MODE == kDw ? outsel : seg0] + from_a + first * move_a;
+    const uint16_t* pb = g.b.p[seg0] + from_b + first * move_b;
+    const uint16_t *const pa_seg1 = g.a.p[1] + from_a, *const pb_seg1 = g.b.p[1] + from_b;
+    const int64_t to_up = MODE == kFwd ? g.b.p[1] - g.b.p[0] : 0;
+    int64_t step_a = s_begin, step_b = s_begin;
+    auto stage_a = [&](lds16 img, int piece) {
+      to_lds16(pa, va[piece], img + (piece * NTHR + uwave * kWave) * 8);
+      if (piece == SA - 1) {
+        pa += move_a;
+        if (SEGS == 2 && ++step_a == g.full) pa = pa_seg1;
       }
     };
-    // Step s is multiplied row by row of fragments.  Its b fragments and first
-    // three a fragments are in registers when it begins; while fragment row i is
-    // multiplied, a fragment i + 3 and one of the next step's b are read, and a
-    // piece of step s + 3 sets out from memory.  The barrier at the beginning
-    // of s makes the image of s + 1 visible to all waves and frees that of s - 1:
-    // its last reads come before the last three a fragments, all that the wait leaves out.
-    constexpr int AOPS = ACOLS ? 2 : 1, BOPS = BCOLS ? 2 : 1;   // LDS reads per fragment
-    constexpr int PIECES = SA + SB;
+    auto stage_b = [&](lds16 img, int piece) {
+      // a wave's 64 slots of the forward's b are 8 rows of one source
+      const bool up = MODE == kFwd && (piece * NTHR + uwave * kWave) / 8 >= BNO;
+      to_lds16(up ? pb + to_up : pb, vb[piece], img + (piece * NTHR + uwave * kWave) * 8);
+      if (piece == SB - 1) {
+        pb += move_b;
+        if (SEGS == 2 && ++step_b == g.full) pb = pb_seg1;
+      }
+    };
+    // A step is 2 MI rows of fragment products.  Row t multiplies fragments that
+    // were read from LDS three rows (a) or more (b) before, so that the products
+    // of neighbouring rows and steps follow each other without a wait.  There are
+    // three images of a and two of b, 160 KB at 256 x 256.  The only barrier of step s
+    // is before row T = 2 MI - 3, when every wave has read all of its fragments
+    // (the wait before it says so).  Past it the images of step s are free: the
+    // pieces of step s + 2 of b and then of s + 3 of a set out from memory, spread over
+    // the rows up to the next barrier, and the fragments of s + 1 are read, whose
+    // images the wait has made sure of.  So b has one step and a two to arrive.
+    constexpr int R = 2 * MI, T = R - 3, PIECES = SA + SB, EARLY = 3 * PIECES / R;
+    static_assert(MI % 4 == 0 && NI <= 4 && EARLY <= SB, "fragment rotation");
     const int64_t n = s_end - s_begin;
     u32x4 fa[4], fb[2][NI];
-    auto iter = [&](auto par, auto steady, int64_t s, const uint16_t* ca, const uint16_t* na, const uint16_t* nb,
-                    uint16_t* sa, uint16_t* sb) {
-      constexpr int P = decltype(par)::value;
-      constexpr bool STEADY = decltype(steady)::value;
-      if (STEADY || s + 2 < n) wait_vm<PIECES, 3 * AOPS>();
-      else wait_vm<0, 3 * AOPS>();
-      block_barrier();
-      const bool more = STEADY || s + 3 < n;
+    auto image_a = [&](auto index) {
+      constexpr int I = decltype(index)::value % 3;
+      if constexpr (I == 0) return la0;
+      else if constexpr (I == 1) return la1;
+      else return la2;
+    };
+    auto image_b = [&](auto index) {
+      if constexpr (decltype(index)::value % 2 == 0) return lb0;
+      else return lb1;
+    };
+    auto step = [&](auto index, auto steady, int64_t s) {
+      constexpr int J = decltype(index)::value;   // s modulo 6, after which the images repeat
+      constexpr bool ALL = decltype(steady)::value;   // every step that this one moves exists
+      constexpr std::integral_constant<int, J + 1> next;
+      constexpr std::integral_constant<int, J + 2> later;
+      const lds16 ca = image_a(index), na = image_a(next), cb = image_b(index), nb = image_b(next);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        // (past the last step these read an image that is not used)
-        if (i + 3 < MI) fa[(i + 3) & 3] = read_a(ca, i + 3);
-        if (i < NI) fb[P ^ 1][i] = read_b(nb, i);
-        if (i + 3 >= MI) fa[(i + 3) & 3] = read_a(na, i + 3 - MI);
-        if (more) {
+      for (int t = 0; t < R; ++t) {
+        if (t == T) {
+          if (ALL || s + 2 < n) wait_vm<SA, 0>();
+          else wait_vm<0, 0>();
+          block_barrier();
+        }
+        // (past the last step these read images that are not used)
+        if (t + 3 < R) fa[(t + 3) & 3] = read_a(ca, (t + 3) % MI, (t + 3) / MI);
+        else fa[(t + 3) & 3] = read_a(na, t + 3 - R, 0);
+        if (t < NI) fb[1][t] = read_b(cb, t, 1);
+        if (t >= T) {
 #pragma unroll
-          for (int q = i * PIECES / MI; q < (i + 1) * PIECES / MI; ++q) stage(s_begin + s + 3, q, sa, sb);
+          for (int j = (t - T) * 2; j < NI && j < (t - T) * 2 + 2; ++j) fb[0][j] = read_b(nb, j, 0);
+        }
+        const int d = (t - T + R) % R;
+        if (t >= T) {
+          if (ALL || s + 2 < n) {
+#pragma unroll
+            for (int q = d * PIECES / R; q < (d + 1) * PIECES / R; ++q) stage_b(image_b(index), q);
+          }
+        } else {
+#pragma unroll
+          for (int q = d * PIECES / R; q < (d + 1) * PIECES / R; ++q) {
+            if (q < SB) {
+              if (ALL || s + 1 < n) stage_b(image_b(next), q);
+            } else {
+              if (ALL || s + 2 < n) stage_a(image_a(later), q - SB);
+            }
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = mfma16<BF>(fb[P][j], fa[i & 3], acc[i][j]);
+        for (int j = 0; j < NI; ++j) acc[t % MI][j] = mfma16<BF>(fb[t / MI][j], fa[t & 3], acc[t % MI][j]);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    static_assert(NI <= MI && MI % 4 == 0, "fragment rotation");
     if (n > 0) {
 #pragma unroll
-      for (int q = 0; q < PIECES; ++q) stage(s_begin, q, la0, lb0);
+      for (int q = 0; q < SA; ++q) stage_a(la0, q);
+#pragma unroll
+      for (int q = 0; q < SB; ++q) stage_b(lb0, q);
       if (n > 1) {
 #pragma unroll
-        for (int q = 0; q < PIECES; ++q) stage(s_begin + 1, q, la1, lb1);
-      }
-      if (n > 2) {
+        for (int q = 0; q < SA; ++q) stage_a(la1, q);
 #pragma unroll
-        for (int q = 0; q < PIECES; ++q) stage(s_begin + 2, q, la2, lb2);
+        for (int q = 0; q < EARLY; ++q) stage_b(lb1, q);
+        wait_vm<SA + EARLY, 0>();
+      } else {
+        wait_vm<0, 0>();
       }
-      if (n > 2) wait_vm<2 * PIECES, 0>();
-      else wait_vm<0, 0>();
       block_barrier();
 #pragma unroll
-      for (int j = 0; j < NI; ++j) fb[0][j] = read_b(lb0, j);
+      for (int j = 0; j < NI; ++j) fb[0][j] = read_b(lb0, j, 0);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) fa[i] = read_a(la0, i);
-      constexpr std::integral_constant<int, 0> p0;
-      constexpr std::integral_constant<int, 1> p1;
-      constexpr std::true_type steady;
-      constexpr std::false_type ending;
+      for (int i = 0; i < 3; ++i) fa[i] = read_a(la0, i, 0);
       int64_t s = 0;
 #pragma unroll 1
-      for (; s + 6 < n; s += 4) {
-        iter(p0, steady, s, la0, la1, lb1, la3, lb3);
-        iter(p1, steady, s + 1, la1, la2, lb2, la0, lb0);
-        iter(p0, steady, s + 2, la2, la3, lb3, la1, lb1);
-        iter(p1, steady, s + 3, la3, la0, lb0, la2, lb2);
-      }
+      for (; s + 7 < n; s += 6)
+        for_constants<6>([&](auto index) { step(index, std::true_type(), s + decltype(index)::value); });
 #pragma unroll 1
-      for (; s < n; s += 4) {
-        iter(p0, ending, s, la0, la1, lb1, la3, lb3);
-        if (s + 1 >= n) break;
-        iter(p1, ending, s + 1, la1, la2, lb2, la0, lb0);
-        if (s + 2 >= n) break;
-        iter(p0, ending, s + 2, la2, la3, lb3, la1, lb1);
-        if (s + 3 >= n) break;
-        iter(p1, ending, s + 3, la3, la0, lb0, la2, lb2);
-      }
+      for (; s < n; s += 6)
+        for_constants<6>([&](auto index) {
+          if (s + decltype(index)::value < n) step(index, std::false_type(), s + decltype(index)::value);
+        });
       __syncthreads();
     }
   } else if (s_begin < s_end) {
@@ -356,15 +411,15 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
         rb[i] = fetch(p, BCOLS, lo, lk);
       }
     };
-    auto store = [&](uint16_t* da, uint16_t* db) {
+    auto store = [&]() {
 #pragma unroll
-      for (int i = 0; i < SA; ++i) *reinterpret_cast<u32x4*>(da + (i * NTHR + tid) * 8) = ra[i];
+      for (int i = 0; i < SA; ++i) *(lds_u32x4*)(la0 + (i * NTHR + tid) * 8) = ra[i];
 #pragma unroll
-      for (int i = 0; i < SB; ++i) *reinterpret_cast<u32x4*>(db + (i * NTHR + tid) * 8) = rb[i];
+      for (int i = 0; i < SB; ++i) *(lds_u32x4*)(lb0 + (i * NTHR + tid) * 8) = rb[i];
     };
     load(s_begin);
     for (int64_t s = s_begin; s < s_end; ++s) {
-      store(la0, lb0);
+      store();
       __syncthreads();
       if (s + 1 < s_end) load(s + 1);
       multiply_all();
