@@ -662,7 +662,7 @@ int externd_gated_forward(const void* x, int64_t tokens, int64_t cols, int64_t l
   if (!aligned_to(x, 2) || !aligned_to(wg, 2) || !aligned_to(wu, 2) || !aligned_to(h, 2) || !aligned_to(g, 4) ||
       !aligned_to(u, 4))
     return fail(EXTERND_EINVAL, "pointers must be aligned to their type");
-  if ((st = check_device(nullptr)) != EXTERND_OK) return st;
+  if ((st = check_device(&a.cus)) != EXTERND_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   Workspace ws;
   if ((st = op_ws(ws, workspace, workspace_bytes, externd::gated_forward_workspace_bytes(tokens, cols, rows), s)) !=
@@ -700,7 +700,7 @@ int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t 
   if (!aligned_to(x, 2) || !aligned_to(wg, 2) || !aligned_to(wu, 2) || !aligned_to(dh, 2) || !aligned_to(dx, 2) ||
       !aligned_to(dwg, 2) || !aligned_to(dwu, 2) || !aligned_to(g, 4) || !aligned_to(u, 4))
     return fail(EXTERND_EINVAL, "pointers must be aligned to their type");
-  if ((st = check_device(nullptr)) != EXTERND_OK) return st;
+  if ((st = check_device(&a.cus)) != EXTERND_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   Workspace ws;
   const size_t need = tokens > 0 ? externd::gated_backward_workspace_bytes(tokens, cols, rows) : 0;

@@ -55,4 +55,45 @@ __device__ __forceinline__ void act_both(int act, float g, float& a, float& slop
   else act_both<EXTERND_ACT_GELU_TANH>(g, a, slope);
 }
 
+// The same for results that are rounded to 16 bits: hardware reciprocal and
+// exponential (about 1e-6 relative), and erfc by Abramowitz and Stegun's 7.1.26
+// (1.5e-7 absolute).
+__device__ __forceinline__ float sigmoid_fast(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+}
+// (1 + erf(g / sqrt 2)) / 2
+__device__ __forceinline__ float normal_cdf_fast(float g) {
+  const float x = 0.7071067811865476f * fabsf(g);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
+  const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                              0.254829592f);
+  const float tail = 0.5f * poly * __builtin_amdgcn_exp2f(-1.4426950408889634f * x * x);
+  return g < 0.f ? tail : 1.f - tail;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_fast(float g) {
+  if constexpr (ACT == EXTERND_ACT_SILU) return g * sigmoid_fast(g);
+  else if constexpr (ACT == EXTERND_ACT_GELU) return g * normal_cdf_fast(g);
+  else return g * sigmoid_fast(gelu_2z(g));
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_both_fast(float g, float& a, float& slope) {
+  if constexpr (ACT == EXTERND_ACT_SILU) {
+    const float p = sigmoid_fast(g);
+    a = g * p;
+    slope = fmaf(a, 1.f - p, p);
+  } else if constexpr (ACT == EXTERND_ACT_GELU) {
+    const float phi = normal_cdf_fast(g);
+    a = g * phi;
+    slope = fmaf(0.3989422804014327f * g, __builtin_amdgcn_exp2f(-0.7213475204444817f * g * g), phi);
+  } else {
+    const float p = sigmoid_fast(gelu_2z(g));
+    a = g * p;
+    const float q = p * (1.f - p);   // 0 where the cubic may overflow
+    slope = p + (q == 0.f ? 0.f : g * q * gelu_2z_slope(g));
+  }
+}
+
 }  // namespace externd

@@ -52,6 +52,7 @@ struct GemmArgs {
   int64_t full;         // whole steps of one segment
   int64_t split_steps;  // whole steps per split; the last split also takes the partial steps
   int64_t mt, nt;       // tiles
+  int64_t splits;
   uint16_t* out[2];     // forward: h; dx: dx; dw: dWg, dWu
   int64_t ldo;          // columns of the outputs
   float* save[2];       // forward: g, u (or null)
@@ -152,45 +153,60 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int wm = wave / WN, wn = wave % WN;
 
-  // tiles are numbered down groups of 8 tile rows, each XCD a run of them
   constexpr int BNO = MODE == kFwd ? BN / 2 : BN;   // output columns per tile
-  int outsel = 0;
-  int64_t m0, n0;
-  {
-    const uint32_t total = (uint32_t)(g.mt * g.nt), x = blockIdx.x & 7, rest = total % 8;
-    const uint32_t id = x * (total / 8) + min(x, rest) + (blockIdx.x >> 3);
-    const uint32_t group = 8 * (uint32_t)g.nt, g0 = id / group * 8, gh = min(8u, (uint32_t)g.mt - g0);
-    uint32_t mt = __builtin_amdgcn_readfirstlane(g0 + id % group % gh);
-    const uint32_t ntile = __builtin_amdgcn_readfirstlane(id % group / gh);
+  constexpr int SEGS = MODE == kDx ? 2 : 1;
+
+  // A workgroup takes units (one tile, one split) id, id + grid, ...  They are
+  // numbered down groups of 8 tile rows, each XCD a run of them, so that the
+  // workgroups of an XCD share operand rows in its L2.
+  struct Unit {
+    int64_t m0, n0;          // first output row and column
+    int64_t s_begin, s_end;  // whole steps of all segments in order
+    int outsel, split;
+    bool last;               // also takes the partial steps
+  };
+  const uint32_t tiles = (uint32_t)(g.mt * g.nt), units = tiles * (uint32_t)g.splits;
+  auto locate = [&](uint32_t at) {
+    Unit q;
+    const uint32_t x = at & 7, rest = units % 8;
+    const uint32_t id = x * (units / 8) + min(x, rest) + (at >> 3);
+    const uint32_t split = id / tiles, tile = id % tiles;
+    const uint32_t group = 8 * (uint32_t)g.nt, g0 = tile / group * 8, gh = min(8u, (uint32_t)g.mt - g0);
+    uint32_t mt = __builtin_amdgcn_readfirstlane(g0 + tile % group % gh);
+    const uint32_t ntile = __builtin_amdgcn_readfirstlane(tile % group / gh);
+    q.split = __builtin_amdgcn_readfirstlane(split);
+    q.outsel = 0;
     if constexpr (MODE == kDw) {   // tile rows: all of dWg, then all of dWu
       const uint32_t half = (uint32_t)g.mt / 2;
-      outsel = mt >= half;
-      mt -= outsel * half;
+      q.outsel = mt >= half;
+      mt -= q.outsel * half;
     }
-    m0 = (int64_t)mt * BM;
-    n0 = (int64_t)ntile * BNO;
-  }
-  // steps of this split: whole steps of all segments in order, then their partial steps
-  constexpr int SEGS = MODE == kDx ? 2 : 1;
-  const int64_t s_begin = (int64_t)blockIdx.y * g.split_steps;
-  const int64_t s_end = min(SEGS * g.full, s_begin + g.split_steps);
-  const bool last = blockIdx.y == gridDim.y - 1;
+    q.m0 = (int64_t)mt * BM;
+    q.n0 = (int64_t)ntile * BNO;
+    q.s_begin = q.split * g.split_steps;
+    q.s_end = min(SEGS * g.full, q.s_begin + g.split_steps);
+    q.last = q.split == g.splits - 1;
+    return q;
+  };
+  Unit u = locate(blockIdx.x);
 
   f32x4 acc[MI][NI];
+  auto clear = [&] {
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
 
   // source of a slot at contraction offset k0
   auto src_a = [&](int slot, int seg, int64_t k0, int64_t& left_o, int64_t& left_k) -> const uint16_t* {
     int o, k;
     TA::place(slot, o, k);
-    const uint16_t* base = g.a.p[MODE == kDx ? seg : outsel];
-    left_o = g.a.outer - (m0 + o);
+    const uint16_t* base = g.a.p[MODE == kDx ? seg : u.outsel];
+    left_o = g.a.outer - (u.m0 + o);
     left_k = g.inner - (k0 + k);
-    if constexpr (!ACOLS) return base + min(m0 + o, g.a.outer - 1) * g.a.ld + (k0 + k);
-    else return base + (k0 + k) * g.a.ld + (m0 + o);
+    if constexpr (!ACOLS) return base + min(u.m0 + o, g.a.outer - 1) * g.a.ld + (k0 + k);
+    else return base + (k0 + k) * g.a.ld + (u.m0 + o);
   };
   auto src_b = [&](int slot, int seg, int64_t k0, int64_t& left_o, int64_t& left_k) -> const uint16_t* {
     int o, k;
@@ -200,12 +216,12 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
       o -= which * BNO;
       left_o = 8;
       left_k = g.inner - (k0 + k);
-      return g.b.p[which] + min(n0 + o, g.b.outer - 1) * g.b.ld + (k0 + k);
+      return g.b.p[which] + min(u.n0 + o, g.b.outer - 1) * g.b.ld + (k0 + k);
     } else {
       const uint16_t* base = g.b.p[MODE == kDx ? seg : 0];
-      left_o = g.b.outer - (n0 + o);
+      left_o = g.b.outer - (u.n0 + o);
       left_k = g.inner - (k0 + k);
-      return base + (k0 + k) * g.b.ld + (n0 + o);
+      return base + (k0 + k) * g.b.ld + (u.n0 + o);
     }
   };
   // eight entries of a slot through registers, zero past either end
@@ -251,52 +267,70 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
       }
     }
   };
-  if constexpr (DMA) {
-    // byte offsets of this thread's slots from the tile's first entry
-    uint32_t va[SA], vb[SB];
-    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+  // Loads to LDS: where the next step of each operand is read.  A wave moves SA or
+  // SB pieces of a step, 64 slots each.
+  uint32_t va[SA], vb[SB];   // byte offsets of this thread's slots from the tile's first entry
+  const uint16_t *pa = nullptr, *pb = nullptr, *pa_seg1 = nullptr, *pb_seg1 = nullptr;
+  int64_t step_a = 0, step_b = 0;
+  const int64_t move_a = ACOLS ? kBK * g.a.ld : kBK, move_b = BCOLS ? kBK * g.b.ld : kBK;
+  const int64_t to_up = MODE == kFwd ? g.b.p[1] - g.b.p[0] : 0;
+  const int uwave = __builtin_amdgcn_readfirstlane(wave);
+  auto stage_a = [&](lds16 img, int piece) {
+    to_lds16(pa, va[piece], img + (piece * NTHR + uwave * kWave) * 8);
+    if (piece == SA - 1) {
+      pa += move_a;
+      if (SEGS == 2 && ++step_a == g.full) pa = pa_seg1;
+    }
+  };
+  auto stage_b = [&](lds16 img, int piece) {
+    // a wave's 64 slots of the forward's b are 8 rows of one source
+    const bool up = MODE == kFwd && (piece * NTHR + uwave * kWave) / 8 >= BNO;
+    to_lds16(up ? pb + to_up : pb, vb[piece], img + (piece * NTHR + uwave * kWave) * 8);
+    if (piece == SB - 1) {
+      pb += move_b;
+      if (SEGS == 2 && ++step_b == g.full) pb = pb_seg1;
+    }
+  };
+  constexpr int R = 2 * MI, T = R - 3, PIECES = SA + SB, EARLY = 3 * PIECES / R;   // see below
+  // Sets out the first loads of a unit; every image is free.
+  auto begin = [&](const Unit& q) {
 #pragma unroll
     for (int i = 0; i < SA; ++i) {
       int o, k;
       TA::place(i * NTHR + tid, o, k);
-      if constexpr (!ACOLS) va[i] = (uint32_t)(min<int64_t>(o, g.a.outer - 1 - m0) * g.a.ld + k) * 2u;
-      else va[i] = (uint32_t)(k * g.a.ld + min<int64_t>(o, g.a.outer - 8 - m0)) * 2u;
+      if constexpr (!ACOLS) va[i] = (uint32_t)(min<int64_t>(o, g.a.outer - 1 - q.m0) * g.a.ld + k) * 2u;
+      else va[i] = (uint32_t)(k * g.a.ld + min<int64_t>(o, g.a.outer - 8 - q.m0)) * 2u;
     }
 #pragma unroll
     for (int i = 0; i < SB; ++i) {
       int o, k;
       TB::place(i * NTHR + tid, o, k);
       if constexpr (MODE == kFwd) o -= (o >= BNO) * BNO;
-      if constexpr (!BCOLS) vb[i] = (uint32_t)(min<int64_t>(o, g.b.outer - 1 - n0) * g.b.ld + k) * 2u;
-      else vb[i] = (uint32_t)(k * g.b.ld + min<int64_t>(o, g.b.outer - 8 - n0)) * 2u;
+      if constexpr (!BCOLS) vb[i] = (uint32_t)(min<int64_t>(o, g.b.outer - 1 - q.n0) * g.b.ld + k) * 2u;
+      else vb[i] = (uint32_t)(k * g.b.ld + min<int64_t>(o, g.b.outer - 8 - q.n0)) * 2u;
     }
-    // Where the next step of each operand is read; a wave moves SA or SB pieces of
-    // a step, 64 slots each.
-    const int64_t move_a = ACOLS ? kBK * g.a.ld : kBK, move_b = BCOLS ? kBK * g.b.ld : kBK;
-    const int seg0 = SEGS == 2 && s_begin >= g.full;
-    const int64_t first = (s_begin - seg0 * g.full);
-    const int64_t from_a = ACOLS ? m0 : m0 * g.a.ld, from_b = BCOLS ? n0 : n0 * g.b.ld;
-    const uint16_t* pa = g.a.p[MODE == kDw ? outsel : seg0] + from_a + first * move_a;
-    const uint16_t* pb = g.b.p[seg0] + from_b + first * move_b;
-    const uint16_t *const pa_seg1 = g.a.p[1] + from_a, *const pb_seg1 = g.b.p[1] + from_b;
-    const int64_t to_up = MODE == kFwd ? g.b.p[1] - g.b.p[0] : 0;
-    int64_t step_a = s_begin, step_b = s_begin;
-    auto stage_a = [&](lds16 img, int piece) {
-      to_lds16(pa, va[piece], img + (piece * NTHR + uwave * kWave) * 8);
-      if (piece == SA - 1) {
-        pa += move_a;
-        if (SEGS == 2 && ++step_a == g.full) pa = pa_seg1;
-      }
-    };
-    auto stage_b = [&](lds16 img, int piece) {
-      // a wave's 64 slots of the forward's b are 8 rows of one source
-      const bool up = MODE == kFwd && (piece * NTHR + uwave * kWave) / 8 >= BNO;
-      to_lds16(up ? pb + to_up : pb, vb[piece], img + (piece * NTHR + uwave * kWave) * 8);
-      if (piece == SB - 1) {
-        pb += move_b;
-        if (SEGS == 2 && ++step_b == g.full) pb = pb_seg1;
-      }
-    };
+    const int seg = SEGS == 2 && q.s_begin >= g.full;
+    const int64_t first = q.s_begin - seg * g.full;
+    const int64_t from_a = ACOLS ? q.m0 : q.m0 * g.a.ld, from_b = BCOLS ? q.n0 : q.n0 * g.b.ld;
+    pa = g.a.p[MODE == kDw ? q.outsel : seg] + from_a + first * move_a;
+    pb = g.b.p[seg] + from_b + first * move_b;
+    pa_seg1 = g.a.p[1] + from_a;
+    pb_seg1 = g.b.p[1] + from_b;
+    step_a = step_b = q.s_begin;
+    if (q.s_begin < q.s_end) {
+#pragma unroll
+      for (int p = 0; p < SA; ++p) stage_a(la0, p);
+#pragma unroll
+      for (int p = 0; p < SB; ++p) stage_b(lb0, p);
+    }
+    if (q.s_begin + 1 < q.s_end) {
+#pragma unroll
+      for (int p = 0; p < SA; ++p) stage_a(la1, p);
+#pragma unroll
+      for (int p = 0; p < EARLY; ++p) stage_b(lb1, p);
+    }
+  };
+  auto contract = [&] {
     // A step is 2 MI rows of fragment products.  Row t multiplies fragments that
     // were read from LDS three rows (a) or more (b) before, so that the products
     // of neighbouring rows and steps follow each other without a wait.  There are
@@ -306,9 +340,8 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
     // pieces of step s + 2 of b and then of s + 3 of a set out from memory, spread over
     // the rows up to the next barrier, and the fragments of s + 1 are read, whose
     // images the wait has made sure of.  So b has one step and a two to arrive.
-    constexpr int R = 2 * MI, T = R - 3, PIECES = SA + SB, EARLY = 3 * PIECES / R;
     static_assert(MI % 4 == 0 && NI <= 4 && EARLY <= SB, "fragment rotation");
-    const int64_t n = s_end - s_begin;
+    const int64_t n = u.s_end - u.s_begin;
     u32x4 fa[4], fb[2][NI];
     auto image_a = [&](auto index) {
       constexpr int I = decltype(index)::value % 3;
@@ -365,20 +398,6 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
     };
     if (n > 0) {
 #pragma unroll
-      for (int q = 0; q < SA; ++q) stage_a(la0, q);
-#pragma unroll
-      for (int q = 0; q < SB; ++q) stage_b(lb0, q);
-      if (n > 1) {
-#pragma unroll
-        for (int q = 0; q < SA; ++q) stage_a(la1, q);
-#pragma unroll
-        for (int q = 0; q < EARLY; ++q) stage_b(lb1, q);
-        wait_vm<SA + EARLY, 0>();
-      } else {
-        wait_vm<0, 0>();
-      }
-      block_barrier();
-#pragma unroll
       for (int j = 0; j < NI; ++j) fb[0][j] = read_b(lb0, j, 0);
 #pragma unroll
       for (int i = 0; i < 3; ++i) fa[i] = read_a(la0, i, 0);
@@ -393,7 +412,9 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
         });
       __syncthreads();
     }
-  } else if (s_begin < s_end) {
+  };
+  auto contract_slow = [&] {
+    if (u.s_begin >= u.s_end) return;
     // the next step is in registers while one is worked on
     u32x4 ra[SA], rb[SB];
     auto load = [&](int64_t step) {
@@ -417,82 +438,148 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
 #pragma unroll
       for (int i = 0; i < SB; ++i) *(lds_u32x4*)(lb0 + (i * NTHR + tid) * 8) = rb[i];
     };
-    load(s_begin);
-    for (int64_t s = s_begin; s < s_end; ++s) {
+    load(u.s_begin);
+    for (int64_t s = u.s_begin; s < u.s_end; ++s) {
       store();
       __syncthreads();
-      if (s + 1 < s_end) load(s + 1);
+      if (s + 1 < u.s_end) load(s + 1);
       multiply_all();
       __syncthreads();
     }
-  }
-  if (last && g.full * kBK < g.inner) {
-#pragma unroll 1
-    for (int seg = 0; seg < SEGS; ++seg) {
-      stage_part(seg, g.full * kBK);
-      __syncthreads();
-      multiply_all();
-      __syncthreads();
-    }
-  }
+  };
 
-  // ---- outputs: lane holds row m, columns n .. n + 3 of each fragment ----
+  // ---- outputs: a lane holds row m, columns n .. n + 3 of each fragment ----
   const int r = lane & 15, p = lane >> 4;
-  const int64_t mend = MODE == kDw ? g.a.outer : g.a.outer;
+  constexpr int NO = MODE == kFwd ? NI / 2 : NI;   // output fragments per fragment row
   const int64_t nend = g.ldo;
-  auto put16 = [&](uint16_t* row, int64_t n, const float (&v)[4]) {
+  auto put16 = [&](uint16_t* row, int64_t n, uint2 w) {
     if (n + 4 <= nend && (reinterpret_cast<uintptr_t>(row + n) & 7) == 0) {
-      uint2 w;
-      w.x = f32_to_16<BF>(v[0]) | (f32_to_16<BF>(v[1]) << 16);
-      w.y = f32_to_16<BF>(v[2]) | (f32_to_16<BF>(v[3]) << 16);
       *reinterpret_cast<uint2*>(row + n) = w;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (n + e < nend) row[n + e] = (uint16_t)f32_to_16<BF>(v[e]);
+        if (n + e < nend) row[n + e] = (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
     }
   };
-  auto put32 = [&](float* row, int64_t n, const float (&v)[4]) {
+  auto put32 = [&](float* row, int64_t n, f32x4 v) {
     if (n + 4 <= nend && (reinterpret_cast<uintptr_t>(row + n) & 15) == 0) {
-      *reinterpret_cast<float4*>(row + n) = float4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(row + n) = v;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (n + e < nend) row[n + e] = v[e];
     }
   };
+  auto pack = [&](f32x4 v) {
+    return uint2{f32_to_16<BF>(v[0]) | (f32_to_16<BF>(v[1]) << 16), f32_to_16<BF>(v[2]) | (f32_to_16<BF>(v[3]) << 16)};
+  };
+  uint2 packed[MI][NO];   // 16-bit outputs
+  auto activate = [&](auto act) {
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int64_t m = m0 + (wm * MI + i) * 16 + r;
-    if (m >= mend) continue;
-    if constexpr (MODE == kFwd) {
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NI / 2; ++j) {
-        const int64_t n = n0 + (wn * (NI / 2) + j) * 16 + 4 * p;
-        if (n >= nend) continue;
-        float gv[4], uv[4], hv[4];
+      for (int j = 0; j < NO; ++j) {
+        f32x4 h;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          gv[e] = acc[i][j][e];
-          uv[e] = acc[i][j + NI / 2][e];
-          hv[e] = act_value(g.act, gv[e]) * uv[e];
-        }
-        put16(g.out[0] + m * g.ldo, n, hv);
-        if (g.save[0]) {
-          put32(g.save[0] + m * g.ldo, n, gv);
-          put32(g.save[1] + m * g.ldo, n, uv);
-        }
+        for (int e = 0; e < 4; ++e) h[e] = act_fast<decltype(act)::value>(acc[i][j][e]) * acc[i][j + NI / 2][e];
+        packed[i][j] = pack(h);
       }
+  };
+  auto round_outputs = [&] {
+    if constexpr (MODE == kFwd) {
+      if (g.act == EXTERND_ACT_SILU) activate(std::integral_constant<int, EXTERND_ACT_SILU>());
+      else if (g.act == EXTERND_ACT_GELU) activate(std::integral_constant<int, EXTERND_ACT_GELU>());
+      else activate(std::integral_constant<int, EXTERND_ACT_GELU_TANH>());
     } else {
 #pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        const int64_t n = n0 + (wn * NI + j) * 16 + 4 * p;
-        if (n >= nend) continue;
-        float v[4];
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e];
-        if (g.part) put32(g.part + ((int64_t)blockIdx.y * mend + m) * g.ldo, n, v);
-        else put16(g.out[outsel] + m * g.ldo, n, v);
+        for (int j = 0; j < NO; ++j) packed[i][j] = pack(acc[i][j]);
+    }
+  };
+  auto put_outputs = [&] {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int64_t m = u.m0 + (wm * MI + i) * 16 + r;
+      if (m >= g.a.outer) continue;
+#pragma unroll
+      for (int j = 0; j < NO; ++j) {
+        const int64_t n = u.n0 + (wn * NO + j) * 16 + 4 * p;
+        if (n >= nend) continue;
+        if (MODE == kDx && g.part) {
+          put32(g.part + ((int64_t)u.split * g.a.outer + m) * g.ldo, n, acc[i][j]);
+        } else {
+          put16(g.out[u.outsel] + m * g.ldo, n, packed[i][j]);
+          if (MODE == kFwd && g.save[0]) {
+            put32(g.save[0] + m * g.ldo, n, acc[i][j]);
+            put32(g.save[1] + m * g.ldo, n, acc[i][j + NI / 2]);
+          }
+        }
+      }
+    }
+  };
+
+  if constexpr (DMA) {
+    begin(u);
+    wait_vm<0, 0>();
+  }
+#pragma unroll 1
+  for (uint32_t at = blockIdx.x;;) {
+    clear();
+    if constexpr (DMA) {
+      block_barrier();   // every wave has waited for its first loads
+      contract();
+    } else {
+      contract_slow();
+    }
+    if (u.last && g.full * kBK < g.inner) {
+#pragma unroll 1
+      for (int seg = 0; seg < SEGS; ++seg) {
+        stage_part(seg, g.full * kBK);
+        __syncthreads();
+        multiply_all();
+        __syncthreads();
+      }
+    }
+    // The next unit's first loads travel while this one's outputs are worked out,
+    // and have arrived before the first output is stored: the stores then drain
+    // behind the next unit's products.
+    at += gridDim.x;
+    const bool more = at < units;
+    const Unit next = locate(more ? at : blockIdx.x);
+    if (DMA && more) begin(next);
+    round_outputs();
+    if constexpr (DMA) wait_vm<0, 0>();
+    put_outputs();
+    if (!more) break;
+    u = next;
+  }
+}
+
+// Sums of a split contraction, in the splits' order, rounded once.
+template <bool BF>
+__global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ part, int64_t count, int64_t splits,
+                                                     uint16_t* __restrict__ out) {
+  const int64_t quads = count / 4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads + (count & 3); i += (int64_t)gridDim.x * 256) {
+    if (i < quads && (count & 3) == 0) {
+      f32x4 s = reinterpret_cast<const f32x4*>(part)[i];
+      for (int64_t q = 1; q < splits; ++q) s += reinterpret_cast<const f32x4*>(part + q * count)[i];
+      uint2 w;
+      w.x = f32_to_16<BF>(s[0]) | (f32_to_16<BF>(s[1]) << 16);
+      w.y = f32_to_16<BF>(s[2]) | (f32_to_16<BF>(s[3]) << 16);
+      if ((reinterpret_cast<uintptr_t>(out) & 7) == 0) {
+        reinterpret_cast<uint2*>(out)[i] = w;
+      } else {
+        for (int e = 0; e < 4; ++e) out[4 * i + e] = (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
+      }
+    } else {
+      // a count that is no multiple of four leaves the later splits unaligned
+      const int64_t e0 = i < quads ? 4 * i : quads * 4 + (i - quads), e1 = i < quads ? e0 + 4 : e0 + 1;
+      for (int64_t e = e0; e < e1; ++e) {
+        float s = part[e];
+        for (int64_t q = 1; q < splits; ++q) s += part[q * count + e];
+        out[e] = (uint16_t)f32_to_16<BF>(s);
       }
     }
   }
@@ -535,11 +622,14 @@ __global__ void k_fill_u16(uint16_t* __restrict__ p, int64_t n) {
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Persistent workgroups: as many as are resident together (160 KB of LDS or 512
+// threads each at 256 x 256: one per CU; at 128 x 128 two).
 template <int MODE, int BM, int BN, int WM, int WN, bool DMA>
-hipError_t launch_tile(GemmArgs g, bool bf, hipStream_t s) {
+hipError_t launch_tile(GemmArgs g, bool bf, int cus, hipStream_t s) {
   g.mt = MODE == kDw ? 2 * up(g.a.outer, BM) : up(g.a.outer, BM);
   g.nt = up(g.b.outer, MODE == kFwd ? BN / 2 : BN);
-  const dim3 grid((unsigned)(g.mt * g.nt), (unsigned)std::max<int64_t>(1, up((MODE == kDx ? 2 : 1) * g.full, g.split_steps))), block(WM * WN * kWave);
+  const int64_t resident = (int64_t)cus * (BM == 256 ? 1 : 2);
+  const dim3 grid((unsigned)std::min<int64_t>(g.mt * g.nt * g.splits, resident)), block(WM * WN * kWave);
   if (bf) hipLaunchKernelGGL((k_gated_gemm<true, MODE, BM, BN, WM, WN, DMA>), grid, block, 0, s, g);
   else hipLaunchKernelGGL((k_gated_gemm<false, MODE, BM, BN, WM, WN, DMA>), grid, block, 0, s, g);
   return hipGetLastError();
@@ -551,13 +641,13 @@ bool dma_ok(const Operand& o, const void* p, bool cols) {
 }
 
 template <int MODE>
-hipError_t launch_gemm(const GemmArgs& g, bool bf, hipStream_t s) {
+hipError_t launch_gemm(const GemmArgs& g, bool bf, int cus, hipStream_t s) {
   const bool two_a = MODE != kFwd, two_b = MODE != kDw;
   const bool dma = dma_ok(g.a, g.a.p[0], MODE == kDw) && dma_ok(g.b, g.b.p[0], MODE != kFwd) &&
                    (!two_a || dma_ok(g.a, g.a.p[1], MODE == kDw)) && (!two_b || dma_ok(g.b, g.b.p[1], MODE != kFwd));
-  if (!dma) return launch_tile<MODE, 128, 128, 2, 2, false>(g, bf, s);
-  if (getenv("T128")) return launch_tile<MODE, 128, 128, 2, 2, true>(g, bf, s);
-  return launch_tile<MODE, 256, 256, 2, 4, true>(g, bf, s);
+  if (!dma) return launch_tile<MODE, 128, 128, 2, 2, false>(g, bf, cus, s);
+  if (getenv("T128")) return launch_tile<MODE, 128, 128, 2, 2, true>(g, bf, cus, s);
+  return launch_tile<MODE, 256, 256, 2, 4, true>(g, bf, cus, s);
 }
 
 int64_t padded(int64_t hidden) { return up(hidden, 8) * 8; }
@@ -577,6 +667,7 @@ size_t gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows)
 hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s) {
   (void)ws;
   GemmArgs g = {};
+  g.splits = 1;
   g.a.p[0] = static_cast<const uint16_t*>(a.x);
   g.a.ld = a.ldx;
   g.a.outer = a.tokens;
@@ -592,7 +683,7 @@ hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s) {
   g.save[0] = a.g;
   g.save[1] = a.u;
   g.act = a.act;
-  return launch_gemm<kFwd>(g, a.dtype == EXTERND_BF16, s);
+  return launch_gemm<kFwd>(g, a.dtype == EXTERND_BF16, a.cus, s);
 }
 
 hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
@@ -621,6 +712,7 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
   }
   if (a.dx) {
     GemmArgs g = {};
+    g.splits = 1;
     g.a.p[0] = dg;
     g.a.p[1] = du;
     g.a.ld = ldd;
@@ -634,10 +726,11 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
     g.split_steps = std::max<int64_t>(1, 2 * g.full);
     g.out[0] = static_cast<uint16_t*>(a.dx);
     g.ldo = a.cols;
-    if ((e = launch_gemm<kDx>(g, bf, s)) != hipSuccess) return e;
+    if ((e = launch_gemm<kDx>(g, bf, a.cus, s)) != hipSuccess) return e;
   }
   if (a.dwg) {
     GemmArgs g = {};
+    g.splits = 1;
     g.a.p[0] = dg;
     g.a.p[1] = du;
     g.a.ld = ldd;
@@ -651,7 +744,7 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
     g.out[0] = static_cast<uint16_t*>(a.dwg);
     g.out[1] = static_cast<uint16_t*>(a.dwu);
     g.ldo = a.cols;
-    if ((e = launch_gemm<kDw>(g, bf, s)) != hipSuccess) return e;
+    if ((e = launch_gemm<kDw>(g, bf, a.cus, s)) != hipSuccess) return e;
   }
   return hipSuccess;
 }

@@ -171,6 +171,7 @@ struct GatedArgs {
   const void* dh;
   int64_t lddh;
   void *dx, *dwg, *dwu;         // backward outputs: dx or null; both of dwg and dwu or null
+  int cus;                      // compute units of the device
 };
 size_t gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows);
 hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s);
