@@ -443,11 +443,13 @@ size_t externd_q4_workspace_bytes(int64_t cols, int64_t tokens, int32_t dtype);
  * (both or neither): tokens x rows fp32, the projections, kept for the
  * backward pass.  Strides are in entries, at least cols.  tokens may be 0.
  * workspace: as for externd_q4_apply, of externd_gated_forward_workspace_bytes
- * bytes (which may be 0). */
+ * bytes (which may be 0).  Its `aligned` says that x, Wg and Wu start on 16 bytes
+ * and that cols, ldx and ldw are multiples of 8; the products of more than 64
+ * tokens read padded copies otherwise, kept in the workspace. */
 int externd_gated_forward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wg, const void* wu,
                           int64_t rows, int64_t ldw, int32_t dtype, int32_t act, void* stream, void* h, float* g,
                           float* u, void* workspace, size_t workspace_bytes);
-size_t externd_gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows);
+size_t externd_gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t aligned);
 
 /* Gradients of the block from dh (tokens x rows, rows lddh entries apart) and
  * the g and u that the forward pass kept:
@@ -460,7 +462,7 @@ int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t 
                            int64_t rows, int64_t ldw, const float* g, const float* u, const void* dh, int64_t lddh,
                            int32_t dtype, int32_t act, void* stream, void* dx, void* dwg, void* dwu, void* workspace,
                            size_t workspace_bytes);
-size_t externd_gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows);
+size_t externd_gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t aligned);
 
 /* Status text and the last error message of the calling thread. */
 const char* externd_status_string(int status);

@@ -115,11 +115,11 @@ _q4_code_words = _sig("externd_q4_code_words", _i64, [_i64, _i64])
 _q4_table_len = _sig("externd_q4_table_len", _i64, [_i64, _i64, _i32])
 _gated_forward = _sig("externd_gated_forward", ctypes.c_int,
                       [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _i32, _i32, _p, _p, _p, _p, _p, _size])
-_gated_forward_ws = _sig("externd_gated_forward_workspace_bytes", _size, [_i64, _i64, _i64])
+_gated_forward_ws = _sig("externd_gated_forward_workspace_bytes", _size, [_i64, _i64, _i64, _i32])
 _gated_backward = _sig("externd_gated_backward", ctypes.c_int,
                        [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _p, _i64, _i32, _i32, _p, _p, _p, _p, _p,
                         _size])
-_gated_backward_ws = _sig("externd_gated_backward_workspace_bytes", _size, [_i64, _i64, _i64])
+_gated_backward_ws = _sig("externd_gated_backward_workspace_bytes", _size, [_i64, _i64, _i64, _i32])
 _status_string = _sig("externd_status_string", ctypes.c_char_p, [ctypes.c_int])
 _last_error = _sig("externd_last_error", ctypes.c_char_p, [])
 
@@ -640,16 +640,26 @@ def q4_workspace_bytes(cols, tokens, dtype):
     return int(_q4_ws(cols, tokens, _dtype_code(dtype, "dtype")))
 
 
+def _q4_scratch(workspace, x, ldx, dtype):
+    """As _gated_scratch, for the staged copy of x that the 4-bit products may need."""
+    if workspace is None:
+        tokens, cols = x.shape
+        if tokens == 0 or dtype != 0 and (cols | ldx) & 7 == 0 and x.data_ptr() & 15 == 0:
+            return None, 0, None
+        workspace = torch.empty((_q4_ws(cols, tokens, dtype),), dtype=torch.uint8, device=x.device)
+    return (*_scratch(workspace), workspace)
+
+
 def q4_apply(q, x, out=None, workspace=None):
     """y = x W^T with 4-bit W: x (..., cols) float32, bfloat16 or float16, y (..., rows) of its type.
     Rows of x may be strided.  Where x needs a staged copy (float32, or rows that are not 16-byte
-    aligned) the library allocates it stream-ordered unless workspace (at least
-    q4_workspace_bytes(...) bytes, 256-byte aligned) is given.  Not differentiable."""
+    aligned) it is made in workspace (at least q4_workspace_bytes(...) bytes, 256-byte aligned), by
+    default one from torch's allocator.  Not differentiable."""
     dtype = _dtype_code(x.dtype, "x")
     _op_device(x, q.codes)
     y = _out_or_new(out, x.shape[:-1] + (q.rows,), x.dtype, x.device)
     x, ldx = _rows_of(x, q.cols, "x")
-    ws, wsb = _scratch(workspace)
+    ws, wsb, keep = _q4_scratch(workspace, x, ldx, dtype)
     _check(_q4_apply(q._c, x.data_ptr(), x.shape[0], ldx, dtype, _stream(), y.data_ptr(), ws, wsb))
     return y
 
@@ -661,7 +671,7 @@ def q4_gated(qg, qu, x, act="silu", out=None, workspace=None):
     _op_device(x, qg.codes, qu.codes)
     h = _out_or_new(out, x.shape[:-1] + (qg.rows,), x.dtype, x.device)
     x, ldx = _rows_of(x, qg.cols, "x")
-    ws, wsb = _scratch(workspace)
+    ws, wsb, keep = _q4_scratch(workspace, x, ldx, dtype)
     _check(_q4_gated(qg._c, qu._c, x.data_ptr(), x.shape[0], ldx, dtype, _act_code(act), _stream(), h.data_ptr(), ws,
                      wsb))
     return h
@@ -685,14 +695,27 @@ def _gated_weights(x, Wg, Wu):
     return Wg, Wu, ldg, _DTYPE[x.dtype]
 
 
-def gated_forward_workspace_bytes(tokens, cols, rows):
-    """Device workspace gated_forward needs (may be 0)."""
-    return int(_gated_forward_ws(tokens, cols, rows))
+def gated_forward_workspace_bytes(tokens, cols, rows, aligned=True):
+    """Device workspace gated_forward needs (may be 0).  aligned: x, Wg and Wu start on 16 bytes, and
+    cols and their row strides are multiples of 8."""
+    return int(_gated_forward_ws(tokens, cols, rows, aligned))
 
 
-def gated_backward_workspace_bytes(tokens, cols, rows):
-    """Device workspace gated_backward needs (0: invalid)."""
-    return int(_gated_backward_ws(tokens, cols, rows))
+def gated_backward_workspace_bytes(tokens, cols, rows, aligned=True):
+    """Device workspace gated_backward needs (0: invalid); aligned as for gated_forward_workspace_bytes."""
+    return int(_gated_backward_ws(tokens, cols, rows, aligned))
+
+
+def _gated_scratch(workspace, bytes_of, x, ldx, Wg, Wu, ldw):
+    """(pointer, bytes, the tensor to keep) of the caller's workspace, or of one from torch's allocator
+    (whose blocks, unlike a stream-ordered allocation, cost next to nothing from one call to the next)."""
+    if workspace is None:
+        aligned = (x.data_ptr() | Wg.data_ptr() | Wu.data_ptr()) & 15 == 0 and (ldx | ldw | Wg.shape[1]) & 7 == 0
+        need = bytes_of(x.shape[0], Wg.shape[1], Wg.shape[0], aligned) if x.shape[0] else 0
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+    return (*_scratch(workspace), workspace)
 
 
 def gated_forward(x, Wg, Wu, act="silu", save=False, out=None, workspace=None):
@@ -712,7 +735,7 @@ def gated_forward(x, Wg, Wu, act="silu", save=False, out=None, workspace=None):
     g = u = None
     if save:
         g, u = torch.empty((2, tokens, rows), dtype=torch.float32, device=x.device)
-    ws, wsb = _scratch(workspace)
+    ws, wsb, keep = _gated_scratch(workspace, _gated_forward_ws, x, ldx, Wg, Wu, ldw)
     _check(_gated_forward(x.data_ptr(), tokens, cols, ldx, Wg.data_ptr(), Wu.data_ptr(), rows, ldw, dtype, act,
                           _stream(), h.data_ptr(), None if g is None else g.data_ptr(),
                           None if u is None else u.data_ptr(), ws, wsb))
@@ -741,7 +764,7 @@ def gated_backward(x, Wg, Wu, g, u, dh, act="silu", need_dx=True, need_dw=True, 
     dx = torch.empty(shape, dtype=x.dtype, device=x.device) if need_dx else None
     dwg = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if need_dw else None
     dwu = torch.empty_like(dwg) if need_dw else None
-    ws, wsb = _scratch(workspace)
+    ws, wsb, keep = _gated_scratch(workspace, _gated_backward_ws, x, ldx, Wg, Wu, ldw)
     _check(_gated_backward(x.data_ptr(), tokens, cols, ldx, Wg.data_ptr(), Wu.data_ptr(), rows, ldw, g.data_ptr(),
                            u.data_ptr(), dh.data_ptr(), lddh, dtype, act, _stream(), _ptr(dx), _ptr(dwg), _ptr(dwu),
                            ws, wsb))

@@ -640,9 +640,11 @@ int externd_q4_gated(const externd_q4* wg, const externd_q4* wu, const void* x, 
   return q4_product(both, 2, x, tokens, ldx, dtype, act, stream, h, workspace, workspace_bytes);
 }
 
-size_t externd_gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows) {
+size_t externd_gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t aligned) {
   if (bad_size(rows, cols) || tokens < 1 || bad_size(tokens, cols) || bad_size(tokens, rows)) return 0;
-  return externd::gated_forward_workspace_bytes(tokens, cols, rows);
+  int cus = 0;
+  if (check_device(&cus) != EXTERND_OK) return 0;
+  return externd::gated_forward_workspace_bytes(tokens, cols, rows, aligned != 0, cus);
 }
 
 int externd_gated_forward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wg, const void* wu,
@@ -665,17 +667,19 @@ int externd_gated_forward(const void* x, int64_t tokens, int64_t cols, int64_t l
   if ((st = check_device(&a.cus)) != EXTERND_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   Workspace ws;
-  if ((st = op_ws(ws, workspace, workspace_bytes, externd::gated_forward_workspace_bytes(tokens, cols, rows), s)) !=
-      EXTERND_OK)
-    return st;
+  const size_t need =
+      externd::gated_forward_workspace_bytes(tokens, cols, rows, externd::gated_is_aligned(a), a.cus);
+  if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
   hipError_t e = externd::run_gated_forward(a, ws.ptr, s);
   if (e != hipSuccess) return hip_fail(e, "gated forward");
   return EXTERND_OK;
 }
 
-size_t externd_gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows) {
+size_t externd_gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t aligned) {
   if (bad_size(rows, cols) || tokens < 1 || bad_size(tokens, cols) || bad_size(tokens, rows)) return 0;
-  return externd::gated_backward_workspace_bytes(tokens, cols, rows);
+  int cus = 0;
+  if (check_device(&cus) != EXTERND_OK) return 0;
+  return externd::gated_backward_workspace_bytes(tokens, cols, rows, aligned != 0, cus);
 }
 
 int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wg, const void* wu,
@@ -703,7 +707,10 @@ int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t 
   if ((st = check_device(&a.cus)) != EXTERND_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   Workspace ws;
-  const size_t need = tokens > 0 ? externd::gated_backward_workspace_bytes(tokens, cols, rows) : 0;
+  const size_t need =
+      tokens > 0
+          ? externd::gated_backward_workspace_bytes(tokens, cols, rows, externd::gated_is_aligned(a), a.cus)
+          : 0;
   if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
   hipError_t e = externd::run_gated_backward(a, ws.ptr, s);
   if (e != hipSuccess) return hip_fail(e, "gated backward");

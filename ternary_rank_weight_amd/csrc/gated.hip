@@ -54,9 +54,9 @@ struct GemmArgs {
   int64_t mt, nt;       // tiles
   int64_t splits;
   uint16_t* out[2];     // forward: h; dx: dx; dw: dWg, dWu
-  int64_t ldo;          // columns of the outputs
+  int64_t mo, ldo;      // rows and columns of the outputs
   float* save[2];       // forward: g, u (or null)
-  float* part;          // partial sums of a split contraction (or null)
+  float* part;          // SPLIT: where the splits' sums go, fp32 (split, output, mo, ldo)
   int act;
 };
 
@@ -133,10 +133,10 @@ __device__ __forceinline__ void for_constants(F&& f) {
 // WM x WN waves.  The products take b's fragment as first and a's as second
 // operand, so that a lane holds four neighbouring output columns of one row.
 //
-// DMA: both operands can be read in 16-byte pieces, and whole steps go from
-// memory to LDS without passing through registers.  Otherwise (and for the
-// last, partial step of a contraction) a step is read through registers.
-template <bool BF, int MODE, int BM, int BN, int WM, int WN, bool DMA>
+// Whole steps go from memory to LDS without passing through registers (so every
+// row starts 16-byte aligned); the last, partial step of a contraction is read
+// through registers.
+template <bool BF, int MODE, int BM, int BN, int WM, int WN, bool SPLIT>
 __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
   constexpr int NTHR = WM * WN * kWave;
   constexpr bool ACOLS = MODE == kDw, BCOLS = MODE != kFwd;
@@ -146,9 +146,8 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
   constexpr int SA = TA::kSlots / NTHR, SB = TB::kSlots / NTHR;
   // separate objects: the compiler then sees that a read of one image need not
   // wait for the loads into another
-  constexpr int A1 = DMA ? BM * kBK : 8, B1 = DMA ? BN * kBK : 8;
-  __shared__ __align__(16) uint16_t sa0[BM * kBK], sa1[A1], sa2[A1];
-  __shared__ __align__(16) uint16_t sb0[BN * kBK], sb1[B1];
+  __shared__ __align__(16) uint16_t sa0[BM * kBK], sa1[BM * kBK], sa2[BM * kBK];
+  __shared__ __align__(16) uint16_t sb0[BN * kBK], sb1[BN * kBK];
   const lds16 la0 = (lds16)sa0, la1 = (lds16)sa1, la2 = (lds16)sa2, lb0 = (lds16)sb0, lb1 = (lds16)sb1;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int wm = wave / WN, wn = wave % WN;
@@ -227,7 +226,7 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
   // eight entries of a slot through registers, zero past either end
   auto fetch = [&](const uint16_t* p, bool cols, int64_t left_o, int64_t left_k) -> u32x4 {
     const int64_t n = cols ? (left_k > 0 ? left_o : 0) : left_k;
-    if (n >= 8) return (reinterpret_cast<uintptr_t>(p) & 15) == 0 ? load8<true>(p) : load8<false>(p);
+    if (n >= 8) return load8<true>(p);
     return n > 0 ? load8_part(p, n) : u32x4{0u, 0u, 0u, 0u};
   };
   // a partial step, slot by slot through registers
@@ -413,61 +412,26 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
       __syncthreads();
     }
   };
-  auto contract_slow = [&] {
-    if (u.s_begin >= u.s_end) return;
-    // the next step is in registers while one is worked on
-    u32x4 ra[SA], rb[SB];
-    auto load = [&](int64_t step) {
-      const int seg = SEGS == 2 ? (int)(step >= g.full) : 0;
-      const int64_t k0 = (step - seg * g.full) * kBK;
-      int64_t lo, lk;
-#pragma unroll
-      for (int i = 0; i < SA; ++i) {
-        const uint16_t* p = src_a(i * NTHR + tid, seg, k0, lo, lk);
-        ra[i] = fetch(p, ACOLS, lo, lk);
-      }
-#pragma unroll
-      for (int i = 0; i < SB; ++i) {
-        const uint16_t* p = src_b(i * NTHR + tid, seg, k0, lo, lk);
-        rb[i] = fetch(p, BCOLS, lo, lk);
-      }
-    };
-    auto store = [&]() {
-#pragma unroll
-      for (int i = 0; i < SA; ++i) *(lds_u32x4*)(la0 + (i * NTHR + tid) * 8) = ra[i];
-#pragma unroll
-      for (int i = 0; i < SB; ++i) *(lds_u32x4*)(lb0 + (i * NTHR + tid) * 8) = rb[i];
-    };
-    load(u.s_begin);
-    for (int64_t s = u.s_begin; s < u.s_end; ++s) {
-      store();
-      __syncthreads();
-      if (s + 1 < u.s_end) load(s + 1);
-      multiply_all();
-      __syncthreads();
-    }
-  };
-
   // ---- outputs: a lane holds row m, columns n .. n + 3 of each fragment ----
   const int r = lane & 15, p = lane >> 4;
   constexpr int NO = MODE == kFwd ? NI / 2 : NI;   // output fragments per fragment row
-  const int64_t nend = g.ldo;
-  auto put16 = [&](uint16_t* row, int64_t n, uint2 w) {
-    if (n + 4 <= nend && (reinterpret_cast<uintptr_t>(row + n) & 7) == 0) {
-      *reinterpret_cast<uint2*>(row + n) = w;
+  // whole: the fragment's four entries exist and may be stored at once
+  auto put16 = [&](uint16_t* q, int64_t left, bool whole, uint2 w) {
+    if (whole) {
+      *reinterpret_cast<uint2*>(q) = w;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (n + e < nend) row[n + e] = (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
+        if (e < left) q[e] = (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
     }
   };
-  auto put32 = [&](float* row, int64_t n, f32x4 v) {
-    if (n + 4 <= nend && (reinterpret_cast<uintptr_t>(row + n) & 15) == 0) {
-      *reinterpret_cast<f32x4*>(row + n) = v;
+  auto put32 = [&](float* q, int64_t left, bool whole, f32x4 v) {
+    if (whole) {
+      *reinterpret_cast<f32x4*>(q) = v;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (n + e < nend) row[n + e] = v[e];
+        if (e < left) q[e] = v[e];
     }
   };
   auto pack = [&](f32x4 v) {
@@ -497,41 +461,43 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
         for (int j = 0; j < NO; ++j) packed[i][j] = pack(acc[i][j]);
     }
   };
-  auto put_outputs = [&] {
+  const int64_t n_lane = wn * NO * 16 + 4 * p, m_lane = wm * MI * 16 + r;
+  auto put_outputs = [&](auto inside) {   // inside: the tile is, and its rows are aligned
+    constexpr bool IN = decltype(inside)::value;
+    constexpr int OUTS = MODE == kDx ? 1 : 2;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int64_t m = u.m0 + (wm * MI + i) * 16 + r;
-      if (m >= g.a.outer) continue;
+      const int64_t m = u.m0 + m_lane + i * 16, at = m * g.ldo + u.n0 + n_lane;
+      if (!IN && m >= g.mo) continue;
 #pragma unroll
       for (int j = 0; j < NO; ++j) {
-        const int64_t n = u.n0 + (wn * NO + j) * 16 + 4 * p;
-        if (n >= nend) continue;
-        if (MODE == kDx && g.part) {
-          put32(g.part + ((int64_t)u.split * g.a.outer + m) * g.ldo, n, acc[i][j]);
+        const int64_t left = g.ldo - (u.n0 + n_lane + j * 16);
+        if (!IN && left <= 0) continue;
+        if constexpr (SPLIT) {
+          float* q = g.part + ((int64_t)u.split * OUTS + u.outsel) * g.mo * g.ldo + at + j * 16;
+          put32(q, left, IN, acc[i][j]);
+          if constexpr (MODE == kFwd) put32(q + g.mo * g.ldo, left, IN, acc[i][j + NI / 2]);
         } else {
-          put16(g.out[u.outsel] + m * g.ldo, n, packed[i][j]);
+          put16(g.out[u.outsel] + at + j * 16, left, IN, packed[i][j]);
           if (MODE == kFwd && g.save[0]) {
-            put32(g.save[0] + m * g.ldo, n, acc[i][j]);
-            put32(g.save[1] + m * g.ldo, n, acc[i][j + NI / 2]);
+            put32(g.save[0] + at + j * 16, left, IN, acc[i][j]);
+            put32(g.save[1] + at + j * 16, left, IN, acc[i][j + NI / 2]);
           }
         }
       }
     }
   };
+  const bool aligned = g.ldo % 4 == 0 &&
+                       ((reinterpret_cast<uintptr_t>(g.out[0]) | reinterpret_cast<uintptr_t>(g.out[1])) & 7) == 0 &&
+                       ((reinterpret_cast<uintptr_t>(g.save[0]) | reinterpret_cast<uintptr_t>(g.save[1])) & 15) == 0;
 
-  if constexpr (DMA) {
-    begin(u);
-    wait_vm<0, 0>();
-  }
+  begin(u);
+  wait_vm<0, 0>();
 #pragma unroll 1
   for (uint32_t at = blockIdx.x;;) {
     clear();
-    if constexpr (DMA) {
-      block_barrier();   // every wave has waited for its first loads
-      contract();
-    } else {
-      contract_slow();
-    }
+    block_barrier();   // every wave has waited for its first loads
+    contract();
     if (u.last && g.full * kBK < g.inner) {
 #pragma unroll 1
       for (int seg = 0; seg < SEGS; ++seg) {
@@ -547,71 +513,95 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
     at += gridDim.x;
     const bool more = at < units;
     const Unit next = locate(more ? at : blockIdx.x);
-    if (DMA && more) begin(next);
-    round_outputs();
-    if constexpr (DMA) wait_vm<0, 0>();
-    put_outputs();
+    if (more) begin(next);
+    if constexpr (!SPLIT) round_outputs();
+    wait_vm<0, 0>();
+    if (aligned && u.m0 + BM <= g.mo && u.n0 + BNO <= g.ldo) put_outputs(std::true_type());
+    else put_outputs(std::false_type());
     if (!more) break;
     u = next;
   }
 }
 
-// Sums of a split contraction, in the splits' order, rounded once.
-template <bool BF>
+// What the split contractions left: the splits' sums in their order, then the
+// outputs as the unsplit kernel makes them.  part: (split, outs, count) fp32.
+// Forward: both projections, the activation and the product.  Bound by HBM.
+template <bool BF, int MODE>
 __global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ part, int64_t count, int64_t splits,
-                                                     uint16_t* __restrict__ out) {
-  const int64_t quads = count / 4;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads + (count & 3); i += (int64_t)gridDim.x * 256) {
-    if (i < quads && (count & 3) == 0) {
-      f32x4 s = reinterpret_cast<const f32x4*>(part)[i];
-      for (int64_t q = 1; q < splits; ++q) s += reinterpret_cast<const f32x4*>(part + q * count)[i];
-      uint2 w;
-      w.x = f32_to_16<BF>(s[0]) | (f32_to_16<BF>(s[1]) << 16);
-      w.y = f32_to_16<BF>(s[2]) | (f32_to_16<BF>(s[3]) << 16);
-      if ((reinterpret_cast<uintptr_t>(out) & 7) == 0) {
-        reinterpret_cast<uint2*>(out)[i] = w;
-      } else {
-        for (int e = 0; e < 4; ++e) out[4 * i + e] = (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
-      }
+                                                     uint16_t* __restrict__ out0, uint16_t* __restrict__ out1,
+                                                     float* __restrict__ g, float* __restrict__ u, int act) {
+  constexpr int OUTS = MODE == kDx ? 1 : 2;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
+    float s[OUTS];
+#pragma unroll
+    for (int o = 0; o < OUTS; ++o) {
+      s[o] = part[o * count + i];
+      for (int64_t q = 1; q < splits; ++q) s[o] += part[(q * OUTS + o) * count + i];
+    }
+    if constexpr (MODE == kFwd) {
+      out0[i] = (uint16_t)f32_to_16<BF>(act_value(act, s[0]) * s[1]);
+      if (g) { g[i] = s[0]; u[i] = s[1]; }
     } else {
-      // a count that is no multiple of four leaves the later splits unaligned
-      const int64_t e0 = i < quads ? 4 * i : quads * 4 + (i - quads), e1 = i < quads ? e0 + 4 : e0 + 1;
-      for (int64_t e = e0; e < e1; ++e) {
-        float s = part[e];
-        for (int64_t q = 1; q < splits; ++q) s += part[q * count + e];
-        out[e] = (uint16_t)f32_to_16<BF>(s);
-      }
+      out0[i] = (uint16_t)f32_to_16<BF>(s[0]);
+      if constexpr (MODE == kDw) out1[i] = (uint16_t)f32_to_16<BF>(s[1]);
     }
   }
 }
 
-// dg and du, rounded to the operands' type, in rows of ldd entries (a
-// multiple of 8; zero past the hidden width).  Bound by HBM: reads 4 + 4 + 2 bytes,
-// writes 2 + 2 per hidden unit and token.
-template <bool BF>
+// dg and du, rounded to the operands' type, in rows of ldd entries (a multiple
+// of 8; zero past the hidden width).  Bound by HBM: reads 4 + 4 + 2 bytes, writes
+// 2 + 2 per hidden unit and token.  VEC: rows of all inputs are 16-byte aligned.
+template <bool BF, bool VEC>
 __global__ __launch_bounds__(256) void k_gated_slopes(const float* __restrict__ g, const float* __restrict__ u,
                                                        const uint16_t* __restrict__ dh, int64_t tokens, int64_t hidden,
                                                        int64_t lddh, int64_t ldd, int act, uint16_t* __restrict__ dg,
                                                        uint16_t* __restrict__ du) {
-  const int64_t total = tokens * (ldd / 4);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / (ldd / 4), c = (i - t * (ldd / 4)) * 4;
-    uint32_t og[4], ou[4];
+  const int64_t per = ldd / 8, total = tokens * per;
+  auto run = [&](auto kind) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+      const int64_t t = i / per, c = (i - t * per) * 8, at = t * hidden + c;
+      float gv[8], uv[8], d[8];
+      if constexpr (VEC) {   // hidden is a multiple of 8 here
+        const u32x4 dv = *reinterpret_cast<const u32x4*>(dh + t * lddh + c);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      og[e] = ou[e] = 0u;
-      if (c + e < hidden) {
-        const float gv = g[t * hidden + c + e], uv = u[t * hidden + c + e];
-        const float d = f32_from_16<BF>(dh[t * lddh + c + e]);
-        float a, slope;
-        act_both(act, gv, a, slope);
-        og[e] = f32_to_16<BF>(d * uv * slope);
-        ou[e] = f32_to_16<BF>(d * a);
+        for (int e = 0; e < 8; e += 4) {
+          const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(g + at + e));
+          const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(u + at + e));
+#pragma unroll
+          for (int f = 0; f < 4; ++f) { gv[e + f] = a[f]; uv[e + f] = b[f]; }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] = f32_from_16<BF>((dv[e / 2] >> (16 * (e & 1))) & 0xffffu);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool ok = c + e < hidden;
+          gv[e] = ok ? g[at + e] : 0.f;
+          uv[e] = ok ? u[at + e] : 0.f;
+          d[e] = ok ? f32_from_16<BF>(dh[t * lddh + c + e]) : 0.f;
+        }
       }
+      u32x4 og, ou;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        uint32_t wg[2], wu[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          float a, slope;
+          act_both_fast<decltype(kind)::value>(gv[e + f], a, slope);
+          wg[f] = f32_to_16<BF>(d[e + f] * uv[e + f] * slope);
+          wu[f] = f32_to_16<BF>(d[e + f] * a);
+        }
+        og[e / 2] = wg[0] | (wg[1] << 16);
+        ou[e / 2] = wu[0] | (wu[1] << 16);
+      }
+      *reinterpret_cast<u32x4*>(dg + t * ldd + c) = og;
+      *reinterpret_cast<u32x4*>(du + t * ldd + c) = ou;
     }
-    *reinterpret_cast<uint2*>(dg + t * ldd + c) = uint2{og[0] | (og[1] << 16), og[2] | (og[3] << 16)};
-    *reinterpret_cast<uint2*>(du + t * ldd + c) = uint2{ou[0] | (ou[1] << 16), ou[2] | (ou[3] << 16)};
-  }
+  };
+  if (act == EXTERND_ACT_SILU) run(std::integral_constant<int, EXTERND_ACT_SILU>());
+  else if (act == EXTERND_ACT_GELU) run(std::integral_constant<int, EXTERND_ACT_GELU>());
+  else run(std::integral_constant<int, EXTERND_ACT_GELU_TANH>());
 }
 
 // Zero outputs (a weight gradient of no tokens).
@@ -620,70 +610,186 @@ __global__ void k_fill_u16(uint16_t* __restrict__ p, int64_t n) {
     p[i] = 0;
 }
 
-int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Up to three matrices of 16-bit entries copied into rows of ldp entries (a
+// multiple of 64), zero past their columns: what the 16-byte loads need where
+// the caller's rows are not aligned.
+struct PadArgs {
+  const uint16_t* src[3];
+  uint16_t* dst[3];
+  int64_t rows[3], ld[3];
+  int64_t cols, ldp;
+};
+__global__ __launch_bounds__(256) void k_pad_rows(PadArgs a) {
+  const int w = blockIdx.y;
+  const int64_t per = a.ldp / 8, total = a.rows[w] * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per, c = (i - row * per) * 8, left = a.cols - c;
+    const uint16_t* p = a.src[w] + row * a.ld[w] + c;
+    const u32x4 v = left >= 8 ? load8<false>(p) : load8_part(p, left);
+    *reinterpret_cast<u32x4*>(a.dst[w] + row * a.ldp + c) = v;
+  }
+}
 
-// Persistent workgroups: as many as are resident together (160 KB of LDS or 512
-// threads each at 256 x 256: one per CU; at 128 x 128 two).
-template <int MODE, int BM, int BN, int WM, int WN, bool DMA>
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t padded(int64_t n, int64_t to) { return up(n, to) * to; }
+unsigned blocks(int64_t items) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(up(items, 256), 1 << 15)); }
+
+// Tile and number of splits of a product of m x n outputs (forward: n hidden
+// units; dW: m rows of each of the two gradients) over `steps` steps: the least
+// of an estimate in microseconds.  At 256 x 256 one workgroup per CU takes about
+// 1.4 us a step and 6 us a tile; at 128 x 128 two per CU take 0.95 us a step and
+// 4 us a tile each, one alone 0.6 us a step (measured on K = 2560 and F = 9728).  A
+// split costs its sums' way to memory and back.
+struct Plan {
+  bool big;
+  int64_t splits;
+};
+int64_t tiles_of(int mode, int64_t m, int64_t n, bool big) {
+  const int64_t b = big ? 256 : 128;
+  return (mode == kDw ? 2 : 1) * up(m, b) * up(n, mode == kFwd ? b / 2 : b);
+}
+Plan plan_of(int mode, int64_t m, int64_t n, int64_t steps, int cus) {
+  Plan best = {false, 1};
+  double least = 1e300;
+  for (const bool big : {true, false}) {
+    const int64_t tiles = tiles_of(mode, m, n, big);
+    // (only dx is split at 256 x 256: the others have 128 x 128 for the shapes that need it)
+    const int64_t most = big && mode != kDx ? 1 : 16;
+    for (int64_t splits = 1; splits <= most && splits <= std::max<int64_t>(1, steps / 4); ++splits) {
+      const int64_t units = tiles * splits, slots = (int64_t)cus * (big ? 1 : 2);
+      const double per = (double)up(std::max<int64_t>(steps, 1), splits);
+      const double rounds = (double)up(units, slots);
+      const double step = big ? 1.4 : units > cus ? 0.95 : 0.6;
+      double us = rounds * (per * step + (big ? 6.0 : 4.0));
+      if (splits > 1) us += 4.0 + (double)(mode == kDx ? 1 : 2) * (double)m * (double)n * 4.0 * (double)(splits * 2) / 4e6;
+      if (us < least) {
+        least = us;
+        best = {big, splits};
+      }
+    }
+  }
+  return best;
+}
+int64_t part_floats(int mode, int64_t m, int64_t n, const Plan& p) {
+  return p.splits > 1 ? p.splits * (mode == kDx ? 1 : 2) * m * n : 0;
+}
+
+// Persistent workgroups: as many as are resident together (160 KB of LDS at 256
+// x 256, one per CU; 80 KB at 128 x 128, two).
+template <int MODE, int BM, int BN, int WM, int WN, bool SPLIT>
 hipError_t launch_tile(GemmArgs g, bool bf, int cus, hipStream_t s) {
   g.mt = MODE == kDw ? 2 * up(g.a.outer, BM) : up(g.a.outer, BM);
   g.nt = up(g.b.outer, MODE == kFwd ? BN / 2 : BN);
   const int64_t resident = (int64_t)cus * (BM == 256 ? 1 : 2);
   const dim3 grid((unsigned)std::min<int64_t>(g.mt * g.nt * g.splits, resident)), block(WM * WN * kWave);
-  if (bf) hipLaunchKernelGGL((k_gated_gemm<true, MODE, BM, BN, WM, WN, DMA>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((k_gated_gemm<false, MODE, BM, BN, WM, WN, DMA>), grid, block, 0, s, g);
+  if (bf) hipLaunchKernelGGL((k_gated_gemm<true, MODE, BM, BN, WM, WN, SPLIT>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((k_gated_gemm<false, MODE, BM, BN, WM, WN, SPLIT>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 
-bool dma_ok(const Operand& o, const void* p, bool cols) {
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && o.ld % 8 == 0 && o.ld < (1 << 22) &&
-         (!cols || o.outer % 8 == 0);
-}
-
+// One product and, when split, its join.  part: room for part_floats.
 template <int MODE>
-hipError_t launch_gemm(const GemmArgs& g, bool bf, int cus, hipStream_t s) {
-  const bool two_a = MODE != kFwd, two_b = MODE != kDw;
-  const bool dma = dma_ok(g.a, g.a.p[0], MODE == kDw) && dma_ok(g.b, g.b.p[0], MODE != kFwd) &&
-                   (!two_a || dma_ok(g.a, g.a.p[1], MODE == kDw)) && (!two_b || dma_ok(g.b, g.b.p[1], MODE != kFwd));
-  if (!dma) return launch_tile<MODE, 128, 128, 2, 2, false>(g, bf, cus, s);
-  if (getenv("T128")) return launch_tile<MODE, 128, 128, 2, 2, true>(g, bf, cus, s);
-  return launch_tile<MODE, 256, 256, 2, 4, true>(g, bf, cus, s);
+hipError_t product(GemmArgs g, const Plan& plan, float* part, bool bf, int cus, hipStream_t s) {
+  constexpr int SEGS = MODE == kDx ? 2 : 1;
+  g.full = g.inner / kBK;
+  const int64_t whole = std::max<int64_t>(1, SEGS * g.full);
+  g.split_steps = up(whole, plan.splits);
+  g.splits = up(whole, g.split_steps);   // none without steps
+  if (plan.splits == 1)
+    return plan.big ? launch_tile<MODE, 256, 256, 2, 4, false>(g, bf, cus, s)
+                    : launch_tile<MODE, 128, 128, 2, 2, false>(g, bf, cus, s);
+  g.part = part;
+  hipError_t e = hipSuccess;
+  if constexpr (MODE == kDx)
+    if (plan.big) e = launch_tile<MODE, 256, 256, 2, 4, true>(g, bf, cus, s);
+  if (MODE != kDx || !plan.big) e = launch_tile<MODE, 128, 128, 2, 2, true>(g, bf, cus, s);
+  if (e != hipSuccess) return e;
+  const int64_t count = g.mo * g.ldo;
+  const dim3 grid(blocks(count)), block(256);
+  if (bf)
+    hipLaunchKernelGGL((k_gated_join<true, MODE>), grid, block, 0, s, part, count, g.splits, g.out[0], g.out[1],
+                       g.save[0], g.save[1], g.act);
+  else
+    hipLaunchKernelGGL((k_gated_join<false, MODE>), grid, block, 0, s, part, count, g.splits, g.out[0], g.out[1],
+                       g.save[0], g.save[1], g.act);
+  return hipGetLastError();
 }
 
-int64_t padded(int64_t hidden) { return up(hidden, 8) * 8; }
+bool rows_aligned(const void* p, int64_t ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && ld < (1 << 22);
+}
+
+// x, Wg and Wu as the products can read them: the caller's, or padded copies in
+// the workspace.
+struct Operands {
+  const uint16_t *x, *wg, *wu;
+  int64_t ldx, ldw, cols;   // cols: padded, when copied
+};
+bool needs_copies(const GatedArgs& a) {
+  return !rows_aligned(a.x, a.ldx) || !rows_aligned(a.wg, a.ldw) || !rows_aligned(a.wu, a.ldw) || a.cols % 8 != 0;
+}
+int64_t copy_entries(int64_t tokens, int64_t cols, int64_t rows) { return (tokens + 2 * rows) * padded(cols, kBK); }
+hipError_t operands(const GatedArgs& a, uint16_t* ws, Operands* o, hipStream_t s) {
+  *o = {static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.wg), static_cast<const uint16_t*>(a.wu),
+        a.ldx, a.ldw, a.cols};
+  if (!needs_copies(a)) return hipSuccess;
+  PadArgs q;
+  q.cols = a.cols;
+  q.ldp = padded(a.cols, kBK);
+  q.src[0] = o->x; q.src[1] = o->wg; q.src[2] = o->wu;
+  q.rows[0] = a.tokens; q.rows[1] = q.rows[2] = a.rows;
+  q.ld[0] = a.ldx; q.ld[1] = q.ld[2] = a.ldw;
+  for (int w = 0; w < 3; ++w) {
+    q.dst[w] = ws;
+    ws += q.rows[w] * q.ldp;
+  }
+  hipLaunchKernelGGL(k_pad_rows, dim3(blocks(std::max(a.tokens, a.rows) * (q.ldp / 8)), 3), dim3(256), 0, s, q);
+  *o = {q.dst[0], q.dst[1], q.dst[2], q.ldp, q.ldp, q.ldp};
+  return hipGetLastError();
+}
+
+int64_t steps_of(int64_t inner) { return inner / kBK; }
+size_t region(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows) {
-  (void)cols;
-  return (size_t)(2 * tokens * padded(rows)) * 2 + 256;
-}
+bool gated_is_aligned(const GatedArgs& a) { return !needs_copies(a); }
 
-size_t gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows) {
-  (void)tokens; (void)cols; (void)rows;
-  return 0;
+// Workspace: dg and du, padded copies unless aligned, then the split sums.
+size_t gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus) {
+  if (gated_takes_rows(tokens)) return 0;
+  const Plan p = plan_of(kFwd, tokens, rows, steps_of(padded(cols, kBK)), cus);
+  return (aligned ? 0 : region(2 * (size_t)copy_entries(tokens, cols, rows))) +
+         region(4 * (size_t)part_floats(kFwd, tokens, rows, p));
 }
 
 hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s) {
-  (void)ws;
+  if (gated_takes_rows(a.tokens)) return run_gated_rows(a, s);
+  const bool bf = a.dtype == EXTERND_BF16;
+  char* w = static_cast<char*>(ws);
+  Operands o;
+  hipError_t e = operands(a, reinterpret_cast<uint16_t*>(w), &o, s);
+  if (e != hipSuccess) return e;
+  if (needs_copies(a)) w += region(2 * (size_t)copy_entries(a.tokens, a.cols, a.rows));
   GemmArgs g = {};
-  g.splits = 1;
-  g.a.p[0] = static_cast<const uint16_t*>(a.x);
-  g.a.ld = a.ldx;
-  g.a.outer = a.tokens;
-  g.b.p[0] = static_cast<const uint16_t*>(a.wg);
-  g.b.p[1] = static_cast<const uint16_t*>(a.wu);
-  g.b.ld = a.ldw;
-  g.b.outer = a.rows;
-  g.inner = a.cols;
-  g.full = a.cols / kBK;
-  g.split_steps = std::max<int64_t>(1, g.full);
+  g.a = {{o.x, o.x}, o.ldx, a.tokens};
+  g.b = {{o.wg, o.wu}, o.ldw, a.rows};
+  g.inner = o.cols;
   g.out[0] = static_cast<uint16_t*>(a.h);
+  g.mo = a.tokens;
   g.ldo = a.rows;
   g.save[0] = a.g;
   g.save[1] = a.u;
   g.act = a.act;
-  return launch_gemm<kFwd>(g, a.dtype == EXTERND_BF16, a.cus, s);
+  const Plan p = plan_of(kFwd, a.tokens, a.rows, steps_of(padded(a.cols, kBK)), a.cus);
+  return product<kFwd>(g, p, reinterpret_cast<float*>(w), bf, a.cus, s);
+}
+
+size_t gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus) {
+  const Plan px = plan_of(kDx, tokens, cols, 2 * steps_of(rows), cus), pw = plan_of(kDw, rows, cols, steps_of(tokens), cus);
+  return region(2 * (size_t)(2 * tokens * padded(rows, 8))) +
+         (aligned ? 0 : region(2 * (size_t)copy_entries(tokens, cols, rows))) +
+         region(4 * (size_t)std::max(part_floats(kDx, tokens, cols, px), part_floats(kDw, rows, cols, pw)));
 }
 
 hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
@@ -697,54 +803,51 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
     }
     return hipSuccess;
   }
-  const int64_t ldd = padded(a.rows);
-  uint16_t* dg = reinterpret_cast<uint16_t*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~(uintptr_t)255);
+  const int64_t ldd = padded(a.rows, 8);
+  char* w = static_cast<char*>(ws);
+  uint16_t* dg = reinterpret_cast<uint16_t*>(w);
   uint16_t* du = dg + a.tokens * ldd;
+  w += region(2 * (size_t)(2 * a.tokens * ldd));
   {
-    const dim3 grid((unsigned)std::min<int64_t>(up(a.tokens * (ldd / 4), 256), 16384));
-    if (bf)
-      hipLaunchKernelGGL(k_gated_slopes<true>, grid, dim3(256), 0, s, a.g, a.u, static_cast<const uint16_t*>(a.dh),
-                         a.tokens, a.rows, a.lddh, ldd, a.act, dg, du);
-    else
-      hipLaunchKernelGGL(k_gated_slopes<false>, grid, dim3(256), 0, s, a.g, a.u, static_cast<const uint16_t*>(a.dh),
-                         a.tokens, a.rows, a.lddh, ldd, a.act, dg, du);
+    const bool vec = a.rows % 8 == 0 && a.lddh % 8 == 0 &&
+                     ((reinterpret_cast<uintptr_t>(a.dh) | reinterpret_cast<uintptr_t>(a.g) |
+                       reinterpret_cast<uintptr_t>(a.u)) & 15) == 0;
+    const dim3 grid(blocks(a.tokens * (ldd / 8))), block(256);
+    auto run = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, block, 0, s, a.g, a.u, static_cast<const uint16_t*>(a.dh), a.tokens, a.rows,
+                         a.lddh, ldd, a.act, dg, du);
+    };
+    if (bf) vec ? run(k_gated_slopes<true, true>) : run(k_gated_slopes<true, false>);
+    else vec ? run(k_gated_slopes<false, true>) : run(k_gated_slopes<false, false>);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
+  Operands o;
+  if ((e = operands(a, reinterpret_cast<uint16_t*>(w), &o, s)) != hipSuccess) return e;
+  if (needs_copies(a)) w += region(2 * (size_t)copy_entries(a.tokens, a.cols, a.rows));
+  float* part = reinterpret_cast<float*>(w);
+  const int64_t cols8 = padded(a.cols, 8);
   if (a.dx) {
     GemmArgs g = {};
-    g.splits = 1;
-    g.a.p[0] = dg;
-    g.a.p[1] = du;
-    g.a.ld = ldd;
-    g.a.outer = a.tokens;
-    g.b.p[0] = static_cast<const uint16_t*>(a.wg);
-    g.b.p[1] = static_cast<const uint16_t*>(a.wu);
-    g.b.ld = a.ldw;
-    g.b.outer = a.cols;
+    g.a = {{dg, du}, ldd, a.tokens};
+    g.b = {{o.wg, o.wu}, o.ldw, cols8};
     g.inner = a.rows;
-    g.full = a.rows / kBK;
-    g.split_steps = std::max<int64_t>(1, 2 * g.full);
     g.out[0] = static_cast<uint16_t*>(a.dx);
+    g.mo = a.tokens;
     g.ldo = a.cols;
-    if ((e = launch_gemm<kDx>(g, bf, a.cus, s)) != hipSuccess) return e;
+    const Plan p = plan_of(kDx, a.tokens, a.cols, 2 * steps_of(a.rows), a.cus);
+    if ((e = product<kDx>(g, p, part, bf, a.cus, s)) != hipSuccess) return e;
   }
   if (a.dwg) {
     GemmArgs g = {};
-    g.splits = 1;
-    g.a.p[0] = dg;
-    g.a.p[1] = du;
-    g.a.ld = ldd;
-    g.a.outer = a.rows;
-    g.b.p[0] = static_cast<const uint16_t*>(a.x);
-    g.b.ld = a.ldx;
-    g.b.outer = a.cols;
+    g.a = {{dg, du}, ldd, ldd};
+    g.b = {{o.x, o.x}, o.ldx, cols8};
     g.inner = a.tokens;
-    g.full = a.tokens / kBK;
-    g.split_steps = std::max<int64_t>(1, g.full);
     g.out[0] = static_cast<uint16_t*>(a.dwg);
     g.out[1] = static_cast<uint16_t*>(a.dwu);
+    g.mo = a.rows;
     g.ldo = a.cols;
-    if ((e = launch_gemm<kDw>(g, bf, a.cus, s)) != hipSuccess) return e;
+    const Plan p = plan_of(kDw, a.rows, a.cols, steps_of(a.tokens), a.cus);
+    if ((e = product<kDw>(g, p, part, bf, a.cus, s)) != hipSuccess) return e;
   }
   return hipSuccess;
 }

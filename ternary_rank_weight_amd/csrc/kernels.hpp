@@ -173,9 +173,15 @@ struct GatedArgs {
   void *dx, *dwg, *dwu;         // backward outputs: dx or null; both of dwg and dwu or null
   int cus;                      // compute units of the device
 };
-size_t gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows);
+// aligned: x, Wg and Wu start 16-byte aligned, their row strides and the
+// columns are multiples of 8 entries.
+bool gated_is_aligned(const GatedArgs& a);
+size_t gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus);
 hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s);
-size_t gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows);
+size_t gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus);
 hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s);
+// the forward pass of a few tokens, without workspace (gated_rows.hip)
+bool gated_takes_rows(int64_t tokens);
+hipError_t run_gated_rows(const GatedArgs& a, hipStream_t s);
 
 }  // namespace externd
