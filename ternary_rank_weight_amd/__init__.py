@@ -484,15 +484,21 @@ _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 
 
+_current_device = torch.cuda.current_device
+# torch's current stream as a plain number, without building a Stream object for every call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _op_device(*tensors):
     """Index of the device that all tensors are on; it has to be the current one, whose stream the call uses."""
-    index = tensors[0].device.index
+    index = tensors[0].get_device()
     for t in tensors:
-        if not t.is_cuda:
-            raise TypeError("tensors must be CUDA (HIP) tensors")
-        if t.device.index != index:
+        if t.get_device() != index or index < 0:
+            if not t.is_cuda or index < 0:
+                raise TypeError("tensors must be CUDA (HIP) tensors")
             raise ValueError("tensors are on different devices")
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         raise ValueError("tensors are not on the current device")
     return index
 
@@ -513,6 +519,8 @@ def _dtype_code(dtype, name):
 
 def _rows_of(x, cols, name):
     """x with `cols` entries in its last dimension as (2-D tensor of unit column stride, row stride)."""
+    if x.dim() == 2 and x.is_contiguous() and x.shape[1] == cols:
+        return x, cols
     if x.dim() == 0 or x.shape[-1] != cols:
         raise ValueError(f"{name} must have {cols} entries in its last dimension, got shape {tuple(x.shape)}")
     if x.dim() != 2:
@@ -541,6 +549,15 @@ def _out_or_new(out, shape, dtype, device, name="out"):
     return out
 
 
+def _q4_part(t, dtype, count, codes, name):
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, name)
+    if t.numel() != count:
+        raise ValueError(f"{name} must hold {count} elements, got {t.numel()}")
+    if t.get_device() != codes.get_device():
+        raise ValueError(f"{name} is on another device than codes")
+
+
 class Q4:
     """A weight matrix in 4 bits with group scales, in the library's layout.
 
@@ -551,18 +568,13 @@ class Q4:
     __slots__ = ("codes", "scales", "mins", "rows", "cols", "group", "_c")
 
     def __init__(self, codes, scales, mins, rows, cols, group):
-        words, table = _q4_code_words(rows, cols), _q4_table_len(rows, cols, group)
-        if words < 0 or table < 0:
+        if group not in (32, 64, 128) or not 0 < rows < 1 << 31 or not 0 < cols < 1 << 31:
             raise ValueError("bad shape or group (32, 64 or 128)")
-        for t, dtype, n, name in ((codes, torch.int32, words, "codes"), (scales, torch.bfloat16, table, "scales"),
-                                  (mins, torch.bfloat16, table, "mins")):
-            if t is None and name == "mins":
-                continue
-            _need(t, dtype, name)
-            if t.numel() != n:
-                raise ValueError(f"{name} must hold {n} elements, got {t.numel()}")
-            if t.device != codes.device:
-                raise ValueError(f"{name} is on another device than codes")
+        blocks = -(-rows // 16) * -(-cols // 128)   # tiles of chunks
+        _q4_part(codes, torch.int32, 256 * blocks, codes, "codes")
+        _q4_part(scales, torch.bfloat16, 2048 // group * blocks, codes, "scales")
+        if mins is not None:
+            _q4_part(mins, torch.bfloat16, 2048 // group * blocks, codes, "mins")
         self.codes, self.scales, self.mins = codes, scales, mins
         self.rows, self.cols, self.group = rows, cols, group
         self._c = _Q4(codes.data_ptr(), scales.data_ptr(), None if mins is None else mins.data_ptr(), rows, cols,
@@ -596,11 +608,11 @@ def q4_quantize(W, group=32, symmetric=True):
     if not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise ValueError("W must be a 2-D tensor")
     dtype = _dtype_code(W.dtype, "W")
-    _op_device(W)
+    index = _op_device(W)
     W, ldw = _rows_of(W, W.shape[1], "W")
     rows, cols = W.shape
     q = _q4_new(rows, cols, group, symmetric, W.device)
-    _check(_q4_quantize(_ptr(W), rows, cols, ldw, dtype, group, _stream(), q._c.codes, q._c.scales, q._c.mins))
+    _check(_q4_quantize(_ptr(W), rows, cols, ldw, dtype, group, _raw_stream(index), q._c.codes, q._c.scales, q._c.mins))
     return q
 
 
@@ -619,9 +631,9 @@ def q4_pack(codes, scales, mins=None, group=32):
             _need(t, torch.bfloat16, name)
             if tuple(t.shape) != (rows, -(-cols // group)):
                 raise ValueError(f"{name} must have shape {(rows, -(-cols // group))}")
-    _op_device(*(t for t in (codes, scales, mins) if t is not None))
+    index = _op_device(*(t for t in (codes, scales, mins) if t is not None))
     q = _q4_new(rows, cols, group, mins is None, codes.device)
-    _check(_q4_pack(_ptr(codes), _ptr(scales), _ptr(mins), rows, cols, group, _stream(), q._c.codes, q._c.scales,
+    _check(_q4_pack(_ptr(codes), _ptr(scales), _ptr(mins), rows, cols, group, _raw_stream(index), q._c.codes, q._c.scales,
                     q._c.mins))
     return q
 
@@ -629,9 +641,9 @@ def q4_pack(codes, scales, mins=None, group=32):
 def q4_reconstruct(q, dtype=torch.float32):
     """The values that q stands for, as a (rows, cols) tensor, each rounded once."""
     code = _dtype_code(dtype, "dtype")
-    _op_device(q.codes)
+    index = _op_device(q.codes)
     out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
-    _check(_q4_reconstruct(q._c, code, _stream(), _ptr(out)))
+    _check(_q4_reconstruct(q._c, code, _raw_stream(index), _ptr(out)))
     return out
 
 
@@ -656,11 +668,11 @@ def q4_apply(q, x, out=None, workspace=None):
     aligned) it is made in workspace (at least q4_workspace_bytes(...) bytes, 256-byte aligned), by
     default one from torch's allocator.  Not differentiable."""
     dtype = _dtype_code(x.dtype, "x")
-    _op_device(x, q.codes)
+    index = _op_device(x, q.codes)
     y = _out_or_new(out, x.shape[:-1] + (q.rows,), x.dtype, x.device)
     x, ldx = _rows_of(x, q.cols, "x")
     ws, wsb, keep = _q4_scratch(workspace, x, ldx, dtype)
-    _check(_q4_apply(q._c, x.data_ptr(), x.shape[0], ldx, dtype, _stream(), y.data_ptr(), ws, wsb))
+    _check(_q4_apply(q._c, x.data_ptr(), x.shape[0], ldx, dtype, _raw_stream(index), y.data_ptr(), ws, wsb))
     return y
 
 
@@ -668,11 +680,11 @@ def q4_gated(qg, qu, x, act="silu", out=None, workspace=None):
     """h = act(x Wg^T) * (x Wu^T) with both matrices in 4 bits (one shape, group and kind), in one
     kernel; everything else as q4_apply.  act: "silu", "gelu" (erf) or "gelu_tanh"."""
     dtype = _dtype_code(x.dtype, "x")
-    _op_device(x, qg.codes, qu.codes)
+    index = _op_device(x, qg.codes, qu.codes)
     h = _out_or_new(out, x.shape[:-1] + (qg.rows,), x.dtype, x.device)
     x, ldx = _rows_of(x, qg.cols, "x")
     ws, wsb, keep = _q4_scratch(workspace, x, ldx, dtype)
-    _check(_q4_gated(qg._c, qu._c, x.data_ptr(), x.shape[0], ldx, dtype, _act_code(act), _stream(), h.data_ptr(), ws,
+    _check(_q4_gated(qg._c, qu._c, x.data_ptr(), x.shape[0], ldx, dtype, _act_code(act), _raw_stream(index), h.data_ptr(), ws,
                      wsb))
     return h
 
@@ -726,7 +738,7 @@ def gated_forward(x, Wg, Wu, act="silu", save=False, out=None, workspace=None):
     gated_backward takes.  Rows of x and of the weights may be strided (both weights alike).  act:
     "silu", "gelu" (erf) or "gelu_tanh".  See gated() for the differentiable form."""
     act = _act_code(act)
-    _op_device(x, Wg, Wu)
+    index = _op_device(x, Wg, Wu)
     Wg, Wu, ldw, dtype = _gated_weights(x, Wg, Wu)
     rows, cols = Wg.shape
     h = _out_or_new(out, x.shape[:-1] + (rows,), x.dtype, x.device)
@@ -737,7 +749,7 @@ def gated_forward(x, Wg, Wu, act="silu", save=False, out=None, workspace=None):
         g, u = torch.empty((2, tokens, rows), dtype=torch.float32, device=x.device)
     ws, wsb, keep = _gated_scratch(workspace, _gated_forward_ws, x, ldx, Wg, Wu, ldw)
     _check(_gated_forward(x.data_ptr(), tokens, cols, ldx, Wg.data_ptr(), Wu.data_ptr(), rows, ldw, dtype, act,
-                          _stream(), h.data_ptr(), None if g is None else g.data_ptr(),
+                          _raw_stream(index), h.data_ptr(), None if g is None else g.data_ptr(),
                           None if u is None else u.data_ptr(), ws, wsb))
     return (h, g, u) if save else h
 
@@ -746,7 +758,7 @@ def gated_backward(x, Wg, Wu, g, u, dh, act="silu", need_dx=True, need_dw=True, 
     """(dx, dWg, dWu) of the gated block from dh (..., rows) and the g, u that gated_forward(...,
     save=True) returned; None for what need_dx / need_dw leave out."""
     act = _act_code(act)
-    _op_device(x, Wg, Wu, g, u, dh)
+    index = _op_device(x, Wg, Wu, g, u, dh)
     Wg, Wu, ldw, dtype = _gated_weights(x, Wg, Wu)
     rows, cols = Wg.shape
     shape = x.shape
@@ -766,7 +778,7 @@ def gated_backward(x, Wg, Wu, g, u, dh, act="silu", need_dx=True, need_dw=True, 
     dwu = torch.empty_like(dwg) if need_dw else None
     ws, wsb, keep = _gated_scratch(workspace, _gated_backward_ws, x, ldx, Wg, Wu, ldw)
     _check(_gated_backward(x.data_ptr(), tokens, cols, ldx, Wg.data_ptr(), Wu.data_ptr(), rows, ldw, g.data_ptr(),
-                           u.data_ptr(), dh.data_ptr(), lddh, dtype, act, _stream(), _ptr(dx), _ptr(dwg), _ptr(dwu),
+                           u.data_ptr(), dh.data_ptr(), lddh, dtype, act, _raw_stream(index), _ptr(dx), _ptr(dwg), _ptr(dwu),
                            ws, wsb))
     return dx, dwg, dwu
 

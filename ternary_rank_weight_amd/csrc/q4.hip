@@ -89,6 +89,15 @@ __device__ inline float row_max(float v) {
   return fmaxf(v, __shfl_xor(v, 32, kWave));
 }
 
+// rint(w / s) as the correctly rounded quotient gives it: by the reciprocal,
+// whose product is within 16 x 2^-23 of the quotient (|w / s| < 16 where it
+// counts), and by a division for the few quotients that near a tie.
+__device__ inline float rint_quotient(float w, float s, float inv) {
+  float t = w * inv;
+  if (!(fabsf(fabsf(t - rintf(t)) - 0.5f) > 1e-5f) || !(fabsf(t) < 64.f)) t = w / s;
+  return rintf(t);
+}
+
 // Bound by HBM: one read of the matrix, one write of 4.5 to 5 bits per entry.
 template <int DT, int GPC, bool MINS>
 __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ W, int64_t rows, int64_t cols,
@@ -133,16 +142,17 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ W,
       }
       if (row_max(bad) != 0.f || !(s < INFINITY) || !(fabsf(m) < INFINITY)) s = m = NAN;
       const bool on = s > 0.f;
+      const float inv = 1.f / s;
   #pragma unroll
       for (int i = g * SPG; i < (g + 1) * SPG; ++i) {
         uint32_t c[8];
   #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if constexpr (MINS) {
-            const float t = on ? rintf((w[i][j] - m) / s) : 0.f;
+            const float t = on ? rint_quotient(w[i][j] - m, s, inv) : 0.f;
             c[j] = j < left[i] ? (uint32_t)fminf(fmaxf(t, 0.f), 15.f) : 0u;
           } else {
-            const float t = on ? rintf(w[i][j] / s) : 0.f;
+            const float t = on ? rint_quotient(w[i][j], s, inv) : 0.f;
             c[j] = j < left[i] ? (uint32_t)(fminf(fmaxf(t, -8.f), 7.f) + 8.f) : 8u;
           }
         }
@@ -311,8 +321,7 @@ struct Q4Args {
 // the group's scale is one multiplication by the lane's own value.
 //
 // The operand is 16 + c, not c - 8 or c: its offset is taken off by a product of x
-// with the constant -24 (or -16), accumulated before the group's own, once
-// for all row tiles.  With minima that product, scaled by -m / 16, is also the
+// with the constant -24 (or -16), made once for all row tiles.  With minima that product, scaled by -m / 16, is also the
 // m sum(x) term.  Sums are fp32 throughout.
 template <bool BF, int GPC, bool MINS, int MATS, int RT, int NT, int WV>
 __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type) {
@@ -368,43 +377,45 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
   };
   constexpr uint32_t off2 = MINS ? (BF ? 0xC180C180u : 0xCC00CC00u) : (BF ? 0xC1C0C1C0u : 0xCE00CE00u);
   const u32x4 off = {off2, off2, off2, off2};
+  // (slots outside, row tiles inside: a slice's x is held for NT tiles only)
   auto work = [&](int64_t c, const Stage& st, bool tail) {
 #pragma unroll
     for (int g = 0; g < GPC; ++g) {
-      u32x4 xf[SPG][NT];
-      f32x4 xo[NT];
-#pragma unroll
-      for (int i = 0; i < SPG; ++i)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int64_t k = kChunk * c + 32 * (g * SPG + i);
-          if (!tail) xf[i][n] = *reinterpret_cast<const u32x4*>(xp[n] + k);
-          else xf[i][n] = k + 8 * p < a.cols ? *reinterpret_cast<const u32x4*>(xp[n] + k) : u32x4{0u, 0u, 0u, 0u};
-        }
+      f32x4 xo[NT], d[F][NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         xo[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < SPG; ++i) xo[n] = mfma16<BF>(xf[i][n], off, xo[n]);
+        for (int f = 0; f < F; ++f) d[f][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int i = 0; i < SPG; ++i) {
+        const int64_t k = kChunk * c + 32 * (g * SPG + i);
+        u32x4 xf[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (!tail) xf[n] = *reinterpret_cast<const u32x4*>(xp[n] + k);
+          else xf[n] = k + 8 * p < a.cols ? *reinterpret_cast<const u32x4*>(xp[n] + k) : u32x4{0u, 0u, 0u, 0u};
+          xo[n] = mfma16<BF>(xf[n], off, xo[n]);
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          const u32x4 wf = unpack_q4<BF>(st.c[f][g * SPG + i]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) d[f][n] = mfma16<BF>(xf[n], wf, d[f][n]);
+        }
       }
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        u32x4 wf[SPG];
-#pragma unroll
-        for (int i = 0; i < SPG; ++i) wf[i] = unpack_q4<BF>(st.c[f][g * SPG + i]);
         const float s = bf16_to_f32((uint32_t)(st.s[f] >> (16 * g)) & 0xffffu);
         const float m = MINS ? -0.0625f * bf16_to_f32((uint32_t)(st.m[f] >> (16 * g)) & 0xffffu) : 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          f32x4 d = xo[n];
-#pragma unroll
-          for (int i = 0; i < SPG; ++i) d = mfma16<BF>(xf[i][n], wf[i], d);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            acc[f][n][e] = fmaf(s, d[e], acc[f][n][e]);
+            acc[f][n][e] = fmaf(s, d[f][n][e] + xo[n][e], acc[f][n][e]);
             if constexpr (MINS) acc[f][n][e] = fmaf(m, xo[n][e], acc[f][n][e]);
           }
-        }
       }
     }
   };
@@ -469,14 +480,16 @@ hipError_t pick_apply(const Q4Args& a, int mats, int out_type, hipStream_t s) {
   if (mats == 2) {
     if (slot_tiles == 1) return launch_apply<BF, GPC, MINS, 2, 1, 1, 8>(a, out_type, s);
     if (slot_tiles == 2) return launch_apply<BF, GPC, MINS, 2, 1, 2, 8>(a, out_type, s);
-    return launch_apply<BF, GPC, MINS, 2, 2, 4, 4>(a, out_type, s);
+    if (slot_tiles == 3) return launch_apply<BF, GPC, MINS, 2, 2, 3, 8>(a, out_type, s);
+    return launch_apply<BF, GPC, MINS, 2, 2, 4, 8>(a, out_type, s);
   }
   if (slot_tiles == 1) {
     if (tiles < 512) return launch_apply<BF, GPC, MINS, 1, 1, 1, 16>(a, out_type, s);
     return launch_apply<BF, GPC, MINS, 1, 2, 1, 8>(a, out_type, s);
   }
   if (slot_tiles == 2) return launch_apply<BF, GPC, MINS, 1, 2, 2, 8>(a, out_type, s);
-  return launch_apply<BF, GPC, MINS, 1, 4, 4, 4>(a, out_type, s);
+  if (slot_tiles == 3) return launch_apply<BF, GPC, MINS, 1, 4, 3, 8>(a, out_type, s);
+  return launch_apply<BF, GPC, MINS, 1, 4, 4, 8>(a, out_type, s);
 }
 
 template <bool BF>
