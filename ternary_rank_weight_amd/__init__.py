@@ -593,13 +593,13 @@ class Q4:
 
 
 def _q4_new(rows, cols, group, symmetric, device):
-    words, table = _q4_code_words(rows, cols), _q4_table_len(rows, cols, group)
-    if words < 0 or table < 0:
-        raise ValueError("bad shape or group (32, 64 or 128)")
-    codes = torch.empty((words,), dtype=torch.int32, device=device)
-    scales = torch.empty((table,), dtype=torch.bfloat16, device=device)
-    mins = None if symmetric else torch.empty((table,), dtype=torch.bfloat16, device=device)
-    return Q4(codes, scales, mins, rows, cols, group)
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    blocks = -(-rows // 16) * -(-cols // 128)
+    table = 2048 // group * blocks
+    codes = torch.empty((256 * blocks,), dtype=torch.int32, device=device)
+    tables = torch.empty((1 if symmetric else 2, table), dtype=torch.bfloat16, device=device)
+    return Q4(codes, tables[0], None if symmetric else tables[1], rows, cols, group)
 
 
 def q4_quantize(W, group=32, symmetric=True):
@@ -656,7 +656,7 @@ def _q4_scratch(workspace, x, ldx, dtype):
     """As _gated_scratch, for the staged copy of x that the 4-bit products may need."""
     if workspace is None:
         tokens, cols = x.shape
-        if tokens == 0 or dtype != 0 and (cols | ldx) & 7 == 0 and x.data_ptr() & 15 == 0:
+        if tokens == 0 or tokens <= 16 and dtype != 0 and (cols | ldx) & 7 == 0 and x.data_ptr() & 15 == 0:
             return None, 0, None
         workspace = torch.empty((_q4_ws(cols, tokens, dtype),), dtype=torch.uint8, device=x.device)
     return (*_scratch(workspace), workspace)
@@ -664,8 +664,8 @@ def _q4_scratch(workspace, x, ldx, dtype):
 
 def q4_apply(q, x, out=None, workspace=None):
     """y = x W^T with 4-bit W: x (..., cols) float32, bfloat16 or float16, y (..., rows) of its type.
-    Rows of x may be strided.  Where x needs a staged copy (float32, or rows that are not 16-byte
-    aligned) it is made in workspace (at least q4_workspace_bytes(...) bytes, 256-byte aligned), by
+    Rows of x may be strided.  Where x needs a staged copy (float32, rows that are not 16-byte aligned,
+    more than 16 tokens on a large matrix) it is made in workspace (at least q4_workspace_bytes(...) bytes, 256-byte aligned), by
     default one from torch's allocator.  Not differentiable."""
     dtype = _dtype_code(x.dtype, "x")
     index = _op_device(x, q.codes)

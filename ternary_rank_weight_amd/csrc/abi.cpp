@@ -158,7 +158,7 @@ int q4_product(const externd_q4* w, int mats, const void* x, int64_t tokens, int
   int st = check_device(nullptr);
   if (st != EXTERND_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const size_t need = externd::q4_stages_x(w->cols, ldx, dtype, x) ? externd::q4_stage_bytes(w->cols, tokens, dtype) : 0;
+  const size_t need = externd::q4_stages_x(w->rows, w->cols, tokens, ldx, dtype, x) ? externd::q4_stage_bytes(w->cols, tokens, dtype) : 0;
   Workspace ws;
   if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
   hipError_t e = externd::run_q4_apply(w, mats, x, tokens, ldx, dtype, act, y, ws.ptr, s);

@@ -147,9 +147,8 @@ hipError_t run_apply(const uint32_t* B2, const uint32_t* C2, const float* D, int
                      const float* x, float* y, void* ws, hipStream_t s);
 
 // 4-bit weights with group scales (q4.hip).  q4_stages_x: whether x goes
-// through a staged 16-bit copy (fp32, or rows that are not 16-byte aligned);
-// then ws holds q4_stage_bytes, else it is null.
-bool q4_stages_x(int64_t cols, int64_t ldx, int dtype, const void* x);
+// through a staged copy; then ws holds q4_stage_bytes, else it is null.
+bool q4_stages_x(int64_t rows, int64_t cols, int64_t tokens, int64_t ldx, int dtype, const void* x);
 size_t q4_stage_bytes(int64_t cols, int64_t tokens, int dtype);
 hipError_t run_q4_quantize(const void* W, int64_t rows, int64_t cols, int64_t ldw, int dtype, int group, void* codes,
                            uint16_t* scales, uint16_t* mins, hipStream_t s);

@@ -89,74 +89,84 @@ __device__ inline float row_max(float v) {
   return fmaxf(v, __shfl_xor(v, 32, kWave));
 }
 
-// rint(w / s) as the correctly rounded quotient gives it: by the reciprocal,
-// whose product is within 16 x 2^-23 of the quotient (|w / s| < 16 where it
-// counts), and by a division for the few quotients that near a tie.
-__device__ inline float rint_quotient(float w, float s, float inv) {
-  float t = w * inv;
-  if (!(fabsf(fabsf(t - rintf(t)) - 0.5f) > 1e-5f) || !(fabsf(t) < 64.f)) t = w / s;
-  return rintf(t);
-}
-
-// Bound by HBM: one read of the matrix, one write of 4.5 to 5 bits per entry.
+// Bound by HBM: one read of the matrix, one write of 4.5 to 5 bits per entry;
+// the arithmetic is kept to about a dozen operations an entry so that it stays
+// below that.  The rounded quotients come from the reciprocal: t = w (1 / s) is
+// within 16 x 2^-23 of w / s (|w / s| < 16 where it counts), so rint(t) is the
+// rounded quotient's unless t is within 1e-5 of a tie; a word with such a t, or
+// a scale whose reciprocal may not be normal, is divided out instead.
 template <int DT, int GPC, bool MINS>
 __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ W, int64_t rows, int64_t cols,
                                                       int64_t ldw, int64_t chunks, int64_t jobs,
                                                       u32x4* __restrict__ codes, uint16_t* __restrict__ scales,
                                                       uint16_t* __restrict__ mins) {
   constexpr int SPG = 4 / GPC;   // words (of 32 columns) per group
+  constexpr float lo = MINS ? 0.f : -8.f, hi = MINS ? 15.f : 7.f;
   const int lane = threadIdx.x & (kWave - 1);
   for (int64_t job = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; job < jobs; job += 4 * (int64_t)gridDim.x) {
     const Place q = place_of(job, chunks, lane);
     float w[4][8];
-    int64_t left[4];
-  #pragma unroll
+    int left[4];
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-      left[i] = q.row < rows ? cols - q.col - 32 * i : 0;
+      left[i] = q.row < rows ? (int)min<int64_t>(max<int64_t>(cols - q.col - 32 * i, 0), 8) : 0;
       load_weights<DT>(W, q.row * ldw + q.col + 32 * i, left[i], w[i]);
+      if (MINS && left[i] > 0 && left[i] < 8) {   // past the end: entries that change no extreme
+#pragma unroll
+        for (int j = 1; j < 8; ++j) w[i][j] = j < left[i] ? w[i][j] : w[i][0];
+      }
     }
     u32x4 out;
-  #pragma unroll
+#pragma unroll
     for (int g = 0; g < GPC; ++g) {
-      float top = 0.f, low = INFINITY, high = -INFINITY, bad = 0.f;
-  #pragma unroll
-      for (int i = g * SPG; i < (g + 1) * SPG; ++i)
-  #pragma unroll
+      // extremes, and a sum of 0 w that is NaN if any entry is not finite (maxima drop NaN)
+      float low = INFINITY, high = MINS ? -INFINITY : 0.f, bad = 0.f;
+#pragma unroll
+      for (int i = g * SPG; i < (g + 1) * SPG; ++i) {
+        if (MINS && left[i] == 0) continue;
+#pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float v = w[i][j];
-          if (j < left[i]) {
-            if (!(fabsf(v) < INFINITY)) bad = 1.f;   // fmaxf drops a NaN: remember it
-            if constexpr (MINS) { low = fminf(low, v); high = fmaxf(high, v); }
-            else top = fmaxf(top, fabsf(v));
-          }
+          bad = fmaf(w[i][j], 0.f, bad);
+          if constexpr (MINS) { low = fminf(low, w[i][j]); high = fmaxf(high, w[i][j]); }
+          else high = fmaxf(high, fabsf(w[i][j]));
         }
+      }
+      bad = bad == 0.f ? 0.f : 1.f;
+      high = row_max(high);
       float s, m = 0.f;
       if constexpr (MINS) {
-        high = row_max(high);
         low = -row_max(-low);
         const bool any = low <= high;   // a group past the row's end has scale and minimum 0
         s = any ? bf16_to_f32(f32_to_bf16((high - low) / 15.f)) : 0.f;
         m = any ? bf16_to_f32(f32_to_bf16(low)) : 0.f;
       } else {
-        s = bf16_to_f32(f32_to_bf16(row_max(top) / 7.f));
+        s = bf16_to_f32(f32_to_bf16(high / 7.f));
       }
       if (row_max(bad) != 0.f || !(s < INFINITY) || !(fabsf(m) < INFINITY)) s = m = NAN;
-      const bool on = s > 0.f;
       const float inv = 1.f / s;
-  #pragma unroll
+      const bool plain = s > 1e-30f;   // its reciprocal is normal (bf16 scales stay below 2^126)
+#pragma unroll
       for (int i = g * SPG; i < (g + 1) * SPG; ++i) {
-        uint32_t c[8];
-  #pragma unroll
+        float c[8], far = plain ? 0.f : 1.f;   // far: largest distance from a whole number
+#pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if constexpr (MINS) {
-            const float t = on ? rint_quotient(w[i][j] - m, s, inv) : 0.f;
-            c[j] = j < left[i] ? (uint32_t)fminf(fmaxf(t, 0.f), 15.f) : 0u;
-          } else {
-            const float t = on ? rint_quotient(w[i][j], s, inv) : 0.f;
-            c[j] = j < left[i] ? (uint32_t)(fminf(fmaxf(t, -8.f), 7.f) + 8.f) : 8u;
+          const float t = (MINS ? w[i][j] - m : w[i][j]) * inv;
+          const float r = rintf(t);
+          far = fmaxf(far, fabsf(t - r));
+          c[j] = fminf(fmaxf(r, lo), hi);
+        }
+        if (!(far < 0.49999f)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float t = s > 0.f ? rintf((MINS ? w[i][j] - m : w[i][j]) / s) : 0.f;
+            c[j] = fminf(fmaxf(t, lo), hi);
           }
         }
-        out[i] = pack_word(c);
+        // four codes to a half word, exact in fp32: c0 + 16 c2 + 256 c4 + 4096 c6
+        const float bias = MINS ? 0.f : 8.f * 4369.f;
+        const uint32_t h0 = (uint32_t)(fmaf(c[6], 4096.f, fmaf(c[4], 256.f, fmaf(c[2], 16.f, c[0]))) + bias);
+        const uint32_t h1 = (uint32_t)(fmaf(c[7], 4096.f, fmaf(c[5], 256.f, fmaf(c[3], 16.f, c[1]))) + bias);
+        out[i] = h0 | (h1 << 16);
       }
       if (q.p == 0) {
         scales[(job * kTile + q.r) * GPC + g] = (uint16_t)f32_to_bf16(s);
@@ -254,28 +264,40 @@ __global__ __launch_bounds__(256) void k_q4_reconstruct(const u32x4* __restrict_
 
 // ---- products ----
 
-// x for the products where it is not already 16-bit rows of 16-byte
-// alignment: rows of chunks * 128 entries, zero past the end.  fp32 x becomes
-// three bf16 rows per token that add up to it exactly (8 of its 24 bits each).
+// x in the order the products read it: for every tile of 16 slots and slice of 32
+// columns the 64 lanes' 16 bytes one after the other, so that a wave reads 1 KB
+// of neighbouring bytes; zero past the columns.  A slot is a token, or one of
+// the three bf16 parts of an fp32 token that add up to it exactly (8 of its 24
+// bits each; 15 slots, 5 tokens, per tile).
 template <int DT>
 __global__ __launch_bounds__(256) void k_q4_stage_x(const void* __restrict__ x, int64_t tokens, int64_t cols,
-                                                     int64_t ldx, int64_t lds, uint16_t* __restrict__ out) {
-  const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (col >= lds) return;
-  for (int64_t t = blockIdx.y; t < tokens; t += gridDim.y) {
-    if constexpr (DT == EXTERND_F32) {
-      const float v = col < cols ? static_cast<const float*>(x)[t * ldx + col] : 0.f;
-      const float hi = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
-      const float r1 = v - hi;
-      const float mid = __uint_as_float(__float_as_uint(r1) & 0xffff0000u);
-      const float lo = r1 - mid;
-      uint16_t* o = out + 3 * t * lds + col;
-      o[0] = (uint16_t)(__float_as_uint(hi) >> 16);
-      o[lds] = (uint16_t)(__float_as_uint(mid) >> 16);
-      o[2 * lds] = (uint16_t)(__float_as_uint(lo) >> 16);
-    } else {
-      out[t * lds + col] = col < cols ? static_cast<const uint16_t*>(x)[t * ldx + col] : (uint16_t)0;
+                                                     int64_t ldx, int64_t slices, int64_t pieces_of_tiles,
+                                                     u32x4* __restrict__ out) {
+  constexpr int PIECES = DT == EXTERND_F32 ? 3 : 1, PER = DT == EXTERND_F32 ? 5 : 16;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces_of_tiles; i += (int64_t)gridDim.x * 256) {
+    const int lane = (int)(i & 63), r = lane & 15, p = lane >> 4;
+    const int64_t tile = (i >> 6) / slices, slice = (i >> 6) - tile * slices;
+    const int64_t t = tile * PER + r / PIECES, col = 32 * slice + 8 * p, left = cols - col;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (r < PER * PIECES && t < tokens && left > 0) {
+      if constexpr (DT == EXTERND_F32) {
+        float f[8];
+        load_weights<EXTERND_F32>(x, t * ldx + col, left, f);
+        const int piece = r % 3;
+        const uint32_t m0 = piece > 0 ? 0xffff0000u : 0u, m1 = piece > 1 ? 0xffff0000u : 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float b = f[j] - __uint_as_float(__float_as_uint(f[j]) & m0);
+          const float c = b - __uint_as_float(__float_as_uint(b) & m1);
+          v[j / 2] |= (__float_as_uint(c) >> 16) << (16 * (j & 1));
+        }
+      } else {
+        const uint16_t* q = static_cast<const uint16_t*>(x) + t * ldx + col;
+        v = left >= 8 ? ((reinterpret_cast<uintptr_t>(q) & 15) == 0 ? load8<true>(q) : load8<false>(q))
+                      : load8_part(q, left);
+      }
     }
+    out[i] = v;
   }
 }
 
@@ -303,9 +325,10 @@ struct Q4Args {
   const u32x4* codes[2];
   const uint16_t* scales[2];
   const uint16_t* mins[2];
-  const uint16_t* x;    // 16-bit rows ("slots": a token, or one of its three parts)
+  const uint16_t* x;    // rows of 16-bit entries, or staged
   void* y;
-  int64_t ldx, rows, cols, chunks, tokens;
+  int64_t ldx, slice, rows, cols, chunks, tokens;   // slice: entries from one slice of x to the next
+  int staged;
   int pieces;           // slots per token: 1, or 3 for fp32
   int act;
 };
@@ -327,6 +350,7 @@ template <bool BF, int GPC, bool MINS, int MATS, int RT, int NT, int WV>
 __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type) {
   constexpr int F = MATS * RT;      // row tiles held by a wave, of all matrices
   constexpr int SPG = 4 / GPC;      // products per group
+  constexpr int PF = F * NT <= 4 ? 3 : 2;
   __shared__ float red[WV][F][256];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int r = lane & 15, p = lane >> 4;
@@ -338,9 +362,10 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
   const uint16_t* xp[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    // a slot past the end repeats the last one: its sums are not written
-    const int64_t s = min(((int64_t)blockIdx.y * NT + n) * per + r, slots - 1);
-    xp[n] = a.x + s * a.ldx + 8 * p;
+    // a slot (or tile) past the end repeats the last one: its sums are not written
+    const int64_t tile = (int64_t)blockIdx.y * NT + n;
+    if (a.staged) xp[n] = a.x + min(tile, (slots + per - 1) / per - 1) * a.chunks * (4 * 64 * 8) + lane * 8;
+    else xp[n] = a.x + min(tile * 16 + r, slots - 1) * a.ldx + 8 * p;
   }
   const u32x4* cp[F];
   const uint16_t* sp[F];
@@ -377,59 +402,92 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
   };
   constexpr uint32_t off2 = MINS ? (BF ? 0xC180C180u : 0xCC00CC00u) : (BF ? 0xC1C0C1C0u : 0xCE00CE00u);
   const u32x4 off = {off2, off2, off2, off2};
-  // (slots outside, row tiles inside: a slice's x is held for NT tiles only)
+  auto load_x = [&](int64_t c, int i, bool tail, u32x4 (&xf)[NT]) {   // slice i of chunk c
+    const int64_t at = (4 * c + i) * a.slice;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (!tail || at + 8 * p < a.cols) xf[n] = *reinterpret_cast<const u32x4*>(xp[n] + at);
+      else xf[n] = u32x4{0u, 0u, 0u, 0u};   // (only unstaged, where `at` is the column)
+    }
+  };
+  auto add_group = [&](const Stage& st, int g, int f, const f32x4 (&d)[NT], const f32x4 (&xo)[NT]) {
+    const float s = bf16_to_f32((uint32_t)(st.s[f] >> (16 * g)) & 0xffffu);
+    const float m = MINS ? -0.0625f * bf16_to_f32((uint32_t)(st.m[f] >> (16 * g)) & 0xffffu) : 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[f][n][e] = fmaf(s, d[n][e] + xo[n][e], acc[f][n][e]);
+        if constexpr (MINS) acc[f][n][e] = fmaf(m, xo[n][e], acc[f][n][e]);
+      }
+  };
+  constexpr f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   auto work = [&](int64_t c, const Stage& st, bool tail) {
 #pragma unroll
     for (int g = 0; g < GPC; ++g) {
-      f32x4 xo[NT], d[F][NT];
+      f32x4 xo[NT];
+      if constexpr (SPG <= 2) {
+        // the group's x in registers, one row tile's products after the other's
+        u32x4 xf[SPG][NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        xo[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < SPG; ++i) {
+          load_x(c, g * SPG + i, tail, xf[i]);
 #pragma unroll
-        for (int f = 0; f < F; ++f) d[f][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-#pragma unroll
-      for (int i = 0; i < SPG; ++i) {
-        const int64_t k = kChunk * c + 32 * (g * SPG + i);
-        u32x4 xf[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (!tail) xf[n] = *reinterpret_cast<const u32x4*>(xp[n] + k);
-          else xf[n] = k + 8 * p < a.cols ? *reinterpret_cast<const u32x4*>(xp[n] + k) : u32x4{0u, 0u, 0u, 0u};
-          xo[n] = mfma16<BF>(xf[n], off, xo[n]);
+          for (int n = 0; n < NT; ++n) xo[n] = mfma16<BF>(xf[i][n], off, i ? xo[n] : zero);
         }
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-          const u32x4 wf = unpack_q4<BF>(st.c[f][g * SPG + i]);
+          f32x4 d[NT];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) d[f][n] = mfma16<BF>(xf[n], wf, d[f][n]);
-        }
-      }
+          for (int i = 0; i < SPG; ++i) {
+            const u32x4 wf = unpack_q4<BF>(st.c[f][g * SPG + i]);
 #pragma unroll
-      for (int f = 0; f < F; ++f) {
-        const float s = bf16_to_f32((uint32_t)(st.s[f] >> (16 * g)) & 0xffffu);
-        const float m = MINS ? -0.0625f * bf16_to_f32((uint32_t)(st.m[f] >> (16 * g)) & 0xffffu) : 0.f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[f][n][e] = fmaf(s, d[f][n][e] + xo[n][e], acc[f][n][e]);
-            if constexpr (MINS) acc[f][n][e] = fmaf(m, xo[n][e], acc[f][n][e]);
+            for (int n = 0; n < NT; ++n) d[n] = mfma16<BF>(xf[i][n], wf, i ? d[n] : zero);
           }
+          add_group(st, g, f, d, xo);
+        }
+      } else {
+        // the group's products in registers, one slice of x after the other
+        f32x4 d[F][NT];
+#pragma unroll
+        for (int i = 0; i < SPG; ++i) {
+          u32x4 xf[NT];
+          load_x(c, g * SPG + i, tail, xf);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) xo[n] = mfma16<BF>(xf[n], off, i ? xo[n] : zero);
+#pragma unroll
+          for (int f = 0; f < F; ++f) {
+            const u32x4 wf = unpack_q4<BF>(st.c[f][g * SPG + i]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) d[f][n] = mfma16<BF>(xf[n], wf, i ? d[f][n] : zero);
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) add_group(st, g, f, d[f], xo);
       }
     }
   };
-  // the next chunk's codes are on their way while one is worked on
-  const int64_t full = a.cols / kChunk;   // chunks without a tail
-  Stage now, next;
+  // PF - 1 chunks of codes are on their way while one is worked on
+  const int64_t full = a.staged ? a.chunks : a.cols / kChunk;   // chunks without a tail
+  Stage st[PF];
   int64_t c = wave;
-  if (c < a.chunks) fetch(c, now);
-  for (; c < full; c += WV) {
-    if (c + WV < a.chunks) fetch(c + WV, next);
-    work(c, now, false);
-    now = next;
+#pragma unroll
+  for (int u = 0; u < PF - 1; ++u)
+    if (c + u * WV < a.chunks) fetch(c + u * WV, st[u]);
+  while (c < full) {
+#pragma unroll
+    for (int u = 0; u < PF; ++u) {
+      if (c < full) {
+        if (c + (PF - 1) * WV < a.chunks) fetch(c + (PF - 1) * WV, st[(u + PF - 1) % PF]);
+        work(c, st[u], false);
+        c += WV;
+      }
+    }
   }
-  if (c < a.chunks) work(c, now, true);
+  if (c < a.chunks) {   // the last chunk, which has a tail
+    fetch(c, st[0]);
+    work(c, st[0], true);
+  }
 
   const int rows_here = (int)min<int64_t>(RT * kTile, a.rows - tile0 * kTile);
 #pragma unroll
@@ -478,6 +536,7 @@ hipError_t pick_apply(const Q4Args& a, int mats, int out_type, hipStream_t s) {
   const int64_t slot_tiles = a.pieces == 3 ? (a.tokens + 4) / 5 : (a.tokens + 15) / 16;
   const int64_t tiles = (a.rows + kTile - 1) / kTile;
   if (mats == 2) {
+    if (slot_tiles == 1 && tiles > 512) return launch_apply<BF, GPC, MINS, 2, 1, 1, 4>(a, out_type, s);
     if (slot_tiles == 1) return launch_apply<BF, GPC, MINS, 2, 1, 1, 8>(a, out_type, s);
     if (slot_tiles == 2) return launch_apply<BF, GPC, MINS, 2, 1, 2, 8>(a, out_type, s);
     if (slot_tiles == 3) return launch_apply<BF, GPC, MINS, 2, 2, 3, 8>(a, out_type, s);
@@ -507,12 +566,20 @@ dim3 jobs_grid(int64_t jobs) { return dim3((unsigned)std::min<int64_t>((jobs + 3
 
 }  // namespace
 
-bool q4_stages_x(int64_t cols, int64_t ldx, int dtype, const void* x) {
-  return dtype == EXTERND_F32 || cols % 8 != 0 || ldx % 8 != 0 || (reinterpret_cast<uintptr_t>(x) & 15) != 0;
+// Staged: fp32, rows that are not all 16-byte aligned, and large matrices with
+// more than one slot tile, where the waves' reads of x outweigh the weights and
+// 64-byte pieces of rows come at half the rate of whole kilobytes (32000 x 8192 with
+// 48 tokens: 66 us unstaged).
+bool q4_stages_x(int64_t rows, int64_t cols, int64_t tokens, int64_t ldx, int dtype, const void* x) {
+  return dtype == EXTERND_F32 || cols % 8 != 0 || ldx % 8 != 0 || (reinterpret_cast<uintptr_t>(x) & 15) != 0 ||
+         (tokens > 16 && rows * cols >= (int64_t)1 << 24);
 }
 
+static int64_t stage_slots(int64_t tokens, int dtype) {
+  return (dtype == EXTERND_F32 ? (tokens + 4) / 5 : (tokens + 15) / 16) * 16;
+}
 size_t q4_stage_bytes(int64_t cols, int64_t tokens, int dtype) {
-  return (size_t)(chunks_of(cols) * kChunk * tokens * (dtype == EXTERND_F32 ? 3 : 1)) * 2;
+  return (size_t)(chunks_of(cols) * kChunk * stage_slots(tokens, dtype)) * 2;
 }
 
 hipError_t run_q4_apply(const externd_q4* w, int mats, const void* x, int64_t tokens, int64_t ldx, int dtype, int act,
@@ -531,22 +598,24 @@ hipError_t run_q4_apply(const externd_q4* w, int mats, const void* x, int64_t to
   a.pieces = dtype == EXTERND_F32 ? 3 : 1;
   a.act = act;
   a.y = y;
+  a.staged = ws != nullptr;
   if (ws) {
-    const int64_t lds = a.chunks * kChunk;
-    uint16_t* o = static_cast<uint16_t*>(ws);
-    const dim3 grid((unsigned)((lds + 255) / 256), (unsigned)std::min<int64_t>(tokens, 32768));
+    const int64_t items = a.chunks * 16 * stage_slots(tokens, dtype);
+    const dim3 grid((unsigned)std::min<int64_t>((items + 255) / 256, 1 << 16));
+    u32x4* o = static_cast<u32x4*>(ws);
     if (dtype == EXTERND_F32)
-      hipLaunchKernelGGL(k_q4_stage_x<EXTERND_F32>, grid, dim3(256), 0, s, x, tokens, a.cols, ldx, lds, o);
+      hipLaunchKernelGGL(k_q4_stage_x<EXTERND_F32>, grid, dim3(256), 0, s, x, tokens, a.cols, ldx, 4 * a.chunks, items, o);
     else
-      hipLaunchKernelGGL(k_q4_stage_x<EXTERND_BF16>, grid, dim3(256), 0, s, x, tokens, a.cols, ldx, lds, o);
+      hipLaunchKernelGGL(k_q4_stage_x<EXTERND_BF16>, grid, dim3(256), 0, s, x, tokens, a.cols, ldx, 4 * a.chunks, items, o);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    a.x = o;
-    a.ldx = lds;
-    a.cols = lds;   // zero past the end: no tail
+    a.x = reinterpret_cast<const uint16_t*>(o);
+    a.ldx = 0;
+    a.slice = 64 * 8;
   } else {
     a.x = static_cast<const uint16_t*>(x);
     a.ldx = ldx;
+    a.slice = 32;
   }
   const int gpc = kChunk / w[0].group;
   if (dtype == EXTERND_F16) return pick_group<false>(a, gpc, mats, EXTERND_F16, s);
