@@ -418,8 +418,8 @@ int externd_q4_reconstruct(const externd_q4* w, int32_t dtype, void* stream, voi
  * order that does not depend on timing; fp32 x is split into three bf16 parts
  * that add up to it exactly.  A non-finite entry of x makes its token's outputs
  * NaN; so does a finite one above 2^120.  tokens may be 0, at most 2^20.
- * workspace: NULL, and where x needs a staged copy (fp32, rows that are not all
- * 16-byte aligned, more than 16 tokens on a large matrix)
+ * workspace: NULL, and where x needs a staged copy (fp32 of more than 5 tokens, rows
+ * that are not all 16-byte aligned, more than 16 tokens on a large matrix)
  * externd_q4_workspace_bytes bytes are allocated and freed stream-ordered; or a caller device buffer, 256-byte aligned, of at least
  * that many bytes, used instead.  Calls that overlap on one workspace race. */
 int externd_q4_apply(const externd_q4* w, const void* x, int64_t tokens, int64_t ldx, int32_t dtype, void* stream,

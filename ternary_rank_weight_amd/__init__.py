@@ -656,7 +656,8 @@ def _q4_scratch(workspace, x, ldx, dtype):
     """As _gated_scratch, for the staged copy of x that the 4-bit products may need."""
     if workspace is None:
         tokens, cols = x.shape
-        if tokens == 0 or tokens <= 16 and dtype != 0 and (cols | ldx) & 7 == 0 and x.data_ptr() & 15 == 0:
+        if tokens <= (5 if dtype == 0 else 0) or \
+                tokens <= 16 and dtype != 0 and (cols | ldx) & 7 == 0 and x.data_ptr() & 15 == 0:
             return None, 0, None
         workspace = torch.empty((_q4_ws(cols, tokens, dtype),), dtype=torch.uint8, device=x.device)
     return (*_scratch(workspace), workspace)
@@ -664,8 +665,8 @@ def _q4_scratch(workspace, x, ldx, dtype):
 
 def q4_apply(q, x, out=None, workspace=None):
     """y = x W^T with 4-bit W: x (..., cols) float32, bfloat16 or float16, y (..., rows) of its type.
-    Rows of x may be strided.  Where x needs a staged copy (float32, rows that are not 16-byte aligned,
-    more than 16 tokens on a large matrix) it is made in workspace (at least q4_workspace_bytes(...) bytes, 256-byte aligned), by
+    Rows of x may be strided.  Where x needs a staged copy (float32 of more than 5 tokens, rows that are not
+    16-byte aligned, more than 16 tokens on a large matrix) it is made in workspace (at least q4_workspace_bytes(...) bytes, 256-byte aligned), by
     default one from torch's allocator.  Not differentiable."""
     dtype = _dtype_code(x.dtype, "x")
     index = _op_device(x, q.codes)

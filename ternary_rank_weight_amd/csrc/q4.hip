@@ -24,16 +24,11 @@
 // neighbouring bf16 values.
 #include <algorithm>
 
-#include "activation.hpp"
-#include "device_common.hpp"
-#include "frag.hpp"
-#include "kernels.hpp"
+#include "q4.hpp"
 
 namespace externd {
 
 namespace {
-
-constexpr int kTile = 16, kChunk = 128;
 
 // ---- quantize, pack, reconstruct: one wave per (tile, chunk) ----
 
@@ -58,29 +53,6 @@ __device__ inline uint32_t pack_word(const uint32_t (&c)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) w |= (c[j] & 15u) << (4 * (j >> 1) + 16 * (j & 1));
   return w;
-}
-
-// Entries col .. col + 7 of a row as fp32 (0 past the end); n: entries left in the row.
-template <int DT>
-__device__ inline void load_weights(const void* W, int64_t at, int64_t n, float (&w)[8]) {
-  if constexpr (DT == EXTERND_F32) {
-    const float* p = static_cast<const float*>(W) + at;
-    if (n >= 8) {
-      const u32x4_a4 a = *reinterpret_cast<const u32x4_a4*>(p), b = *reinterpret_cast<const u32x4_a4*>(p + 4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) { w[j] = __uint_as_float(a[j]); w[4 + j] = __uint_as_float(b[j]); }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = j < n ? p[j] : 0.f;
-    }
-  } else {
-    const uint16_t* p = static_cast<const uint16_t*>(W) + at;
-    u32x4 v;
-    if (n >= 8) v = (reinterpret_cast<uintptr_t>(p) & 15) == 0 ? load8<true>(p) : load8<false>(p);
-    else v = load8_part(p, n);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = f32_from_16<DT == EXTERND_BF16>((v[j / 2] >> (16 * (j & 1))) & 0xffffu);
-  }
 }
 
 // Max of a value over the four lanes that share a row.
@@ -286,11 +258,7 @@ __global__ __launch_bounds__(256) void k_q4_stage_x(const void* __restrict__ x, 
         const int piece = r % 3;
         const uint32_t m0 = piece > 0 ? 0xffff0000u : 0u, m1 = piece > 1 ? 0xffff0000u : 0u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float b = f[j] - __uint_as_float(__float_as_uint(f[j]) & m0);
-          const float c = b - __uint_as_float(__float_as_uint(b) & m1);
-          v[j / 2] |= (__float_as_uint(c) >> 16) << (16 * (j & 1));
-        }
+        for (int j = 0; j < 8; ++j) v[j / 2] |= third_of(f[j], m0, m1) << (16 * (j & 1));
       } else {
         const uint16_t* q = static_cast<const uint16_t*>(x) + t * ldx + col;
         v = left >= 8 ? ((reinterpret_cast<uintptr_t>(q) & 15) == 0 ? load8<true>(q) : load8<false>(q))
@@ -301,264 +269,6 @@ __global__ __launch_bounds__(256) void k_q4_stage_x(const void* __restrict__ x, 
   }
 }
 
-// Codes of one word as the operand 16 + c (exact in bf16 and fp16: the code
-// sits in the four mantissa bits below 16's units).
-template <bool BF>
-__device__ __forceinline__ u32x4 unpack_q4(uint32_t w) {
-  constexpr uint32_t mask = BF ? 0x00780078u : 0x03C003C0u, base = BF ? 0x41804180u : 0x4C004C00u;
-  u32x4 r;
-  if constexpr (BF) {
-    r.x = ((w << 3) & mask) | base;
-    r.y = ((w >> 1) & mask) | base;
-    r.z = ((w >> 5) & mask) | base;
-    r.w = ((w >> 9) & mask) | base;
-  } else {
-    r.x = ((w << 6) & mask) | base;
-    r.y = ((w << 2) & mask) | base;
-    r.z = ((w >> 2) & mask) | base;
-    r.w = ((w >> 6) & mask) | base;
-  }
-  return r;
-}
-
-struct Q4Args {
-  const u32x4* codes[2];
-  const uint16_t* scales[2];
-  const uint16_t* mins[2];
-  const uint16_t* x;    // rows of 16-bit entries, or staged
-  void* y;
-  int64_t ldx, slice, rows, cols, chunks, tokens;   // slice: entries from one slice of x to the next
-  int staged;
-  int pieces;           // slots per token: 1, or 3 for fp32
-  int act;
-};
-
-// y = W x (MATS = 1) or act(Wg x) (Wu x) (MATS = 2) for tiles of 16 slots.
-//
-// A workgroup of WV waves takes RT row tiles and NT slot tiles; its waves take
-// every WV-th chunk, so neighbouring waves read neighbouring kilobytes, and
-// their sums are joined in LDS in wave order (the result does not depend on
-// timing).  Per chunk a wave makes four 16x16x32 products per row and slot
-// tile, with the slots as rows of the first operand and weight rows as columns
-// of the second: D[slot][weight row] then has one weight row per lane, and
-// the group's scale is one multiplication by the lane's own value.
-//
-// The operand is 16 + c, not c - 8 or c: its offset is taken off by a product of x
-// with the constant -24 (or -16), made once for all row tiles.  With minima that product, scaled by -m / 16, is also the
-// m sum(x) term.  Sums are fp32 throughout.
-template <bool BF, int GPC, bool MINS, int MATS, int RT, int NT, int WV>
-__global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type) {
-  constexpr int F = MATS * RT;      // row tiles held by a wave, of all matrices
-  constexpr int SPG = 4 / GPC;      // products per group
-  constexpr int PF = F * NT <= 4 ? 3 : 2;
-  __shared__ float red[WV][F][256];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int r = lane & 15, p = lane >> 4;
-  const int64_t tiles = (a.rows + kTile - 1) / kTile;
-  const int64_t tile0 = (int64_t)blockIdx.x * RT;
-  const int per = a.pieces == 3 ? 15 : 16;         // slots of a slot tile
-  const int64_t slots = a.tokens * a.pieces;
-
-  const uint16_t* xp[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    // a slot (or tile) past the end repeats the last one: its sums are not written
-    const int64_t tile = (int64_t)blockIdx.y * NT + n;
-    if (a.staged) xp[n] = a.x + min(tile, (slots + per - 1) / per - 1) * a.chunks * (4 * 64 * 8) + lane * 8;
-    else xp[n] = a.x + min(tile * 16 + r, slots - 1) * a.ldx + 8 * p;
-  }
-  const u32x4* cp[F];
-  const uint16_t* sp[F];
-  const uint16_t* mp[F];
-#pragma unroll
-  for (int f = 0; f < F; ++f) {
-    const int64_t tile = min(tile0 + f % RT, tiles - 1);   // as for slots
-    cp[f] = a.codes[f / RT] + tile * a.chunks * kWave + lane;
-    sp[f] = a.scales[f / RT] + (tile * a.chunks * kTile + r) * GPC;
-    if constexpr (MINS) mp[f] = a.mins[f / RT] + (tile * a.chunks * kTile + r) * GPC;
-  }
-  f32x4 acc[F][NT];
-#pragma unroll
-  for (int f = 0; f < F; ++f)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[f][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  struct Stage {
-    u32x4 c[F];
-    uint64_t s[F], m[F];   // GPC bf16 values in the low bits
-  };
-  auto table = [](const uint16_t* q) -> uint64_t {
-    if constexpr (GPC == 4) return *reinterpret_cast<const uint64_t*>(q);
-    else if constexpr (GPC == 2) return *reinterpret_cast<const uint32_t*>(q);
-    else return *q;
-  };
-  auto fetch = [&](int64_t c, Stage& st) {
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      st.c[f] = __builtin_nontemporal_load(cp[f] + c * kWave);
-      st.s[f] = table(sp[f] + c * kTile * GPC);
-      if constexpr (MINS) st.m[f] = table(mp[f] + c * kTile * GPC);
-    }
-  };
-  constexpr uint32_t off2 = MINS ? (BF ? 0xC180C180u : 0xCC00CC00u) : (BF ? 0xC1C0C1C0u : 0xCE00CE00u);
-  const u32x4 off = {off2, off2, off2, off2};
-  auto load_x = [&](int64_t c, int i, bool tail, u32x4 (&xf)[NT]) {   // slice i of chunk c
-    const int64_t at = (4 * c + i) * a.slice;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (!tail || at + 8 * p < a.cols) xf[n] = *reinterpret_cast<const u32x4*>(xp[n] + at);
-      else xf[n] = u32x4{0u, 0u, 0u, 0u};   // (only unstaged, where `at` is the column)
-    }
-  };
-  auto add_group = [&](const Stage& st, int g, int f, const f32x4 (&d)[NT], const f32x4 (&xo)[NT]) {
-    const float s = bf16_to_f32((uint32_t)(st.s[f] >> (16 * g)) & 0xffffu);
-    const float m = MINS ? -0.0625f * bf16_to_f32((uint32_t)(st.m[f] >> (16 * g)) & 0xffffu) : 0.f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[f][n][e] = fmaf(s, d[n][e] + xo[n][e], acc[f][n][e]);
-        if constexpr (MINS) acc[f][n][e] = fmaf(m, xo[n][e], acc[f][n][e]);
-      }
-  };
-  constexpr f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  auto work = [&](int64_t c, const Stage& st, bool tail) {
-#pragma unroll
-    for (int g = 0; g < GPC; ++g) {
-      f32x4 xo[NT];
-      if constexpr (SPG <= 2) {
-        // the group's x in registers, one row tile's products after the other's
-        u32x4 xf[SPG][NT];
-#pragma unroll
-        for (int i = 0; i < SPG; ++i) {
-          load_x(c, g * SPG + i, tail, xf[i]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) xo[n] = mfma16<BF>(xf[i][n], off, i ? xo[n] : zero);
-        }
-#pragma unroll
-        for (int f = 0; f < F; ++f) {
-          f32x4 d[NT];
-#pragma unroll
-          for (int i = 0; i < SPG; ++i) {
-            const u32x4 wf = unpack_q4<BF>(st.c[f][g * SPG + i]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) d[n] = mfma16<BF>(xf[i][n], wf, i ? d[n] : zero);
-          }
-          add_group(st, g, f, d, xo);
-        }
-      } else {
-        // the group's products in registers, one slice of x after the other
-        f32x4 d[F][NT];
-#pragma unroll
-        for (int i = 0; i < SPG; ++i) {
-          u32x4 xf[NT];
-          load_x(c, g * SPG + i, tail, xf);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) xo[n] = mfma16<BF>(xf[n], off, i ? xo[n] : zero);
-#pragma unroll
-          for (int f = 0; f < F; ++f) {
-            const u32x4 wf = unpack_q4<BF>(st.c[f][g * SPG + i]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) d[f][n] = mfma16<BF>(xf[n], wf, i ? d[f][n] : zero);
-          }
-        }
-#pragma unroll
-        for (int f = 0; f < F; ++f) add_group(st, g, f, d[f], xo);
-      }
-    }
-  };
-  // PF - 1 chunks of codes are on their way while one is worked on
-  const int64_t full = a.staged ? a.chunks : a.cols / kChunk;   // chunks without a tail
-  Stage st[PF];
-  int64_t c = wave;
-#pragma unroll
-  for (int u = 0; u < PF - 1; ++u)
-    if (c + u * WV < a.chunks) fetch(c + u * WV, st[u]);
-  while (c < full) {
-#pragma unroll
-    for (int u = 0; u < PF; ++u) {
-      if (c < full) {
-        if (c + (PF - 1) * WV < a.chunks) fetch(c + (PF - 1) * WV, st[(u + PF - 1) % PF]);
-        work(c, st[u], false);
-        c += WV;
-      }
-    }
-  }
-  if (c < a.chunks) {   // the last chunk, which has a tail
-    fetch(c, st[0]);
-    work(c, st[0], true);
-  }
-
-  const int rows_here = (int)min<int64_t>(RT * kTile, a.rows - tile0 * kTile);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    if (n) __syncthreads();
-#pragma unroll
-    for (int f = 0; f < F; ++f)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][f][(4 * p + e) * kTile + r] = acc[f][n][e];
-    __syncthreads();
-    const int64_t tok0 = ((int64_t)blockIdx.y * NT + n) * (per / a.pieces);
-    for (int o = threadIdx.x; o < RT * 256; o += WV * kWave) {
-      const int f = o >> 8, tk = (o >> 4) & 15, row = o & 15;
-      if (tk >= per / a.pieces || tok0 + tk >= a.tokens || f * kTile + row >= rows_here) continue;
-      float v[MATS];
-#pragma unroll
-      for (int q = 0; q < MATS; ++q) {
-        float sum = 0.f;
-        for (int e = 0; e < a.pieces; ++e)
-#pragma unroll
-          for (int w = 0; w < WV; ++w) sum += red[w][q * RT + f][(tk * a.pieces + e) * kTile + row];
-        v[q] = sum;
-      }
-      float out = v[0];
-      if constexpr (MATS == 2) out = act_value(a.act, v[0]) * v[1];
-      const int64_t at = (tok0 + tk) * a.rows + (tile0 + f) * kTile + row;
-      if (out_type == EXTERND_F32) static_cast<float*>(a.y)[at] = out;
-      else static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_16<BF>(out);
-    }
-  }
-}
-
-template <bool BF, int GPC, bool MINS, int MATS, int RT, int NT, int WV>
-hipError_t launch_apply(const Q4Args& a, int out_type, hipStream_t s) {
-  const int64_t tiles = (a.rows + kTile - 1) / kTile;
-  const int64_t tpt = a.pieces == 3 ? 5 : 16;   // tokens of a slot tile
-  const int64_t gy = (a.tokens + tpt * NT - 1) / (tpt * NT);
-  const int64_t gx = (tiles + RT - 1) / RT;
-  hipLaunchKernelGGL((k_q4_apply<BF, GPC, MINS, MATS, RT, NT, WV>), dim3((unsigned)gx, (unsigned)gy),
-                     dim3(WV * kWave), 0, s, a, out_type);
-  return hipGetLastError();
-}
-
-template <bool BF, int GPC, bool MINS>
-hipError_t pick_apply(const Q4Args& a, int mats, int out_type, hipStream_t s) {
-  const int64_t slot_tiles = a.pieces == 3 ? (a.tokens + 4) / 5 : (a.tokens + 15) / 16;
-  const int64_t tiles = (a.rows + kTile - 1) / kTile;
-  if (mats == 2) {
-    if (slot_tiles == 1 && tiles > 512) return launch_apply<BF, GPC, MINS, 2, 1, 1, 4>(a, out_type, s);
-    if (slot_tiles == 1) return launch_apply<BF, GPC, MINS, 2, 1, 1, 8>(a, out_type, s);
-    if (slot_tiles == 2) return launch_apply<BF, GPC, MINS, 2, 1, 2, 8>(a, out_type, s);
-    if (slot_tiles == 3) return launch_apply<BF, GPC, MINS, 2, 2, 3, 8>(a, out_type, s);
-    return launch_apply<BF, GPC, MINS, 2, 2, 4, 8>(a, out_type, s);
-  }
-  if (slot_tiles == 1) {
-    if (tiles < 512) return launch_apply<BF, GPC, MINS, 1, 1, 1, 16>(a, out_type, s);
-    return launch_apply<BF, GPC, MINS, 1, 2, 1, 8>(a, out_type, s);
-  }
-  if (slot_tiles == 2) return launch_apply<BF, GPC, MINS, 1, 2, 2, 8>(a, out_type, s);
-  if (slot_tiles == 3) return launch_apply<BF, GPC, MINS, 1, 4, 3, 8>(a, out_type, s);
-  return launch_apply<BF, GPC, MINS, 1, 4, 4, 8>(a, out_type, s);
-}
-
-template <bool BF>
-hipError_t pick_group(const Q4Args& a, int gpc, int mats, int out_type, hipStream_t s) {
-  const bool mins = a.mins[0] != nullptr;
-  if (gpc == 4) return mins ? pick_apply<BF, 4, true>(a, mats, out_type, s) : pick_apply<BF, 4, false>(a, mats, out_type, s);
-  if (gpc == 2) return mins ? pick_apply<BF, 2, true>(a, mats, out_type, s) : pick_apply<BF, 2, false>(a, mats, out_type, s);
-  return mins ? pick_apply<BF, 1, true>(a, mats, out_type, s) : pick_apply<BF, 1, false>(a, mats, out_type, s);
-}
-
 int64_t chunks_of(int64_t cols) { return (cols + kChunk - 1) / kChunk; }
 int64_t jobs_of(int64_t rows, int64_t cols) { return (rows + kTile - 1) / kTile * chunks_of(cols); }
 // Workgroups of four waves, one job each until the grid's limit.
@@ -566,12 +276,13 @@ dim3 jobs_grid(int64_t jobs) { return dim3((unsigned)std::min<int64_t>((jobs + 3
 
 }  // namespace
 
-// Staged: fp32, rows that are not all 16-byte aligned, and large matrices with
+// Staged: fp32 of more than five tokens, rows that are not all 16-byte aligned, and large matrices with
 // more than one slot tile, where the waves' reads of x outweigh the weights and
 // 64-byte pieces of rows come at half the rate of whole kilobytes (32000 x 8192 with
 // 48 tokens: 66 us unstaged).
 bool q4_stages_x(int64_t rows, int64_t cols, int64_t tokens, int64_t ldx, int dtype, const void* x) {
-  return dtype == EXTERND_F32 || cols % 8 != 0 || ldx % 8 != 0 || (reinterpret_cast<uintptr_t>(x) & 15) != 0 ||
+  if (dtype == EXTERND_F32) return tokens > 5;   // five tokens fill a slot tile, which splits them itself
+  return cols % 8 != 0 || ldx % 8 != 0 || (reinterpret_cast<uintptr_t>(x) & 15) != 0 ||
          (tokens > 16 && rows * cols >= (int64_t)1 << 24);
 }
 
@@ -599,6 +310,7 @@ hipError_t run_q4_apply(const externd_q4* w, int mats, const void* x, int64_t to
   a.act = act;
   a.y = y;
   a.staged = ws != nullptr;
+  a.x32 = nullptr;
   if (ws) {
     const int64_t items = a.chunks * 16 * stage_slots(tokens, dtype);
     const dim3 grid((unsigned)std::min<int64_t>((items + 255) / 256, 1 << 16));
@@ -614,12 +326,12 @@ hipError_t run_q4_apply(const externd_q4* w, int mats, const void* x, int64_t to
     a.slice = 64 * 8;
   } else {
     a.x = static_cast<const uint16_t*>(x);
+    if (dtype == EXTERND_F32) a.x32 = static_cast<const float*>(x);
     a.ldx = ldx;
     a.slice = 32;
   }
   const int gpc = kChunk / w[0].group;
-  if (dtype == EXTERND_F16) return pick_group<false>(a, gpc, mats, EXTERND_F16, s);
-  return pick_group<true>(a, gpc, mats, dtype, s);
+  return dtype == EXTERND_F16 ? q4_product_f16(a, gpc, mats, EXTERND_F16, s) : q4_product_bf16(a, gpc, mats, dtype, s);
 }
 
 template <int DT>
