@@ -1,5 +1,7 @@
 // k_q4_apply and its dispatch; each including unit instantiates one operand type.
 #pragma once
+#include <type_traits>
+
 #include "q4.hpp"
 
 namespace externd {
@@ -26,7 +28,7 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
   constexpr int PF = F * NT <= 4 ? 3 : 2;
   static_assert(!X32 || (BF && NT == 1), "fp32 x is read for one slot tile");
   __shared__ float red[WV][F][64 * SL];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane & 15, p = lane >> 4;
   const int64_t tiles = (a.rows + kTile - 1) / kTile;
   const int64_t tile0 = (int64_t)blockIdx.x * RT;
@@ -48,15 +50,16 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
   const int64_t last_slot = min<int64_t>(slot, slots - 1);
   const float* xf32 = a.x32 + (X32 ? last_slot / 3 * a.ldx + 8 * p : 0);
   const uint32_t part0 = X32 && last_slot % 3 > 0 ? 0xffff0000u : 0u, part1 = X32 && last_slot % 3 > 1 ? 0xffff0000u : 0u;
+  // row tile f's blocks of chunks: the same in all lanes
   const u32x4* cp[F];
   const uint16_t* sp[F];
   const uint16_t* mp[F];
 #pragma unroll
   for (int f = 0; f < F; ++f) {
     const int64_t tile = min(tile0 + f % RT, tiles - 1);   // as for slots
-    cp[f] = a.codes[f / RT] + tile * a.chunks * kWave + lane;
-    sp[f] = a.scales[f / RT] + (tile * a.chunks * kTile + r) * GPC;
-    if constexpr (MINS) mp[f] = a.mins[f / RT] + (tile * a.chunks * kTile + r) * GPC;
+    cp[f] = a.codes[f / RT] + tile * a.chunks * kWave;
+    sp[f] = a.scales[f / RT] + tile * a.chunks * kTile * GPC;
+    if constexpr (MINS) mp[f] = a.mins[f / RT] + tile * a.chunks * kTile * GPC;
   }
   float acc[F][NT][SL];   // result rows 4 p + e, e < SL
 #pragma unroll
@@ -78,27 +81,46 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
   auto fetch = [&](int64_t c, Stage& st) {
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      st.c[f] = __builtin_nontemporal_load(cp[f] + c * kWave);
-      st.s[f] = table(sp[f] + c * kTile * GPC);
-      if constexpr (MINS) st.m[f] = table(mp[f] + c * kTile * GPC);
+      st.c[f] = __builtin_nontemporal_load(cp[f] + c * kWave + lane);
+      st.s[f] = table(sp[f] + c * kTile * GPC + r * GPC);
+      if constexpr (MINS) st.m[f] = table(mp[f] + c * kTile * GPC + r * GPC);
     }
   };
   constexpr uint32_t off2 = MINS ? (BF ? 0xC180C180u : 0xCC00CC00u) : (BF ? 0xC1C0C1C0u : 0xCE00CE00u);
   const u32x4 off = {off2, off2, off2, off2};
-  auto load_x = [&](int64_t c, int i, bool tail, u32x4 (&xf)[NT]) {   // slice i of chunk c
+  // x of the four slices of a chunk, on its way one chunk ahead: fp32 as it is,
+  // split when it is used
+  struct Slice {
+    u32x4 v[X32 ? 2 : NT];
+  };
+  Slice xs[4];
+  const int64_t full = a.staged ? a.chunks : a.cols / kChunk;   // chunks without a tail
+  auto load_x = [&](int64_t c, int i, bool tail) {   // slice i of chunk c
     if constexpr (X32) {
       const int64_t col = kChunk * c + 32 * i;
       float f[8];
       load_weights<EXTERND_F32>(xf32, col, tail ? a.cols - col - 8 * p : 8, f);
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) xf[0][j / 2] = third_of(f[j], part0, part1) | (third_of(f[j + 1], part0, part1) << 16);
-      return;
-    }
-    const int64_t at = (4 * c + i) * a.slice;
+      for (int j = 0; j < 8; ++j) xs[i].v[j / 4][j & 3] = __float_as_uint(f[j]);
+    } else {
+      const int64_t at = (4 * c + i) * a.slice;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (!tail || at + 8 * p < a.cols) xf[n] = *reinterpret_cast<const u32x4*>(xp[n] + at);
-      else xf[n] = u32x4{0u, 0u, 0u, 0u};   // (only unstaged, where `at` is the column)
+      for (int n = 0; n < NT; ++n) {
+        if (!tail || at + 8 * p < a.cols) xs[i].v[n] = *reinterpret_cast<const u32x4*>(xp[n] + at);
+        else xs[i].v[n] = u32x4{0u, 0u, 0u, 0u};   // (only unstaged, where `at` is the column)
+      }
+    }
+  };
+  auto operand = [&](int i, int n) {
+    if constexpr (X32) {
+      u32x4 r;
+#pragma unroll
+      for (int j = 0; j < 8; j += 2)
+        r[j / 2] = third_of(__uint_as_float(xs[i].v[j / 4][j & 3]), part0, part1) |
+                   (third_of(__uint_as_float(xs[i].v[j / 4][(j & 3) + 1]), part0, part1) << 16);
+      return r;
+    } else {
+      return xs[i].v[n];
     }
   };
   auto add_group = [&](const Stage& st, int g, int f, const f32x4 (&d)[NT], const f32x4 (&xo)[NT]) {
@@ -113,21 +135,24 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
       }
   };
   constexpr f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  auto work = [&](int64_t c, const Stage& st, bool tail) {
+  constexpr bool MANY = F * NT >= 8;   // accumulators: products started further ahead would spill them
+  // One chunk; the x of chunk cn sets out behind each group.  (Without conditions, here
+  // and in the loop below: with them the compiler moves the sums behind all
+  // groups' products, which then spill.)
+  auto work_on = [&](const Stage& st, int64_t cn, auto ahead) {
 #pragma unroll
     for (int g = 0; g < GPC; ++g) {
-      // (many accumulators: reading every group's x ahead would spill them)
-      if constexpr (F * NT >= 12) __builtin_amdgcn_sched_barrier(0);
       f32x4 xo[NT];
       if constexpr (SPG <= 2) {
-        // the group's x in registers, one row tile's products after the other's
+        // one row tile's products after the other's
         u32x4 xf[SPG][NT];
 #pragma unroll
-        for (int i = 0; i < SPG; ++i) {
-          load_x(c, g * SPG + i, tail, xf[i]);
+        for (int i = 0; i < SPG; ++i)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) xo[n] = mfma16<BF>(xf[i][n], off, i ? xo[n] : zero);
-        }
+          for (int n = 0; n < NT; ++n) {
+            xf[i][n] = operand(g * SPG + i, n);
+            xo[n] = mfma16<BF>(xf[i][n], off, i ? xo[n] : zero);
+          }
 #pragma unroll
         for (int f = 0; f < F; ++f) {
           f32x4 d[NT];
@@ -138,48 +163,57 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
             for (int n = 0; n < NT; ++n) d[n] = mfma16<BF>(xf[i][n], wf, i ? d[n] : zero);
           }
           add_group(st, g, f, d, xo);
+          if constexpr (MANY) __builtin_amdgcn_sched_barrier(0);
         }
       } else {
-        // the group's products in registers, one slice of x after the other
+        // one slice after the other, all row tiles' products in registers
         f32x4 d[F][NT];
 #pragma unroll
         for (int i = 0; i < SPG; ++i) {
           u32x4 xf[NT];
-          load_x(c, g * SPG + i, tail, xf);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) xo[n] = mfma16<BF>(xf[n], off, i ? xo[n] : zero);
+          for (int n = 0; n < NT; ++n) {
+            xf[n] = operand(i, n);
+            xo[n] = mfma16<BF>(xf[n], off, i ? xo[n] : zero);
+          }
 #pragma unroll
           for (int f = 0; f < F; ++f) {
-            const u32x4 wf = unpack_q4<BF>(st.c[f][g * SPG + i]);
+            const u32x4 wf = unpack_q4<BF>(st.c[f][i]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) d[f][n] = mfma16<BF>(xf[n], wf, i ? d[f][n] : zero);
           }
         }
 #pragma unroll
         for (int f = 0; f < F; ++f) add_group(st, g, f, d[f], xo);
+        if constexpr (MANY) __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int i = 0; i < SPG; ++i)
+        if (decltype(ahead)::value) load_x(cn, g * SPG + i, false);
     }
   };
-  // PF - 1 chunks of codes are on their way while one is worked on
-  const int64_t full = a.staged ? a.chunks : a.cols / kChunk;   // chunks without a tail
+  // PF - 1 chunks of codes are on their way while one is worked on (past the
+  // end, the last one again)
   Stage st[PF];
   int64_t c = wave;
+  if (c < full) {
 #pragma unroll
-  for (int u = 0; u < PF - 1; ++u)
-    if (c + u * WV < a.chunks) fetch(c + u * WV, st[u]);
-  while (c < full) {
+    for (int u = 0; u < PF - 1; ++u) fetch(min(c + u * WV, full - 1), st[u]);
 #pragma unroll
-    for (int u = 0; u < PF; ++u) {
-      if (c < full) {
-        if (c + (PF - 1) * WV < a.chunks) fetch(c + (PF - 1) * WV, st[(u + PF - 1) % PF]);
-        work(c, st[u], false);
-        c += WV;
-      }
+    for (int i = 0; i < 4; ++i) load_x(c, i, false);
+#pragma unroll 1
+    for (; c < full; c += WV) {
+      fetch(min(c + (PF - 1) * WV, full - 1), st[PF - 1]);
+      work_on(st[0], min(c + WV, full - 1), std::true_type());
+#pragma unroll
+      for (int u = 0; u + 1 < PF; ++u) st[u] = st[u + 1];
     }
   }
   if (c < a.chunks) {   // the last chunk, which has a tail
     fetch(c, st[0]);
-    work(c, st[0], true);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_x(c, i, true);
+    work_on(st[0], 0, std::false_type());
   }
 
   const int rows_here = (int)min<int64_t>(RT * kTile, a.rows - tile0 * kTile);
@@ -249,13 +283,13 @@ hipError_t pick_apply(const Q4Args& a, int mats, int out_type, hipStream_t s) {
     if (slot_tiles == 1) return one_tile<BF, GPC, MINS, 2, 8>(a, out_type, s);
     if (slot_tiles == 2) return launch_apply<BF, GPC, MINS, 2, 1, 2, 8, 4, false>(a, out_type, s);
     if (slot_tiles == 3) return launch_apply<BF, GPC, MINS, 2, 2, 3, 8, 4, false>(a, out_type, s);
-    return launch_apply<BF, GPC, MINS, 2, 2, 4, 8, 4, false>(a, out_type, s);
+    return launch_apply<BF, GPC, MINS, 2, 1, 4, 8, 4, false>(a, out_type, s);
   }
   if (slot_tiles == 1)
     return tiles < 512 ? one_tile<BF, GPC, MINS, 1, 16>(a, out_type, s) : one_tile<BF, GPC, MINS, 1, 8>(a, out_type, s);
   if (slot_tiles == 2) return launch_apply<BF, GPC, MINS, 1, 2, 2, 8, 4, false>(a, out_type, s);
   if (slot_tiles == 3) return launch_apply<BF, GPC, MINS, 1, 4, 3, 8, 4, false>(a, out_type, s);
-  return launch_apply<BF, GPC, MINS, 1, 4, 4, 8, 4, false>(a, out_type, s);
+  return launch_apply<BF, GPC, MINS, 1, 3, 4, 8, 4, false>(a, out_type, s);
 }
 
 template <bool BF>
