@@ -441,7 +441,8 @@ size_t externd_q4_workspace_bytes(int64_t cols, int64_t tokens, int32_t dtype);
  * EXTERND_BF16 or EXTERND_F16 (fp32 is EXTERND_EUNSUPPORTED: its matrix rate is
  * a sixteenth).  Sums and the activation are fp32 and h is rounded once.  g and u
  * (both or neither): tokens x rows fp32, the projections, kept for the
- * backward pass.  Strides are in entries, at least cols.  tokens may be 0.
+ * backward pass.  Strides are in entries, at least cols; rows and cols are at
+ * most 2^21 (EXTERND_EUNSUPPORTED beyond).  tokens may be 0.
  * workspace: as for externd_q4_apply, of externd_gated_forward_workspace_bytes
  * bytes (which may be 0).  Its `aligned` says that x, Wg and Wu start on 16 bytes
  * and that cols, ldx and ldw are multiples of 8; the products of more than 64

@@ -134,6 +134,7 @@ bool bad_group(int group) { return group != 32 && group != 64 && group != 128; }
 // Row strides: at least the row, and small enough that offsets fit 63 bits with room.
 bool bad_stride(int64_t ld, int64_t cols) { return ld < cols || ld > int64_t(1) << 40; }
 constexpr int64_t kMaxTokens = int64_t(1) << 20;   // of the 4-bit products
+constexpr int64_t kMaxGated = int64_t(1) << 21;    // widths of the gated block
 
 int check_q4(const externd_q4* w, const char* name) {
   if (!w) return fail(EXTERND_EINVAL, "null %s", name);
@@ -172,6 +173,8 @@ int check_gated(const externd::GatedArgs& a) {
   if (a.dtype == EXTERND_F32) return fail(EXTERND_EUNSUPPORTED, "the gated block takes bf16 or fp16");
   if (bad_act(a.act)) return fail(EXTERND_EINVAL, "unknown activation %d", a.act);
   if (bad_size(a.rows, a.cols)) return fail(EXTERND_EINVAL, "bad weight shape");
+  if (a.rows > kMaxGated || a.cols > kMaxGated)   // a tile's offsets are 32 bits
+    return fail(EXTERND_EUNSUPPORTED, "the gated block takes at most 2^21 rows and columns of the weights");
   if (a.tokens < 0 || (a.tokens > 0 && (bad_size(a.tokens, a.cols) || bad_size(a.tokens, a.rows))))
     return fail(EXTERND_EINVAL, "bad number of tokens");
   if (bad_stride(a.ldx, a.cols) || bad_stride(a.ldw, a.cols))

@@ -462,7 +462,10 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
     }
   };
   const int64_t n_lane = wn * NO * 16 + 4 * p, m_lane = wm * MI * 16 + r;
-  auto put_outputs = [&](auto inside) {   // inside: the tile is, and its rows are aligned
+  const bool aligned = g.ldo % 4 == 0 &&
+                       ((reinterpret_cast<uintptr_t>(g.out[0]) | reinterpret_cast<uintptr_t>(g.out[1])) & 7) == 0 &&
+                       ((reinterpret_cast<uintptr_t>(g.save[0]) | reinterpret_cast<uintptr_t>(g.save[1])) & 15) == 0;
+  auto put_outputs = [&](auto inside) {   // inside: the whole tile is, and its rows are aligned
     constexpr bool IN = decltype(inside)::value;
     constexpr int OUTS = MODE == kDx ? 1 : 2;
 #pragma unroll
@@ -473,24 +476,21 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gated_gemm(GemmArgs g) {
       for (int j = 0; j < NO; ++j) {
         const int64_t left = g.ldo - (u.n0 + n_lane + j * 16);
         if (!IN && left <= 0) continue;
+        const bool whole = IN || (aligned && left >= 4);
         if constexpr (SPLIT) {
           float* q = g.part + ((int64_t)u.split * OUTS + u.outsel) * g.mo * g.ldo + at + j * 16;
-          put32(q, left, IN, acc[i][j]);
-          if constexpr (MODE == kFwd) put32(q + g.mo * g.ldo, left, IN, acc[i][j + NI / 2]);
+          put32(q, left, whole, acc[i][j]);
+          if constexpr (MODE == kFwd) put32(q + g.mo * g.ldo, left, whole, acc[i][j + NI / 2]);
         } else {
-          put16(g.out[u.outsel] + at + j * 16, left, IN, packed[i][j]);
+          put16(g.out[u.outsel] + at + j * 16, left, whole, packed[i][j]);
           if (MODE == kFwd && g.save[0]) {
-            put32(g.save[0] + at + j * 16, left, IN, acc[i][j]);
-            put32(g.save[1] + at + j * 16, left, IN, acc[i][j + NI / 2]);
+            put32(g.save[0] + at + j * 16, left, whole, acc[i][j]);
+            put32(g.save[1] + at + j * 16, left, whole, acc[i][j + NI / 2]);
           }
         }
       }
     }
   };
-  const bool aligned = g.ldo % 4 == 0 &&
-                       ((reinterpret_cast<uintptr_t>(g.out[0]) | reinterpret_cast<uintptr_t>(g.out[1])) & 7) == 0 &&
-                       ((reinterpret_cast<uintptr_t>(g.save[0]) | reinterpret_cast<uintptr_t>(g.save[1])) & 15) == 0;
-
   begin(u);
   wait_vm<0, 0>();
 #pragma unroll 1

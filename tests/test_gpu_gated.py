@@ -263,3 +263,47 @@ def test_refusals(lib):
         lib.gated_backward(x, wg, wu, g.half(), u, dh)
     with pytest.raises(TypeError):
         lib.gated_backward(x, wg, wu, g, u, dh.float())
+
+
+@pytest.mark.parametrize("cols", [64 * k for k in range(2, 17)])
+def test_every_number_of_steps(lib, cols):
+    # the contraction's loop begins, repeats after six steps and ends at every phase
+    _check(lib, 70, cols, 72, torch.bfloat16, "silu", cols)
+
+
+@pytest.mark.parametrize("tokens,cols,rows", [(4096, 136, 2320), (4100, 192, 2304), (2000, 4160, 40), (70, 200, 9000)])
+def test_more_tiles_than_units_resident(lib, tokens, cols, rows):
+    # workgroups that take several tiles, contractions split over workgroups, both tile sizes
+    _check_on_device(lib, tokens, cols, rows, torch.bfloat16, "silu")
+    _check_on_device(lib, tokens, cols, rows, torch.float16, "gelu")
+
+
+def _check_on_device(lib, tokens, cols, rows, dtype, act):
+    """As _check, with the fp64 reference on the device (the shapes are too large for the host)."""
+    x, wg, wu, dh = _inputs(tokens, cols, rows, dtype, tokens)
+    X, G, U_, D = (t.double() for t in (x, wg, wu, dh))
+    gv, uv = X @ G.t(), X @ U_.t()
+    a, slope = (torch.from_numpy(t).cuda() for t in og.act(act, _host(gv)))
+    eg, eu = (cols + 64) * E * (X.abs() @ G.abs().t()), (cols + 64) * E * (X.abs() @ U_.abs().t())
+    ea, es = 1.13 * eg + 16 * E * gv.abs(), 0.9 * eg + 32 * E * (1 + gv.abs())
+    un, tiny = U[dtype] * 1.02, TINY[dtype]
+    h, g, u = lib.gated_forward(x, wg, wu, act, save=True)
+    dx, dwg, dwu = lib.gated_backward(x, wg, wu, g, u, dh, act)
+    ref = a * uv
+    dg, du = D * uv * slope, D * a
+    edg = D.abs() * ((uv.abs() + eu) * es + eu * slope.abs()) + un * dg.abs() + tiny
+    edu = D.abs() * ea + un * du.abs() + tiny
+    rows_of = lambda d, e: d.abs() + e
+    checks = [("g", g, gv, eg + 1e-30), ("u", u, uv, eu + 1e-30),
+              ("h", h, ref, ea * (uv.abs() + eu) + a.abs() * eu + un * ref.abs() + tiny)]
+    want = dg @ G + du @ U_
+    mdx = rows_of(dg, edg) @ G.abs() + rows_of(du, edu) @ U_.abs()
+    checks.append(("dx", dx, want,
+                   edg @ G.abs() + edu @ U_.abs() + (2 * rows + 128) * E * mdx + un * want.abs() + tiny))
+    for name, got, d, e in (("dWg", dwg, dg, edg), ("dWu", dwu, du, edu)):
+        want = d.t() @ X
+        m = rows_of(d, e).t() @ X.abs()
+        checks.append((name, got, want, e.t() @ X.abs() + (tokens + 64) * E * m + un * want.abs() + tiny))
+    for name, got, want, tol in checks:
+        err = (got.double() - want).abs()
+        assert bool((err <= tol).all()), (name, float((err / tol).max()))
