@@ -61,12 +61,17 @@ __device__ inline float row_max(float v) {
   return fmaxf(v, __shfl_xor(v, 32, kWave));
 }
 
+// Minimum and maximum of numbers (not NaN) in one instruction: the median with an
+// infinity.  (fminf and fmaxf first quiet both operands.)
+__device__ inline float max_of(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+__device__ inline float min_of(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -INFINITY); }
+
 // Bound by HBM: one read of the matrix, one write of 4.5 to 5 bits per entry;
 // the arithmetic is kept to about a dozen operations an entry so that it stays
-// below that.  The rounded quotients come from the reciprocal: t = w (1 / s) is
-// within 16 x 2^-23 of w / s (|w / s| < 16 where it counts), so rint(t) is the
-// rounded quotient's unless t is within 1e-5 of a tie; a word with such a t, or
-// a scale whose reciprocal may not be normal, is divided out instead.
+// below that.  Quotients are those of a division, without one: y = 1 / s correctly
+// rounded, q = w y, and q + (w - q s) y by two fused operations is the correctly
+// rounded w / s (Markstein's theorem).  Scales so small that y may not be a
+// normal number are divided by.
 template <int DT, int GPC, bool MINS>
 __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ W, int64_t rows, int64_t cols,
                                                       int64_t ldw, int64_t chunks, int64_t jobs,
@@ -99,8 +104,8 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ W,
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           bad = fmaf(w[i][j], 0.f, bad);
-          if constexpr (MINS) { low = fminf(low, w[i][j]); high = fmaxf(high, w[i][j]); }
-          else high = fmaxf(high, fabsf(w[i][j]));
+          if constexpr (MINS) { low = min_of(low, w[i][j]); high = max_of(high, w[i][j]); }
+          else high = max_of(high, fabsf(w[i][j]));
         }
       }
       bad = bad == 0.f ? 0.f : 1.f;
@@ -116,18 +121,17 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ W,
       }
       if (row_max(bad) != 0.f || !(s < INFINITY) || !(fabsf(m) < INFINITY)) s = m = NAN;
       const float inv = 1.f / s;
-      const bool plain = s > 1e-30f;   // its reciprocal is normal (bf16 scales stay below 2^126)
+      const bool plain = s > 1e-30f;   // (bf16 scales stay below 2^126)
 #pragma unroll
       for (int i = g * SPG; i < (g + 1) * SPG; ++i) {
-        float c[8], far = plain ? 0.f : 1.f;   // far: largest distance from a whole number
+        float c[8];
+        if (plain) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float t = (MINS ? w[i][j] - m : w[i][j]) * inv;
-          const float r = rintf(t);
-          far = fmaxf(far, fabsf(t - r));
-          c[j] = fminf(fmaxf(r, lo), hi);
-        }
-        if (!(far < 0.49999f)) {
+          for (int j = 0; j < 8; ++j) {
+            const float v = MINS ? w[i][j] - m : w[i][j], t = v * inv;
+            c[j] = __builtin_amdgcn_fmed3f(rintf(fmaf(fmaf(-t, s, v), inv, t)), lo, hi);
+          }
+        } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float t = s > 0.f ? rintf((MINS ? w[i][j] - m : w[i][j]) / s) : 0.f;

@@ -136,7 +136,7 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
   };
   constexpr f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   constexpr bool MANY = F * NT >= 8;   // accumulators: products started further ahead would spill them
-  // One chunk; the x of chunk cn sets out behind each group.  (Without conditions, here
+  // One chunk; the x of chunk cn sets out behind each group (with one group: each slice).  (Without conditions, here
   // and in the loop below: with them the compiler moves the sums behind all
   // groups' products, which then spill.)
   auto work_on = [&](const Stage& st, int64_t cn, auto ahead) {
@@ -182,14 +182,17 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
 #pragma unroll
             for (int n = 0; n < NT; ++n) d[f][n] = mfma16<BF>(xf[n], wf, i ? d[f][n] : zero);
           }
+          if (decltype(ahead)::value) load_x(cn, i, false);
+          if constexpr (MANY) __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int f = 0; f < F; ++f) add_group(st, g, f, d[f], xo);
         if constexpr (MANY) __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (SPG <= 2 && decltype(ahead)::value) {
 #pragma unroll
-      for (int i = 0; i < SPG; ++i)
-        if (decltype(ahead)::value) load_x(cn, g * SPG + i, false);
+        for (int i = 0; i < SPG; ++i) load_x(cn, g * SPG + i, false);
+      }
     }
   };
   // PF - 1 chunks of codes are on their way while one is worked on (past the

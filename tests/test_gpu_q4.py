@@ -306,3 +306,14 @@ def test_refusals(lib):
         lib.q4_pack(torch.zeros(4, 64, device="cuda"), q.scales, group=32)
     with pytest.raises(ValueError):
         lib.q4_pack(torch.zeros(4, 64, device="cuda", dtype=torch.uint8), q.scales, group=32)
+
+
+def test_quantize_quotients_round_as_divisions(lib):
+    # many scales and quotients at and next to ties: weights on coarse grids times odd scales
+    rng = np.random.default_rng(11)
+    W = (rng.integers(-255, 256, size=(512, 2048)) * rng.integers(128, 256, size=(512, 1)) * 2.0 ** -17).astype(np.float32)
+    W[::2] = np.nextafter(W[::2], np.float32(np.inf)) * rng.uniform(0.5, 2, size=(256, 2048)).astype(np.float32)
+    for symmetric in (True, False):
+        codes, s, m = oq.quantize(W, 32, symmetric)
+        v = lib.q4_reconstruct(lib.q4_quantize(torch.from_numpy(W).cuda(), 32, symmetric))
+        assert np.array_equal(v.cpu().numpy(), oq.values(codes, s, m, 32).astype(np.float32))
