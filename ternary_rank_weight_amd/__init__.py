@@ -565,7 +565,7 @@ class Q4:
     include/externd.h says (tiles of 16 rows by chunks of 128 columns).
     q4_quantize and q4_pack make them.  Its shape is (rows, cols)."""
 
-    __slots__ = ("codes", "scales", "mins", "rows", "cols", "group", "_c")
+    __slots__ = ("codes", "scales", "mins", "rows", "cols", "group", "_c", "_index")
 
     def __init__(self, codes, scales, mins, rows, cols, group):
         if group not in (32, 64, 128) or not 0 < rows < 1 << 31 or not 0 < cols < 1 << 31:
@@ -577,6 +577,7 @@ class Q4:
             _q4_part(mins, torch.bfloat16, 2048 // group * blocks, codes, "mins")
         self.codes, self.scales, self.mins = codes, scales, mins
         self.rows, self.cols, self.group = rows, cols, group
+        self._index = codes.get_device()
         self._c = _Q4(codes.data_ptr(), scales.data_ptr(), None if mins is None else mins.data_ptr(), rows, cols,
                       group, 0)
 
@@ -668,21 +669,33 @@ def q4_apply(q, x, out=None, workspace=None):
     Rows of x may be strided.  Where x needs a staged copy (float32 of more than 5 tokens, rows that are not
     16-byte aligned, more than 16 tokens on a large matrix) it is made in workspace (at least q4_workspace_bytes(...) bytes, 256-byte aligned), by
     default one from torch's allocator.  Not differentiable."""
-    dtype = _dtype_code(x.dtype, "x")
-    index = _op_device(x, q.codes)
-    y = _out_or_new(out, x.shape[:-1] + (q.rows,), x.dtype, x.device)
+    dtype = _DTYPE.get(x.dtype)
+    if dtype is None:
+        _dtype_code(x.dtype, "x")
+    index = q._index
+    if x.get_device() != index or index != _current_device():
+        _op_device(x, q.codes)
+    y = x.new_empty((*x.shape[:-1], q.rows)) if out is None else \
+        _out_or_new(out, (*x.shape[:-1], q.rows), x.dtype, x.device)
     x, ldx = _rows_of(x, q.cols, "x")
     ws, wsb, keep = _q4_scratch(workspace, x, ldx, dtype)
-    _check(_q4_apply(q._c, x.data_ptr(), x.shape[0], ldx, dtype, _raw_stream(index), y.data_ptr(), ws, wsb))
+    status = _q4_apply(q._c, x.data_ptr(), x.shape[0], ldx, dtype, _raw_stream(index), y.data_ptr(), ws, wsb)
+    if status:
+        _check(status)
     return y
 
 
 def q4_gated(qg, qu, x, act="silu", out=None, workspace=None):
     """h = act(x Wg^T) * (x Wu^T) with both matrices in 4 bits (one shape, group and kind), in one
     kernel; everything else as q4_apply.  act: "silu", "gelu" (erf) or "gelu_tanh"."""
-    dtype = _dtype_code(x.dtype, "x")
-    index = _op_device(x, qg.codes, qu.codes)
-    h = _out_or_new(out, x.shape[:-1] + (qg.rows,), x.dtype, x.device)
+    dtype = _DTYPE.get(x.dtype)
+    if dtype is None:
+        _dtype_code(x.dtype, "x")
+    index = qg._index
+    if x.get_device() != index or qu._index != index or index != _current_device():
+        _op_device(x, qg.codes, qu.codes)
+    h = x.new_empty((*x.shape[:-1], qg.rows)) if out is None else \
+        _out_or_new(out, (*x.shape[:-1], qg.rows), x.dtype, x.device)
     x, ldx = _rows_of(x, qg.cols, "x")
     ws, wsb, keep = _q4_scratch(workspace, x, ldx, dtype)
     _check(_q4_gated(qg._c, qu._c, x.data_ptr(), x.shape[0], ldx, dtype, _act_code(act), _raw_stream(index), h.data_ptr(), ws,
@@ -742,7 +755,8 @@ def gated_forward(x, Wg, Wu, act="silu", save=False, out=None, workspace=None):
     index = _op_device(x, Wg, Wu)
     Wg, Wu, ldw, dtype = _gated_weights(x, Wg, Wu)
     rows, cols = Wg.shape
-    h = _out_or_new(out, x.shape[:-1] + (rows,), x.dtype, x.device)
+    h = x.new_empty((*x.shape[:-1], rows)) if out is None else \
+        _out_or_new(out, (*x.shape[:-1], rows), x.dtype, x.device)
     x, ldx = _rows_of(x, cols, "x")
     tokens = x.shape[0]
     g = u = None
