@@ -736,7 +736,8 @@ def _gated_scratch(workspace, bytes_of, x, ldx, Wg, Wu, ldw):
     """(pointer, bytes, the tensor to keep) of the caller's workspace, or of one from torch's allocator
     (whose blocks, unlike a stream-ordered allocation, cost next to nothing from one call to the next)."""
     if workspace is None:
-        aligned = (x.data_ptr() | Wg.data_ptr() | Wu.data_ptr()) & 15 == 0 and (ldx | ldw | Wg.shape[1]) & 7 == 0
+        aligned = (x.data_ptr() | Wg.data_ptr() | Wu.data_ptr()) & 15 == 0 and (ldx | ldw | Wg.shape[1]) & 7 == 0 \
+            and max(ldx, ldw) < 1 << 22
         need = bytes_of(x.shape[0], Wg.shape[1], Wg.shape[0], aligned) if x.shape[0] else 0
         if need == 0:
             return None, 0, None

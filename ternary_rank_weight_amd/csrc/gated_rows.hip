@@ -1,6 +1,7 @@
 // The gated block's forward pass for a few tokens (up to 64):
 // h = act(x Wg^T) (x Wu^T) with every weight read once from memory, which is
-// what bounds it: 2 F K 16-bit weights against 2 products each per token.
+// what bounds it: 2 F K 16-bit weights against one product each per token.
+// F = 9728, K = 2560, one token: 20 us, 5.0 TB/s (a large copy: 5.16).
 //
 // A workgroup takes 16 hidden units.  Its waves take every WV-th stretch of 64
 // columns; a lane reads 16 bytes of its row (lane % 16) of each matrix per 32

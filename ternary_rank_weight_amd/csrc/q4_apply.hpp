@@ -21,6 +21,13 @@ namespace {
 // The operand is 16 + c, not c - 8 or c: its offset is taken off by a product of x
 // with the constant -24 (or -16), made once for all row tiles.  With minima that product, scaled by -m / 16, is also the
 // m sum(x) term.  Sums are fp32 throughout.
+//
+// Bound by the weights' way from memory for a few tokens: 2560 x 9728 with minima,
+// one token, 8 us (2.0 TB/s: 160 workgroups' latency, not bandwidth); gate and up of
+// 9728 x 2560, 8 us (3.4 TB/s).  With 48 tokens on 32000 x 8192, 48 us (2.9 TB/s, 0.52
+// PFLOP/s): the matrix instructions take 14, unpacking 15, x from L2 15 and the
+// weights 27 us, and the two waves per SIMD that the accumulators leave room for
+// overlap them only in part.
 template <bool BF, int GPC, bool MINS, int MATS, int RT, int NT, int WV, int SL, bool X32>
 __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type) {
   constexpr int F = MATS * RT;      // row tiles held by a wave, of all matrices
@@ -81,7 +88,7 @@ __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type)
   auto fetch = [&](int64_t c, Stage& st) {
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      st.c[f] = __builtin_nontemporal_load(cp[f] + c * kWave + lane);
+      st.c[f] = cp[f][c * kWave + lane];
       st.s[f] = table(sp[f] + c * kTile * GPC + r * GPC);
       if constexpr (MINS) st.m[f] = table(mp[f] + c * kTile * GPC + r * GPC);
     }
