@@ -1,0 +1,53 @@
+// The products of the gated block: arguments shared by the planning (gated.hip)
+// and the units that instantiate the kernels (one per operand type).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+namespace externd {
+
+enum GatedProduct { kFwd = 0, kDx = 1, kDw = 2 };
+constexpr int kBK = 64;   // contraction entries per step: two 16x16x32 products, 128 bytes of a row
+
+// One operand of a product: `outer` output rows (or columns) by `inner`
+// contraction entries.  Two sources: the forward's gate and up rows, dx's two
+// segments of the contraction, dW's two outputs.
+struct GatedOperand {
+  const uint16_t* p[2];
+  int64_t ld;
+  int64_t outer;
+};
+
+struct GatedGemm {
+  GatedOperand a, b;         // a: output rows, b: output columns
+  int64_t inner;        // contraction length of one segment
+  int64_t full;         // whole steps of one segment
+  int64_t split_steps;  // whole steps per split; the last split also takes the partial steps
+  int64_t mt, nt;       // tiles
+  int64_t splits;
+  uint16_t* out[2];     // forward: h; dx: dx; dw: dWg, dWu
+  int64_t mo, ldo;      // rows and columns of the outputs
+  float* save[2];       // forward: g, u (or null)
+  float* part;          // SPLIT: where the splits' sums go, fp32 (split, output, mo, ldo)
+  int act;
+};
+
+// How a product is run: 256 x 256 tiles, 128 x 128 tiles two to a CU, or one to a CU
+// with loads three steps ahead; and the splits of its contraction.
+enum GatedKind { kBig, kPair, kDeep };
+struct GatedPlan {
+  GatedKind kind;
+  int64_t splits;
+};
+
+inline int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// One product and, when split, its join.  part: room for the splits' sums.
+hipError_t gated_product_bf16(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, int cus,
+                              hipStream_t s);
+hipError_t gated_product_f16(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, int cus,
+                             hipStream_t s);
+
+}  // namespace externd

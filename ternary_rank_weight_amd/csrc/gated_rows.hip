@@ -1,4 +1,4 @@
-// The gated block's forward pass for a few tokens (up to 64):
+// The gated block's forward pass for a few tokens (up to 32):
 // h = act(x Wg^T) (x Wu^T) with every weight read once from memory, which is
 // what bounds it: 2 F K 16-bit weights against one product each per token.
 // F = 9728, K = 2560, one token: 20 us, 5.0 TB/s (a large copy: 5.16).
@@ -20,7 +20,15 @@ namespace externd {
 
 namespace {
 
-constexpr int kRowsMostTokens = 64;
+// Most tokens of this form.  Past 16 tokens a workgroup reads two tiles of x for its one
+// tile of each weight matrix, and time grows with what it reads, the columns times the
+// tiles that one CU takes in turn.  Aligned operands (a product that needs no copies) go
+// to the tiled product where that is long: 32 tokens here against 33 there, in us,
+//   9728 x 9728: 121, 86   300 x 9728: 36, 19   9728 x 2560: 35, 30   4096 x 4096: 19, 20
+//   9728 x 1024: 14, 13    1024 x 2560: 13, 17  4096 x 2048: 11, 16
+// Rows that are not aligned (9728 x 2559): 61 here, 67 there.
+constexpr int kRowsMostTokens = 32, kRowsShortTokens = 16;
+constexpr int64_t kRowsMostColumns = 5000;
 
 struct RowsArgs {
   const uint16_t *x, *w[2];
@@ -132,8 +140,8 @@ template <bool BF, int NT, bool AL>
 hipError_t launch(const RowsArgs& q, hipStream_t s) {
   const int64_t tiles = (q.rows + 15) / 16;
   // few row tiles: twice the waves on each, to have the whole matrix on its way at once
-  if (NT <= 2 && tiles < 512) {
-    hipLaunchKernelGGL((k_gated_rows<BF, NT <= 2 ? NT : 1, 16, AL>), dim3((unsigned)tiles), dim3(16 * kWave), 0, s, q);
+  if (tiles < 512) {
+    hipLaunchKernelGGL((k_gated_rows<BF, NT, 16, AL>), dim3((unsigned)tiles), dim3(16 * kWave), 0, s, q);
   } else {
     hipLaunchKernelGGL((k_gated_rows<BF, NT, 8, AL>), dim3((unsigned)tiles), dim3(8 * kWave), 0, s, q);
   }
@@ -143,13 +151,15 @@ hipError_t launch(const RowsArgs& q, hipStream_t s) {
 template <bool BF, bool AL>
 hipError_t pick(const RowsArgs& q, hipStream_t s) {
   if (q.tokens <= 16) return launch<BF, 1, AL>(q, s);
-  if (q.tokens <= 32) return launch<BF, 2, AL>(q, s);
-  return launch<BF, 4, AL>(q, s);
+  return launch<BF, 2, AL>(q, s);
 }
 
 }  // namespace
 
-bool gated_takes_rows(int64_t tokens) { return tokens <= kRowsMostTokens; }
+bool gated_takes_rows(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus) {
+  if (tokens <= kRowsShortTokens || tokens > kRowsMostTokens) return tokens <= kRowsShortTokens;
+  return !aligned || cols * std::max<int64_t>((rows + 15) / 16, cus) <= kRowsMostColumns * cus;
+}
 
 hipError_t run_gated_rows(const GatedArgs& a, hipStream_t s) {
   RowsArgs q;

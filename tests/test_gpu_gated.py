@@ -307,3 +307,11 @@ def _check_on_device(lib, tokens, cols, rows, dtype, act):
     for name, got, want, tol in checks:
         err = (got.double() - want).abs()
         assert bool((err <= tol).all()), (name, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("tokens", [16, 17, 32, 33])
+@pytest.mark.parametrize("cols,rows", [(5000, 40), (5008, 40), (5001, 24), (9736, 72), (1024, 21008)])
+def test_token_counts_where_the_form_changes(lib, tokens, cols, rows):
+    # few tokens take one kernel, more of them another, by the columns a compute unit reads
+    _check_on_device(lib, tokens, cols, rows, torch.bfloat16, "silu")
+    _check_on_device(lib, tokens, cols, rows, torch.float16, "gelu_tanh")
