@@ -64,13 +64,28 @@ __device__ __forceinline__ u32x4 load8(const uint16_t* p) {
   }
 }
 
-// The first `n` (any sign, may exceed 8) of eight 16-bit values at p, the others 0.
-__device__ __forceinline__ u32x4 load8_part(const uint16_t* p, int64_t n) {
+// Loads written before stay before, uses written after stay after: the loads are in
+// flight together.  (Left to itself the compiler waits for each of a fragment's narrow
+// loads before it makes the next, or gives each a branch.)
+__device__ __forceinline__ void loads_made() { asm volatile("" ::: "memory"); }
+
+// Eight 16-bit values into a fragment; those outside first .. end - 1 are 0.
+__device__ __forceinline__ u32x4 pack8(const uint16_t (&v)[8], int64_t first, int64_t end) {
   u32x4 r = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < n) r[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+  for (int j = 0; j < 8; ++j) r[j / 2] |= (j >= first && j < end ? (uint32_t)v[j] : 0u) << (16 * (j & 1));
   return r;
+}
+
+// The first `n` (any sign, may exceed 8) of eight 16-bit values at p, the others 0.
+__device__ __forceinline__ u32x4 load8_part(const uint16_t* p, int64_t n) {
+  if (n <= 0) return u32x4{0u, 0u, 0u, 0u};
+  const int last = (int)(n < 8 ? n : 8) - 1;
+  uint16_t v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = p[j < last ? j : last];
+  loads_made();
+  return pack8(v, 0, n);
 }
 
 // 16 bytes per lane from base + offset (bytes, the lane's own) straight to LDS,

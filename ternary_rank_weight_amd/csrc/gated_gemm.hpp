@@ -94,7 +94,7 @@ __device__ __forceinline__ void for_constants(F&& f) {
 //
 // Whole steps go from memory to LDS without passing through registers (so every
 // row starts 16-byte aligned); the last, partial step of a contraction is read
-// through registers.  Rows are read in pieces of 128 bytes: pieces of 64 come
+// through registers, zero past its end.  Rows are read in pieces of 128 bytes: pieces of 64 come
 // from L2 at half the rate.
 //
 // Bound by the matrix instructions: at K = 10240 the forward runs at 1.38
@@ -206,26 +206,40 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
       return base + (k0 + k) * g.b.ld + (u.n0 + o);
     }
   };
-  // eight entries of a slot through registers, zero past either end
-  auto fetch = [&](const uint16_t* p, bool cols, int64_t left_o, int64_t left_k) -> u32x4 {
-    const int64_t n = cols ? (left_k > 0 ? left_o : 0) : left_k;
-    if (n >= 8) return load8<true>(p);
-    return n > 0 ? load8_part(p, n) : u32x4{0u, 0u, 0u, 0u};
+  // A partial step through registers.  A slot's eight entries are all inside or all past
+  // an end: rows are padded to 8 entries (with zeros, where they were padded here).
+  // A thread's loads are in flight together; a slot past an end loads the operand's first.
+  auto stage_operand = [&](auto n, lds16 image, const uint16_t* inside, auto source) {
+    constexpr int PER = NA == 4 ? 4 : BM == 128 ? 2 : 1;   // (what each kind has registers for)
+    static_assert(decltype(n)::value % (PER * NTHR) == 0);
+#pragma unroll 1
+    for (int slot = tid; slot < decltype(n)::value; slot += PER * NTHR) {
+      u32x4 v[PER];
+      bool in[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        int64_t lo, lk;
+        const uint16_t* q = source(slot + i * NTHR, lo, lk);
+        in[i] = lo > 0 && lk > 0;
+        v[i] = load8<true>(in[i] ? q : inside);
+      }
+      loads_made();
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        *(lds_u32x4*)(image + (slot + i * NTHR) * 8) = in[i] ? v[i] : u32x4{0u, 0u, 0u, 0u};
+    }
   };
-  // a partial step, slot by slot through registers
   auto stage_part = [&](int seg, int64_t k0) {
-#pragma unroll 1
-    for (int slot = tid; slot < TA::kSlots; slot += NTHR) {
-      int64_t lo, lk;
-      const uint16_t* p = src_a(slot, seg, k0, lo, lk);
-      *(lds_u32x4*)(la0 + slot * 8) = fetch(p, ACOLS, lo, lk);
-    }
-#pragma unroll 1
-    for (int slot = tid; slot < TB::kSlots; slot += NTHR) {
-      int64_t lo, lk;
-      const uint16_t* p = src_b(slot, seg, k0, lo, lk);
-      *(lds_u32x4*)(lb0 + slot * 8) = fetch(p, BCOLS, lo, lk);
-    }
+    stage_operand(std::integral_constant<int, TA::kSlots>(), la0, g.a.p[0], [&](int slot, int64_t& lo, int64_t& lk) {
+      const uint16_t* q = src_a(slot, seg, k0, lo, lk);
+      if constexpr (!ACOLS) lo = 1;   // (a row past the end repeats the last)
+      return q;
+    });
+    stage_operand(std::integral_constant<int, TB::kSlots>(), lb0, g.b.p[0], [&](int slot, int64_t& lo, int64_t& lk) {
+      const uint16_t* q = src_b(slot, seg, k0, lo, lk);
+      if constexpr (!BCOLS) lo = 1;
+      return q;
+    });
   };
   // the forward's b: half of a wave's fragments in the gate rows, half in the up rows
   const typename TA::Lane lane_a(wm * MI * 16, lane);

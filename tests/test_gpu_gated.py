@@ -315,3 +315,31 @@ def test_token_counts_where_the_form_changes(lib, tokens, cols, rows):
     # few tokens take one kernel, more of them another, by the columns a compute unit reads
     _check_on_device(lib, tokens, cols, rows, torch.bfloat16, "silu")
     _check_on_device(lib, tokens, cols, rows, torch.float16, "gelu_tanh")
+
+
+@pytest.mark.parametrize("tokens", [1, 16, 17, 32])
+@pytest.mark.parametrize("cols,rows,lead", [(1, 1, (1, 1)), (7, 9, (3, 3)), (57, 130, (7, 0)), (64, 17, (5, 5)),
+                                            (65, 300, (0, 1)), (121, 129, (1, 7)), (127, 300, (2, 2)),
+                                            (1237, 260, (0, 0)), (2559, 4200, (0, 0)), (2001, 4200, (6, 3))])
+def test_few_tokens_on_rows_of_any_alignment(lib, tokens, cols, rows, lead):
+    # what lies around the operands is NaN, and each starts at its own distance from 16 bytes
+    def inside(t, first, pad):
+        buf = torch.full((first + t.shape[0] * (t.shape[1] + pad) + 8,), float("nan"), dtype=t.dtype, device="cuda")
+        v = torch.as_strided(buf, t.shape, (t.shape[1] + pad, 1), first)
+        v.copy_(t)
+        return v
+    for dtype, act in ((torch.bfloat16, "silu"), (torch.float16, "gelu")):
+        x, wg, wu, dh = _inputs(tokens, cols, rows, dtype, tokens + cols)
+        want = lib.gated_forward(torch.nn.functional.pad(x, (0, -cols % 8)), torch.nn.functional.pad(wg, (0, -cols % 8)),
+                                 torch.nn.functional.pad(wu, (0, -cols % 8)), act, save=True)
+        for pad in (0, 3):
+            got = lib.gated_forward(inside(x, 1, pad), inside(wg, lead[0], pad), inside(wu, lead[1], pad), act, save=True)
+            X, G, U_ = (t.double() for t in (x, wg, wu))
+            for g, W in ((got[1], G), (got[2], U_)):
+                tol = (cols + 64) * E * (X.abs() @ W.abs().t()) + 1e-30
+                assert bool(((g.double() - X @ W.t()).abs() <= tol).all())
+            # the projections differ by the order of their sums only, and h by what that does to it
+            tol = 3 * (cols + 64) * E * ((X.abs() @ G.abs().t()) * (U_.abs() @ X.abs().t()).t() * 2.26 +
+                                         (X.abs() @ G.abs().t())) + 64 * E * want[0].double().abs()
+            un = 2 * 1.02 * U[dtype] * want[0].double().abs() + 2 * TINY[dtype]
+            assert bool(((got[0].double() - want[0].double()).abs() <= tol + un).all())
