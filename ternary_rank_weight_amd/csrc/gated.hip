@@ -15,7 +15,7 @@
 // activation and the product are done on the accumulators and neither g nor u
 // goes to memory unless the caller keeps them for the backward pass.  They are
 // kept in fp32: dg and du are then the only roundings that the gradients see
-// besides their own (16-bit g and u would add two more of the same size).
+// besides their own, and for few tokens dx does not see those either (16-bit g and u would add two more of the same size).
 #include <algorithm>
 #include <type_traits>
 
@@ -32,12 +32,13 @@ namespace {
 // dg and du, rounded to the operands' type, in rows of ldd entries (a multiple
 // of 8; zero past the hidden width).  Bound by HBM: reads 4 + 4 + 2 bytes, writes
 // 2 + 2 per hidden unit and token; 46 us for 2048 x 9728 (6.0 TB/s).  VEC: rows of all
-// inputs are 16-byte aligned.
+// inputs are 16-byte aligned.  rest: what the rounding took away goes this many entries
+// further on (0: nowhere).
 template <bool BF, bool VEC>
 __global__ __launch_bounds__(256) void k_gated_slopes(const float* __restrict__ g, const float* __restrict__ u,
                                                        const uint16_t* __restrict__ dh, int64_t tokens, int64_t hidden,
-                                                       int64_t lddh, int64_t ldd, int act, uint16_t* __restrict__ dg,
-                                                       uint16_t* __restrict__ du) {
+                                                       int64_t lddh, int64_t ldd, int act, int64_t rest,
+                                                       uint16_t* __restrict__ dg, uint16_t* __restrict__ du) {
   const int64_t per = ldd / 8, total = tokens * per;
   auto run = [&](auto kind) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
@@ -63,22 +64,32 @@ __global__ __launch_bounds__(256) void k_gated_slopes(const float* __restrict__ 
           d[e] = ok ? f32_from_16<BF>(dh[t * lddh + c + e]) : 0.f;
         }
       }
-      u32x4 og, ou;
+      u32x4 og, ou, rg, ru;
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        uint32_t wg[2], wu[2];
+        uint32_t wg[2], wu[2], lg[2], lu[2];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           float a, slope;
           act_both_fast<decltype(kind)::value>(gv[e + f], a, slope);
-          wg[f] = f32_to_16<BF>(d[e + f] * uv[e + f] * slope);
-          wu[f] = f32_to_16<BF>(d[e + f] * a);
+          const float vg = d[e + f] * uv[e + f] * slope, vu = d[e + f] * a;
+          wg[f] = f32_to_16<BF>(vg);
+          wu[f] = f32_to_16<BF>(vu);
+          const float tg = vg - f32_from_16<BF>(wg[f]), tu = vu - f32_from_16<BF>(wu[f]);
+          lg[f] = __builtin_isfinite(tg) ? f32_to_16<BF>(tg) : 0u;   // (infinite and NaN are in the first part)
+          lu[f] = __builtin_isfinite(tu) ? f32_to_16<BF>(tu) : 0u;
         }
         og[e / 2] = wg[0] | (wg[1] << 16);
         ou[e / 2] = wu[0] | (wu[1] << 16);
+        rg[e / 2] = lg[0] | (lg[1] << 16);
+        ru[e / 2] = lu[0] | (lu[1] << 16);
       }
       *reinterpret_cast<u32x4*>(dg + t * ldd + c) = og;
       *reinterpret_cast<u32x4*>(du + t * ldd + c) = ou;
+      if (rest) {
+        *reinterpret_cast<u32x4*>(dg + rest + t * ldd + c) = rg;
+        *reinterpret_cast<u32x4*>(du + rest + t * ldd + c) = ru;
+      }
     }
   };
   if (act == EXTERND_ACT_SILU) run(std::integral_constant<int, EXTERND_ACT_SILU>());
@@ -151,8 +162,24 @@ GatedPlan plan_of(int mode, int64_t m, int64_t n, int64_t steps, int cus) {
   }
   return best;
 }
+int64_t steps_of(int64_t inner) { return inner / kBK; }
+
+// dx.  For few tokens dg and du are kept in two 16-bit parts each, the rounded value and
+// what the rounding took away, stacked as twice the rows: a 128-row tile has room for
+// both, so the second costs no matrix instruction, and dx is then rounded once.  (With
+// one part dx has 1.4 times the error of a rounded result; 1.48 measured for two tokens,
+// where a few roundings decide.)
+GatedPlan plan_dx(int64_t tokens, int64_t cols, int64_t rows, int cus) {
+  const bool stack = tokens <= 64 && tiles_of(kDx, 2 * tokens, cols, false) <= cus;
+  GatedPlan p = plan_of(kDx, stack ? 2 * tokens : tokens, cols, 2 * steps_of(rows), cus);
+  if (stack) {
+    if (p.kind != kDeep) p = {kDeep, 1};
+    p.stacked = 2;
+  }
+  return p;
+}
 int64_t part_floats(int mode, int64_t m, int64_t n, const GatedPlan& p) {
-  return p.splits > 1 ? p.splits * (mode == kDx ? 1 : 2) * m * n : 0;
+  return p.splits * p.stacked > 1 ? p.splits * p.stacked * (mode == kDx ? 1 : 2) * m * n : 0;
 }
 
 hipError_t product(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, bool bf, int cus,
@@ -192,8 +219,6 @@ hipError_t operands(const GatedArgs& a, uint16_t* ws, Operands* o, hipStream_t s
   *o = {q.dst[0], q.dst[1], q.dst[2], q.ldp, q.ldp, q.ldp};
   return hipGetLastError();
 }
-
-int64_t steps_of(int64_t inner) { return inner / kBK; }
 size_t region(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace
@@ -231,8 +256,8 @@ hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s) {
 }
 
 size_t gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus) {
-  const GatedPlan px = plan_of(kDx, tokens, cols, 2 * steps_of(rows), cus), pw = plan_of(kDw, rows, cols, steps_of(tokens), cus);
-  return region(2 * (size_t)(2 * tokens * padded(rows, 8))) +
+  const GatedPlan px = plan_dx(tokens, cols, rows, cus), pw = plan_of(kDw, rows, cols, steps_of(tokens), cus);
+  return region(2 * (size_t)(2 * px.stacked * tokens * padded(rows, 8))) +
          (aligned ? 0 : region(2 * (size_t)copy_entries(tokens, cols, rows))) +
          region(4 * (size_t)std::max(part_floats(kDx, tokens, cols, px), part_floats(kDw, rows, cols, pw)));
 }
@@ -251,8 +276,9 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
   const int64_t ldd = padded(a.rows, 8);
   char* w = static_cast<char*>(ws);
   uint16_t* dg = reinterpret_cast<uint16_t*>(w);
-  uint16_t* du = dg + a.tokens * ldd;
-  w += region(2 * (size_t)(2 * a.tokens * ldd));
+  const GatedPlan px = plan_dx(a.tokens, a.cols, a.rows, a.cus);
+  uint16_t* du = dg + px.stacked * a.tokens * ldd;
+  w += region(2 * (size_t)(2 * px.stacked * a.tokens * ldd));
   {
     const bool vec = a.rows % 8 == 0 && a.lddh % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(a.dh) | reinterpret_cast<uintptr_t>(a.g) |
@@ -260,7 +286,7 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
     const dim3 grid(blocks(a.tokens * (ldd / 8))), block(256);
     auto run = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, block, 0, s, a.g, a.u, static_cast<const uint16_t*>(a.dh), a.tokens, a.rows,
-                         a.lddh, ldd, a.act, dg, du);
+                         a.lddh, ldd, a.act, px.stacked == 2 ? a.tokens * ldd : 0, dg, du);
     };
     if (bf) vec ? run(k_gated_slopes<true, true>) : run(k_gated_slopes<true, false>);
     else vec ? run(k_gated_slopes<false, true>) : run(k_gated_slopes<false, false>);
@@ -273,14 +299,13 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
   const int64_t cols8 = padded(a.cols, 8);
   if (a.dx) {
     GatedGemm g = {};
-    g.a = {{dg, du}, ldd, a.tokens};
+    g.a = {{dg, du}, ldd, px.stacked * a.tokens};
     g.b = {{o.wg, o.wu}, o.ldw, cols8};
     g.inner = a.rows;
     g.out[0] = static_cast<uint16_t*>(a.dx);
-    g.mo = a.tokens;
+    g.mo = px.stacked * a.tokens;
     g.ldo = a.cols;
-    const GatedPlan p = plan_of(kDx, a.tokens, a.cols, 2 * steps_of(a.rows), a.cus);
-    if ((e = product(kDx, g, p, part, bf, a.cus, s)) != hipSuccess) return e;
+    if ((e = product(kDx, g, px, part, bf, a.cus, s)) != hipSuccess) return e;
   }
   if (a.dwg) {
     GatedGemm g = {};

@@ -40,6 +40,7 @@ enum GatedKind { kBig, kPair, kDeep };
 struct GatedPlan {
   GatedKind kind;
   int64_t splits;
+  int64_t stacked = 1;   // 2 (kDeep only): output rows are the sums of the first and the second half of a's
 };
 
 inline int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -568,7 +568,7 @@ hipError_t product(GatedGemm g, const GatedPlan& plan, float* part, int cus, hip
   const int64_t whole = std::max<int64_t>(1, SEGS * g.full);
   g.split_steps = ceil_div64(whole, plan.splits);
   g.splits = ceil_div64(whole, g.split_steps);   // none without steps
-  if (plan.splits == 1)
+  if (plan.splits == 1 && plan.stacked == 1)
     return plan.kind == kBig    ? launch_tile<BF, MODE, kBig, false>(g, cus, s)
            : plan.kind == kPair ? launch_tile<BF, MODE, kPair, false>(g, cus, s)
                                 : launch_tile<BF, MODE, kDeep, false>(g, cus, s);
@@ -578,9 +578,9 @@ hipError_t product(GatedGemm g, const GatedPlan& plan, float* part, int cus, hip
     if (plan.kind == kBig) e = launch_tile<BF, MODE, kBig, true>(g, cus, s);
   if (plan.kind == kDeep) e = launch_tile<BF, MODE, kDeep, true>(g, cus, s);
   if (e != hipSuccess) return e;
-  const int64_t count = g.mo * g.ldo;
+  const int64_t count = g.mo / plan.stacked * g.ldo;   // (a half is as good as a split)
   const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(ceil_div64(count, 256), 1 << 15))), block(256);
-  hipLaunchKernelGGL((k_gated_join<BF, MODE>), grid, block, 0, s, part, count, g.splits, g.out[0], g.out[1], g.save[0],
+  hipLaunchKernelGGL((k_gated_join<BF, MODE>), grid, block, 0, s, part, count, g.splits * plan.stacked, g.out[0], g.out[1], g.save[0],
                      g.save[1], g.act);
   return hipGetLastError();
 }

@@ -343,3 +343,36 @@ def test_few_tokens_on_rows_of_any_alignment(lib, tokens, cols, rows, lead):
                                          (X.abs() @ G.abs().t())) + 64 * E * want[0].double().abs()
             un = 2 * 1.02 * U[dtype] * want[0].double().abs() + 2 * TINY[dtype]
             assert bool(((got[0].double() - want[0].double()).abs() <= tol + un).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("tokens,cols,rows", [(1, 64, 40), (2, 470, 2211), (33, 130, 63), (64, 200, 640), (5, 33000, 72)])
+def test_few_tokens_dx_is_rounded_once(lib, dtype, tokens, cols, rows):
+    # dg and du enter dx with both of their 16-bit parts: what is left of their rounding is its square
+    x, wg, wu, dh = _inputs(tokens, cols, rows, dtype, cols)
+    X, G, U_, D = (t.double() for t in (x, wg, wu, dh))
+    gv, uv = X @ G.t(), X @ U_.t()
+    a, slope = (torch.from_numpy(t).cuda() for t in og.act("gelu", _host(gv)))
+    eg, eu = (cols + 64) * E * (X.abs() @ G.abs().t()), (cols + 64) * E * (X.abs() @ U_.abs().t())
+    ea, es = 1.13 * eg + 16 * E * gv.abs(), 0.9 * eg + 32 * E * (1 + gv.abs())
+    un, tiny = U[dtype] * 1.02, TINY[dtype]
+    parts = un ** 2 if cols <= 32768 else un   # (wider than that, one part is kept)
+    dg, du = D * uv * slope, D * a
+    edg = D.abs() * ((uv.abs() + eu) * es + eu * slope.abs()) + parts * dg.abs() + tiny
+    edu = D.abs() * ea + parts * du.abs() + tiny
+    _, g, u = lib.gated_forward(x, wg, wu, "gelu", save=True)
+    dx, _, _ = lib.gated_backward(x, wg, wu, g, u, dh, "gelu")
+    want = dg @ G + du @ U_
+    m = (dg.abs() + edg) @ G.abs() + (du.abs() + edu) @ U_.abs()
+    tol = edg @ G.abs() + edu @ U_.abs() + (4 * rows + 128) * E * m + un * want.abs() + tiny
+    assert bool(((dx.double() - want).abs() <= tol).all())
+
+
+def test_few_tokens_overflow_stays_infinite(lib):
+    # a dg past fp16's range is infinite in its first part, and the second adds nothing to that
+    x, wg, wu, dh = _inputs(2, 64, 40, torch.float16, 3)
+    wg, wu, x = wg.abs() + 1, wu.abs() + 1, x.abs() + 1
+    dh = torch.full_like(dh, 60000.0)
+    _, g, u = lib.gated_forward(x, wg, wu, "silu", save=True)
+    dx, _, _ = lib.gated_backward(x, wg, wu, g, u, dh, "silu")
+    assert bool(torch.isinf(dx).all()) and bool((dx > 0).all())
