@@ -455,8 +455,7 @@ size_t externd_gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64
 
 /* Gradients of the block from dh (tokens x rows, rows lddh entries apart) and
  * the g and u that the forward pass kept:
- *   dg = dh u act'(g), du = dh act(g)   (rounded once to dtype; for up to 64 tokens
- *     and 32768 cols dx takes them in two parts of dtype, to twice its bits)
+ *   dg = dh u act'(g), du = dh act(g)   (held in two parts of dtype, to twice its bits)
  *   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x   (fp32 sums, rounded once).
  * dx (tokens x cols) may be NULL; dwg and dwu (rows x cols) are both given or
  * both NULL.  Outputs are packed.  With tokens = 0, dwg and dwu are zero.

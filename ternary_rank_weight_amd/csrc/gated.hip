@@ -1,8 +1,8 @@
 // The gated feed-forward block: g = x Wg^T, u = x Wu^T, h = act(g) u in one
 // kernel, and its backward pass
 //   dg = dh u act'(g), du = dh act(g)           (one pass over T x F)
-//   dx = dg Wg + du Wu                          (one product over 2 F)
-//   dWg = dg^T x, dWu = du^T x                  (one launch)
+//   dx = dg Wg + du Wu                          (one product over 4 F)
+//   dWg = dg^T x, dWu = du^T x                  (one launch, over 2 T)
 // for T tokens, K columns (the model's width) and F rows of each weight
 // matrix (the hidden width).
 //
@@ -14,8 +14,11 @@
 // forward tile, gate and up rows of the same hidden units, so that the
 // activation and the product are done on the accumulators and neither g nor u
 // goes to memory unless the caller keeps them for the backward pass.  They are
-// kept in fp32: dg and du are then the only roundings that the gradients see
-// besides their own, and for few tokens dx does not see those either (16-bit g and u would add two more of the same size).
+// kept in fp32, and dg and du are held in two 16-bit parts each, the rounded value and
+// what the rounding took away, which the products take one after the other: the
+// gradients then see no rounding to 16 bits but their own.  (With the rounded
+// dg and du alone the products take half the matrix instructions and the
+// gradients have 1.4 times the error, for few tokens more: a few roundings decide there.)
 #include <algorithm>
 #include <type_traits>
 
@@ -29,11 +32,10 @@ namespace externd {
 
 namespace {
 
-// dg and du, rounded to the operands' type, in rows of ldd entries (a multiple
-// of 8; zero past the hidden width).  Bound by HBM: reads 4 + 4 + 2 bytes, writes
-// 2 + 2 per hidden unit and token; 46 us for 2048 x 9728 (6.0 TB/s).  VEC: rows of all
-// inputs are 16-byte aligned.  rest: what the rounding took away goes this many entries
-// further on (0: nowhere).
+// dg and du in rows of ldd entries (a multiple of 8; zero past the hidden width), each
+// in two parts of the operands' type: the rounded value, and `rest` entries further on
+// what the rounding took away.  Bound by HBM: reads 4 + 4 + 2 bytes, writes
+// 4 + 4 per hidden unit and token.  VEC: rows of all inputs are 16-byte aligned.
 template <bool BF, bool VEC>
 __global__ __launch_bounds__(256) void k_gated_slopes(const float* __restrict__ g, const float* __restrict__ u,
                                                        const uint16_t* __restrict__ dh, int64_t tokens, int64_t hidden,
@@ -86,10 +88,8 @@ __global__ __launch_bounds__(256) void k_gated_slopes(const float* __restrict__ 
       }
       *reinterpret_cast<u32x4*>(dg + t * ldd + c) = og;
       *reinterpret_cast<u32x4*>(du + t * ldd + c) = ou;
-      if (rest) {
-        *reinterpret_cast<u32x4*>(dg + rest + t * ldd + c) = rg;
-        *reinterpret_cast<u32x4*>(du + rest + t * ldd + c) = ru;
-      }
+      *reinterpret_cast<u32x4*>(dg + rest + t * ldd + c) = rg;
+      *reinterpret_cast<u32x4*>(du + rest + t * ldd + c) = ru;
     }
   };
   if (act == EXTERND_ACT_SILU) run(std::integral_constant<int, EXTERND_ACT_SILU>());
@@ -164,19 +164,20 @@ GatedPlan plan_of(int mode, int64_t m, int64_t n, int64_t steps, int cus) {
 }
 int64_t steps_of(int64_t inner) { return inner / kBK; }
 
-// dx.  For few tokens dg and du are kept in two 16-bit parts each, the rounded value and
-// what the rounding took away, stacked as twice the rows: a 128-row tile has room for
-// both, so the second costs no matrix instruction, and dx is then rounded once.  (With
-// one part dx has 1.4 times the error of a rounded result; 1.48 measured for two tokens,
-// where a few roundings decide.)
+// dx.  For few tokens the two parts of dg and du are stacked as twice the rows, which are
+// added at the end: a 128-row tile has room for both, so the second costs no matrix
+// instruction.  Otherwise they follow each other in the contraction.
 GatedPlan plan_dx(int64_t tokens, int64_t cols, int64_t rows, int cus) {
   const bool stack = tokens <= 64 && tiles_of(kDx, 2 * tokens, cols, false) <= cus;
-  GatedPlan p = plan_of(kDx, stack ? 2 * tokens : tokens, cols, 2 * steps_of(rows), cus);
+  GatedPlan p = plan_of(kDx, stack ? 2 * tokens : tokens, cols, (stack ? 2 : 4) * steps_of(rows), cus);
   if (stack) {
     if (p.kind != kDeep) p = {kDeep, 1};
     p.stacked = 2;
   }
   return p;
+}
+GatedPlan plan_dw(int64_t tokens, int64_t cols, int64_t rows, int cus) {
+  return plan_of(kDw, rows, cols, 2 * steps_of(tokens), cus);
 }
 int64_t part_floats(int mode, int64_t m, int64_t n, const GatedPlan& p) {
   return p.splits * p.stacked > 1 ? p.splits * p.stacked * (mode == kDx ? 1 : 2) * m * n : 0;
@@ -244,6 +245,7 @@ hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s) {
   GatedGemm g = {};
   g.a = {{o.x, o.x}, o.ldx, a.tokens};
   g.b = {{o.wg, o.wu}, o.ldw, a.rows};
+  g.segs = 1;
   g.inner = o.cols;
   g.out[0] = static_cast<uint16_t*>(a.h);
   g.mo = a.tokens;
@@ -256,8 +258,8 @@ hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s) {
 }
 
 size_t gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus) {
-  const GatedPlan px = plan_dx(tokens, cols, rows, cus), pw = plan_of(kDw, rows, cols, steps_of(tokens), cus);
-  return region(2 * (size_t)(2 * px.stacked * tokens * padded(rows, 8))) +
+  const GatedPlan px = plan_dx(tokens, cols, rows, cus), pw = plan_dw(tokens, cols, rows, cus);
+  return region(2 * (size_t)(4 * tokens * padded(rows, 8))) +
          (aligned ? 0 : region(2 * (size_t)copy_entries(tokens, cols, rows))) +
          region(4 * (size_t)std::max(part_floats(kDx, tokens, cols, px), part_floats(kDw, rows, cols, pw)));
 }
@@ -273,12 +275,11 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
     }
     return hipSuccess;
   }
-  const int64_t ldd = padded(a.rows, 8);
+  // dg, its rest, du, its rest
+  const int64_t ldd = padded(a.rows, 8), part_len = a.tokens * ldd;
   char* w = static_cast<char*>(ws);
-  uint16_t* dg = reinterpret_cast<uint16_t*>(w);
-  const GatedPlan px = plan_dx(a.tokens, a.cols, a.rows, a.cus);
-  uint16_t* du = dg + px.stacked * a.tokens * ldd;
-  w += region(2 * (size_t)(2 * px.stacked * a.tokens * ldd));
+  uint16_t *dg = reinterpret_cast<uint16_t*>(w), *du = dg + 2 * part_len;
+  w += region(2 * (size_t)(4 * part_len));
   {
     const bool vec = a.rows % 8 == 0 && a.lddh % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(a.dh) | reinterpret_cast<uintptr_t>(a.g) |
@@ -286,7 +287,7 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
     const dim3 grid(blocks(a.tokens * (ldd / 8))), block(256);
     auto run = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, block, 0, s, a.g, a.u, static_cast<const uint16_t*>(a.dh), a.tokens, a.rows,
-                         a.lddh, ldd, a.act, px.stacked == 2 ? a.tokens * ldd : 0, dg, du);
+                         a.lddh, ldd, a.act, part_len, dg, du);
     };
     if (bf) vec ? run(k_gated_slopes<true, true>) : run(k_gated_slopes<true, false>);
     else vec ? run(k_gated_slopes<false, true>) : run(k_gated_slopes<false, false>);
@@ -298,9 +299,12 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
   float* part = reinterpret_cast<float*>(w);
   const int64_t cols8 = padded(a.cols, 8);
   if (a.dx) {
+    const GatedPlan px = plan_dx(a.tokens, a.cols, a.rows, a.cus);
     GatedGemm g = {};
-    g.a = {{dg, du}, ldd, px.stacked * a.tokens};
+    g.a = {{dg, dg}, ldd, px.stacked * a.tokens};
     g.b = {{o.wg, o.wu}, o.ldw, cols8};
+    g.segs = px.stacked == 2 ? 2 : 4;   // stacked: a segment's rows are both parts
+    g.rest = px.stacked * part_len;
     g.inner = a.rows;
     g.out[0] = static_cast<uint16_t*>(a.dx);
     g.mo = px.stacked * a.tokens;
@@ -311,12 +315,14 @@ hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s) {
     GatedGemm g = {};
     g.a = {{dg, du}, ldd, ldd};
     g.b = {{o.x, o.x}, o.ldx, cols8};
+    g.segs = 2;
+    g.rest = part_len;
     g.inner = a.tokens;
     g.out[0] = static_cast<uint16_t*>(a.dwg);
     g.out[1] = static_cast<uint16_t*>(a.dwu);
     g.mo = a.rows;
     g.ldo = a.cols;
-    const GatedPlan p = plan_of(kDw, a.rows, a.cols, steps_of(a.tokens), a.cus);
+    const GatedPlan p = plan_dw(a.tokens, a.cols, a.rows, a.cus);
     if ((e = product(kDw, g, p, part, bf, a.cus, s)) != hipSuccess) return e;
   }
   return hipSuccess;

@@ -12,8 +12,8 @@ enum GatedProduct { kFwd = 0, kDx = 1, kDw = 2 };
 constexpr int kBK = 64;   // contraction entries per step: two 16x16x32 products, 128 bytes of a row
 
 // One operand of a product: `outer` output rows (or columns) by `inner`
-// contraction entries.  Two sources: the forward's gate and up rows, dx's two
-// segments of the contraction, dW's two outputs.
+// contraction entries.  Two sources: the forward's gate and up rows, dx's weights,
+// dW's two outputs.
 struct GatedOperand {
   const uint16_t* p[2];
   int64_t ld;
@@ -22,6 +22,11 @@ struct GatedOperand {
 
 struct GatedGemm {
   GatedOperand a, b;         // a: output rows, b: output columns
+  // The contraction is `segs` segments of `inner` entries each.  Segment s of a lies
+  // s * rest entries past its source; b's source is the second from segment segs / 2 on in
+  // dx, whose a has dg's parts and then du's, and the same for both parts of dW.
+  int segs;
+  int64_t rest;
   int64_t inner;        // contraction length of one segment
   int64_t full;         // whole steps of one segment
   int64_t split_steps;  // whole steps per split; the last split also takes the partial steps

@@ -136,7 +136,8 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   const int wm = wave / WN, wn = wave % WN;
 
   constexpr int BNO = MODE == kFwd ? BN / 2 : BN;   // output columns per tile
-  constexpr int SEGS = MODE == kDx ? 2 : 1;
+  constexpr bool SEGS = MODE != kFwd;   // a contraction of several segments
+  const int segs = SEGS ? g.segs : 1;
 
   // A workgroup takes units (one tile, one split) id, id + grid, ...  They are
   // numbered down groups of 8 tile rows, each XCD a run of them, so that the
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
     q.m0 = (int64_t)mt * BM;
     q.n0 = (int64_t)ntile * BNO;
     q.s_begin = q.split * g.split_steps;
-    q.s_end = min(SEGS * g.full, q.s_begin + g.split_steps);
+    q.s_end = min(segs * g.full, q.s_begin + g.split_steps);
     q.last = q.split == g.splits - 1;
     return q;
   };
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   auto src_a = [&](int slot, int seg, int64_t k0, int64_t& left_o, int64_t& left_k) -> const uint16_t* {
     int o, k;
     TA::place(slot, o, k);
-    const uint16_t* base = g.a.p[MODE == kDx ? seg : u.outsel];
+    const uint16_t* base = g.a.p[u.outsel] + seg * g.rest;
     left_o = g.a.outer - (u.m0 + o);
     left_k = g.inner - (k0 + k);
     if constexpr (!ACOLS) return base + min(u.m0 + o, g.a.outer - 1) * g.a.ld + (k0 + k);
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
       left_k = g.inner - (k0 + k);
       return g.b.p[which] + min(u.n0 + o, g.b.outer - 1) * g.b.ld + (k0 + k);
     } else {
-      const uint16_t* base = g.b.p[MODE == kDx ? seg : 0];
+      const uint16_t* base = g.b.p[MODE == kDx && 2 * seg >= segs];
       left_o = g.b.outer - (u.n0 + o);
       left_k = g.inner - (k0 + k);
       return base + (k0 + k) * g.b.ld + (u.n0 + o);
@@ -266,16 +267,20 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   // Loads to LDS: where the next step of each operand is read.  A wave moves SA or
   // SB pieces of a step, 64 slots each.
   uint32_t va[SA], vb[SB];   // byte offsets of this thread's slots from the tile's first entry
-  const uint16_t *pa = nullptr, *pb = nullptr, *pa_seg1 = nullptr, *pb_seg1 = nullptr;
-  int64_t step_a = 0, step_b = 0;
+  const uint16_t *pa = nullptr, *pb = nullptr;
+  int64_t step_a = 0, step_b = 0;   // within the segment
+  int seg_b = 0;
   const int64_t move_a = ACOLS ? kBK * g.a.ld : kBK, move_b = BCOLS ? kBK * g.b.ld : kBK;
-  const int64_t to_up = MODE == kFwd ? g.b.p[1] - g.b.p[0] : 0;
+  const int64_t to_up = MODE != kDw ? g.b.p[1] - g.b.p[0] : 0;
   const int uwave = __builtin_amdgcn_readfirstlane(wave);
   auto stage_a = [&](lds16 img, int piece) {
     to_lds16(pa, va[piece], img + (piece * NTHR + uwave * kWave) * 8);
     if (piece == SA - 1) {
       pa += move_a;
-      if (SEGS == 2 && ++step_a == g.full) pa = pa_seg1;
+      if (SEGS && ++step_a == g.full) {
+        step_a = 0;
+        pa += g.rest - g.full * move_a;
+      }
     }
   };
   auto stage_b = [&](lds16 img, int piece) {
@@ -284,7 +289,11 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
     to_lds16(up ? pb + to_up : pb, vb[piece], img + (piece * NTHR + uwave * kWave) * 8);
     if (piece == SB - 1) {
       pb += move_b;
-      if (SEGS == 2 && ++step_b == g.full) pb = pb_seg1;
+      if (SEGS && ++step_b == g.full) {
+        step_b = 0;
+        pb -= g.full * move_b;
+        if (MODE == kDx && 2 * ++seg_b == segs) pb += to_up;
+      }
     }
   };
   constexpr int R = 2 * MI, T = R - 3, PIECES = SA + SB, EARLY = 3 * PIECES / R;   // see below
@@ -305,14 +314,17 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
       if constexpr (!BCOLS) vb[i] = (uint32_t)(min<int64_t>(o, g.b.outer - 1 - q.n0) * g.b.ld + k) * 2u;
       else vb[i] = (uint32_t)(k * g.b.ld + min<int64_t>(o, g.b.outer - 8 - q.n0)) * 2u;
     }
-    const int seg = SEGS == 2 && q.s_begin >= g.full;
-    const int64_t first = q.s_begin - seg * g.full;
+    int seg = 0;
+    int64_t first = q.s_begin;
+    while (SEGS && seg + 1 < segs && first >= g.full) {
+      first -= g.full;
+      ++seg;
+    }
     const int64_t from_a = ACOLS ? q.m0 : q.m0 * g.a.ld, from_b = BCOLS ? q.n0 : q.n0 * g.b.ld;
-    pa = g.a.p[MODE == kDw ? q.outsel : seg] + from_a + first * move_a;
-    pb = g.b.p[seg] + from_b + first * move_b;
-    pa_seg1 = g.a.p[1] + from_a;
-    pb_seg1 = g.b.p[1] + from_b;
-    step_a = step_b = q.s_begin;
+    pa = g.a.p[q.outsel] + seg * g.rest + from_a + first * move_a;
+    pb = g.b.p[MODE == kDx && 2 * seg >= segs] + from_b + first * move_b;
+    step_a = step_b = first;
+    seg_b = seg;
     // as the barriers of steps -NA .. -1 would: see below
     for_constants<NA - 1>([&](auto index) {
       constexpr int J = decltype(index)::value, JB = J - NA + NB;
@@ -499,7 +511,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
     contract();
     if (u.last && g.full * kBK < g.inner) {
 #pragma unroll 1
-      for (int seg = 0; seg < SEGS; ++seg) {
+      for (int seg = 0; seg < segs; ++seg) {
         stage_part(seg, g.full * kBK);
         __syncthreads();
         multiply_all();
@@ -563,9 +575,8 @@ hipError_t launch_tile(GatedGemm g, int cus, hipStream_t s) {
 
 template <bool BF, int MODE>
 hipError_t product(GatedGemm g, const GatedPlan& plan, float* part, int cus, hipStream_t s) {
-  constexpr int SEGS = MODE == kDx ? 2 : 1;
   g.full = g.inner / kBK;
-  const int64_t whole = std::max<int64_t>(1, SEGS * g.full);
+  const int64_t whole = std::max<int64_t>(1, g.segs * g.full);
   g.split_steps = ceil_div64(whole, plan.splits);
   g.splits = ceil_div64(whole, g.split_steps);   // none without steps
   if (plan.splits == 1 && plan.stacked == 1)
