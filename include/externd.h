@@ -455,7 +455,9 @@ size_t externd_gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64
 
 /* Gradients of the block from dh (tokens x rows, rows lddh entries apart) and
  * the g and u that the forward pass kept:
- *   dg = dh u act'(g), du = dh act(g)   (held in two parts of dtype, to twice its bits)
+ *   dg = dh u act'(g), du = dh act(g)   (held in two parts of dtype, to twice its bits; in
+ *     fp16 scaled by a power of two per token for dx and per hidden unit for dWg and dWu, so
+ *     that a gradient in fp16's range does not overflow or vanish on its way)
  *   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x   (fp32 sums, rounded once).
  * dx (tokens x cols) may be NULL; dwg and dwu (rows x cols) are both given or
  * both NULL.  Outputs are packed.  With tokens = 0, dwg and dwu are zero.

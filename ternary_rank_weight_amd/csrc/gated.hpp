@@ -37,7 +37,17 @@ struct GatedGemm {
   float* save[2];       // forward: g, u (or null)
   float* part;          // SPLIT: where the splits' sums go, fp32 (split, output, mo, ldo)
   int act;
+  // fp16 gradients: a's row m was scaled by scale_of(tops[m]), for dWu tops[tops_of_up + m]
+  const uint32_t* tops;
+  int64_t tops_of_up;
 };
+
+// The power of two that brings a magnitude (its fp32 bits) to 2^14 .. 2^15, the largest
+// that fp16 holds with room for a rounding, and the power that takes it back.  (Not past 2^100:
+// what is that small leaves no gradient in fp16.)
+__device__ __forceinline__ int scale_shift(uint32_t top) { return min(141 - (int)(top >> 23), 100); }
+__device__ __forceinline__ float scale_of(uint32_t top) { return __uint_as_float((uint32_t)(127 + scale_shift(top)) << 23); }
+__device__ __forceinline__ float unscale_of(uint32_t top) { return __uint_as_float((uint32_t)(127 - scale_shift(top)) << 23); }
 
 // How a product is run: 256 x 256 tiles, 128 x 128 tiles two to a CU, or one to a CU
 // with loads three steps ahead; and the splits of its contraction.

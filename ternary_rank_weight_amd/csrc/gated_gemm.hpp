@@ -460,19 +460,23 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
         packed[i][j] = pack(h);
       }
   };
+  const int64_t n_lane = wn * NO * 16 + 4 * p, m_lane = wm * MI * 16 + r;
   auto round_outputs = [&] {
     if constexpr (MODE == kFwd) {
       if (g.act == EXTERND_ACT_SILU) activate(std::integral_constant<int, EXTERND_ACT_SILU>());
       else if (g.act == EXTERND_ACT_GELU) activate(std::integral_constant<int, EXTERND_ACT_GELU>());
       else activate(std::integral_constant<int, EXTERND_ACT_GELU_TANH>());
     } else {
+      float back[MI];   // fp16: what takes the scale of a's row off
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        if constexpr (!BF) back[i] = unscale_of(g.tops[u.outsel * g.tops_of_up + min(u.m0 + m_lane + i * 16, g.mo - 1)]);
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NO; ++j) packed[i][j] = pack(acc[i][j]);
+        for (int j = 0; j < NO; ++j) packed[i][j] = pack(BF ? acc[i][j] : acc[i][j] * back[i]);
     }
   };
-  const int64_t n_lane = wn * NO * 16 + 4 * p, m_lane = wm * MI * 16 + r;
   const bool aligned = g.ldo % 4 == 0 &&
                        ((reinterpret_cast<uintptr_t>(g.out[0]) | reinterpret_cast<uintptr_t>(g.out[1])) & 7) == 0 &&
                        ((reinterpret_cast<uintptr_t>(g.save[0]) | reinterpret_cast<uintptr_t>(g.save[1])) & 15) == 0;
@@ -535,13 +539,15 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
 }
 
 // What the split contractions left: the splits' sums in their order, then the
-// outputs as the unsplit kernel makes them.  part: (split, outs, count) fp32.
+// outputs as the unsplit kernel makes them.  part: (split, outs, count) fp32, rows of ldo;
+// tops: as in GatedGemm.
 // Forward: both projections, the activation and the product.  Bound by HBM: 17 us for
 // three splits of 2048 x 2560 (4.3 TB/s).
 template <bool BF, int MODE>
 __global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ part, int64_t count, int64_t splits,
                                                      uint16_t* __restrict__ out0, uint16_t* __restrict__ out1,
-                                                     float* __restrict__ g, float* __restrict__ u, int act) {
+                                                     float* __restrict__ g, float* __restrict__ u, int act,
+                                                     const uint32_t* __restrict__ tops, int64_t tops_of_up, int64_t ldo) {
   constexpr int OUTS = MODE == kDx ? 1 : 2;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
     float s[OUTS];
@@ -554,6 +560,11 @@ __global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ pa
       out0[i] = (uint16_t)f32_to_16<BF>(act_value(act, s[0]) * s[1]);
       if (g) { g[i] = s[0]; u[i] = s[1]; }
     } else {
+      if constexpr (!BF) {
+        const int64_t row = i / ldo;
+#pragma unroll
+        for (int o = 0; o < OUTS; ++o) s[o] *= unscale_of(tops[o * tops_of_up + row]);
+      }
       out0[i] = (uint16_t)f32_to_16<BF>(s[0]);
       if constexpr (MODE == kDw) out1[i] = (uint16_t)f32_to_16<BF>(s[1]);
     }
@@ -592,7 +603,7 @@ hipError_t product(GatedGemm g, const GatedPlan& plan, float* part, int cus, hip
   const int64_t count = g.mo / plan.stacked * g.ldo;   // (a half is as good as a split)
   const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(ceil_div64(count, 256), 1 << 15))), block(256);
   hipLaunchKernelGGL((k_gated_join<BF, MODE>), grid, block, 0, s, part, count, g.splits * plan.stacked, g.out[0], g.out[1], g.save[0],
-                     g.save[1], g.act);
+                     g.save[1], g.act, g.tops, g.tops_of_up, g.ldo);
   return hipGetLastError();
 }
 

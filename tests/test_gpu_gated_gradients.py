@@ -78,3 +78,76 @@ def test_error_is_that_of_rounded_gradients(lib, dtype, tokens):
     for have, (name, want, _) in zip(got, _references(x, wg, wu, dh, "silu")):
         rounded = float((want.to(dtype).double() - want).norm())
         assert float((have.double() - want).norm()) <= 1.1 * rounded, name
+
+
+def _scaled(tokens, cols, rows, x, wg, wu, dh, seed):
+    """fp16 operands of the given standard deviations."""
+    rng = np.random.default_rng(seed)
+    t = lambda s, *shape: torch.from_numpy((s * rng.standard_normal(shape)).astype(np.float32)).half().cuda()
+    return t(x, tokens, cols), t(wg, rows, cols), t(wu, rows, cols), t(dh, tokens, rows)
+
+
+def _check_fp16_range(lib, ops, names, large):
+    x, wg, wu, dh = ops
+    X, G, U_, D = (t.double() for t in ops)
+    gv, uv = X @ G.t(), X @ U_.t()
+    a, slope = (torch.from_numpy(t).cuda() for t in og.act("silu", gv.cpu().numpy()))
+    top = max(float((D * uv * slope).abs().max()), float((D * a).abs().max()))
+    assert (top > 2e5) if large else (top < 1e-4)
+    got = _gradients(lib, x, wg, wu, dh, "silu")
+    # the smaller part holds steps of 2^-24 where the largest value is brought to 2^14 or more
+    refs = _references(x, wg, wu, dh, "silu", step=2.0 ** -39 * top)
+    for have, (name, want, tol) in zip(got, refs):
+        if name not in names:
+            continue
+        assert float(want.abs().max()) < 60000 and float(want.abs().max()) > 2.0 ** -12
+        err = (have.double() - want).abs() / (tol + 1.02 * 2.0 ** -11 * want.abs() + 2.0 ** -25)
+        assert bool((err <= 1).all()), (name, float(err.max()))
+
+
+@pytest.mark.parametrize("tokens,cols,rows", [(1, 256, 32), (9, 256, 32), (70, 251, 31), (300, 256, 32)])
+def test_fp16_gradients_in_range_from_larger_dg_and_du(lib, tokens, cols, rows):
+    # dg and du pass 65504 (dh of 5000 times projections of 32), dx or dWg and dWu do not
+    _check_fp16_range(lib, _scaled(tokens, cols, rows, 400, 0.005, 0.005, 5000, tokens), ("dx",), True)
+    _check_fp16_range(lib, _scaled(tokens, cols, rows, 0.002, 1000, 1000, 5000, tokens), ("dWg", "dWu"), True)
+
+
+@pytest.mark.parametrize("tokens,cols,rows", [(2, 256, 1000), (70, 256, 1000), (900, 251, 65)])
+def test_fp16_gradients_from_small_dg_and_du(lib, tokens, cols, rows):
+    # dg and du of 1e-6, in fp16 a dozen steps, add up to gradients with all their bits
+    _check_fp16_range(lib, _scaled(tokens, cols, rows, 0.002, 30, 30, 1e-6, tokens), ("dx",), False)
+    _check_fp16_range(lib, _scaled(tokens, cols, rows, 900, 7e-5, 7e-5, 1e-6, tokens), ("dWg", "dWu"), False)
+
+
+@pytest.mark.parametrize("tokens", [8, 150])
+def test_fp16_large_token_or_unit_leaves_the_others_bits(lib, tokens):
+    # one token's dh is 2^30 times the others': their rows of dx keep their values bit for bit
+    x, wg, wu, dh = _scaled(tokens, 128, 96, 1, 0.05, 0.05, 2.0 ** -16, tokens)
+    _, g, u = lib.gated_forward(x, wg, wu, save=True)
+    dx, dwg, dwu = lib.gated_backward(x, wg, wu, g, u, dh)
+    loud = dh.clone()
+    loud[3] = (dh[3].float().sign() * 2.0 ** 14).half()
+    other = lib.gated_backward(x, wg, wu, g, u, loud)[0]
+    keep = [t for t in range(tokens) if t != 3]
+    assert torch.equal(other[keep], dx[keep]) and not torch.equal(other[3], dx[3])
+    # and one hidden unit's: the others' rows of dWg and dWu
+    loud = dh.clone()
+    loud[:, 5] = (dh[:, 5].float().sign() * 2.0 ** 14).half()
+    other = lib.gated_backward(x, wg, wu, g, u, loud)
+    keep = [f for f in range(96) if f != 5]
+    assert torch.equal(other[1][keep], dwg[keep]) and torch.equal(other[2][keep], dwu[keep])
+
+
+@pytest.mark.parametrize("tokens", [5, 100])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_bad_token_stays_in_its_row_of_dx(lib, dtype, tokens):
+    x, wg, wu, dh = _inputs(tokens, 72, 136, dtype, 6)
+    _, g, u = lib.gated_forward(x, wg, wu, save=True)
+    dx = lib.gated_backward(x, wg, wu, g, u, dh)[0]
+    bad = dh.clone()
+    bad[2, 9], bad[4, 0] = float("nan"), float("inf")
+    got, dwg, _ = lib.gated_backward(x, wg, wu, g, u, bad)
+    keep = [t for t in range(tokens) if t not in (2, 4)]
+    assert torch.equal(got[keep], dx[keep])
+    assert bool(torch.isnan(got[2]).all()) and not bool(torch.isfinite(got[4]).any())
+    assert bool(torch.isnan(dwg[9]).all()) and bool(torch.isfinite(dwg[[f for f in range(136) if f not in (0, 9)]]).all())
