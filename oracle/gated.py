@@ -13,9 +13,10 @@ def act(name, g):
         phi = 0.5 * erfc(-g / np.sqrt(2))
         return g * phi, phi + g * np.exp(-0.5 * g * g) / np.sqrt(2 * np.pi)
     if name == "gelu_tanh":
-        c = np.sqrt(2 / np.pi)
-        t = np.tanh(c * (g + 0.044715 * g ** 3))
-        return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * c * (1 + 3 * 0.044715 * g * g)
+        # (1 + tanh(z)) / 2 = 1 / (1 + exp(-2 z)), which keeps its bits where tanh is near -1
+        c = 2 * np.sqrt(2 / np.pi)
+        z = c * (g + 0.044715 * g ** 3)
+        return g * expit(z), expit(z) + g * expit(z) * expit(-z) * c * (1 + 3 * 0.044715 * g * g)
     raise ValueError(name)
 
 
