@@ -24,37 +24,11 @@ __device__ __forceinline__ float act_value(float g) {
   else return g * sigmoid_f32(gelu_2z(g));
 }
 
-// act(g) and act'(g).
-template <int ACT>
-__device__ __forceinline__ void act_both(float g, float& a, float& slope) {
-  if constexpr (ACT == EXTERND_ACT_SILU) {
-    const float p = sigmoid_f32(g);
-    a = g * p;
-    slope = p + a * (1.f - p);
-  } else if constexpr (ACT == EXTERND_ACT_GELU) {
-    const float phi = 0.5f * erfcf(-0.7071067811865476f * g);
-    a = g * phi;
-    slope = phi + g * 0.3989422804014327f * expf(-0.5f * g * g);
-  } else {
-    const float p = sigmoid_f32(gelu_2z(g));
-    a = g * p;
-    // 0 where p is 0 or 1: the cubic may overflow there
-    const float q = p * (1.f - p);
-    slope = p + (q == 0.f ? 0.f : g * q * gelu_2z_slope(g));
-  }
-}
-
 __device__ __forceinline__ float act_value(int act, float g) {
   if (act == EXTERND_ACT_SILU) return act_value<EXTERND_ACT_SILU>(g);
   if (act == EXTERND_ACT_GELU) return act_value<EXTERND_ACT_GELU>(g);
   return act_value<EXTERND_ACT_GELU_TANH>(g);
 }
-__device__ __forceinline__ void act_both(int act, float g, float& a, float& slope) {
-  if (act == EXTERND_ACT_SILU) act_both<EXTERND_ACT_SILU>(g, a, slope);
-  else if (act == EXTERND_ACT_GELU) act_both<EXTERND_ACT_GELU>(g, a, slope);
-  else act_both<EXTERND_ACT_GELU_TANH>(g, a, slope);
-}
-
 // The same for results that are rounded to 16 bits: hardware reciprocal and
 // exponential.  Their relative error is a few 2^-24, and 2^-23 of the exponent's size more, whose
 // rounding the exponential passes on: 1e-6 at an exponent of 8, 1e-5 at 80.
@@ -86,6 +60,7 @@ __device__ __forceinline__ float act_fast(float g) {
   else return g * sigmoid_fast(gelu_2z(g));
 }
 
+// act(g) and act'(g).
 template <int ACT>
 __device__ __forceinline__ void act_both_fast(float g, float& a, float& slope) {
   if constexpr (ACT == EXTERND_ACT_SILU) {
@@ -99,7 +74,7 @@ __device__ __forceinline__ void act_both_fast(float g, float& a, float& slope) {
   } else {
     const float p = sigmoid_fast(gelu_2z(g));
     a = g * p;
-    const float q = p * (1.f - p);   // 0 where the cubic may overflow
+    const float q = p * (1.f - p);   // 0 where p is 0 or 1: the cubic may overflow there
     slope = p + (q == 0.f ? 0.f : g * q * gelu_2z_slope(g));
   }
 }
