@@ -803,8 +803,6 @@ class _Gated(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, Wg, Wu, act):
         ctx.act = act
-        if not any(ctx.needs_input_grad[:3]):
-            return gated_forward(x, Wg, Wu, act)
         h, g, u = gated_forward(x, Wg, Wu, act, save=True)
         ctx.save_for_backward(x, Wg, Wu, g, u)
         return h
@@ -820,5 +818,7 @@ class _Gated(torch.autograd.Function):
 
 def gated(x, Wg, Wu, act="silu"):
     """gated_forward as a differentiable torch operation (gradients of x, Wg and Wu; g and u are kept
-    in float32 only where a gradient is needed)."""
+    in float32 only where a gradient is needed: not under torch.no_grad())."""
+    if not (torch.is_grad_enabled() and (x.requires_grad or Wg.requires_grad or Wu.requires_grad)):
+        return gated_forward(x, Wg, Wu, act)
     return _Gated.apply(x, Wg, Wu, act)

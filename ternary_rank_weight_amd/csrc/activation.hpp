@@ -29,6 +29,7 @@ __device__ __forceinline__ float act_value(int act, float g) {
   if (act == EXTERND_ACT_GELU) return act_value<EXTERND_ACT_GELU>(g);
   return act_value<EXTERND_ACT_GELU_TANH>(g);
 }
+
 // The same for results that are rounded to 16 bits: hardware reciprocal and
 // exponential.  Their relative error is a few 2^-24, and 2^-23 of the exponent's size more, whose
 // rounding the exponential passes on: 1e-6 at an exponent of 8, 1e-5 at 80.

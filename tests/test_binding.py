@@ -1,0 +1,37 @@
+"""CPU checks of the Python binding's own decisions, with the library's calls replaced."""
+import pytest
+import torch
+
+import ternary_rank_weight_amd as trw
+
+
+@pytest.fixture
+def forward_calls(monkeypatch):
+    """gated_forward by plain products; the list of its calls' `save`."""
+    calls = []
+
+    def forward(x, Wg, Wu, act="silu", save=False, **kw):
+        calls.append(save)
+        g, u = (x @ Wg.t()).detach(), (x @ Wu.t()).detach()
+        h = torch.nn.functional.silu(g) * u
+        return (h, g, u) if save else h
+    monkeypatch.setattr(trw, "gated_forward", forward)
+    return calls
+
+
+def _block():
+    gen = torch.Generator().manual_seed(0)
+    t = lambda *s: torch.randn(*s, generator=gen)
+    return t(3, 8), torch.nn.Parameter(t(5, 8)), torch.nn.Parameter(t(5, 8))
+
+
+def test_gated_keeps_projections_only_for_a_gradient(forward_calls):
+    x, wg, wu = _block()
+    with torch.no_grad():
+        h = trw.gated(x, wg, wu)
+    with torch.inference_mode():
+        trw.gated(x, wg, wu)
+    trw.gated(x, wg.detach(), wu.detach())
+    assert forward_calls == [False] * 3 and not h.requires_grad
+    assert trw.gated(x, wg, wu).requires_grad and trw.gated(x.requires_grad_(), wg.detach(), wu.detach()).requires_grad
+    assert forward_calls[3:] == [True] * 2
