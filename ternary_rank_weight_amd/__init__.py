@@ -563,9 +563,13 @@ class Q4:
 
     codes: int32 words, scales and mins (None: symmetric): bfloat16, laid out as
     include/externd.h says (tiles of 16 rows by chunks of 128 columns).
-    q4_quantize and q4_pack make them.  Its shape is (rows, cols)."""
+    q4_quantize and q4_pack make them.  Its shape is (rows, cols).  It is read only, and
+    the tensors are not to be resized or given other storage while it is in use."""
 
-    __slots__ = ("codes", "scales", "mins", "rows", "cols", "group", "_c", "_index")
+    __slots__ = ("_codes", "_scales", "_mins", "_rows", "_cols", "_group", "_c", "_index")
+    # read only: _c holds the tensors' addresses
+    codes, scales, mins, rows, cols, group = (
+        property(lambda self, name=name: getattr(self, name)) for name in __slots__[:6])
 
     def __init__(self, codes, scales, mins, rows, cols, group):
         if group not in (32, 64, 128) or not 0 < rows < 1 << 31 or not 0 < cols < 1 << 31:
@@ -575,8 +579,8 @@ class Q4:
         _q4_part(scales, torch.bfloat16, 2048 // group * blocks, codes, "scales")
         if mins is not None:
             _q4_part(mins, torch.bfloat16, 2048 // group * blocks, codes, "mins")
-        self.codes, self.scales, self.mins = codes, scales, mins
-        self.rows, self.cols, self.group = rows, cols, group
+        self._codes, self._scales, self._mins = codes, scales, mins
+        self._rows, self._cols, self._group = rows, cols, group
         self._index = codes.get_device()
         self._c = _Q4(codes.data_ptr(), scales.data_ptr(), None if mins is None else mins.data_ptr(), rows, cols,
                       group, 0)
@@ -674,10 +678,10 @@ def q4_apply(q, x, out=None, workspace=None):
         _dtype_code(x.dtype, "x")
     index = q._index
     if x.get_device() != index or index != _current_device():
-        _op_device(x, q.codes)
-    y = x.new_empty((*x.shape[:-1], q.rows)) if out is None else \
-        _out_or_new(out, (*x.shape[:-1], q.rows), x.dtype, x.device)
-    x, ldx = _rows_of(x, q.cols, "x")
+        _op_device(x, q._codes)
+    y = x.new_empty((*x.shape[:-1], q._rows)) if out is None else \
+        _out_or_new(out, (*x.shape[:-1], q._rows), x.dtype, x.device)
+    x, ldx = _rows_of(x, q._cols, "x")
     ws, wsb, keep = _q4_scratch(workspace, x, ldx, dtype)
     status = _q4_apply(q._c, x.data_ptr(), x.shape[0], ldx, dtype, _raw_stream(index), y.data_ptr(), ws, wsb)
     if status:
@@ -693,10 +697,10 @@ def q4_gated(qg, qu, x, act="silu", out=None, workspace=None):
         _dtype_code(x.dtype, "x")
     index = qg._index
     if x.get_device() != index or qu._index != index or index != _current_device():
-        _op_device(x, qg.codes, qu.codes)
-    h = x.new_empty((*x.shape[:-1], qg.rows)) if out is None else \
-        _out_or_new(out, (*x.shape[:-1], qg.rows), x.dtype, x.device)
-    x, ldx = _rows_of(x, qg.cols, "x")
+        _op_device(x, qg._codes, qu._codes)
+    h = x.new_empty((*x.shape[:-1], qg._rows)) if out is None else \
+        _out_or_new(out, (*x.shape[:-1], qg._rows), x.dtype, x.device)
+    x, ldx = _rows_of(x, qg._cols, "x")
     ws, wsb, keep = _q4_scratch(workspace, x, ldx, dtype)
     _check(_q4_gated(qg._c, qu._c, x.data_ptr(), x.shape[0], ldx, dtype, _act_code(act), _raw_stream(index), h.data_ptr(), ws,
                      wsb))

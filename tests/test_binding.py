@@ -35,3 +35,13 @@ def test_gated_keeps_projections_only_for_a_gradient(forward_calls):
     assert forward_calls == [False] * 3 and not h.requires_grad
     assert trw.gated(x, wg, wu).requires_grad and trw.gated(x.requires_grad_(), wg.detach(), wu.detach()).requires_grad
     assert forward_calls[3:] == [True] * 2
+
+
+def test_q4_is_read_only():
+    # the handle holds addresses: a tensor put in the place of another would leave them to freed memory
+    q = trw.Q4.__new__(trw.Q4)
+    for name in ("codes", "scales", "mins", "rows", "cols", "group"):
+        with pytest.raises(AttributeError):
+            setattr(q, name, torch.zeros(4))
+        with pytest.raises(AttributeError):
+            delattr(q, name)
