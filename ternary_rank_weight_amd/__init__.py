@@ -532,11 +532,14 @@ def _rows_of(x, cols, name):
     return x, max(ld, cols)
 
 
-def _scratch(workspace):
+def _scratch(workspace, index):
+    """(pointer, bytes) of a workspace on the device of that index."""
     if workspace is None:
         return None, 0
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
+    if workspace.get_device() != index:
+        raise ValueError("workspace is on another device than the operands")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -665,7 +668,7 @@ def _q4_scratch(workspace, x, ldx, dtype):
                 tokens <= 16 and dtype != 0 and (cols | ldx) & 7 == 0 and x.data_ptr() & 15 == 0:
             return None, 0, None
         workspace = torch.empty((_q4_ws(cols, tokens, dtype),), dtype=torch.uint8, device=x.device)
-    return (*_scratch(workspace), workspace)
+    return (*_scratch(workspace, x.get_device()), workspace)
 
 
 def q4_apply(q, x, out=None, workspace=None):
@@ -746,7 +749,7 @@ def _gated_scratch(workspace, bytes_of, x, ldx, Wg, Wu, ldw):
         if need == 0:
             return None, 0, None
         workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
-    return (*_scratch(workspace), workspace)
+    return (*_scratch(workspace, x.get_device()), workspace)
 
 
 def gated_forward(x, Wg, Wu, act="silu", save=False, out=None, workspace=None):

@@ -45,3 +45,21 @@ def test_q4_is_read_only():
             setattr(q, name, torch.zeros(4))
         with pytest.raises(AttributeError):
             delattr(q, name)
+
+
+class _On(torch.Tensor):
+    """A host tensor that says it is on CUDA device 1."""
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 1
+
+
+def test_workspace_has_to_be_on_the_operands_device():
+    ws = torch.zeros(512, dtype=torch.uint8).as_subclass(_On)
+    assert trw._scratch(ws, 1) == (ws.data_ptr(), 512)
+    assert trw._scratch(None, 0) == (None, 0)
+    with pytest.raises(ValueError):
+        trw._scratch(ws, 0)
+    with pytest.raises(TypeError):
+        trw._scratch(torch.zeros(512), 0)
