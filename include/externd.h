@@ -377,7 +377,11 @@ int externd_deflate(float* R, int64_t m, int64_t n, const uint32_t* u_codes,
  *   scales, mins: bf16, 16 x (128 / group) per tile of a chunk, row r's groups
  *           at r * (128 / group).
  * Padding entries may hold any code; padding scales and minima must be
- * finite.  codes must be 16-byte aligned, scales and mins 8-byte. */
+ * finite.  codes must be 16-byte aligned, scales and mins 8-byte.
+ *
+ * What these functions and those of the gated block below write, the workspace
+ * included, must have no byte in common with what they read or write besides
+ * (EXTERND_EINVAL); what they only read may overlap. */
 enum externd_dtype { EXTERND_F32 = 0, EXTERND_BF16 = 1, EXTERND_F16 = 2 };
 enum externd_activation {
   EXTERND_ACT_SILU = 0,      /* g / (1 + exp(-g)) */

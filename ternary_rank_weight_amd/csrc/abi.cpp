@@ -1,5 +1,6 @@
 // C ABI of the ExTernD library: argument validation, device checks,
 // workspace management and dispatch to the HIP kernels.
+#include <initializer_list>
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -126,6 +127,36 @@ int op_ws(Workspace& w, void* workspace, size_t workspace_bytes, size_t need, hi
   return EXTERND_OK;
 }
 
+// Rows of `width` bytes, `stride` bytes apart; a null pointer is an empty region.
+struct Region {
+  const void* p;
+  int64_t rows, width, stride;
+  const char* name;
+};
+Region packed(const void* p, int64_t bytes, const char* name) { return {p, 1, bytes, bytes, name}; }
+
+// Whether a region of one row has a byte in common with another.
+bool overlaps(const Region& one, const Region& r) {
+  if (!one.p || !r.p || one.width <= 0 || r.width <= 0 || r.rows <= 0) return false;
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(one.p), end = begin + one.width, at = reinterpret_cast<uintptr_t>(r.p);
+  if (end <= at) return false;
+  // r's first row that ends past `begin`
+  const uintptr_t row = begin < at + r.width ? 0 : (begin - at - r.width) / r.stride + 1;
+  return row < (uintptr_t)r.rows && at + row * r.stride < end;
+}
+
+// What a call writes has no byte in common with what it reads or writes besides: the
+// kernels read and write in no set order.
+int check_apart(std::initializer_list<Region> written, std::initializer_list<Region> read) {
+  for (auto w = written.begin(); w != written.end(); ++w) {
+    for (auto o = written.begin(); o != w; ++o)
+      if (overlaps(*w, *o)) return fail(EXTERND_EINVAL, "%s overlaps %s", w->name, o->name);
+    for (const Region& r : read)
+      if (overlaps(*w, r)) return fail(EXTERND_EINVAL, "%s overlaps %s", w->name, r.name);
+  }
+  return EXTERND_OK;
+}
+
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t dtype_bytes(int dtype) { return dtype == EXTERND_F32 ? 4 : 2; }
 bool bad_dtype(int dtype) { return dtype != EXTERND_F32 && dtype != EXTERND_BF16 && dtype != EXTERND_F16; }
@@ -146,6 +177,10 @@ int check_q4(const externd_q4* w, const char* name) {
   return EXTERND_OK;
 }
 
+int64_t q4_blocks(int64_t rows, int64_t cols) { return (rows + 15) / 16 * ((cols + 127) / 128); }
+int64_t q4_code_bytes(const externd_q4& w) { return 1024 * q4_blocks(w.rows, w.cols); }
+int64_t q4_table_bytes(const externd_q4& w) { return 4096 / w.group * q4_blocks(w.rows, w.cols); }
+
 // The common part of the 4-bit products.
 int q4_product(const externd_q4* w, int mats, const void* x, int64_t tokens, int64_t ldx, int dtype, int act,
                void* stream, void* y, void* workspace, size_t workspace_bytes) {
@@ -156,10 +191,17 @@ int q4_product(const externd_q4* w, int mats, const void* x, int64_t tokens, int
   if (!x || !y) return fail(EXTERND_EINVAL, "null x or output pointer");
   if (!aligned_to(x, dtype_bytes(dtype)) || !aligned_to(y, dtype_bytes(dtype)))
     return fail(EXTERND_EINVAL, "x and the output must be aligned to their type");
-  int st = check_device(nullptr);
-  if (st != EXTERND_OK) return st;
-  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t e_bytes = (int64_t)dtype_bytes(dtype);
+  const externd_q4 &a = w[0], &b = w[mats - 1];
   const size_t need = externd::q4_stages_x(w->rows, w->cols, tokens, ldx, dtype, x) ? externd::q4_stage_bytes(w->cols, tokens, dtype) : 0;
+  int st = check_apart({packed(y, tokens * w->rows * e_bytes, "the output"), packed(workspace, (int64_t)need, "workspace")},
+                       {{x, tokens, w->cols * e_bytes, ldx * e_bytes, "x"},
+                        packed(a.codes, q4_code_bytes(a), "codes"), packed(a.scales, q4_table_bytes(a), "scales"),
+                        packed(a.mins, q4_table_bytes(a), "mins"), packed(b.codes, q4_code_bytes(b), "codes"),
+                        packed(b.scales, q4_table_bytes(b), "scales"), packed(b.mins, q4_table_bytes(b), "mins")});
+  if (st != EXTERND_OK) return st;
+  if ((st = check_device(nullptr)) != EXTERND_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
   Workspace ws;
   if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
   hipError_t e = externd::run_q4_apply(w, mats, x, tokens, ldx, dtype, act, y, ws.ptr, s);
@@ -568,12 +610,12 @@ int externd_deflate(float* R, int64_t m, int64_t n, const uint32_t* u_codes,
 
 int64_t externd_q4_code_words(int64_t rows, int64_t cols) {
   if (bad_size(rows, cols)) return -1;
-  return (rows + 15) / 16 * ((cols + 127) / 128) * 256;
+  return 256 * q4_blocks(rows, cols);
 }
 
 int64_t externd_q4_table_len(int64_t rows, int64_t cols, int32_t group) {
   if (bad_size(rows, cols) || bad_group(group)) return -1;
-  return (rows + 15) / 16 * ((cols + 127) / 128) * 16 * (128 / group);
+  return 2048 / group * q4_blocks(rows, cols);
 }
 
 size_t externd_q4_workspace_bytes(int64_t cols, int64_t tokens, int32_t dtype) {
@@ -590,6 +632,11 @@ int externd_q4_quantize(const void* W, int64_t rows, int64_t cols, int64_t ldw, 
   const externd_q4 w = {codes, scales, mins, rows, cols, group, 0};
   int st = check_q4(&w, "output");
   if (st != EXTERND_OK) return st;
+  const int64_t e_bytes = (int64_t)dtype_bytes(dtype);
+  st = check_apart({packed(codes, q4_code_bytes(w), "codes"), packed(scales, q4_table_bytes(w), "scales"),
+                    packed(mins, q4_table_bytes(w), "mins")},
+                   {{W, rows, cols * e_bytes, ldw * e_bytes, "W"}});
+  if (st != EXTERND_OK) return st;
   if ((st = check_device(nullptr)) != EXTERND_OK) return st;
   hipError_t e = externd::run_q4_quantize(W, rows, cols, ldw, dtype, group, codes, scales, mins,
                                           static_cast<hipStream_t>(stream));
@@ -605,6 +652,12 @@ int externd_q4_pack(const uint8_t* codes_in, const uint16_t* scales_in, const ui
   const externd_q4 w = {codes, scales, mins, rows, cols, group, 0};
   int st = check_q4(&w, "output");
   if (st != EXTERND_OK) return st;
+  const int64_t table_in = 2 * rows * ((cols + group - 1) / group);
+  st = check_apart({packed(codes, q4_code_bytes(w), "codes"), packed(scales, q4_table_bytes(w), "scales"),
+                    packed(mins, q4_table_bytes(w), "mins")},
+                   {packed(codes_in, rows * cols, "codes_in"), packed(scales_in, table_in, "scales_in"),
+                    packed(mins_in, table_in, "mins_in")});
+  if (st != EXTERND_OK) return st;
   if ((st = check_device(nullptr)) != EXTERND_OK) return st;
   hipError_t e = externd::run_q4_pack(codes_in, scales_in, mins_in, rows, cols, group, codes, scales, mins,
                                       static_cast<hipStream_t>(stream));
@@ -617,6 +670,10 @@ int externd_q4_reconstruct(const externd_q4* w, int32_t dtype, void* stream, voi
   if (st != EXTERND_OK) return st;
   if (bad_dtype(dtype)) return fail(EXTERND_EINVAL, "unknown dtype %d", dtype);
   if (!out || !aligned_to(out, dtype_bytes(dtype))) return fail(EXTERND_EINVAL, "null or misaligned output");
+  st = check_apart({packed(out, w->rows * w->cols * (int64_t)dtype_bytes(dtype), "the output")},
+                   {packed(w->codes, q4_code_bytes(*w), "codes"), packed(w->scales, q4_table_bytes(*w), "scales"),
+                    packed(w->mins, q4_table_bytes(*w), "mins")});
+  if (st != EXTERND_OK) return st;
   if ((st = check_device(nullptr)) != EXTERND_OK) return st;
   hipError_t e = externd::run_q4_reconstruct(*w, dtype, out, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "q4_reconstruct");
@@ -667,11 +724,16 @@ int externd_gated_forward(const void* x, int64_t tokens, int64_t cols, int64_t l
   if (!aligned_to(x, 2) || !aligned_to(wg, 2) || !aligned_to(wu, 2) || !aligned_to(h, 2) || !aligned_to(g, 4) ||
       !aligned_to(u, 4))
     return fail(EXTERND_EINVAL, "pointers must be aligned to their type");
+  const Region rx = {x, tokens, 2 * cols, 2 * ldx, "x"}, rg = {wg, rows, 2 * cols, 2 * ldw, "wg"},
+               ru = {wu, rows, 2 * cols, 2 * ldw, "wu"}, oh = packed(h, 2 * tokens * rows, "h"),
+               og = packed(g, 4 * tokens * rows, "g"), ou = packed(u, 4 * tokens * rows, "u");
+  if ((st = check_apart({oh, og, ou}, {rx, rg, ru})) != EXTERND_OK) return st;
   if ((st = check_device(&a.cus)) != EXTERND_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   Workspace ws;
   const size_t need =
       externd::gated_forward_workspace_bytes(tokens, cols, rows, externd::gated_is_aligned(a), a.cus);
+  if ((st = check_apart({packed(workspace, (int64_t)need, "workspace")}, {rx, rg, ru, oh, og, ou})) != EXTERND_OK) return st;
   if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
   hipError_t e = externd::run_gated_forward(a, ws.ptr, s);
   if (e != hipSuccess) return hip_fail(e, "gated forward");
@@ -707,6 +769,12 @@ int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t 
   if (!aligned_to(x, 2) || !aligned_to(wg, 2) || !aligned_to(wu, 2) || !aligned_to(dh, 2) || !aligned_to(dx, 2) ||
       !aligned_to(dwg, 2) || !aligned_to(dwu, 2) || !aligned_to(g, 4) || !aligned_to(u, 4))
     return fail(EXTERND_EINVAL, "pointers must be aligned to their type");
+  const Region rx = {x, tokens, 2 * cols, 2 * ldx, "x"}, rwg = {wg, rows, 2 * cols, 2 * ldw, "wg"},
+               rwu = {wu, rows, 2 * cols, 2 * ldw, "wu"}, rg = packed(g, 4 * tokens * rows, "g"),
+               ru = packed(u, 4 * tokens * rows, "u"), rdh = {dh, tokens, 2 * rows, 2 * lddh, "dh"},
+               ox = packed(dx, 2 * tokens * cols, "dx"), og = packed(dwg, 2 * rows * cols, "dwg"),
+               ou = packed(dwu, 2 * rows * cols, "dwu");
+  if ((st = check_apart({ox, og, ou}, {rx, rwg, rwu, rg, ru, rdh})) != EXTERND_OK) return st;
   if ((st = check_device(&a.cus)) != EXTERND_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   Workspace ws;
@@ -714,6 +782,8 @@ int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t 
       tokens > 0
           ? externd::gated_backward_workspace_bytes(tokens, cols, rows, externd::gated_is_aligned(a), a.cus)
           : 0;
+  if ((st = check_apart({packed(workspace, (int64_t)need, "workspace")}, {rx, rwg, rwu, rg, ru, rdh, ox, og, ou})) != EXTERND_OK)
+    return st;
   if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
   hipError_t e = externd::run_gated_backward(a, ws.ptr, s);
   if (e != hipSuccess) return hip_fail(e, "gated backward");
