@@ -552,6 +552,27 @@ def _out_or_new(out, shape, dtype, device, name="out"):
     return out
 
 
+class _NoGradient(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, message, out, *inputs):
+        ctx.message = message
+        return out.detach()
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError(ctx.message)
+
+
+def _records(out):
+    """Whether autograd records a call whose input requires a gradient; an error where it writes into a
+    tensor of the caller's."""
+    if not torch.is_grad_enabled():
+        return False
+    if out is not None:
+        raise RuntimeError("out cannot be given where an input requires a gradient (torch.no_grad() turns that off)")
+    return True
+
+
 def _q4_part(t, dtype, count, codes, name):
     if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         _need(t, dtype, name)
@@ -675,13 +696,15 @@ def q4_apply(q, x, out=None, workspace=None):
     """y = x W^T with 4-bit W: x (..., cols) float32, bfloat16 or float16, y (..., rows) of its type.
     Rows of x may be strided.  Where x needs a staged copy (float32 of more than 5 tokens, rows that are not
     16-byte aligned, more than 16 tokens on a large matrix) it is made in workspace (at least q4_workspace_bytes(...) bytes, 256-byte aligned), by
-    default one from torch's allocator.  Not differentiable."""
+    default one from torch's allocator.  There is no gradient: asking for one raises an error."""
     dtype = _DTYPE.get(x.dtype)
     if dtype is None:
         _dtype_code(x.dtype, "x")
     index = q._index
     if x.get_device() != index or index != _current_device():
         _op_device(x, q._codes)
+    record = x.requires_grad and _records(out)
+    given = x
     y = x.new_empty((*x.shape[:-1], q._rows)) if out is None else \
         _out_or_new(out, (*x.shape[:-1], q._rows), x.dtype, x.device)
     x, ldx = _rows_of(x, q._cols, "x")
@@ -689,7 +712,7 @@ def q4_apply(q, x, out=None, workspace=None):
     status = _q4_apply(q._c, x.data_ptr(), x.shape[0], ldx, dtype, _raw_stream(index), y.data_ptr(), ws, wsb)
     if status:
         _check(status)
-    return y
+    return _NoGradient.apply("q4_apply has no gradient", y, given) if record else y
 
 
 def q4_gated(qg, qu, x, act="silu", out=None, workspace=None):
@@ -701,13 +724,15 @@ def q4_gated(qg, qu, x, act="silu", out=None, workspace=None):
     index = qg._index
     if x.get_device() != index or qu._index != index or index != _current_device():
         _op_device(x, qg._codes, qu._codes)
+    record = x.requires_grad and _records(out)
+    given = x
     h = x.new_empty((*x.shape[:-1], qg._rows)) if out is None else \
         _out_or_new(out, (*x.shape[:-1], qg._rows), x.dtype, x.device)
     x, ldx = _rows_of(x, qg._cols, "x")
     ws, wsb, keep = _q4_scratch(workspace, x, ldx, dtype)
     _check(_q4_gated(qg._c, qu._c, x.data_ptr(), x.shape[0], ldx, dtype, _act_code(act), _raw_stream(index), h.data_ptr(), ws,
                      wsb))
-    return h
+    return _NoGradient.apply("q4_gated has no gradient", h, given) if record else h
 
 
 def _gated_weights(x, Wg, Wu):
@@ -758,8 +783,11 @@ def gated_forward(x, Wg, Wu, act="silu", save=False, out=None, workspace=None):
     x (..., cols) and Wg, Wu (rows, cols) bfloat16 or float16; h (..., rows) of their type.  With
     save, returns (h, g, u): g and u are the projections (tokens, rows) in float32, which
     gated_backward takes.  Rows of x and of the weights may be strided (both weights alike).  act:
-    "silu", "gelu" (erf) or "gelu_tanh".  See gated() for the differentiable form."""
+    "silu", "gelu" (erf) or "gelu_tanh".  gated() is the differentiable form: asking for a gradient
+    of this one raises an error (with save, its result carries none)."""
     act = _act_code(act)
+    record = not save and (x.requires_grad or Wg.requires_grad or Wu.requires_grad) and _records(out)
+    given = x, Wg, Wu
     index = _op_device(x, Wg, Wu)
     Wg, Wu, ldw, dtype = _gated_weights(x, Wg, Wu)
     rows, cols = Wg.shape
@@ -774,6 +802,8 @@ def gated_forward(x, Wg, Wu, act="silu", save=False, out=None, workspace=None):
     _check(_gated_forward(x.data_ptr(), tokens, cols, ldx, Wg.data_ptr(), Wu.data_ptr(), rows, ldw, dtype, act,
                           _raw_stream(index), h.data_ptr(), None if g is None else g.data_ptr(),
                           None if u is None else u.data_ptr(), ws, wsb))
+    if record:
+        return _NoGradient.apply("gated_forward has no gradient; gated has", h, *given)
     return (h, g, u) if save else h
 
 

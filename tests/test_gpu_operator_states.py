@@ -26,3 +26,28 @@ def test_outputs_on_inputs_are_refused(lib):
     # apart: rows of one buffer
     both = torch.randn(16, 64, device="cuda")
     assert torch.equal(lib.q4_apply(q, both[:8], out=both[8:]), lib.q4_apply(q, both[:8].clone()))
+
+
+def test_a_gradient_that_is_not_there_raises(lib):
+    # the 4-bit products and gated_forward have no gradient: asked for one, they say so and do not leave it out
+    W = torch.randn(64, 64, device="cuda")
+    q = lib.q4_quantize(W)
+    x = torch.randn(8, 64, device="cuda", requires_grad=True)
+    half = W.bfloat16().requires_grad_()
+    for y, what in ((lib.q4_apply(q, x), "q4_apply"), (lib.q4_gated(q, q, x), "q4_gated"),
+                    (lib.gated_forward(x.detach().bfloat16(), half, half), "gated")):
+        assert y.requires_grad
+        with pytest.raises(RuntimeError, match=what):
+            y.float().sum().backward()
+        assert x.grad is None and half.grad is None
+    with pytest.raises(RuntimeError, match="out"):
+        lib.q4_apply(q, x, out=torch.empty(8, 64, device="cuda"))
+    with torch.no_grad():
+        y = lib.q4_apply(q, x)
+        assert not y.requires_grad and torch.equal(y, lib.q4_apply(q, x.detach()))
+        out = torch.empty(8, 64, device="cuda")
+        assert lib.q4_apply(q, x, out=out) is out
+    assert torch.equal(lib.q4_apply(q, x), y) and not lib.q4_apply(q, x.detach()).requires_grad
+    # with save the caller takes the gradient by gated_backward
+    h, g, u = lib.gated_forward(x.detach().bfloat16(), half, half, save=True)
+    assert not h.requires_grad
