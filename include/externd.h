@@ -451,7 +451,8 @@ size_t externd_q4_workspace_bytes(int64_t cols, int64_t tokens, int32_t dtype);
  * bytes (which may be 0).  Its `aligned` says that x, Wg and Wu start on 16 bytes
  * and that cols, ldx and ldw are multiples of 8 (strides below 2^22); the
  * products of more than 32 tokens read padded copies otherwise, kept in the
- * workspace. */
+ * workspace.  aligned = 0 gives what covers any alignment.  The bytes are those of this
+ * number of tokens: fewer tokens may need more, as their sums are split. */
 int externd_gated_forward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wg, const void* wu,
                           int64_t rows, int64_t ldw, int32_t dtype, int32_t act, void* stream, void* h, float* g,
                           float* u, void* workspace, size_t workspace_bytes);

@@ -755,7 +755,7 @@ def _gated_weights(x, Wg, Wu):
 
 def gated_forward_workspace_bytes(tokens, cols, rows, aligned=True):
     """Device workspace gated_forward needs (may be 0).  aligned: x, Wg and Wu start on 16 bytes, and
-    cols and their row strides are multiples of 8."""
+    cols and their row strides are multiples of 8; False covers any alignment.  Fewer tokens may need more."""
     return int(_gated_forward_ws(tokens, cols, rows, aligned))
 
 

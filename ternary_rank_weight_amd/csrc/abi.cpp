@@ -1,13 +1,14 @@
 // C ABI of the ExTernD library: argument validation, device checks,
 // workspace management and dispatch to the HIP kernels.
-#include <initializer_list>
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -704,7 +705,10 @@ size_t externd_gated_forward_workspace_bytes(int64_t tokens, int64_t cols, int64
   if (bad_size(rows, cols) || tokens < 1 || bad_size(tokens, cols) || bad_size(tokens, rows)) return 0;
   int cus = 0;
   if (check_device(&cus) != EXTERND_OK) return 0;
-  return externd::gated_forward_workspace_bytes(tokens, cols, rows, aligned != 0, cus);
+  const size_t with = externd::gated_forward_workspace_bytes(tokens, cols, rows, true, cus);
+  if (aligned) return with;
+  // for any alignment: few unaligned tokens may need none where aligned ones have split sums
+  return std::max(with, externd::gated_forward_workspace_bytes(tokens, cols, rows, false, cus));
 }
 
 int externd_gated_forward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wg, const void* wu,

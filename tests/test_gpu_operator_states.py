@@ -51,3 +51,29 @@ def test_a_gradient_that_is_not_there_raises(lib):
     # with save the caller takes the gradient by gated_backward
     h, g, u = lib.gated_forward(x.detach().bfloat16(), half, half, save=True)
     assert not h.requires_grad
+
+
+def test_forward_workspace_covers_any_alignment(lib):
+    for cols in (9728, 4096, 1024, 264):
+        for rows in (300, 40, 2048):
+            for tokens in (1, 16, 17, 32, 33, 64, 300):
+                any_ = lib.gated_forward_workspace_bytes(tokens, cols, rows, aligned=False)
+                assert any_ >= lib.gated_forward_workspace_bytes(tokens, cols, rows), (tokens, cols, rows)
+                any_ = lib.gated_backward_workspace_bytes(tokens, cols, rows, aligned=False)
+                assert any_ >= lib.gated_backward_workspace_bytes(tokens, cols, rows), (tokens, cols, rows)
+
+
+@pytest.mark.parametrize("tokens,cols,rows,aligned", [(32, 9728, 300, True), (100, 4096, 72, True), (40, 203, 72, False),
+                                                      (100, 4095, 72, False)])
+def test_forward_in_a_caller_workspace(lib, tokens, cols, rows, aligned):
+    # split sums, padded copies, both: with what was there before, just enough, and not enough
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    x, wg, wu = (torch.randn(n, cols, generator=gen, device="cuda").bfloat16() for n in (tokens, rows, rows))
+    want = lib.gated_forward(x, wg, wu, save=True)
+    need = lib.gated_forward_workspace_bytes(tokens, cols, rows, aligned)
+    assert need > 0
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = lib.gated_forward(x, wg, wu, save=True, workspace=ws[:need])
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and bool((ws[need:] == 0xFF).all())
+    with pytest.raises(lib.ExterndError):
+        lib.gated_forward(x, wg, wu, workspace=ws[:min(need - 256, 256)])
