@@ -184,6 +184,15 @@ __global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ src
   }
 }
 
+// p + m rounded to fp32, towards the neighbour with an odd last bit where it is inexact:
+// rounding that to fewer bits gives what rounding the exact sum would.
+__device__ inline float add_to_odd(float p, float m) {
+  const float v = p + m, b = v - p, rest = (p - (v - b)) + (m - b);   // v + rest = p + m
+  const uint32_t bits = __float_as_uint(v);
+  if (!(fabsf(rest) > 0.f) || (bits & 1u)) return v;   // (rest is NaN where v is not finite)
+  return __uint_as_float((rest > 0.f) == (v > 0.f) ? bits + 1 : bits - 1);
+}
+
 // The values, rounded once to the output's type.  Bound by HBM: the write.  9728 x
 // 2559 to fp32: 25 us, 4.5 TB/s.
 template <int DT>
@@ -208,7 +217,12 @@ __global__ __launch_bounds__(256) void k_q4_reconstruct(const u32x4* __restrict_
   #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t c = (cw[i] >> (4 * (j >> 1) + 16 * (j & 1))) & 15u;
-        v[j] = s * ((float)c - mid) + m;   // the product is exact: 8 by 4 bits
+        // (the product is exact, 8 by 4 bits, unless it passes fp32's range, which s c + m may not)
+        v[j] = fmaf(s, (float)c - mid, m);
+        if constexpr (DT != EXTERND_F32) {
+          const float p = s * ((float)c - mid);
+          if (mins && __builtin_isfinite(p)) v[j] = add_to_odd(p, m);
+        }
       }
       if constexpr (DT == EXTERND_F32) {
         float* p = static_cast<float*>(out) + q.row * cols + col;
