@@ -420,8 +420,10 @@ int externd_q4_reconstruct(const externd_q4* w, int32_t dtype, void* stream, voi
 /* y[t] = W x[t] for `tokens` rows of x (cols entries of dtype, ldx >= cols
  * entries apart); y is tokens x rows of dtype, packed.  Sums are fp32, in an
  * order that does not depend on timing; fp32 x is split into three bf16 parts
- * that add up to it exactly.  A non-finite entry of x makes its token's outputs
- * NaN; so does a finite one above 2^120.  tokens may be 0, at most 2^20.
+ * that add up to it exactly.  Codes enter as 16 + c, and the 16 (or 24) is taken off
+ * again: so the |x| of each group have to add up to less than 2^123, past which
+ * a sum may overflow that W x does not, and an infinite entry of x makes its token's
+ * outputs NaN, as a NaN does.  tokens may be 0, at most 2^20.
  * workspace: NULL, and where x needs a staged copy (fp32 of more than 5 tokens, rows
  * that are not all 16-byte aligned, more than 16 tokens on a large matrix)
  * externd_q4_workspace_bytes bytes are allocated and freed stream-ordered; or a caller device buffer, 256-byte aligned, of at least
