@@ -37,7 +37,7 @@ def quantized(w, group):
 def tune(x, target, wg, wu, group, steps, rate):
     """Gate and up weights whose 4-bit values bring h(x) nearer to target: gradients are taken at
     the quantized values and applied to the weights behind them."""
-    wg, wu = wg.float(), wu.float()
+    wg, wu = (w.float().clone() for w in (wg, wu))
     for _ in range(steps):
         leaves = [quantized(w, group)[0].requires_grad_() for w in (wg, wu)]
         h = trw.gated(x, *leaves)
