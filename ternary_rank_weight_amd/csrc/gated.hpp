@@ -1,15 +1,12 @@
-// The products of the gated block: arguments shared by the planning (gated.hip)
+// The products of the gated block: arguments shared by the passes (gated.hip)
 // and the units that instantiate the kernels (one per operand type).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
+#include "gated_plan.hpp"
 
 namespace externd {
-
-enum GatedProduct { kFwd = 0, kDx = 1, kDw = 2 };
-constexpr int kBK = 64;   // contraction entries per step: two 16x16x32 products, 128 bytes of a row
 
 // One operand of a product: `outer` output rows (or columns) by `inner`
 // contraction entries.  Two sources: the forward's gate and up rows, dx's weights,
@@ -48,17 +45,6 @@ struct GatedGemm {
 __device__ __forceinline__ int scale_shift(uint32_t top) { return min(141 - (int)(top >> 23), 100); }
 __device__ __forceinline__ float scale_of(uint32_t top) { return __uint_as_float((uint32_t)(127 + scale_shift(top)) << 23); }
 __device__ __forceinline__ float unscale_of(uint32_t top) { return __uint_as_float((uint32_t)(127 - scale_shift(top)) << 23); }
-
-// How a product is run: 256 x 256 tiles, 128 x 128 tiles two to a CU, or one to a CU
-// with loads three steps ahead; and the splits of its contraction.
-enum GatedKind { kBig, kPair, kDeep };
-struct GatedPlan {
-  GatedKind kind;
-  int64_t splits;
-  int64_t stacked = 1;   // 2 (kDeep only): output rows are the sums of the first and the second half of a's
-};
-
-inline int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // One product and, when split, its join.  part: room for the splits' sums.
 hipError_t gated_product_bf16(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, int cus,

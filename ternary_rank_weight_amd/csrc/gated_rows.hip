@@ -20,16 +20,6 @@ namespace externd {
 
 namespace {
 
-// Most tokens of this form.  Past 16 tokens a workgroup reads two tiles of x for its one
-// tile of each weight matrix, and time grows with what it reads, the columns times the
-// tiles that one CU takes in turn.  Aligned operands (a product that needs no copies) go
-// to the tiled product where that is long: 32 tokens here against 33 there, in us,
-//   9728 x 9728: 121, 86   300 x 9728: 36, 19   9728 x 2560: 35, 30   4096 x 4096: 19, 20
-//   9728 x 1024: 14, 13    1024 x 2560: 13, 17  4096 x 2048: 11, 16
-// Rows that are not aligned, 32 tokens at 9728 x 2559: 53 here, 58 there.
-constexpr int kRowsMostTokens = 32, kRowsShortTokens = 16;
-constexpr int64_t kRowsMostColumns = 5000;
-
 struct RowsArgs {
   const uint16_t *x, *w[2];
   int64_t tokens, cols, rows, ldx, ldw;
@@ -205,11 +195,6 @@ hipError_t any(const RowsArgs& q, bool aligned, hipStream_t s) {
 }
 
 }  // namespace
-
-bool gated_takes_rows(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus) {
-  if (tokens <= kRowsShortTokens || tokens > kRowsMostTokens) return tokens <= kRowsShortTokens;
-  return !aligned || cols * std::max<int64_t>((rows + 15) / 16, cus) <= kRowsMostColumns * cus;
-}
 
 hipError_t run_gated_rows(const GatedArgs& a, hipStream_t s) {
   RowsArgs q;

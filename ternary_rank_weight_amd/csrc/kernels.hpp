@@ -180,7 +180,6 @@ hipError_t run_gated_forward(const GatedArgs& a, void* ws, hipStream_t s);
 size_t gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus);
 hipError_t run_gated_backward(const GatedArgs& a, void* ws, hipStream_t s);
 // the forward pass of a few tokens, without workspace (gated_rows.hip)
-bool gated_takes_rows(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus);
 hipError_t run_gated_rows(const GatedArgs& a, hipStream_t s);
 
 }  // namespace externd

@@ -12,42 +12,10 @@ import numpy as np
 import pytest
 import torch
 
+from gated_reference import TINY, U, inputs, references
 from oracle import gated as og
 
 pytestmark = pytest.mark.gpu
-
-U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
-TINY = {torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -25}
-E = 2.0 ** -24
-
-
-def _inputs(tokens, cols, rows, dtype, seed):
-    rng = np.random.default_rng(seed)
-    t = lambda a: torch.from_numpy(a.astype(np.float32)).to(dtype).cuda()
-    scale = 1.0 / np.sqrt(cols)
-    return (t(rng.standard_normal((tokens, cols))), t(scale * 1.5 * rng.standard_normal((rows, cols))),
-            t(scale * rng.standard_normal((rows, cols))), t(rng.standard_normal((tokens, rows))))
-
-
-def _references(x, wg, wu, dh, act, step=None):
-    """[(name, fp64 gradient, tolerance before the output's rounding)].  step: the smallest difference of
-    two dg or du that the parts hold (the subnormal step of dh's type by default)."""
-    dtype, cols, tokens, rows = x.dtype, x.shape[1], x.shape[0], wg.shape[0]
-    X, G, U_, D = (t.double() for t in (x, wg, wu, dh))
-    gv, uv = X @ G.t(), X @ U_.t()
-    a, slope = (torch.from_numpy(t).cuda() for t in og.act(act, gv.cpu().numpy()))
-    eg, eu = (cols + 64) * E * (X.abs() @ G.abs().t()), (cols + 64) * E * (X.abs() @ U_.abs().t())
-    ea, es = 1.13 * eg + 16 * E * gv.abs(), 0.9 * eg + 32 * E * (1 + gv.abs())
-    un = U[dtype] * 1.02
-    dg, du = D * uv * slope, D * a
-    if step is None:
-        step = TINY[dtype]
-    edg = D.abs() * ((uv.abs() + eu) * es + eu * slope.abs()) + un ** 2 * dg.abs() + step
-    edu = D.abs() * ea + un ** 2 * du.abs() + step
-    mg, mu = dg.abs() + edg, du.abs() + edu
-    return [("dx", dg @ G + du @ U_, edg @ G.abs() + edu @ U_.abs() + (4 * rows + 128) * E * (mg @ G.abs() + mu @ U_.abs())),
-            ("dWg", dg.t() @ X, edg.t() @ X.abs() + (2 * tokens + 64) * E * (mg.t() @ X.abs())),
-            ("dWu", du.t() @ X, edu.t() @ X.abs() + (2 * tokens + 64) * E * (mu.t() @ X.abs()))]
 
 
 def _gradients(lib, x, wg, wu, dh, act):
@@ -61,10 +29,10 @@ def _gradients(lib, x, wg, wu, dh, act):
     (96, 264, 100), (128, 256, 512), (129, 333, 129), (300, 520, 1032), (777, 141, 201), (1024, 512, 384), (5, 33000, 72)])
 def test_each_gradient_is_rounded_once(lib, dtype, tokens, cols, rows):
     act = ("silu", "gelu", "gelu_tanh")[(tokens + cols) % 3]
-    x, wg, wu, dh = _inputs(tokens, cols, rows, dtype, tokens + cols)
+    x, wg, wu, dh = inputs(tokens, cols, rows, dtype, tokens + cols)
     got = _gradients(lib, x, wg, wu, dh, act)
     un, tiny = U[dtype] * 1.02, TINY[dtype]
-    for have, (name, want, tol) in zip(got, _references(x, wg, wu, dh, act)):
+    for have, (name, want, tol) in zip(got, references(x, wg, wu, dh, act)):
         err = (have.double() - want).abs() / (tol + un * want.abs() + tiny)
         assert bool((err <= 1).all()), (name, float(err.max()))
 
@@ -73,9 +41,9 @@ def test_each_gradient_is_rounded_once(lib, dtype, tokens, cols, rows):
 @pytest.mark.parametrize("tokens", [1, 3, 40, 200, 800])
 def test_error_is_that_of_rounded_gradients(lib, dtype, tokens):
     # over a whole gradient the error is what rounding its exact value leaves, to a tenth
-    x, wg, wu, dh = _inputs(tokens, 256, 320, dtype, tokens)
+    x, wg, wu, dh = inputs(tokens, 256, 320, dtype, tokens)
     got = _gradients(lib, x, wg, wu, dh, "silu")
-    for have, (name, want, _) in zip(got, _references(x, wg, wu, dh, "silu")):
+    for have, (name, want, _) in zip(got, references(x, wg, wu, dh, "silu")):
         rounded = float((want.to(dtype).double() - want).norm())
         assert float((have.double() - want).norm()) <= 1.1 * rounded, name
 
@@ -96,7 +64,7 @@ def _check_fp16_range(lib, ops, names, large):
     assert (top > 2e5) if large else (top < 1e-4)
     got = _gradients(lib, x, wg, wu, dh, "silu")
     # the smaller part holds steps of 2^-24 where the largest value is brought to 2^14 or more
-    refs = _references(x, wg, wu, dh, "silu", step=2.0 ** -39 * top)
+    refs = references(x, wg, wu, dh, "silu", step=2.0 ** -39 * top)
     for have, (name, want, tol) in zip(got, refs):
         if name not in names:
             continue
@@ -141,7 +109,7 @@ def test_fp16_large_token_or_unit_leaves_the_others_bits(lib, tokens):
 @pytest.mark.parametrize("tokens", [5, 100])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_bad_token_stays_in_its_row_of_dx(lib, dtype, tokens):
-    x, wg, wu, dh = _inputs(tokens, 72, 136, dtype, 6)
+    x, wg, wu, dh = inputs(tokens, 72, 136, dtype, 6)
     _, g, u = lib.gated_forward(x, wg, wu, save=True)
     dx = lib.gated_backward(x, wg, wu, g, u, dh)[0]
     bad = dh.clone()
