@@ -148,7 +148,8 @@ __global__ __launch_bounds__(256) void k_gated_tops(SlopeArgs a, int64_t ldd, in
 // dg and du in rows of ldd entries (a multiple of 8; zero past the hidden width), each
 // in two parts of the operands' type: the rounded value, and `rest` entries further on
 // what the rounding took away.  Bound by HBM: reads 4 + 4 + 2 bytes, writes
-// 4 + 4 per hidden unit and token; 56 us for 2048 x 9728 (358 MB).  fp16: scaled by the power of two that
+// 4 + 4 per hidden unit and token; 62 us for 2048 x 9728 (5.8 TB/s: part of what
+// it writes stays in the last-level cache).  fp16: scaled by the power of two that
 // k_gated_tops' bits give for the token, or for the hidden unit of dg and of du (the other null).
 template <bool BF>
 __global__ __launch_bounds__(256) void k_gated_slopes(SlopeArgs a, int64_t ldd, int act, int64_t rest,

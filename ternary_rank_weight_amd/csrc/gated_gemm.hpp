@@ -101,8 +101,9 @@ __device__ __forceinline__ void for_constants(F&& f) {
 // PFLOP/s (a large library product without the activation: 1.43).  K = 2560, F = 9728,
 // bf16: forward of 4096 tokens 330 us (1.24 PFLOP/s; the same two products by the
 // library, without activation and product: 428 us); of 2048 tokens with g and u
-// kept 230 us; dx 174 us and its join 17; dW 180 us (1.13 PFLOP/s).  What is lost is the
-// end of a tile (6 of 62 us a tile of 40 steps) and the last round of tiles.
+// kept 234 us; dx, both parts of dg and du, 337 us and its join 16; dW, both parts, 333 us
+// (1.23 PFLOP/s).  What is lost is the end of a tile (6 of 62 us a tile of 40 steps) and
+// the last round of tiles.
 template <bool BF, int MODE, int BM, int BN, int WM, int WN, int NA, int NB, bool SPLIT>
 __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void k_gated_gemm(GatedGemm g) {
   constexpr int NTHR = WM * WN * kWave;
@@ -541,7 +542,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
 // What the split contractions left: the splits' sums in their order, then the
 // outputs as the unsplit kernel makes them.  part: (split, outs, count) fp32, rows of ldo;
 // tops: as in GatedGemm.
-// Forward: both projections, the activation and the product.  Bound by HBM: 17 us for
+// Forward: both projections, the activation and the product.  Bound by HBM: 16 us for
 // three splits of 2048 x 2560 (4.3 TB/s).
 template <bool BF, int MODE>
 __global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ part, int64_t count, int64_t splits,

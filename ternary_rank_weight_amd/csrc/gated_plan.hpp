@@ -45,7 +45,8 @@ inline bool gated_takes_rows(int64_t tokens, int64_t cols, int64_t rows, bool al
 //   pair  128 x 128 tiles, two a CU: 0.95 us a step and 4 a tile each;
 //   deep  128 x 128 tiles, one a CU with loads three steps ahead, where there are
 //         no more units than CUs: 0.45 us a step and 8 in all.
-// A split costs its sums' way to memory and back.
+// A split costs its sums' way to memory and back.  (Low by a quarter for few steps on
+// ragged rows: 777 tokens at 1001 x 1237, 17, 27 and 19 us against 24, 33 and 26 measured.)
 inline int64_t tiles_of(int mode, int64_t m, int64_t n, bool big) {
   const int64_t b = big ? 256 : 128;
   return (mode == kDw ? 2 : 1) * ceil_div64(m, b) * ceil_div64(n, mode == kFwd ? b / 2 : b);

@@ -1,7 +1,9 @@
 // The gated block's forward pass for a few tokens (up to 32):
 // h = act(x Wg^T) (x Wu^T) with every weight read once from memory, which is
 // what bounds it: 2 F K 16-bit weights against one product each per token.
-// F = 9728, K = 2560, one token: 20 us, 5.0 TB/s (a large copy: 5.16); K = 2559: 24.
+// F = 9728, K = 2560, one token: 22 us where the weights come from memory, 4.5 TB/s (reading
+// 1 GiB: 5.3), 20 where one layer's 100 MB stay in the last-level cache; K = 2559: 27 and 22.
+// (Nontemporal loads: 27 and 26; 36 and 34: a line is taken by two of them.)
 //
 // A workgroup takes 16 hidden units (neighbours, where rows are aligned).  Its waves
 // take every WV-th stretch of 64 columns; a lane reads 16 bytes of its row (lane % 16) of each matrix per 32
@@ -171,7 +173,10 @@ template <bool BF, int NT, bool AL, int NX>
 hipError_t launch(const RowsArgs& q, hipStream_t s) {
   const int64_t group = (int64_t)16 << q.apart_bits, tiles = ((q.rows + group - 1) / group) << q.apart_bits;
   // few row tiles: twice the waves on each, to have the whole matrix on its way at once
-  // (not where a wave needs more than the 128 registers that sixteen waves leave it)
+  // (not where a wave needs more than the 128 registers that sixteen waves leave it).  Weights
+  // from memory, one token, in us with 8 and 16 waves: 1024 x 2560 (64 tiles) 8.7, 8.0;
+  // 4096 x 4096 (256) 15.5, 14.5; 6144 x 2560 (384) 16.0, 16.8; 8000 x 2560 (500) 17.9, 17.9;
+  // 9728 x 2560 (608) 23.2, 24.0; 16384 x 2560 (1024) 32.6, 33.8.
   constexpr int most = NX == 2 && NT == 2 ? 8 : 16;
   if (tiles < 512) {
     hipLaunchKernelGGL((k_gated_rows<BF, NT, most, AL, NX>), dim3((unsigned)tiles), dim3(most * kWave), 0, s, q);

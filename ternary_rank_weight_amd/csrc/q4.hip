@@ -72,7 +72,7 @@ __device__ inline float min_of(float a, float b) { return __builtin_amdgcn_fmed3
 // rounded, q = w y, and q + (w - q s) y by two fused operations is the correctly
 // rounded w / s (Markstein's theorem).  Scales so small that y may not be a
 // normal number are divided by.  9728 x 2559 in bf16 (odd rows, read by shifted
-// dwords): 21 us, 3.0 TB/s; 1024 x 2560 in fp32: 6 us, mostly latency.
+// dwords): 21 us, 3.0 TB/s; 1024 x 2560 in fp32: 6.5 us, mostly latency.
 template <int DT, int GPC, bool MINS>
 __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ W, int64_t rows, int64_t cols,
                                                       int64_t ldw, int64_t chunks, int64_t jobs,
@@ -154,7 +154,8 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const void* __restrict__ W,
   }
 }
 
-// One pass when weights are loaded, bound by HBM (1.6 bytes an entry), not tuned.
+// One pass when weights are loaded, not tuned: 56 us for 9728 x 2560, 0.7 TB/s (1.6 bytes an
+// entry), bound by its byte loads.
 // Codes one byte each and tables row by row (rows x ceil(cols / group)) into
 // the layout; padding gets code 0, scale 0, minimum 0.
 __global__ __launch_bounds__(256) void k_q4_pack(const uint8_t* __restrict__ src, const uint16_t* __restrict__ ssrc,
@@ -194,7 +195,7 @@ __device__ inline float add_to_odd(float p, float m) {
 }
 
 // The values, rounded once to the output's type.  Bound by HBM: the write.  9728 x
-// 2559 to fp32: 25 us, 4.5 TB/s.
+// 2559 to fp32: 26 us, 4.4 TB/s.
 template <int DT>
 __global__ __launch_bounds__(256) void k_q4_reconstruct(const u32x4* __restrict__ codes,
                                                          const uint16_t* __restrict__ scales,
@@ -299,8 +300,13 @@ dim3 jobs_grid(int64_t jobs) { return dim3((unsigned)std::min<int64_t>((jobs + 3
 
 // Staged: fp32 of more than five tokens, rows that are not all 16-byte aligned, and large matrices with
 // more than one slot tile, where the waves' reads of x outweigh the weights and
-// 64-byte pieces of rows come at half the rate of whole kilobytes (32000 x 8192 with
-// 48 tokens: 66 us unstaged, 58 + 5 staged when this was chosen).
+// 64-byte pieces of rows come at half the rate of whole kilobytes.  In us, bf16, read in
+// place and staged (the copy's launch with it):
+//                          17 tokens     32 tokens     48 tokens     64 tokens
+//   2560 x 2560 (2^22.6)    9.1 11.4     10.0 11.6     14.6 13.4     17.8 14.6
+//   4096 x 4096 (2^24)     14.1 17.0     15.5 17.1     20.8 18.3     24.9 19.7
+//   9728 x 2560 (2^24.6)   14.5 16.1     17.1 16.2     16.5 14.9     20.3 16.9
+//   32000 x 8192 (2^28)    68.7 66.2     79.3 66.3     74.7 61.0    125.5 88.6
 bool q4_stages_x(int64_t rows, int64_t cols, int64_t tokens, int64_t ldx, int dtype, const void* x) {
   if (dtype == EXTERND_F32) return tokens > 5;   // five tokens fill a slot tile, which splits them itself
   return cols % 8 != 0 || ldx % 8 != 0 || (reinterpret_cast<uintptr_t>(x) & 15) != 0 ||

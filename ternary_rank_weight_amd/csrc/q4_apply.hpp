@@ -22,12 +22,16 @@ namespace {
 // with the constant -24 (or -16), made once for all row tiles.  With minima that product, scaled by -m / 16, is also the
 // m sum(x) term.  Sums are fp32 throughout.
 //
-// Bound by the weights' way from memory for a few tokens: 2560 x 9728 with minima,
-// one token, 8 us (2.0 TB/s: 160 workgroups' latency, not bandwidth); gate and up of
-// 9728 x 2560, 8 us (3.4 TB/s).  With 48 tokens on 32000 x 8192, 48 us (2.9 TB/s, 0.52
-// PFLOP/s): the matrix instructions take 14, unpacking 15, x from L2 15 and the
-// weights 27 us, and the two waves per SIMD that the accumulators leave room for
-// overlap them only in part.
+// Bound by the weights' latency for a few tokens: 2560 x 9728 with minima, one token, 9.9 us
+// where they come from memory (1.6 TB/s of 160 workgroups; reading 1 GiB: 5.3) and 8.1 where
+// three layers of them stay in the last-level cache; gate and up of 9728 x 2560, 10.0 us
+// (2.8 TB/s) and 8.6.  (The loads keep what they read in that cache; with nontemporal ones, in a
+// graph: 9.2 against 9.6 and 9.5 against 9.9 us from memory, 8.8 against 7.7 and 9.0 against 8.2 from the
+// cache.)  With 48 tokens on 32000 x 8192, 50 us (2.8 TB/s, 0.50 PFLOP/s): the matrix instructions take
+// 14, unpacking 15, x from L2 15 and the weights 27 us, and the two waves per SIMD that the
+// accumulators leave room for overlap them only in part.  Past 64 tokens every four slot
+// tiles (fp32: 20 tokens) read and unpack the weights again: 512 tokens on 9728 x 2560,
+// 86 us in bf16 (0.30 PFLOP/s), 267 in fp32.
 template <bool BF, int GPC, bool MINS, int MATS, int RT, int NT, int WV, int SL, bool X32>
 __global__ __launch_bounds__(WV * kWave) void k_q4_apply(Q4Args a, int out_type) {
   constexpr int F = MATS * RT;      // row tiles held by a wave, of all matrices
@@ -284,7 +288,15 @@ hipError_t one_tile(const Q4Args& a, int out_type, hipStream_t s) {
 // Row tiles per wave and waves per workgroup: with one slot tile the weights'
 // way from memory counts, and few row tiles get sixteen waves so that a whole
 // matrix is on its way at once; with more, x is read again for every row tile that
-// a wave does not hold.
+// a wave does not hold.  In us, weights from memory, one token with 8 and 16 waves:
+// 2560 x 9728 (160 row tiles) 10.3, 8.0; 4096 x 4096 (256) 6.2, 5.3; 8000 x 2560 (500) 5.9,
+// 5.8; 9728 x 2560 (608) 7.4, 7.7; two matrices of that 8.9, 12.6 (of 2560 x 9728 11.8, 11.3).
+// Row tiles a wave, 1, 2 and 4 (64 tokens: 3), bf16, group 32:
+//                  32 tokens         48 tokens          64 tokens
+//   32000 x 8192   79.8 66.3 50.0    103.4 89.5 61.1    155.8 90.8 87.8
+//   9728 x 2560    17.2 16.2 12.8    19.4 21.5 15.0     28.9 22.0 16.8
+//   4096 x 4096    11.1 17.1 14.8    13.1 15.4 18.2     21.8 16.0 19.5
+// (matrices of few row tiles would rather have one a wave).
 template <bool BF, int GPC, bool MINS>
 hipError_t pick_apply(const Q4Args& a, int mats, int out_type, hipStream_t s) {
   const int64_t slot_tiles = a.pieces == 3 ? (a.tokens + 4) / 5 : (a.tokens + 15) / 16;
