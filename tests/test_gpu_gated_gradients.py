@@ -119,3 +119,25 @@ def test_bad_token_stays_in_its_row_of_dx(lib, dtype, tokens):
     assert torch.equal(got[keep], dx[keep])
     assert bool(torch.isnan(got[2]).all()) and not bool(torch.isfinite(got[4]).any())
     assert bool(torch.isnan(dwg[9]).all()) and bool(torch.isfinite(dwg[[f for f in range(136) if f not in (0, 9)]]).all())
+
+
+@pytest.mark.parametrize("tokens,cols,rows", [(2, 136, 72), (70, 136, 72), (150, 203, 65)])
+def test_fp16_scales_in_a_used_workspace_and_in_a_graph(lib, tokens, cols, rows):
+    # the largest magnitudes of the call before, in the workspace, do not reach the next
+    x, wg, wu, dh = inputs(tokens, cols, rows, torch.float16, 3)
+    _, g, u = lib.gated_forward(x, wg, wu, save=True)
+    want = lib.gated_backward(x, wg, wu, g, u, dh)
+    need = lib.gated_backward_workspace_bytes(tokens, cols, rows, cols % 8 == 0)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    lib.gated_backward(x, wg, wu, g, u, dh * 1000, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(lib.gated_backward(x, wg, wu, g, u, dh, workspace=ws), want))
+    static = dh.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = lib.gated_backward(x, wg, wu, g, u, static, workspace=ws)
+    for k in (1000, 0.01, 1, 30):
+        static.copy_(dh * k)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, lib.gated_backward(x, wg, wu, g, u, dh * k)))
