@@ -475,6 +475,54 @@ int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t 
                            size_t workspace_bytes);
 size_t externd_gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t aligned);
 
+/* ---- AdamW step over many tensors ----
+ *
+ * Per entry, steps in fp32:
+ *   g1 = g grad_scale, m1 = beta1 m + (1 - beta1) g1, v1 = beta2 v + (1 - beta2) (g1 g1),
+ *   w1 = (1 - lr decay) w - lr / (1 - beta1^t) * m1 / (sqrt(v1) / sqrt(1 - beta2^t) + eps)
+ * with t the number of this step.  w is the tensor's master weight where it has one, and
+ * the parameter becomes its rounding; else the parameter.
+ *
+ * Moments are kept for whole blocks of EXTERND_ADAMW_BLOCK entries (as is the master weight),
+ * 0 past the tensor's end.  bits = 32: fp32.  bits = 8: a byte per entry, and a byte b per
+ * block, max(15, the exponent field of the largest finite fp32 magnitude in it):
+ *   m: the OCP e4m3 number nearest to m 2^(134 - b); 0x7f or 0xff, a NaN, where m is not finite;
+ *   v: the number nearest to v 2^(141 - b) with five bits of exponent (bias 15, subnormals)
+ *      and three of mantissa, no sign; 1 rather than 0 where v > 0; 0xf8 for infinity and 0xff for a NaN.
+ * Ties go to the even code.  All codes 0 and b = 15 are zeros. */
+#define EXTERND_ADAMW_BLOCK 256
+
+typedef struct externd_adamw_tensor {
+  void* param;             /* device, n entries of param_dtype */
+  const void* grad;        /* device, n entries of grad_dtype */
+  float* master;           /* device, 16-byte aligned, or NULL; not for fp32 parameters */
+  void *m, *v;             /* device: fp32 and 16-byte aligned, or codes, 4-byte aligned */
+  uint8_t *m_exp, *v_exp;  /* device, a byte per block; NULL with bits = 32 */
+  int64_t n;               /* 0: left out */
+  float decay;             /* weight decay */
+  int32_t param_dtype, grad_dtype;   /* externd_dtype */
+  int32_t reserved;
+} externd_adamw_tensor;
+
+typedef struct externd_adamw_opts {
+  double lr, beta1, beta2, eps;     /* betas in 0 <= beta < 1, eps >= 0 */
+  const float* lr_device;           /* device, read by the kernel instead of lr; or NULL */
+  const float* grad_scale_device;   /* device, read instead of grad_scale; or NULL */
+  float grad_scale;
+  int32_t bits;                     /* 8 or 32 */
+  double* step;                     /* device, four: steps taken, beta1 and beta2 to that power, 0 (the
+                                       kernel's own).  0, 1, 1, 0 before the first step. */
+} externd_adamw_opts;
+
+/* One step of `count` tensors (a HOST array); the step is counted on the device, so that a
+ * captured call counts in each replay.  What is written must have no byte in common with
+ * anything else that the call reads or writes.  Calls that overlap on one state race. */
+int externd_adamw_step(const externd_adamw_tensor* tensors, int64_t count, const externd_adamw_opts* opts, void* stream);
+
+/* The fp32 values of 8-bit moments of `blocks` blocks. */
+int externd_adamw_moments(const uint8_t* m, const uint8_t* m_exp, const uint8_t* v, const uint8_t* v_exp, int64_t blocks,
+                          void* stream, float* m_out, float* v_out);
+
 /* Status text and the last error message of the calling thread. */
 const char* externd_status_string(int status);
 const char* externd_last_error(void);

@@ -20,6 +20,7 @@ __all__ = [
     "ternarize", "gemv_t", "gemv_n", "deflate", "Decomposition", "ExterndError",
     "Q4", "q4_quantize", "q4_pack", "q4_reconstruct", "q4_apply", "q4_gated", "q4_workspace_bytes",
     "gated", "gated_forward", "gated_backward", "gated_forward_workspace_bytes", "gated_backward_workspace_bytes",
+    "AdamW",
     "STAT", "MODE_AUTO", "MODE_STREAMING", "MODE_RESIDENT", "MODE_PERSISTENT", "library_path",
 ]
 
@@ -67,6 +68,16 @@ class _Opts(ctypes.Structure):
         ("importance", _p), ("importance_lambda", ctypes.c_float), ("safeguard", _i32),
         ("block_capture", ctypes.POINTER(_BlockCapture)),
     ]
+
+
+class _AdamTensor(ctypes.Structure):
+    _fields_ = [("param", _p), ("grad", _p), ("master", _p), ("m", _p), ("v", _p), ("m_exp", _p), ("v_exp", _p),
+                ("n", _i64), ("decay", ctypes.c_float), ("param_dtype", _i32), ("grad_dtype", _i32), ("reserved", _i32)]
+
+
+class _AdamOpts(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("lr_device", _p), ("grad_scale_device", _p), ("grad_scale", ctypes.c_float), ("bits", _i32), ("step", _p)]
 
 
 class _Q4(ctypes.Structure):
@@ -120,6 +131,8 @@ _gated_backward = _sig("externd_gated_backward", ctypes.c_int,
                        [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _p, _i64, _i32, _i32, _p, _p, _p, _p, _p,
                         _size])
 _gated_backward_ws = _sig("externd_gated_backward_workspace_bytes", _size, [_i64, _i64, _i64, _i32])
+_adamw_step = _sig("externd_adamw_step", ctypes.c_int, [ctypes.POINTER(_AdamTensor), _i64, ctypes.POINTER(_AdamOpts), _p])
+_adamw_moments = _sig("externd_adamw_moments", ctypes.c_int, [_p, _p, _p, _p, _i64, _p, _p, _p])
 _status_string = _sig("externd_status_string", ctypes.c_char_p, [ctypes.c_int])
 _last_error = _sig("externd_last_error", ctypes.c_char_p, [])
 
@@ -134,6 +147,7 @@ ABI_SYMBOLS = ("externd_decompose", "externd_decompose_noalloc", "externd_energy
                "externd_q4_reconstruct", "externd_q4_apply", "externd_q4_gated", "externd_q4_workspace_bytes",
                "externd_gated_forward", "externd_gated_forward_workspace_bytes",
                "externd_gated_backward", "externd_gated_backward_workspace_bytes",
+               "externd_adamw_step", "externd_adamw_moments",
                "externd_status_string", "externd_last_error")
 
 
@@ -859,3 +873,151 @@ def gated(x, Wg, Wu, act="silu"):
     if not (torch.is_grad_enabled() and (x.requires_grad or Wg.requires_grad or Wu.requires_grad)):
         return gated_forward(x, Wg, Wu, act)
     return _Gated.apply(x, Wg, Wu, act)
+
+
+# ---- the step that applies gradients ----
+
+ADAMW_BLOCK = 256
+
+
+def _one_float(value, name, device):
+    """(value, None), or (0, address) of a one-element float32 tensor that the kernel reads."""
+    if not isinstance(value, torch.Tensor):
+        return float(value), None
+    _need(value, torch.float32, name)
+    if value.numel() != 1 or value.device != device:
+        raise ValueError(f"{name} must be a number or a float32 tensor of one element on {device}")
+    return 0.0, value.data_ptr()
+
+
+class AdamW:
+    """AdamW over a list of tensors, each step one launch per 48 of them.
+
+    params: contiguous float32, bfloat16 or float16 tensors on one device, updated in place.  bits: 32, or 8 for
+    moments of a byte per entry and a byte per 256 (include/externd.h has the formulas and the codes).  master:
+    float32 weights behind the 16-bit parameters, which become their rounding.  weight_decay: a number, or one per
+    tensor.  The step is counted on the device, so that a captured step counts in each replay of its graph.
+
+    state, as the property of that name returns it, takes the place of new zeros (its tensors are used, not
+    copied): "step" float64 (4,): steps taken, beta1 and beta2 to that power, 0; "m", "v" and "master" (or
+    None) have every tensor's entries filled up with zeros to a multiple of 256, one tensor after the other; m
+    and v are float32, or with bits = 8 uint8: the codes of all, then the blocks' exponent bytes.
+
+    Calls of one object belong on one stream, or in an order."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, master=False, state=None):
+        self._params = list(params)
+        if not self._params:
+            raise ValueError("params must hold at least one tensor")
+        if bits not in (8, 32):
+            raise ValueError("bits must be 8 or 32")
+        for p in self._params:
+            if not isinstance(p, torch.Tensor):
+                raise TypeError("params must be tensors")
+            _need(p, p.dtype if p.dtype in _DTYPE else torch.float32, "a parameter")
+        index = _op_device(*self._params)
+        device = self._params[0].device
+        decay = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * len(self._params)
+        if len(decay) != len(self._params):
+            raise ValueError("weight_decay must be a number or one per tensor")
+        self.lr = lr
+        self._bits, self._index, self._device = bits, index, device
+        sizes = [-(-p.numel() // ADAMW_BLOCK) * ADAMW_BLOCK for p in self._params]
+        self._starts = [0]
+        for n in sizes:
+            self._starts.append(self._starts[-1] + n)
+        total = self._starts[-1]
+        length = total if bits == 32 else total + total // ADAMW_BLOCK
+        dtype = torch.float32 if bits == 32 else torch.uint8
+        if state is None:
+            self._step = torch.tensor([0.0, 1.0, 1.0, 0.0], dtype=torch.float64, device=device)
+            self._m, self._v = (torch.zeros(length, dtype=dtype, device=device) for _ in range(2))
+            if bits == 8:
+                self._m[total:] = self._v[total:] = 15
+            self._master = None
+            if master:
+                self._master = torch.zeros(total, dtype=torch.float32, device=device)
+                for p, at in zip(self._params, self._starts):
+                    self._master[at:at + p.numel()] = p.detach().reshape(-1)
+        else:
+            self._step, self._m, self._v, self._master = (state[k] for k in ("step", "m", "v", "master"))
+            wanted = [(self._step, "step", torch.float64, 4), (self._m, "m", dtype, length), (self._v, "v", dtype, length)]
+            if (self._master is None) == bool(master):
+                raise ValueError("the state has master weights, or has none, unlike this optimizer")
+            if master:
+                wanted.append((self._master, "master", torch.float32, total))
+            for t, name, kind, count in wanted:
+                _need(t, kind, name)
+                if t.numel() != count or t.device != device:
+                    raise ValueError(f"{name} must hold {count} entries on {device}")
+        step = 4 if bits == 32 else 1
+        self._table = (_AdamTensor * len(self._params))()
+        for t, p, at, d in zip(self._table, self._params, self._starts, decay):
+            t.param, t.n, t.decay, t.param_dtype = p.data_ptr(), p.numel(), d, _DTYPE[p.dtype]
+            t.m, t.v = self._m.data_ptr() + at * step, self._v.data_ptr() + at * step
+            if bits == 8:
+                t.m_exp, t.v_exp = (s.data_ptr() + total + at // ADAMW_BLOCK for s in (self._m, self._v))
+            if master and p.dtype != torch.float32:
+                t.master = self._master.data_ptr() + 4 * at
+        self._opts = _AdamOpts(0.0, betas[0], betas[1], eps, None, None, 1.0, bits, self._step.data_ptr())
+
+    @property
+    def state(self):
+        """The tensors that the next step starts from."""
+        return {"step": self._step, "m": self._m, "v": self._v, "master": self._master}
+
+    def step(self, grads=None, lr=None, grad_scale=1.0):
+        """Applies one gradient per tensor (by default their .grad; a tensor whose gradient is None stays as it is).
+        lr (by default the attribute lr) and grad_scale, which every gradient is multiplied by first, are numbers or
+        float32 tensors of one element on the device, which a captured step reads in each replay."""
+        params, table, opts = self._params, self._table, self._opts
+        if grads is None:
+            grads = [p.grad for p in params]
+        if len(grads) != len(params):
+            raise ValueError(f"{len(grads)} gradients for {len(params)} tensors")
+        if self._index != _current_device():
+            _op_device(*params)
+        keep, changed = [], []
+        for t, p, g in zip(table, params, grads):
+            if g is None:
+                t.n = 0
+                continue
+            if g.shape != p.shape or g.get_device() != self._index:
+                raise ValueError(f"a gradient must have its tensor's shape {tuple(p.shape)} and device")
+            code = _DTYPE.get(g.dtype)
+            if code is None:
+                _dtype_code(g.dtype, "a gradient")
+            if not g.is_contiguous():
+                g = g.contiguous()
+                keep.append(g)
+            if p.data_ptr() != t.param:
+                # (another storage of the same kind, as after p.data = ...)
+                _need(p, p.dtype, "a parameter")
+                if p.get_device() != self._index or _DTYPE.get(p.dtype) != t.param_dtype:
+                    raise ValueError("a parameter's type or device has changed")
+                t.param = p.data_ptr()
+            t.grad, t.grad_dtype, t.n = g.data_ptr(), code, p.numel()
+            changed.append(p)
+        opts.lr, opts.lr_device = _one_float(self.lr if lr is None else lr, "lr", self._device)
+        opts.grad_scale, opts.grad_scale_device = _one_float(grad_scale, "grad_scale", self._device)
+        _check(_adamw_step(table, len(params), opts, _raw_stream(self._index)))
+        for p in changed:   # so that autograd sees a saved parameter's change
+            if not p.is_inference():
+                torch.autograd.graph.increment_version(p)
+
+    def moments(self):
+        """(m, v) in float32, in the state's order; piece() takes a tensor's entries out of them."""
+        if self._bits == 32:
+            return self._m, self._v
+        total = self._starts[-1]
+        _op_device(self._m)
+        m, v = torch.empty((2, total), dtype=torch.float32, device=self._device)
+        at, bt = self._m.data_ptr(), self._v.data_ptr()
+        _check(_adamw_moments(at, at + total, bt, bt + total, total // ADAMW_BLOCK, _raw_stream(self._index), m.data_ptr(),
+                              v.data_ptr()))
+        return m, v
+
+    def piece(self, flat, i):
+        """Tensor i's entries of a flat tensor in the state's order (master, or one of moments()), in its shape."""
+        p = self._params[i]
+        return flat[self._starts[i]:self._starts[i] + p.numel()].view(p.shape)

@@ -11,8 +11,10 @@
 #include <initializer_list>
 #include <mutex>
 #include <string>
+#include <vector>
 
 #include "../../include/externd.h"
+#include "adamw.hpp"
 #include "kernels.hpp"
 
 namespace {
@@ -222,6 +224,66 @@ int check_gated(const externd::GatedArgs& a) {
     return fail(EXTERND_EINVAL, "bad number of tokens");
   if (bad_stride(a.ldx, a.cols) || bad_stride(a.ldw, a.cols))
     return fail(EXTERND_EINVAL, "ldx and ldw must be at least the columns");
+  return EXTERND_OK;
+}
+
+// Checks of an AdamW call; what is written has no byte in common with anything else.
+int check_adamw(const externd_adamw_tensor* tensors, int64_t count, const externd_adamw_opts& o) {
+  if (o.bits != 8 && o.bits != 32) return fail(EXTERND_EINVAL, "bits must be 8 or 32");
+  if (!(o.beta1 >= 0 && o.beta1 < 1) || !(o.beta2 >= 0 && o.beta2 < 1) || !(o.eps >= 0) || !std::isfinite(o.eps))
+    return fail(EXTERND_EINVAL, "betas must be in [0, 1) and eps finite and not negative");
+  if (!o.lr_device && !std::isfinite(o.lr)) return fail(EXTERND_EINVAL, "lr must be finite");
+  if (!o.step || !aligned_to(o.step, 8) || !aligned_to(o.lr_device, 4) || !aligned_to(o.grad_scale_device, 4))
+    return fail(EXTERND_EINVAL, "null or misaligned step, lr or grad_scale");
+  struct Span {
+    uintptr_t begin, end;
+    bool written;
+    int64_t tensor;   // -1: of the options
+  };
+  std::vector<Span> spans;
+  auto add = [&](const void* p, int64_t bytes, bool written, int64_t tensor) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (p && bytes > 0) spans.push_back({at, at + (uintptr_t)bytes, written, tensor});
+  };
+  add(o.step, 32, true, -1);
+  add(o.lr_device, 4, false, -1);
+  add(o.grad_scale_device, 4, false, -1);
+  for (int64_t i = 0; i < count; ++i) {
+    const externd_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.n > int64_t(1) << 40) return fail(EXTERND_EINVAL, "tensor %lld: bad size", (long long)i);
+    if (t.n == 0) continue;
+    if (bad_dtype(t.param_dtype) || bad_dtype(t.grad_dtype)) return fail(EXTERND_EINVAL, "tensor %lld: unknown dtype", (long long)i);
+    if (t.master && t.param_dtype == EXTERND_F32)
+      return fail(EXTERND_EINVAL, "tensor %lld: fp32 parameters have no master weights", (long long)i);
+    if (!std::isfinite(t.decay)) return fail(EXTERND_EINVAL, "tensor %lld: decay must be finite", (long long)i);
+    const bool eight = o.bits == 8;
+    if (!t.param || !t.grad || !t.m || !t.v || (eight && (!t.m_exp || !t.v_exp)))
+      return fail(EXTERND_EINVAL, "tensor %lld: null pointer", (long long)i);
+    if (!aligned_to(t.param, dtype_bytes(t.param_dtype)) || !aligned_to(t.grad, dtype_bytes(t.grad_dtype)) ||
+        !aligned_to(t.master, 16) || !aligned_to(t.m, eight ? 4 : 16) || !aligned_to(t.v, eight ? 4 : 16))
+      return fail(EXTERND_EINVAL, "tensor %lld: misaligned pointer", (long long)i);
+    const int64_t blocks = (t.n + EXTERND_ADAMW_BLOCK - 1) / EXTERND_ADAMW_BLOCK, full = blocks * EXTERND_ADAMW_BLOCK;
+    add(t.param, t.n * (int64_t)dtype_bytes(t.param_dtype), true, i);
+    add(t.grad, t.n * (int64_t)dtype_bytes(t.grad_dtype), false, i);
+    add(t.master, 4 * full, true, i);
+    add(t.m, (eight ? 1 : 4) * full, true, i);
+    add(t.v, (eight ? 1 : 4) * full, true, i);
+    if (eight) {
+      add(t.m_exp, blocks, true, i);
+      add(t.v_exp, blocks, true, i);
+    }
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  // the furthest ends so far of what is written and of all
+  const Span *written = nullptr, *any = nullptr;
+  for (const Span& s : spans) {
+    const Span* hit = s.written ? any : written;
+    if (hit && hit->end > s.begin)
+      return fail(EXTERND_EINVAL, "arrays of tensors %lld and %lld overlap (-1: of the options)", (long long)hit->tensor,
+                  (long long)s.tensor);
+    if (!any || s.end > any->end) any = &s;
+    if (s.written && (!written || s.end > written->end)) written = &s;
+  }
   return EXTERND_OK;
 }
 
@@ -791,6 +853,39 @@ int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t 
   if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
   hipError_t e = externd::run_gated_backward(a, ws.ptr, s);
   if (e != hipSuccess) return hip_fail(e, "gated backward");
+  return EXTERND_OK;
+}
+
+int externd_adamw_step(const externd_adamw_tensor* tensors, int64_t count, const externd_adamw_opts* opts, void* stream) {
+  if (!opts || count < 0 || (count > 0 && !tensors)) return fail(EXTERND_EINVAL, "null tensors or options");
+  try {
+    int st = check_adamw(tensors, count, *opts);
+    if (st != EXTERND_OK) return st;
+    int cus = 0;
+    if ((st = check_device(&cus)) != EXTERND_OK) return st;
+    hipError_t e = externd::run_adamw(tensors, count, *opts, cus, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "adamw step");
+    return EXTERND_OK;
+  } catch (...) {
+    return fail(EXTERND_ENOMEM, "out of host memory");
+  }
+}
+
+int externd_adamw_moments(const uint8_t* m, const uint8_t* m_exp, const uint8_t* v, const uint8_t* v_exp, int64_t blocks,
+                          void* stream, float* m_out, float* v_out) {
+  if (blocks < 0 || blocks > int64_t(1) << 32) return fail(EXTERND_EINVAL, "bad number of blocks");
+  if (blocks == 0) return EXTERND_OK;
+  if (!m || !m_exp || !v || !v_exp || !m_out || !v_out) return fail(EXTERND_EINVAL, "null pointer");
+  if (!aligned_to(m, 4) || !aligned_to(v, 4) || !aligned_to(m_out, 16) || !aligned_to(v_out, 16))
+    return fail(EXTERND_EINVAL, "codes must be 4-byte and outputs 16-byte aligned");
+  const int64_t n = blocks * EXTERND_ADAMW_BLOCK;
+  int st = check_apart({packed(m_out, 4 * n, "m_out"), packed(v_out, 4 * n, "v_out")},
+                       {packed(m, n, "m"), packed(v, n, "v"), packed(m_exp, blocks, "m_exp"), packed(v_exp, blocks, "v_exp")});
+  if (st != EXTERND_OK) return st;
+  int cus = 0;
+  if ((st = check_device(&cus)) != EXTERND_OK) return st;
+  hipError_t e = externd::run_adamw_moments(m, m_exp, v, v_exp, blocks, m_out, v_out, cus, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "adamw moments");
   return EXTERND_OK;
 }
 
