@@ -379,14 +379,15 @@ int externd_deflate(float* R, int64_t m, int64_t n, const uint32_t* u_codes,
  * Padding entries may hold any code; padding scales and minima must be
  * finite.  codes must be 16-byte aligned, scales and mins 8-byte.
  *
- * What these functions and those of the gated block below write, the workspace
+ * What these functions and those of the gated block and the linear layer below write, the workspace
  * included, must have no byte in common with what they read or write besides
  * (EXTERND_EINVAL); what they only read may overlap. */
 enum externd_dtype { EXTERND_F32 = 0, EXTERND_BF16 = 1, EXTERND_F16 = 2 };
 enum externd_activation {
   EXTERND_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
   EXTERND_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
-  EXTERND_ACT_GELU_TANH = 2  /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+  EXTERND_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+  EXTERND_ACT_NONE = 3       /* g; of the linear layer alone */
 };
 
 typedef struct externd_q4 {
@@ -474,6 +475,32 @@ int externd_gated_backward(const void* x, int64_t tokens, int64_t cols, int64_t 
                            int32_t dtype, int32_t act, void* stream, void* dx, void* dwg, void* dwu, void* workspace,
                            size_t workspace_bytes);
 size_t externd_gated_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t aligned);
+
+/* ---- linear layer, dense 16-bit weights ----
+ *
+ * z = x W^T + bias, y = act(z) + residual: x tokens x cols (rows ldx entries apart), W rows x cols
+ * (rows ldw entries apart), bias (rows entries) and residual (tokens x rows, rows ldr entries apart)
+ * NULL or of dtype, y tokens x rows, packed; dtype EXTERND_BF16 or EXTERND_F16.  Sums, the activation
+ * and the residual's sum are fp32, and y is rounded once.  z (or NULL): tokens x rows fp32, kept for the
+ * backward pass of an activation.  Limits, workspace and its `aligned` (of x and W) as for
+ * externd_gated_forward. */
+int externd_linear_forward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* w, int64_t rows,
+                           int64_t ldw, const void* bias, const void* residual, int64_t ldr, int32_t dtype, int32_t act,
+                           void* stream, void* y, float* z, void* workspace, size_t workspace_bytes);
+size_t externd_linear_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t aligned);
+
+/* Gradients of the layer from dy (tokens x rows, rows lddy entries apart) and, unless act is
+ * EXTERND_ACT_NONE, the z that the forward pass kept:
+ *   dz = dy act'(z)   (held in two parts of dtype, in fp16 scaled, as the gated block's dg; without an
+ *     activation dz is dy)
+ *   dx = dz W, dW = dz^T x, db = the sum of dz over the tokens   (fp32 sums, rounded once).
+ * Each of dx (tokens x cols), dw (rows x cols) and db (rows) may be NULL; they are packed.  The
+ * residual's gradient is dy.  With tokens = 0, dw and db are zero.  `aligned` says besides that dy starts on 16
+ * bytes and that lddy and rows are multiples of 8. */
+int externd_linear_backward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* w, int64_t rows,
+                            int64_t ldw, const float* z, const void* dy, int64_t lddy, int32_t dtype, int32_t act,
+                            void* stream, void* dx, void* dw, void* db, void* workspace, size_t workspace_bytes);
+size_t externd_linear_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t act, int32_t aligned);
 
 /* ---- AdamW step over many tensors ----
  *

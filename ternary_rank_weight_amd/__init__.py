@@ -20,6 +20,7 @@ __all__ = [
     "ternarize", "gemv_t", "gemv_n", "deflate", "Decomposition", "ExterndError",
     "Q4", "q4_quantize", "q4_pack", "q4_reconstruct", "q4_apply", "q4_gated", "q4_workspace_bytes",
     "gated", "gated_forward", "gated_backward", "gated_forward_workspace_bytes", "gated_backward_workspace_bytes",
+    "linear", "linear_forward", "linear_backward", "linear_forward_workspace_bytes", "linear_backward_workspace_bytes",
     "AdamW",
     "STAT", "MODE_AUTO", "MODE_STREAMING", "MODE_RESIDENT", "MODE_PERSISTENT", "library_path",
 ]
@@ -131,6 +132,12 @@ _gated_backward = _sig("externd_gated_backward", ctypes.c_int,
                        [_p, _i64, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _p, _i64, _i32, _i32, _p, _p, _p, _p, _p,
                         _size])
 _gated_backward_ws = _sig("externd_gated_backward_workspace_bytes", _size, [_i64, _i64, _i64, _i32])
+_linear_forward = _sig("externd_linear_forward", ctypes.c_int,
+                       [_p, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, _i32, _i32, _p, _p, _p, _p, _size])
+_linear_forward_ws = _sig("externd_linear_forward_workspace_bytes", _size, [_i64, _i64, _i64, _i32])
+_linear_backward = _sig("externd_linear_backward", ctypes.c_int,
+                        [_p, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, _i32, _i32, _p, _p, _p, _p, _p, _size])
+_linear_backward_ws = _sig("externd_linear_backward_workspace_bytes", _size, [_i64, _i64, _i64, _i32, _i32])
 _adamw_step = _sig("externd_adamw_step", ctypes.c_int, [ctypes.POINTER(_AdamTensor), _i64, ctypes.POINTER(_AdamOpts), _p])
 _adamw_moments = _sig("externd_adamw_moments", ctypes.c_int, [_p, _p, _p, _p, _i64, _p, _p, _p])
 _status_string = _sig("externd_status_string", ctypes.c_char_p, [ctypes.c_int])
@@ -147,6 +154,8 @@ ABI_SYMBOLS = ("externd_decompose", "externd_decompose_noalloc", "externd_energy
                "externd_q4_reconstruct", "externd_q4_apply", "externd_q4_gated", "externd_q4_workspace_bytes",
                "externd_gated_forward", "externd_gated_forward_workspace_bytes",
                "externd_gated_backward", "externd_gated_backward_workspace_bytes",
+               "externd_linear_forward", "externd_linear_forward_workspace_bytes",
+               "externd_linear_backward", "externd_linear_backward_workspace_bytes",
                "externd_adamw_step", "externd_adamw_moments",
                "externd_status_string", "externd_last_error")
 
@@ -873,6 +882,153 @@ def gated(x, Wg, Wu, act="silu"):
     if not (torch.is_grad_enabled() and (x.requires_grad or Wg.requires_grad or Wu.requires_grad)):
         return gated_forward(x, Wg, Wu, act)
     return _Gated.apply(x, Wg, Wu, act)
+
+
+# ---- linear layer ----
+
+_LINEAR_ACT = {None: 3, **_ACT}
+
+
+def _linear_act(act):
+    code = _LINEAR_ACT.get(act)
+    if code is None:
+        raise ValueError(f"act must be None or one of {', '.join(_ACT)}, got {act!r}")
+    return code
+
+
+def _linear_weights(x, W):
+    """Checks W against x; returns (W, its row stride, dtype code)."""
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"x must be bfloat16 or float16, got {x.dtype}")
+    if W.dtype != x.dtype:
+        raise TypeError(f"W must be {x.dtype} like x, got {W.dtype}")
+    if W.dim() != 2:
+        raise ValueError("W must be 2-D")
+    W, ldw = _rows_of(W, W.shape[1], "W")
+    return W, ldw, _DTYPE[x.dtype]
+
+
+def linear_forward_workspace_bytes(tokens, cols, rows, aligned=True):
+    """Device workspace linear_forward needs (may be 0).  aligned: x and W start on 16 bytes, and cols and
+    their row strides are multiples of 8; False covers any alignment.  Fewer tokens may need more."""
+    return int(_linear_forward_ws(tokens, cols, rows, aligned))
+
+
+def linear_backward_workspace_bytes(tokens, cols, rows, act=None, aligned=True):
+    """Device workspace linear_backward needs (may be 0); aligned as for linear_forward_workspace_bytes, of dy and
+    rows too."""
+    return int(_linear_backward_ws(tokens, cols, rows, _linear_act(act), aligned))
+
+
+def _linear_scratch(workspace, bytes_of, x, aligned):
+    """As _gated_scratch."""
+    if workspace is None:
+        need = bytes_of(aligned) if x.shape[0] else 0
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+    return (*_scratch(workspace, x.get_device()), workspace)
+
+
+def linear_forward(x, W, bias=None, act=None, residual=None, save=False, out=None, workspace=None):
+    """y = act(x W^T + bias) + residual in one kernel, rounded once.
+
+    x (..., cols), W (rows, cols), bias (rows,) and residual (..., rows) bfloat16 or float16, all alike; y
+    (..., rows) of their type.  act: None, "silu", "gelu" (erf) or "gelu_tanh".  With save, returns (y, z): z =
+    x W^T + bias (tokens, rows) in float32, which linear_backward takes, or None without an activation, whose
+    gradients need none.  Rows of x, W and residual may be strided.  linear() is the differentiable form: asking for a
+    gradient of this one raises an error (with save, its result carries none)."""
+    code = _linear_act(act)
+    given = [t for t in (x, W, bias, residual) if t is not None]
+    record = not save and any(t.requires_grad for t in given) and _records(out)
+    index = _op_device(*given)
+    wanted = x, W, bias, residual
+    W, ldw, dtype = _linear_weights(x, W)
+    rows, cols = W.shape
+    shape = (*x.shape[:-1], rows)
+    if bias is not None:
+        _need(bias, x.dtype, "bias")
+        if tuple(bias.shape) != (rows,):
+            raise ValueError(f"bias must have shape {(rows,)}")
+    ldr = rows
+    if residual is not None:
+        if residual.dtype != x.dtype or tuple(residual.shape) != shape:
+            raise ValueError(f"residual must be {x.dtype} of shape {shape}")
+        residual, ldr = _rows_of(residual, rows, "residual")
+    y = x.new_empty(shape) if out is None else _out_or_new(out, shape, x.dtype, x.device)
+    x, ldx = _rows_of(x, cols, "x")
+    tokens = x.shape[0]
+    z = torch.empty((tokens, rows), dtype=torch.float32, device=x.device) if save and act is not None else None
+    xp, wp = x.data_ptr(), W.data_ptr()
+    aligned = (xp | wp) & 15 == 0 and (ldx | ldw | cols) & 7 == 0 and max(ldx, ldw) < 1 << 22
+    ws, wsb, keep = _linear_scratch(workspace, lambda al: _linear_forward_ws(tokens, cols, rows, al), x, aligned)
+    status = _linear_forward(xp, tokens, cols, ldx, wp, rows, ldw, None if bias is None else bias.data_ptr(),
+                             None if residual is None else residual.data_ptr(), ldr, dtype, code, _raw_stream(index),
+                             y.data_ptr(), None if z is None else z.data_ptr(), ws, wsb)
+    if status:
+        _check(status)
+    if record:
+        return _NoGradient.apply("linear_forward has no gradient; linear has", y, *wanted)
+    return (y, z) if save else y
+
+
+def linear_backward(x, W, z, dy, act=None, need_dx=True, need_dw=True, need_db=True, workspace=None):
+    """(dx, dW, db) of the linear layer from dy (..., rows) and the z that linear_forward(..., save=True) returned (None
+    without an activation); None for what need_dx, need_dw and need_db leave out.  The residual's gradient is dy."""
+    code = _linear_act(act)
+    index = _op_device(*(t for t in (x, W, z, dy) if t is not None))
+    W, ldw, dtype = _linear_weights(x, W)
+    rows, cols = W.shape
+    shape = x.shape
+    x, ldx = _rows_of(x, cols, "x")
+    tokens = x.shape[0]
+    if dy.dtype != x.dtype:
+        raise TypeError(f"dy must be {x.dtype} like x, got {dy.dtype}")
+    if dy.shape[:-1] != shape[:-1]:
+        raise ValueError("dy and x must have the same leading dimensions")
+    dy, lddy = _rows_of(dy, rows, "dy")
+    if act is None:
+        z = None
+    else:
+        _need(z, torch.float32, "z")
+        if z.numel() != tokens * rows:
+            raise ValueError(f"z must have {tokens} x {rows} entries")
+    dx = torch.empty(shape, dtype=x.dtype, device=x.device) if need_dx else None
+    dw = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if need_dw else None
+    db = torch.empty((rows,), dtype=x.dtype, device=x.device) if need_db else None
+    aligned = (x.data_ptr() | W.data_ptr()) & 15 == 0 and (ldx | ldw | cols) & 7 == 0 and max(ldx, ldw) < 1 << 22 and \
+        (act is not None or dy.data_ptr() & 15 == 0 and (lddy | rows) & 7 == 0 and lddy < 1 << 22)
+    ws, wsb, keep = _linear_scratch(workspace, lambda al: _linear_backward_ws(tokens, cols, rows, code, al), x, aligned)
+    _check(_linear_backward(x.data_ptr(), tokens, cols, ldx, W.data_ptr(), rows, ldw, None if z is None else z.data_ptr(),
+                            dy.data_ptr(), lddy, dtype, code, _raw_stream(index), _ptr(dx), _ptr(dw), _ptr(db), ws, wsb))
+    return dx, dw, db
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, bias, act, residual):
+        ctx.act = act
+        y, z = linear_forward(x, W, bias, act, residual, save=True)
+        ctx.save_for_backward(x, W, z)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, W, z = ctx.saved_tensors
+        need_dx, need_dw, need_db, _, need_dr = ctx.needs_input_grad
+        dx = dw = db = None
+        if need_dx or need_dw or need_db:
+            dx, dw, db = linear_backward(x, W, z, dy, ctx.act, need_dx, need_dw, need_db)
+        return dx, dw, db, None, dy if need_dr else None
+
+
+def linear(x, W, bias=None, act=None, residual=None):
+    """linear_forward as a differentiable torch operation (gradients of x, W, bias and residual; z is kept in float32
+    only where a gradient of an activation is needed)."""
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, W, bias, residual))):
+        return linear_forward(x, W, bias, act, residual)
+    return _Linear.apply(x, W, bias, act, residual)
 
 
 # ---- the step that applies gradients ----

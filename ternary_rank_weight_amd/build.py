@@ -16,7 +16,8 @@ LIB = os.path.join(HERE, "libexternd.so")
 SOURCES = ["abi.cpp", "seq_stream.hip", "seq_resident.hip", "factors.hip", "block.hip", "apply.hip",
            "noalloc.hip", "seq_persist.hip", "apply_rows.hip", "q4.hip", "q4_apply_bf16.hip",
            "q4_apply_f16.hip", "gated.hip", "gated_gemm_bf16.hip", "gated_gemm_f16.hip",
-           "gated_rows.hip", "adamw.hip"]
+           "gated_rows.hip", "adamw.hip", "linear.hip", "linear_rows.hip",
+           "linear_gemm_bf16.hip", "linear_gemm_f16.hip"]
 ARCH = "gfx950"
 
 COMMON = [

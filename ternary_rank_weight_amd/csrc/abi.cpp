@@ -16,6 +16,7 @@
 #include "../../include/externd.h"
 #include "adamw.hpp"
 #include "kernels.hpp"
+#include "linear.hpp"
 
 namespace {
 
@@ -224,6 +225,24 @@ int check_gated(const externd::GatedArgs& a) {
     return fail(EXTERND_EINVAL, "bad number of tokens");
   if (bad_stride(a.ldx, a.cols) || bad_stride(a.ldw, a.cols))
     return fail(EXTERND_EINVAL, "ldx and ldw must be at least the columns");
+  return EXTERND_OK;
+}
+
+// Checks that both passes of the linear layer share.
+int check_linear(const externd::LinearArgs& a) {
+  if (bad_dtype(a.dtype)) return fail(EXTERND_EINVAL, "unknown dtype %d", a.dtype);
+  if (a.dtype == EXTERND_F32) return fail(EXTERND_EUNSUPPORTED, "the linear layer takes bf16 or fp16");
+  if (bad_act(a.act) && a.act != EXTERND_ACT_NONE) return fail(EXTERND_EINVAL, "unknown activation %d", a.act);
+  if (bad_size(a.rows, a.cols)) return fail(EXTERND_EINVAL, "bad weight shape");
+  if (a.rows > kMaxGated || a.cols > kMaxGated)   // a tile's offsets are 32 bits
+    return fail(EXTERND_EUNSUPPORTED, "the linear layer takes at most 2^21 rows and columns of the weights");
+  if (a.tokens < 0 || (a.tokens > 0 && (bad_size(a.tokens, a.cols) || bad_size(a.tokens, a.rows))))
+    return fail(EXTERND_EINVAL, "bad number of tokens");
+  if (bad_stride(a.ldx, a.cols) || bad_stride(a.ldw, a.cols))
+    return fail(EXTERND_EINVAL, "ldx and ldw must be at least the columns");
+  for (const void* p : {a.x, a.w, a.bias, a.residual, (const void*)a.y, a.dy, (const void*)a.dx, (const void*)a.dw, (const void*)a.db})
+    if (!aligned_to(p, 2)) return fail(EXTERND_EINVAL, "pointers must be aligned to their type");
+  if (!aligned_to(a.z, 4)) return fail(EXTERND_EINVAL, "z must be aligned to its type");
   return EXTERND_OK;
 }
 
@@ -886,6 +905,85 @@ int externd_adamw_moments(const uint8_t* m, const uint8_t* m_exp, const uint8_t*
   if ((st = check_device(&cus)) != EXTERND_OK) return st;
   hipError_t e = externd::run_adamw_moments(m, m_exp, v, v_exp, blocks, m_out, v_out, cus, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "adamw moments");
+  return EXTERND_OK;
+}
+
+size_t externd_linear_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t aligned) {
+  if (bad_size(rows, cols) || tokens < 1 || bad_size(tokens, cols) || bad_size(tokens, rows)) return 0;
+  int cus = 0;
+  if (check_device(&cus) != EXTERND_OK) return 0;
+  const size_t with = externd::linear_forward_workspace_bytes(tokens, cols, rows, true, cus);
+  return aligned ? with : std::max(with, externd::linear_forward_workspace_bytes(tokens, cols, rows, false, cus));
+}
+
+int externd_linear_forward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* w, int64_t rows,
+                           int64_t ldw, const void* bias, const void* residual, int64_t ldr, int32_t dtype, int32_t act,
+                           void* stream, void* y, float* z, void* workspace, size_t workspace_bytes) {
+  externd::LinearArgs a = {};
+  a.x = x; a.w = w; a.bias = bias; a.residual = residual;
+  a.tokens = tokens; a.cols = cols; a.rows = rows;
+  a.ldx = ldx; a.ldw = ldw; a.ldr = ldr;
+  a.dtype = dtype; a.act = act;
+  a.y = y; a.z = z;
+  int st = check_linear(a);
+  if (st != EXTERND_OK) return st;
+  if (residual && bad_stride(ldr, rows)) return fail(EXTERND_EINVAL, "ldr must be at least the rows of W");
+  if (tokens == 0) return EXTERND_OK;
+  if (!x || !w || !y) return fail(EXTERND_EINVAL, "null pointer");
+  const Region rx = {x, tokens, 2 * cols, 2 * ldx, "x"}, rw = {w, rows, 2 * cols, 2 * ldw, "w"}, rb = packed(bias, 2 * rows, "bias"),
+               rr = {residual, tokens, 2 * rows, 2 * ldr, "residual"}, oy = packed(y, 2 * tokens * rows, "y"),
+               oz = packed(z, 4 * tokens * rows, "z");
+  if ((st = check_apart({oy, oz}, {rx, rw, rb, rr})) != EXTERND_OK) return st;
+  if ((st = check_device(&a.cus)) != EXTERND_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Workspace ws;
+  const size_t need = externd::linear_forward_workspace_bytes(tokens, cols, rows, externd::linear_is_aligned(a), a.cus);
+  if ((st = check_apart({packed(workspace, (int64_t)need, "workspace")}, {rx, rw, rb, rr, oy, oz})) != EXTERND_OK) return st;
+  if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
+  hipError_t e = externd::run_linear_forward(a, ws.ptr, s);
+  if (e != hipSuccess) return hip_fail(e, "linear forward");
+  return EXTERND_OK;
+}
+
+size_t externd_linear_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t act, int32_t aligned) {
+  if (bad_size(rows, cols) || tokens < 1 || bad_size(tokens, cols) || bad_size(tokens, rows)) return 0;
+  if (bad_act(act) && act != EXTERND_ACT_NONE) return 0;
+  int cus = 0;
+  if (check_device(&cus) != EXTERND_OK) return 0;
+  return externd::linear_backward_workspace_bytes(tokens, cols, rows, act, aligned != 0, aligned != 0, cus);
+}
+
+int externd_linear_backward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* w, int64_t rows,
+                            int64_t ldw, const float* z, const void* dy, int64_t lddy, int32_t dtype, int32_t act,
+                            void* stream, void* dx, void* dw, void* db, void* workspace, size_t workspace_bytes) {
+  externd::LinearArgs a = {};
+  a.x = x; a.w = w;
+  a.tokens = tokens; a.cols = cols; a.rows = rows;
+  a.ldx = ldx; a.ldw = ldw;
+  a.dtype = dtype; a.act = act;
+  a.z = const_cast<float*>(z);
+  a.dy = dy; a.lddy = lddy;
+  a.dx = dx; a.dw = dw; a.db = db;
+  int st = check_linear(a);
+  if (st != EXTERND_OK) return st;
+  if (bad_stride(lddy, rows)) return fail(EXTERND_EINVAL, "lddy must be at least the rows of W");
+  if (tokens == 0 ? !dw && !db : !dx && !dw && !db) return EXTERND_OK;
+  if (tokens > 0 && (!x || !w || !dy || (act != EXTERND_ACT_NONE && !z))) return fail(EXTERND_EINVAL, "null pointer");
+  const Region rx = {x, tokens, 2 * cols, 2 * ldx, "x"}, rw = {w, rows, 2 * cols, 2 * ldw, "w"},
+               rz = packed(act == EXTERND_ACT_NONE ? nullptr : z, 4 * tokens * rows, "z"),
+               rdy = {dy, tokens, 2 * rows, 2 * lddy, "dy"}, ox = packed(dx, 2 * tokens * cols, "dx"),
+               ow = packed(dw, 2 * rows * cols, "dw"), ob = packed(db, 2 * rows, "db");
+  if ((st = check_apart({ox, ow, ob}, {rx, rw, rz, rdy})) != EXTERND_OK) return st;
+  if ((st = check_device(&a.cus)) != EXTERND_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Workspace ws;
+  const size_t need = tokens > 0 && (dx || dw) ? externd::linear_backward_workspace_bytes(tokens, cols, rows, act, externd::linear_is_aligned(a),
+                                                                                           externd::linear_reads_dy(a), a.cus)
+                                               : 0;
+  if ((st = check_apart({packed(workspace, (int64_t)need, "workspace")}, {rx, rw, rz, rdy, ox, ow, ob})) != EXTERND_OK) return st;
+  if ((st = op_ws(ws, workspace, workspace_bytes, need, s)) != EXTERND_OK) return st;
+  hipError_t e = externd::run_linear_backward(a, ws.ptr, s);
+  if (e != hipSuccess) return hip_fail(e, "linear backward");
   return EXTERND_OK;
 }
 

@@ -7,6 +7,8 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "../../include/externd.h"
 
 namespace externd {
@@ -78,6 +80,14 @@ __device__ __forceinline__ void act_both_fast(float g, float& a, float& slope) {
     const float q = p * (1.f - p);   // 0 where p is 0 or 1: the cubic may overflow there
     slope = p + (q == 0.f ? 0.f : g * q * gelu_2z_slope(g));
   }
+}
+
+// run(act) with the activation as a compile-time constant.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& run) {
+  if (act == EXTERND_ACT_SILU) run(std::integral_constant<int, EXTERND_ACT_SILU>());
+  else if (act == EXTERND_ACT_GELU) run(std::integral_constant<int, EXTERND_ACT_GELU>());
+  else run(std::integral_constant<int, EXTERND_ACT_GELU_TANH>());
 }
 
 }  // namespace externd

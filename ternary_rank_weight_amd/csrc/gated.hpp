@@ -1,5 +1,5 @@
-// The products of the gated block: arguments shared by the passes (gated.hip)
-// and the units that instantiate the kernels (one per operand type).
+// The products of the gated block and of the linear layer: arguments shared by the passes (gated.hip,
+// linear.hip) and the units that instantiate the kernels (one per operand type).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -21,7 +21,8 @@ struct GatedGemm {
   GatedOperand a, b;         // a: output rows, b: output columns
   // The contraction is `segs` segments of `inner` entries each.  Segment s of a lies
   // s * rest entries past its source; b's source is the second from segment segs / 2 on in
-  // dx, whose a has dg's parts and then du's, and the same for both parts of dW.
+  // dx, whose a has dg's parts and then du's, and the same for both parts of dW.  (The linear layer's
+  // dx has one weight matrix: both of b's sources.)
   int segs;
   int64_t rest;
   int64_t inner;        // contraction length of one segment
@@ -29,12 +30,14 @@ struct GatedGemm {
   int64_t split_steps;  // whole steps per split; the last split also takes the partial steps
   int64_t mt, nt;       // tiles
   int64_t splits;
-  uint16_t* out[2];     // forward: h; dx: dx; dw: dWg, dWu
+  uint16_t* out[2];     // forward: h (linear: y); dx: dx; dw: dWg, dWu (linear: dW)
   int64_t mo, ldo;      // rows and columns of the outputs
-  float* save[2];       // forward: g, u (or null)
+  float* save[2];       // forward: g, u (linear: z) or null
   float* part;          // SPLIT: where the splits' sums go, fp32 (split, output, mo, ldo)
   int act;
-  // fp16 gradients: a's row m was scaled by scale_of(tops[m]), for dWu tops[tops_of_up + m]
+  const uint16_t *bias, *residual;   // linear forward, or null
+  int64_t ldr;          // entries from one row of the residual to the next
+  // fp16 gradients: a's row m was scaled by scale_of(tops[m]), for dWu tops[tops_of_up + m]; null: not scaled
   const uint32_t* tops;
   int64_t tops_of_up;
 };
@@ -51,5 +54,9 @@ hipError_t gated_product_bf16(GatedProduct mode, const GatedGemm& g, const Gated
                               hipStream_t s);
 hipError_t gated_product_f16(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, int cus,
                              hipStream_t s);
+hipError_t linear_product_bf16(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, int cus,
+                               hipStream_t s);
+hipError_t linear_product_f16(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, int cus,
+                              hipStream_t s);
 
 }  // namespace externd

@@ -1,5 +1,5 @@
-// The tiled product of the gated block and the join of its splits; each including
-// unit instantiates one operand type.
+// The tiled product of the gated block and of the linear layer and the join of its splits; each
+// including unit instantiates one operand type.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -42,7 +42,7 @@ struct Tile {
     }
   }
   // A lane's offsets (entries) into an image for the fragments of a wave whose
-  // first outer entry is w0 (a multiple of 64 for COLS): rows, by the half of the
+  // first outer entry is w0 (for COLS a multiple of 64, or of 16 if it has at most four fragments): rows, by the half of the
   // step; cols, by the fragment number modulo 4.  Kept as plain values so that
   // a fragment's address is image + offset + constant.
   struct Lane {
@@ -52,7 +52,7 @@ struct Tile {
 #pragma unroll
       for (int q = 0; q < (COLS ? 4 : 2); ++q) {
         if constexpr (!COLS) at[q] = (w0 + r) * 64 + (((q * 4 + p) ^ (r & 7)) * 8);
-        else at[q] = (8 * p + (r >> 2)) * O + ((w0 >> 4) + (q ^ (r >> 2))) * 16 + 4 * (r & 3);
+        else at[q] = (8 * p + (r >> 2)) * O + (((w0 >> 4) + q) ^ (r >> 2)) * 16 + 4 * (r & 3);
         asm("" : "+v"(at[q]));
       }
     }
@@ -78,6 +78,9 @@ struct Tile {
     }
   }
 };
+
+// Output matrices of a product.
+constexpr int outs_of(int mode) { return mode == kFwd || mode == kDw ? 2 : 1; }
 
 // f(0), f(1), ..., f(N - 1) with the index as a compile-time constant.
 template <int N, int I = 0, typename F>
@@ -107,7 +110,7 @@ __device__ __forceinline__ void for_constants(F&& f) {
 template <bool BF, int MODE, int BM, int BN, int WM, int WN, int NA, int NB, bool SPLIT>
 __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void k_gated_gemm(GatedGemm g) {
   constexpr int NTHR = WM * WN * kWave;
-  constexpr bool ACOLS = MODE == kDw, BCOLS = MODE != kFwd;
+  constexpr bool ACOLS = MODE == kDw || MODE == kLinDw, BCOLS = MODE != kFwd && MODE != kLin;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   using TA = Tile<ACOLS, BM>;
   using TB = Tile<BCOLS, BN>;
@@ -137,7 +140,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   const int wm = wave / WN, wn = wave % WN;
 
   constexpr int BNO = MODE == kFwd ? BN / 2 : BN;   // output columns per tile
-  constexpr bool SEGS = MODE != kFwd;   // a contraction of several segments
+  constexpr bool SEGS = BCOLS;   // a contraction of several segments
   const int segs = SEGS ? g.segs : 1;
 
   // A workgroup takes units (one tile, one split) id, id + grid, ...  They are
@@ -195,8 +198,8 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   auto src_b = [&](int slot, int seg, int64_t k0, int64_t& left_o, int64_t& left_k) -> const uint16_t* {
     int o, k;
     TB::place(slot, o, k);
-    if constexpr (MODE == kFwd) {   // the tile's first half gate rows, its second up rows
-      const int which = o >= BNO;
+    if constexpr (!BCOLS) {   // gated: the tile's first half gate rows, its second up rows
+      const int which = MODE == kFwd && o >= BNO;
       o -= which * BNO;
       left_o = 8;
       left_k = g.inner - (k0 + k);
@@ -272,7 +275,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   int64_t step_a = 0, step_b = 0;   // within the segment
   int seg_b = 0;
   const int64_t move_a = ACOLS ? kBK * g.a.ld : kBK, move_b = BCOLS ? kBK * g.b.ld : kBK;
-  const int64_t to_up = MODE != kDw ? g.b.p[1] - g.b.p[0] : 0;
+  const int64_t to_up = MODE == kFwd || MODE == kDx ? g.b.p[1] - g.b.p[0] : 0;
   const int uwave = __builtin_amdgcn_readfirstlane(wave);
   auto stage_a = [&](lds16 img, int piece) {
     to_lds16(pa, va[piece], img + (piece * NTHR + uwave * kWave) * 8);
@@ -462,28 +465,28 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
       }
   };
   const int64_t n_lane = wn * NO * 16 + 4 * p, m_lane = wm * MI * 16 + r;
+  const bool aligned = g.ldo % 4 == 0 &&
+                       ((reinterpret_cast<uintptr_t>(g.out[0]) | reinterpret_cast<uintptr_t>(g.out[1])) & 7) == 0 &&
+                       ((reinterpret_cast<uintptr_t>(g.save[0]) | reinterpret_cast<uintptr_t>(g.save[1])) & 15) == 0;
   auto round_outputs = [&] {
     if constexpr (MODE == kFwd) {
       if (g.act == EXTERND_ACT_SILU) activate(std::integral_constant<int, EXTERND_ACT_SILU>());
       else if (g.act == EXTERND_ACT_GELU) activate(std::integral_constant<int, EXTERND_ACT_GELU>());
       else activate(std::integral_constant<int, EXTERND_ACT_GELU_TANH>());
-    } else {
+    } else if constexpr (MODE != kLin) {
       float back[MI];   // fp16: what takes the scale of a's row off
 #pragma unroll
       for (int i = 0; i < MI; ++i)
-        if constexpr (!BF) back[i] = unscale_of(g.tops[u.outsel * g.tops_of_up + min(u.m0 + m_lane + i * 16, g.mo - 1)]);
+        if constexpr (!BF) back[i] = !g.tops ? 1.f : unscale_of(g.tops[u.outsel * g.tops_of_up + min(u.m0 + m_lane + i * 16, g.mo - 1)]);
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < NO; ++j) packed[i][j] = pack(BF ? acc[i][j] : acc[i][j] * back[i]);
     }
   };
-  const bool aligned = g.ldo % 4 == 0 &&
-                       ((reinterpret_cast<uintptr_t>(g.out[0]) | reinterpret_cast<uintptr_t>(g.out[1])) & 7) == 0 &&
-                       ((reinterpret_cast<uintptr_t>(g.save[0]) | reinterpret_cast<uintptr_t>(g.save[1])) & 15) == 0;
   auto put_outputs = [&](auto inside) {   // inside: the whole tile is, and its rows are aligned
     constexpr bool IN = decltype(inside)::value;
-    constexpr int OUTS = MODE == kDx ? 1 : 2;
+    constexpr int OUTS = outs_of(MODE);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       const int64_t m = u.m0 + m_lane + i * 16, at = m * g.ldo + u.n0 + n_lane;
@@ -504,6 +507,68 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
             put32(g.save[1] + at + j * 16, left, whole, acc[i][j + NI / 2]);
           }
         }
+      }
+    }
+  };
+  // Linear forward, a row of fragments at a time: z = acc + bias, y = act(z) + residual.  A row's
+  // residual is on its way while the row before it is put out.
+  auto put_linear = [&](auto inside) {   // inside: as above, and the residual's rows are read 8 bytes at a time
+    constexpr bool IN = decltype(inside)::value;
+    f32x4 bias[NO];
+#pragma unroll
+    for (int j = 0; j < NO; ++j) {
+      bias[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (g.bias) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bias[j][e] = f32_from_16<BF>(g.bias[min(u.n0 + n_lane + j * 16 + e, g.ldo - 1)]);
+      }
+    }
+    uint2 res[2][NO];
+    auto fetch = [&](int i) {
+      const uint16_t* row = g.residual + min(u.m0 + m_lane + i * 16, g.mo - 1) * g.ldr;
+#pragma unroll
+      for (int j = 0; j < NO; ++j) {
+        const int64_t n = u.n0 + n_lane + j * 16;
+        if constexpr (IN) {
+          res[i & 1][j] = *reinterpret_cast<const uint2*>(row + n);
+        } else {
+          uint32_t v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = row[min(n + e, g.ldo - 1)];
+          res[i & 1][j] = uint2{v[0] | (v[1] << 16), v[2] | (v[3] << 16)};
+        }
+      }
+    };
+    if (g.residual) fetch(0);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      if (g.residual && i + 1 < MI) fetch(i + 1);
+      const int64_t m = u.m0 + m_lane + i * 16, at = m * g.ldo + u.n0 + n_lane;
+      f32x4 y[NO];
+#pragma unroll
+      for (int j = 0; j < NO; ++j) {
+        y[j] = acc[i][j] + bias[j];
+        const int64_t left = g.ldo - (u.n0 + n_lane + j * 16);
+        if (g.save[0] && (IN || (m < g.mo && left > 0)))
+          put32(g.save[0] + at + j * 16, left, IN || (aligned && left >= 4), y[j]);
+      }
+      if (g.act != EXTERND_ACT_NONE)
+        with_act(g.act, [&](auto act) {
+#pragma unroll
+          for (int j = 0; j < NO; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[j][e] = act_fast<decltype(act)::value>(y[j][e]);
+        });
+#pragma unroll
+      for (int j = 0; j < NO; ++j) {
+        if (g.residual) {
+          const uint2 v = res[i & 1][j];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[j][e] += f32_from_16<BF>(((e < 2 ? v.x : v.y) >> (16 * (e & 1))) & 0xffffu);
+        }
+        const int64_t left = g.ldo - (u.n0 + n_lane + j * 16);
+        if (IN || (m < g.mo && left > 0))
+          put16(g.out[0] + at + j * 16, left, IN || (aligned && left >= 4), pack(y[j]));
       }
     }
   };
@@ -530,14 +595,25 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
     const bool more = at < units;
     const Unit next = locate(more ? at : blockIdx.x);
     if (more) begin(next);
+    const bool inside = aligned && u.m0 + BM <= g.mo && u.n0 + BNO <= g.ldo;
     if constexpr (!SPLIT) round_outputs();
     wait_vm<0, 0>();
-    if (aligned && u.m0 + BM <= g.mo && u.n0 + BNO <= g.ldo) put_outputs(std::true_type());
+    if constexpr (MODE == kLin && !SPLIT) {
+      if (inside && g.ldr % 4 == 0 && (reinterpret_cast<uintptr_t>(g.residual) & 7) == 0) put_linear(std::true_type());
+      else put_linear(std::false_type());
+    } else if (inside) put_outputs(std::true_type());
     else put_outputs(std::false_type());
     if (!more) break;
     u = next;
   }
 }
+
+// Outputs of a product, and of a join.
+struct JoinEnd {
+  int64_t ldo, tops_of_up, ldr;
+  const uint32_t* tops;
+  const uint16_t *bias, *residual;
+};
 
 // What the split contractions left: the splits' sums in their order, then the
 // outputs as the unsplit kernel makes them.  part: (split, outs, count) fp32, rows of ldo;
@@ -547,9 +623,8 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
 template <bool BF, int MODE>
 __global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ part, int64_t count, int64_t splits,
                                                      uint16_t* __restrict__ out0, uint16_t* __restrict__ out1,
-                                                     float* __restrict__ g, float* __restrict__ u, int act,
-                                                     const uint32_t* __restrict__ tops, int64_t tops_of_up, int64_t ldo) {
-  constexpr int OUTS = MODE == kDx ? 1 : 2;
+                                                     float* __restrict__ g, float* __restrict__ u, int act, JoinEnd z) {
+  constexpr int OUTS = outs_of(MODE);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
     float s[OUTS];
 #pragma unroll
@@ -560,11 +635,20 @@ __global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ pa
     if constexpr (MODE == kFwd) {
       out0[i] = (uint16_t)f32_to_16<BF>(act_value(act, s[0]) * s[1]);
       if (g) { g[i] = s[0]; u[i] = s[1]; }
+    } else if constexpr (MODE == kLin) {
+      const int64_t row = i / z.ldo, col = i - row * z.ldo;
+      if (z.bias) s[0] += f32_from_16<BF>(z.bias[col]);
+      if (g) g[i] = s[0];
+      float y = act == EXTERND_ACT_NONE ? s[0] : act_value(act, s[0]);
+      if (z.residual) y += f32_from_16<BF>(z.residual[row * z.ldr + col]);
+      out0[i] = (uint16_t)f32_to_16<BF>(y);
     } else {
       if constexpr (!BF) {
-        const int64_t row = i / ldo;
+        const int64_t row = i / z.ldo;
+        if (z.tops) {
 #pragma unroll
-        for (int o = 0; o < OUTS; ++o) s[o] *= unscale_of(tops[o * tops_of_up + row]);
+          for (int o = 0; o < OUTS; ++o) s[o] *= unscale_of(z.tops[o * z.tops_of_up + row]);
+        }
       }
       out0[i] = (uint16_t)f32_to_16<BF>(s[0]);
       if constexpr (MODE == kDw) out1[i] = (uint16_t)f32_to_16<BF>(s[1]);
@@ -575,45 +659,57 @@ __global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ pa
 // Persistent workgroups: as many as are resident together.
 template <bool BF, int MODE, GatedKind KIND, bool SPLIT>
 hipError_t launch_tile(GatedGemm g, int cus, hipStream_t s) {
-  constexpr int B = KIND == kBig ? 256 : 128, WN = KIND == kBig ? 4 : 2;
+  constexpr int B = KIND == kBig || KIND == kMid ? 256 : 128, BN = KIND == kMid ? 192 : B, WN = B == 256 ? 4 : 2;
   constexpr int NA = KIND == kDeep ? 4 : 3, NB = KIND == kDeep ? 4 : 2;
   g.mt = MODE == kDw ? 2 * ceil_div64(g.a.outer, B) : ceil_div64(g.a.outer, B);
-  g.nt = ceil_div64(g.b.outer, MODE == kFwd ? B / 2 : B);
+  g.nt = ceil_div64(g.b.outer, MODE == kFwd ? B / 2 : BN);
   const int64_t resident = (int64_t)cus * (KIND == kPair ? 2 : 1);
   const dim3 grid((unsigned)std::min<int64_t>(g.mt * g.nt * g.splits, resident)), block(2 * WN * kWave);
-  hipLaunchKernelGGL((k_gated_gemm<BF, MODE, B, B, 2, WN, NA, NB, SPLIT>), grid, block, 0, s, g);
+  hipLaunchKernelGGL((k_gated_gemm<BF, MODE, B, BN, 2, WN, NA, NB, SPLIT>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 
-template <bool BF, int MODE>
+// WIDE: the kinds of tiles of the linear layer's products, which are all split too.
+template <bool BF, int MODE, bool WIDE>
 hipError_t product(GatedGemm g, const GatedPlan& plan, float* part, int cus, hipStream_t s) {
   g.full = g.inner / kBK;
   const int64_t whole = std::max<int64_t>(1, g.segs * g.full);
   g.split_steps = ceil_div64(whole, plan.splits);
   g.splits = ceil_div64(whole, g.split_steps);   // none without steps
+  if constexpr (WIDE)
+    if (plan.splits == 1 && plan.kind == kMid) return launch_tile<BF, MODE, kMid, false>(g, cus, s);
   if (plan.splits == 1 && plan.stacked == 1)
     return plan.kind == kBig    ? launch_tile<BF, MODE, kBig, false>(g, cus, s)
            : plan.kind == kPair ? launch_tile<BF, MODE, kPair, false>(g, cus, s)
                                 : launch_tile<BF, MODE, kDeep, false>(g, cus, s);
   g.part = part;
   hipError_t e = hipSuccess;
-  if constexpr (MODE == kDx)
+  if constexpr (WIDE)
+    if (plan.kind == kMid) e = launch_tile<BF, MODE, kMid, true>(g, cus, s);
+  if constexpr (MODE == kDx || WIDE)
     if (plan.kind == kBig) e = launch_tile<BF, MODE, kBig, true>(g, cus, s);
   if (plan.kind == kDeep) e = launch_tile<BF, MODE, kDeep, true>(g, cus, s);
   if (e != hipSuccess) return e;
   const int64_t count = g.mo / plan.stacked * g.ldo;   // (a half is as good as a split)
   const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(ceil_div64(count, 256), 1 << 15))), block(256);
   hipLaunchKernelGGL((k_gated_join<BF, MODE>), grid, block, 0, s, part, count, g.splits * plan.stacked, g.out[0], g.out[1], g.save[0],
-                     g.save[1], g.act, g.tops, g.tops_of_up, g.ldo);
+                     g.save[1], g.act, JoinEnd{g.ldo, g.tops_of_up, g.ldr, g.tops, g.bias, g.residual});
   return hipGetLastError();
 }
 
 template <bool BF>
 hipError_t any_product(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, int cus,
                        hipStream_t s) {
-  if (mode == kFwd) return product<BF, kFwd>(g, plan, part, cus, s);
-  if (mode == kDx) return product<BF, kDx>(g, plan, part, cus, s);
-  return product<BF, kDw>(g, plan, part, cus, s);
+  if (mode == kFwd) return product<BF, kFwd, false>(g, plan, part, cus, s);
+  if (mode == kDx) return product<BF, kDx, false>(g, plan, part, cus, s);
+  return product<BF, kDw, false>(g, plan, part, cus, s);
+}
+
+template <bool BF>
+hipError_t any_linear(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, int cus, hipStream_t s) {
+  if (mode == kLin) return product<BF, kLin, true>(g, plan, part, cus, s);
+  if (mode == kDx) return product<BF, kDx, true>(g, plan, part, cus, s);
+  return product<BF, kLinDw, true>(g, plan, part, cus, s);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
-// How the products of the gated block are run: which kernel, which tiles, how many
-// splits.  Host code without HIP.
+// How the products of the gated block and of the linear layer are run: which kernel, which tiles, how
+// many splits.  Host code without HIP.
 #pragma once
 #include <stdint.h>
 
@@ -7,12 +7,14 @@
 
 namespace externd {
 
-enum GatedProduct { kFwd = 0, kDx = 1, kDw = 2 };
+// The gated block's forward, dx and both dW; the linear layer's forward and dW (its dx is kDx).
+enum GatedProduct { kFwd = 0, kDx = 1, kDw = 2, kLin = 3, kLinDw = 4 };
 constexpr int kBK = 64;   // contraction entries per step: two 16x16x32 products, 128 bytes of a row
 
 // How a product is run: 256 x 256 tiles, 128 x 128 tiles two to a CU, or one to a CU
-// with loads three steps ahead; and the splits of its contraction.
-enum GatedKind { kBig, kPair, kDeep };
+// with loads three steps ahead; and the splits of its contraction.  The linear layer's also
+// in 256 x 192 tiles.
+enum GatedKind { kBig, kPair, kDeep, kMid };
 struct GatedPlan {
   GatedKind kind;
   int64_t splits;
@@ -91,7 +93,7 @@ inline GatedPlan plan_dw(int64_t tokens, int64_t cols, int64_t rows, int cus) {
   return plan_of(kDw, rows, cols, 2 * steps_of(tokens), cus);
 }
 inline int64_t part_floats(int mode, int64_t m, int64_t n, const GatedPlan& p) {
-  return p.splits * p.stacked > 1 ? p.splits * p.stacked * (mode == kDx ? 1 : 2) * m * n : 0;
+  return p.splits * p.stacked > 1 ? p.splits * p.stacked * (mode == kFwd || mode == kDw ? 2 : 1) * m * n : 0;
 }
 
 }  // namespace externd

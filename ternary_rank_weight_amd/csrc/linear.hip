@@ -1,0 +1,247 @@
+// The linear layer: z = x W^T + bias, y = act(z) + residual in one kernel, and its
+// backward pass
+//   dz = dy act'(z)                       (one pass over T x F; without an activation dz is dy)
+//   dx = dz W, dW = dz^T x                (a product each)
+//   db = the sum of dz over the tokens    (one pass)
+// for T tokens, K columns and F rows of W.  The products are the tiled kernel of the gated block
+// (gated_gemm.hpp) in forms of one weight matrix; with an activation dz is held in two 16-bit
+// parts as dg and du are there, so that each gradient is rounded once.
+#include <algorithm>
+
+#include "activation.hpp"
+#include "device_common.hpp"
+#include "frag.hpp"
+#include "gated.hpp"
+#include "linear.hpp"
+#include "linear_plan.hpp"
+#include "pad.hpp"
+#include "slopes.hpp"
+
+namespace externd {
+
+namespace {
+
+// db: sums over the tokens of dz in fp32, in an order that does not depend on timing.  A workgroup takes
+// 64 columns, a wave every sixteenth token; the waves' sums are joined in wave order.
+constexpr int kSumWaves = 16;
+template <bool BF>
+__global__ __launch_bounds__(kSumWaves * kWave) void k_bias_sums(const uint16_t* __restrict__ dy, int64_t lddy,
+                                                                  const float* __restrict__ z, int act, int64_t tokens,
+                                                                  int64_t rows, uint16_t* __restrict__ db) {
+  __shared__ float red[kSumWaves][kWave];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int64_t c = (int64_t)blockIdx.x * kWave + lane, at = min(c, rows - 1);
+  constexpr int U = 4;   // tokens on their way
+  float sum[U] = {};
+  auto add = [&](auto slope) {
+    for (int64_t t0 = wave; t0 < tokens; t0 += U * kSumWaves) {
+      float d[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t t = t0 + u * kSumWaves;
+        d[u] = t < tokens ? f32_from_16<BF>(dy[t * lddy + at]) : 0.f;
+        if (z) d[u] = t < tokens ? d[u] * slope(z[t * rows + at]) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) sum[u] += d[u];
+    }
+  };
+  if (z)
+    with_act(act, [&](auto kind) {
+      add([](float v) {
+        float a, s;
+        act_both_fast<decltype(kind)::value>(v, a, s);
+        return s;
+      });
+    });
+  else add([](float) { return 1.f; });
+  red[wave][lane] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  __syncthreads();
+  if (wave == 0 && c < rows) {
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kSumWaves; ++q) v += red[q][lane];
+    db[c] = (uint16_t)f32_to_16<BF>(v);
+  }
+}
+
+hipError_t product(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, bool bf, int cus,
+                   hipStream_t s) {
+  return bf ? linear_product_bf16(mode, g, plan, part, cus, s) : linear_product_f16(mode, g, plan, part, cus, s);
+}
+
+// x, W and dy as the products can read them: the caller's, or padded copies in the workspace.
+struct Operands {
+  const uint16_t *x, *w, *dy;
+  int64_t ldx, ldw, lddy, cols;   // cols: padded, when copied
+};
+int64_t copy_entries(int64_t tokens, int64_t cols, int64_t rows) { return (tokens + rows) * padded(cols, kBK); }
+
+// ws: room for the copies of x and W, then of dy; `forward`: dy is not looked at.
+hipError_t operands(const LinearArgs& a, bool copy_xw, bool copy_dy, uint16_t* ws, Operands* o, hipStream_t s) {
+  *o = {static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.w), static_cast<const uint16_t*>(a.dy),
+        a.ldx, a.ldw, a.lddy, a.cols};
+  PadArgs q = {};
+  int n = 0;
+  int64_t most = 0;
+  auto copy = [&](const uint16_t*& src, int64_t& ld, int64_t rows, int64_t cols) {
+    const int64_t ldp = padded(cols, kBK);
+    q.src[n] = src;
+    q.dst[n] = ws;
+    q.rows[n] = rows;
+    q.cols[n] = cols;
+    q.ld[n] = ld;
+    q.ldp[n++] = ldp;
+    src = ws;
+    ld = ldp;
+    ws += rows * ldp;
+    most = std::max(most, rows * (ldp / 8));
+  };
+  if (copy_xw) {
+    copy(o->x, o->ldx, a.tokens, a.cols);
+    copy(o->w, o->ldw, a.rows, a.cols);
+    o->cols = padded(a.cols, kBK);
+  }
+  if (copy_dy) copy(o->dy, o->lddy, a.tokens, a.rows);
+  if (n == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_pad_rows, dim3(blocks(most), n), dim3(256), 0, s, q);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool linear_is_aligned(const LinearArgs& a) { return rows_aligned(a.x, a.ldx) && rows_aligned(a.w, a.ldw) && a.cols % 8 == 0; }
+bool linear_reads_dy(const LinearArgs& a) {
+  return a.act == EXTERND_ACT_NONE && rows_aligned(a.dy, a.lddy) && a.rows % 8 == 0;
+}
+
+size_t linear_forward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, bool aligned, int cus) {
+  if (linear_takes_rows(tokens, cols, rows, aligned, cus)) return 0;
+  const GatedPlan p = plan_linear(kLin, tokens, rows, steps_of(padded(cols, kBK)), cus);
+  return (aligned ? 0 : region(2 * (size_t)copy_entries(tokens, cols, rows))) + region(4 * (size_t)part_floats(kLin, tokens, rows, p));
+}
+
+hipError_t run_linear_forward(const LinearArgs& a, void* ws, hipStream_t s) {
+  const bool al = linear_is_aligned(a);
+  if (linear_takes_rows(a.tokens, a.cols, a.rows, al, a.cus)) return run_linear_rows(a, s);
+  char* w = static_cast<char*>(ws);
+  Operands o;
+  const hipError_t e = operands(a, !al, false, reinterpret_cast<uint16_t*>(w), &o, s);
+  if (e != hipSuccess) return e;
+  if (!al) w += region(2 * (size_t)copy_entries(a.tokens, a.cols, a.rows));
+  GatedGemm g = {};
+  g.a = {{o.x, o.x}, o.ldx, a.tokens};
+  g.b = {{o.w, o.w}, o.ldw, a.rows};
+  g.segs = 1;
+  g.inner = o.cols;
+  g.out[0] = static_cast<uint16_t*>(a.y);
+  g.mo = a.tokens;
+  g.ldo = a.rows;
+  g.save[0] = a.z;
+  g.act = a.act;
+  g.bias = static_cast<const uint16_t*>(a.bias);
+  g.residual = static_cast<const uint16_t*>(a.residual);
+  g.ldr = a.ldr;
+  const GatedPlan p = plan_linear(kLin, a.tokens, a.rows, steps_of(padded(a.cols, kBK)), a.cus);
+  return product(kLin, g, p, reinterpret_cast<float*>(w), a.dtype == EXTERND_BF16, a.cus, s);
+}
+
+// Workspace: dz in two parts and its largest magnitudes where there is an activation, padded copies, the
+// split sums.
+size_t linear_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int act, bool aligned, bool reads_dy, int cus) {
+  const bool parts = act != EXTERND_ACT_NONE;
+  const GatedPlan px = plan_linear_dx(tokens, cols, rows, parts, cus), pw = plan_linear_dw(tokens, cols, rows, parts, cus);
+  return (parts ? region(2 * (size_t)(2 * tokens * padded(rows, 8))) + region(4 * (size_t)(tokens + padded(rows, 8))) : 0) +
+         region(2 * (size_t)((aligned ? 0 : copy_entries(tokens, cols, rows)) + (parts || reads_dy ? 0 : tokens * padded(rows, kBK)))) +
+         region(4 * (size_t)std::max(part_floats(kDx, tokens, cols, px), part_floats(kLinDw, rows, cols, pw)));
+}
+
+hipError_t run_linear_backward(const LinearArgs& a, void* ws, hipStream_t s) {
+  const bool bf = a.dtype == EXTERND_BF16, parts = a.act != EXTERND_ACT_NONE;
+  hipError_t e;
+  if (a.tokens == 0) {
+    const struct { void* p; int64_t n; } zero[2] = {{a.dw, a.rows * a.cols}, {a.db, a.rows}};
+    for (const auto& z : zero) {
+      if (!z.p) continue;
+      hipLaunchKernelGGL(k_fill_zero<uint16_t>, dim3(1024), dim3(256), 0, s, static_cast<uint16_t*>(z.p), z.n);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+  if (a.db) {
+    const dim3 grid((unsigned)ceil_div64(a.rows, kWave)), block(kSumWaves * kWave);
+    const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
+    const float* z = parts ? a.z : nullptr;
+    if (bf) hipLaunchKernelGGL(k_bias_sums<true>, grid, block, 0, s, dy, a.lddy, z, a.act, a.tokens, a.rows, static_cast<uint16_t*>(a.db));
+    else hipLaunchKernelGGL(k_bias_sums<false>, grid, block, 0, s, dy, a.lddy, z, a.act, a.tokens, a.rows, static_cast<uint16_t*>(a.db));
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (!a.dx && !a.dw) return hipSuccess;
+  char* w = static_cast<char*>(ws);
+  // dz and its rest
+  const int64_t ldd = padded(a.rows, 8), part_len = a.tokens * ldd;
+  uint16_t* dz = reinterpret_cast<uint16_t*>(w);
+  uint32_t *by_unit = nullptr, *by_token = nullptr;
+  const SlopeArgs sa = {a.z, nullptr, static_cast<const uint16_t*>(a.dy), a.tokens, a.rows, a.lddy};
+  if (parts) {
+    w += region(2 * (size_t)(2 * part_len));
+    by_unit = reinterpret_cast<uint32_t*>(w);
+    by_token = by_unit + ldd;
+    w += region(4 * (size_t)(a.tokens + ldd));
+    if (!bf) {
+      const int64_t strips = ceil_div64(a.rows, 256);
+      const int strip = ceil_div64(a.tokens, 64) * strips >= 2 * a.cus ? 64 : 16;
+      hipLaunchKernelGGL(k_fill_zero<uint32_t>, dim3(64), dim3(256), 0, s, by_unit, a.tokens + ldd);
+      hipLaunchKernelGGL(k_gated_tops<false>, dim3((unsigned)(ceil_div64(a.tokens, strip) * strips)), dim3(256), 0, s, sa, ldd,
+                         a.act, strip, by_token, by_unit);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+  }
+  // fp16: for dx scaled by token, for dW by row of W
+  auto slopes = [&](const uint32_t* token, const uint32_t* unit) {
+    const dim3 grid(blocks(a.tokens * (ldd / 8))), block(256);
+    if (bf) hipLaunchKernelGGL((k_gated_slopes<true, false>), grid, block, 0, s, sa, ldd, a.act, part_len, token, unit, dz, nullptr);
+    else hipLaunchKernelGGL((k_gated_slopes<false, false>), grid, block, 0, s, sa, ldd, a.act, part_len, token, unit, dz, nullptr);
+    return hipGetLastError();
+  };
+  const bool al = linear_is_aligned(a), reads_dy = linear_reads_dy(a);
+  Operands o;
+  if ((e = operands(a, !al, !parts && !reads_dy, reinterpret_cast<uint16_t*>(w), &o, s)) != hipSuccess) return e;
+  w += region(2 * (size_t)((al ? 0 : copy_entries(a.tokens, a.cols, a.rows)) + (parts || reads_dy ? 0 : a.tokens * padded(a.rows, kBK))));
+  float* part = reinterpret_cast<float*>(w);
+  const int64_t cols8 = padded(a.cols, 8);
+  const uint16_t* d = parts ? dz : o.dy;
+  const int64_t ld = parts ? ldd : o.lddy;
+  if (a.dx) {
+    if (parts && (e = slopes(by_token, nullptr)) != hipSuccess) return e;
+    const GatedPlan px = plan_linear_dx(a.tokens, a.cols, a.rows, parts, a.cus);
+    GatedGemm g = {};
+    g.a = {{d, d}, ld, px.stacked * a.tokens};
+    g.b = {{o.w, o.w}, o.ldw, cols8};
+    g.segs = parts && px.stacked == 1 ? 2 : 1;   // stacked: a segment's rows are both parts
+    g.rest = part_len;
+    g.tops = parts && !bf ? by_token : nullptr;
+    g.inner = a.rows;
+    g.out[0] = static_cast<uint16_t*>(a.dx);
+    g.mo = px.stacked * a.tokens;
+    g.ldo = a.cols;
+    if ((e = product(kDx, g, px, part, bf, a.cus, s)) != hipSuccess) return e;
+  }
+  if (a.dw) {
+    if (parts && (!bf || !a.dx) && (e = slopes(nullptr, by_unit)) != hipSuccess) return e;
+    GatedGemm g = {};
+    g.a = {{d, d}, ld, ldd};
+    g.b = {{o.x, o.x}, o.ldx, cols8};
+    g.segs = parts ? 2 : 1;
+    g.rest = part_len;
+    g.tops = parts && !bf ? by_unit : nullptr;
+    g.inner = a.tokens;
+    g.out[0] = static_cast<uint16_t*>(a.dw);
+    g.mo = a.rows;
+    g.ldo = a.cols;
+    if ((e = product(kLinDw, g, plan_linear_dw(a.tokens, a.cols, a.rows, parts, a.cus), part, bf, a.cus, s)) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace externd

@@ -1,0 +1,11 @@
+// The linear layer's products on fp16 operands.
+#include "gated_gemm.hpp"
+
+namespace externd {
+
+hipError_t linear_product_f16(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, int cus,
+                              hipStream_t s) {
+  return any_linear<false>(mode, g, plan, part, cus, s);
+}
+
+}  // namespace externd

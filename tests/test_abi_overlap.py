@@ -99,3 +99,35 @@ def test_gated_backward():
         assert refused(backward(dx=at), "dx", name)
         assert refused(backward(dwg=H, dwu=at), "dwu", name)
     assert refused(backward(dwg=H, dwu=off(H, 4094)), "dwu", "dwg") and refused(backward(dx=H, dwg=H, dwu=A))
+
+
+def linear(x=A, w=B, bias=None, residual=None, y=D, z=None, ldr=32, act=0, dtype=1, tokens=4, ws=None, wsb=0):
+    return trw._linear_forward(x, tokens, 64, 64, w, 32, 64, bias, residual, ldr, dtype, act, None, y, z, ws, wsb)
+
+
+def test_linear_forward():
+    assert not refused(linear()) and not refused(linear(bias=C, residual=F, z=G)) and not refused(linear(residual=A, bias=B))
+    assert refused(linear(y=A), "y", "x") and refused(linear(y=off(B, 32 * 128 - 2)), "w") and not refused(linear(y=off(B, 32 * 128)))
+    assert refused(linear(bias=off(D, 254)), "bias") and not refused(linear(bias=off(D, 256)))
+    assert refused(linear(residual=D), "residual") and not refused(linear(residual=off(D, 256), ldr=1 << 20)) and refused(linear(residual=off(D, 254), ldr=1 << 20))
+    assert refused(linear(z=off(D, 252)), "z", "y") and refused(linear(z=A), "z", "x")
+    bad = lambda **kw: linear(**kw) == EINVAL
+    assert bad(act=4) and bad(act=-1) and bad(dtype=3) and bad(tokens=-1) and bad(residual=F, ldr=31) and bad(x=None) and bad(y=None)
+    assert bad(x=off(A, 1)) and bad(z=off(G, 2)) and bad(bias=off(C, 1)) and linear(dtype=0) == 4 and linear(tokens=0) == 0
+
+
+def linear_backward(z=D, dy=G, dx=None, dw=None, db=None, act=0, tokens=4, x=A):
+    return trw._linear_backward(x, tokens, 64, 64, B, 32, 64, z, dy, 32, 1, act, None, dx, dw, db, None, 0)
+
+
+def test_linear_backward():
+    H = ctypes.c_void_p(9 << 32)
+    assert not refused(linear_backward(dx=H, dw=C, db=F)) and not refused(linear_backward(act=3, dx=D))
+    for at, name in ((A, "x"), (B, "w"), (D, "z"), (G, "dy")):
+        assert refused(linear_backward(dx=at), "dx", name) and refused(linear_backward(dw=at), "dw", name)
+        assert refused(linear_backward(db=at), "db", name)
+    assert refused(linear_backward(dx=H, dw=off(H, 510)), "dw", "dx") and refused(linear_backward(dw=H, db=off(H, 4094)), "db", "dw")
+    bad = lambda **kw: linear_backward(**kw) == EINVAL
+    assert bad(dx=H, z=None) and bad(dx=H, dy=None) and bad(dx=H, x=None) and bad(act=5, dx=H) and not bad(dx=H, z=None, act=3)
+    assert linear_backward() == 0 and linear_backward(tokens=0, dx=H) == 0
+    assert trw._linear_forward_ws(0, 64, 32, 1) == 0 and trw._linear_backward_ws(4, 64, 32, 7, 1) == 0
