@@ -379,7 +379,7 @@ int externd_deflate(float* R, int64_t m, int64_t n, const uint32_t* u_codes,
  * Padding entries may hold any code; padding scales and minima must be
  * finite.  codes must be 16-byte aligned, scales and mins 8-byte.
  *
- * What these functions and those of the gated block and the linear layer below write, the workspace
+ * What these functions and those of the gated block, the linear layer and the experts below write, the workspace
  * included, must have no byte in common with what they read or write besides
  * (EXTERND_EINVAL); what they only read may overlap. */
 enum externd_dtype { EXTERND_F32 = 0, EXTERND_BF16 = 1, EXTERND_F16 = 2 };
@@ -501,6 +501,45 @@ int externd_linear_backward(const void* x, int64_t tokens, int64_t cols, int64_t
                             int64_t ldw, const float* z, const void* dy, int64_t lddy, int32_t dtype, int32_t act,
                             void* stream, void* dx, void* dw, void* db, void* workspace, size_t workspace_bytes);
 size_t externd_linear_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int32_t act, int32_t aligned);
+
+/* ---- mixture-of-experts layer for a few tokens, dense 16-bit weights ----
+ *
+ * Each token goes through `top` of the experts, gated blocks with a projection back:
+ *   y[t] = sum over j of weights[t][j] * Wd_e (act(Wg_e x[t]) * (Wu_e x[t])),  e = ids[t][j].
+ * Sums, activations and what lies between the products are fp32 or more, and y is rounded once.  dtype of x, the
+ * experts and y: EXTERND_BF16 or EXTERND_F16.  tokens * top at most EXTERND_MOE_SLOTS, experts at most 1024, top at
+ * most 64 and at most the experts, rows and cols at most 2^21 (EXTERND_EUNSUPPORTED beyond). */
+#define EXTERND_MOE_SLOTS 8192
+
+typedef struct externd_moe_weights {
+  const void *wg, *wu;   /* device: experts x rows x cols, rows up_ld and experts up_stride entries apart */
+  const void* wd;        /* device: experts x cols x rows, rows down_ld and experts down_stride entries apart */
+  int64_t experts, rows, cols;   /* rows: hidden units of an expert; cols: the layer's width */
+  int64_t up_ld, up_stride, down_ld, down_stride;
+} externd_moe_weights;
+
+/* Routing: logits x Wr^T (Wr experts x cols of wr_dtype, dtype or EXTERND_F32, rows ldr entries apart), summed
+ * in 64 bits; ids (tokens x top): the experts of the largest logits, largest first, the lower index where
+ * logits are equal, NaN after all others; weights (tokens x top, fp32): exp(logit) over the sum of those of the chosen experts
+ * (normalize) or of all.  workspace: NULL, and externd_moe_workspace_bytes(tokens, cols, 0, experts, top) bytes are
+ * allocated and freed stream-ordered; or a caller buffer of at least as many, 256-byte aligned. */
+int externd_moe_route(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wr, int64_t experts, int64_t ldr,
+                      int32_t wr_dtype, int32_t dtype, int32_t top, int32_t normalize, void* stream, int32_t* ids,
+                      float* weights, void* workspace, size_t workspace_bytes);
+
+/* The experts' sum for a choice that was made before: ids (tokens x top; one outside the experts adds nothing, one twice adds
+ * twice) and weights.  workspace as above, of externd_moe_workspace_bytes(tokens, cols, rows, experts, top) bytes. */
+int externd_moe_experts(const void* x, int64_t tokens, int64_t ldx, const int32_t* ids, const float* weights, int32_t top,
+                        const externd_moe_weights* w, int32_t dtype, int32_t act, void* stream, void* y, void* workspace,
+                        size_t workspace_bytes);
+
+/* Both: the whole layer, ids and weights written too. */
+int externd_moe(const void* x, int64_t tokens, int64_t ldx, const void* wr, int64_t ldr, int32_t wr_dtype, int32_t top,
+                int32_t normalize, const externd_moe_weights* w, int32_t dtype, int32_t act, void* stream, void* y,
+                int32_t* ids, float* weights, void* workspace, size_t workspace_bytes);
+
+/* Workspace that covers the three calls (rows = 0: externd_moe_route alone); 0 for what they refuse. */
+size_t externd_moe_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int64_t experts, int32_t top);
 
 /* ---- AdamW step over many tensors ----
  *

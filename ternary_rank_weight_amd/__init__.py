@@ -21,6 +21,7 @@ __all__ = [
     "Q4", "q4_quantize", "q4_pack", "q4_reconstruct", "q4_apply", "q4_gated", "q4_workspace_bytes",
     "gated", "gated_forward", "gated_backward", "gated_forward_workspace_bytes", "gated_backward_workspace_bytes",
     "linear", "linear_forward", "linear_backward", "linear_forward_workspace_bytes", "linear_backward_workspace_bytes",
+    "moe", "moe_route", "moe_experts", "moe_workspace_bytes",
     "AdamW",
     "STAT", "MODE_AUTO", "MODE_STREAMING", "MODE_RESIDENT", "MODE_PERSISTENT", "library_path",
 ]
@@ -69,6 +70,11 @@ class _Opts(ctypes.Structure):
         ("importance", _p), ("importance_lambda", ctypes.c_float), ("safeguard", _i32),
         ("block_capture", ctypes.POINTER(_BlockCapture)),
     ]
+
+
+class _MoeWeights(ctypes.Structure):
+    _fields_ = [("wg", _p), ("wu", _p), ("wd", _p)] + [(name, _i64) for name in (
+        "experts", "rows", "cols", "up_ld", "up_stride", "down_ld", "down_stride")]
 
 
 class _AdamTensor(ctypes.Structure):
@@ -138,6 +144,14 @@ _linear_forward_ws = _sig("externd_linear_forward_workspace_bytes", _size, [_i64
 _linear_backward = _sig("externd_linear_backward", ctypes.c_int,
                         [_p, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, _i32, _i32, _p, _p, _p, _p, _p, _size])
 _linear_backward_ws = _sig("externd_linear_backward_workspace_bytes", _size, [_i64, _i64, _i64, _i32, _i32])
+_pmoe = ctypes.POINTER(_MoeWeights)
+_moe_route = _sig("externd_moe_route", ctypes.c_int,
+                  [_p, _i64, _i64, _i64, _p, _i64, _i64, _i32, _i32, _i32, _i32, _p, _p, _p, _p, _size])
+_moe_experts = _sig("externd_moe_experts", ctypes.c_int,
+                    [_p, _i64, _i64, _p, _p, _i32, _pmoe, _i32, _i32, _p, _p, _p, _size])
+_moe = _sig("externd_moe", ctypes.c_int,
+            [_p, _i64, _i64, _p, _i64, _i32, _i32, _i32, _pmoe, _i32, _i32, _p, _p, _p, _p, _p, _size])
+_moe_ws = _sig("externd_moe_workspace_bytes", _size, [_i64, _i64, _i64, _i64, _i32])
 _adamw_step = _sig("externd_adamw_step", ctypes.c_int, [ctypes.POINTER(_AdamTensor), _i64, ctypes.POINTER(_AdamOpts), _p])
 _adamw_moments = _sig("externd_adamw_moments", ctypes.c_int, [_p, _p, _p, _p, _i64, _p, _p, _p])
 _status_string = _sig("externd_status_string", ctypes.c_char_p, [ctypes.c_int])
@@ -156,6 +170,7 @@ ABI_SYMBOLS = ("externd_decompose", "externd_decompose_noalloc", "externd_energy
                "externd_gated_backward", "externd_gated_backward_workspace_bytes",
                "externd_linear_forward", "externd_linear_forward_workspace_bytes",
                "externd_linear_backward", "externd_linear_backward_workspace_bytes",
+               "externd_moe", "externd_moe_route", "externd_moe_experts", "externd_moe_workspace_bytes",
                "externd_adamw_step", "externd_adamw_moments",
                "externd_status_string", "externd_last_error")
 
@@ -1029,6 +1044,128 @@ def linear(x, W, bias=None, act=None, residual=None):
     if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, W, bias, residual))):
         return linear_forward(x, W, bias, act, residual)
     return _Linear.apply(x, W, bias, act, residual)
+
+
+# ---- mixture-of-experts layer for a few tokens ----
+
+def moe_workspace_bytes(tokens, cols, rows, experts, top):
+    """Device workspace that covers moe, moe_experts and moe_route (rows = 0: moe_route alone); 0: refused."""
+    return int(_moe_ws(tokens, cols, rows, experts, top))
+
+
+def _moe_scratch(workspace, x, rows, experts, top):
+    if workspace is None:
+        need = _moe_ws(x.shape[0], x.shape[1], rows, experts, top) if x.shape[0] else 0
+        if need == 0:   # the call refuses the sizes
+            return None, 0, None
+        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+    return (*_scratch(workspace, x.get_device()), workspace)
+
+
+def _moe_input(x, cols):
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"x must be bfloat16 or float16, got {x.dtype}")
+    x, ldx = _rows_of(x, cols, "x")
+    return x, ldx, _DTYPE[x.dtype]
+
+
+def _moe_router(x, Wr):
+    """Checks Wr against x; returns (Wr, its row stride, dtype code)."""
+    if Wr.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"Wr must be {x.dtype} like x, or float32, got {Wr.dtype}")
+    if Wr.dim() != 2:
+        raise ValueError("Wr must be 2-D")
+    return (*_rows_of(Wr, Wr.shape[1], "Wr"), _DTYPE[Wr.dtype])
+
+
+def _moe_weights(x, Wg, Wu, Wd):
+    """The experts' matrices as the C structure."""
+    for w, name in ((Wg, "Wg"), (Wu, "Wu"), (Wd, "Wd")):
+        if w.dtype != x.dtype:
+            raise TypeError(f"{name} must be {x.dtype} like x, got {w.dtype}")
+        if w.dim() != 3:
+            raise ValueError(f"{name} must be 3-D")
+    experts, rows, cols = Wg.shape
+    if Wu.shape != Wg.shape or tuple(Wd.shape) != (experts, cols, rows):
+        raise ValueError(f"Wg and Wu must be of one shape (experts, rows, cols) and Wd (experts, cols, rows), got "
+                         f"{tuple(Wg.shape)}, {tuple(Wu.shape)}, {tuple(Wd.shape)}")
+    (gs, gl, g1), (us, ul, u1), (ds, dl, d1) = Wg.stride(), Wu.stride(), Wd.stride()
+    # (a dimension of one entry may have any stride)
+    gl, ul = (gl, ul) if rows > 1 else (cols, cols)
+    dl = dl if cols > 1 else rows
+    gs, us, ds = (gs, us, ds) if experts > 1 else (rows * cols,) * 3
+    if g1 != 1 and cols > 1 or u1 != 1 and cols > 1 or d1 != 1 and rows > 1 or gs != us or gl != ul or \
+            gl < cols or dl < rows or gs < 1 or ds < 1:
+        raise ValueError("each expert's rows must be contiguous, and Wg and Wu strided alike")
+    return _MoeWeights(Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), experts, rows, cols, gl, gs, dl, ds)
+
+
+def moe_route(x, Wr, top, normalize=True, workspace=None):
+    """(ids int32, weights float32), both (..., top): the experts of each token's largest logits x Wr^T, largest first
+    and the lower index of equal ones, and exp(logit) over the sum of those of the chosen experts (normalize) or of all.
+
+    x (..., cols) bfloat16 or float16, Wr (experts, cols) of its type or float32.  Logits are summed in 64 bits.  There is no
+    gradient: asking for one raises an error."""
+    given = x, Wr
+    record = (x.requires_grad or Wr.requires_grad) and _records(None)
+    index = _op_device(x, Wr)
+    Wr, ldr, kind = _moe_router(x, Wr)
+    experts, cols = Wr.shape
+    shape = (*x.shape[:-1], top)
+    x, ldx, dtype = _moe_input(x, cols)
+    ids = torch.empty(shape, dtype=torch.int32, device=x.device)
+    weights = torch.empty(shape, dtype=torch.float32, device=x.device)
+    ws, wsb, keep = _moe_scratch(workspace, x, 0, experts, top)
+    _check(_moe_route(x.data_ptr(), x.shape[0], cols, ldx, Wr.data_ptr(), experts, ldr, kind, dtype, top, normalize,
+                      _raw_stream(index), ids.data_ptr(), weights.data_ptr(), ws, wsb))
+    return ids, _NoGradient.apply("moe_route has no gradient", weights, *given) if record else weights
+
+
+def moe_experts(x, ids, weights, Wg, Wu, Wd, act="silu", out=None, workspace=None):
+    """y[t] = the sum over j of weights[t, j] Wd[e] (act(Wg[e] x[t]) * (Wu[e] x[t])), e = ids[t, j], rounded once.
+
+    x (..., cols) bfloat16 or float16, Wg and Wu (experts, rows, cols) and Wd (experts, cols, rows) of its type, ids
+    (..., top) int32 and weights (..., top) float32, as moe_route gives them or made elsewhere: an id outside the experts
+    adds nothing, one that comes twice adds twice.  Experts may be strided (Wg and Wu alike, as halves of one tensor).
+    For a few tokens: at most 8192 ids.  There is no gradient: asking for one raises an error."""
+    given = x, weights, Wg, Wu, Wd
+    record = any(t.requires_grad for t in given) and _records(out)
+    index = _op_device(ids, *given)
+    w = _moe_weights(x, Wg, Wu, Wd)
+    if ids.dim() == 0 or ids.shape[:-1] != x.shape[:-1] or ids.shape != weights.shape:
+        raise ValueError("ids and weights must be of one shape (..., top), with x's leading dimensions")
+    _need(ids, torch.int32, "ids")
+    _need(weights, torch.float32, "weights")
+    top = ids.shape[-1]
+    y = x.new_empty(x.shape) if out is None else _out_or_new(out, x.shape, x.dtype, x.device)
+    x, ldx, dtype = _moe_input(x, w.cols)
+    ws, wsb, keep = _moe_scratch(workspace, x, w.rows, w.experts, top)
+    _check(_moe_experts(x.data_ptr(), x.shape[0], ldx, ids.data_ptr(), weights.data_ptr(), top, w, dtype, _act_code(act),
+                        _raw_stream(index), y.data_ptr(), ws, wsb))
+    return _NoGradient.apply("moe_experts has no gradient", y, *given) if record else y
+
+
+def moe(x, Wr, Wg, Wu, Wd, top, act="silu", normalize=True, routing=False, out=None, workspace=None):
+    """A mixture-of-experts layer for a few tokens: moe_experts with the choice that moe_route makes, in one call.  With
+    routing, returns (y, ids, weights)."""
+    given = x, Wr, Wg, Wu, Wd
+    record = any(t.requires_grad for t in given) and _records(out)
+    index = _op_device(*given)
+    w = _moe_weights(x, Wg, Wu, Wd)
+    Wr, ldr, kind = _moe_router(x, Wr)
+    if tuple(Wr.shape) != (w.experts, w.cols):
+        raise ValueError(f"Wr must have shape {(w.experts, w.cols)}")
+    shape = (*x.shape[:-1], top)
+    y = x.new_empty(x.shape) if out is None else _out_or_new(out, x.shape, x.dtype, x.device)
+    x, ldx, dtype = _moe_input(x, w.cols)
+    ids = torch.empty(shape, dtype=torch.int32, device=x.device)
+    weights = torch.empty(shape, dtype=torch.float32, device=x.device)
+    ws, wsb, keep = _moe_scratch(workspace, x, w.rows, w.experts, top)
+    _check(_moe(x.data_ptr(), x.shape[0], ldx, Wr.data_ptr(), ldr, kind, top, normalize, w, dtype, _act_code(act),
+                _raw_stream(index), y.data_ptr(), ids.data_ptr(), weights.data_ptr(), ws, wsb))
+    if record:
+        y = _NoGradient.apply("moe has no gradient", y, *given)
+    return (y, ids, weights) if routing else y
 
 
 # ---- the step that applies gradients ----

@@ -17,7 +17,7 @@ SOURCES = ["abi.cpp", "seq_stream.hip", "seq_resident.hip", "factors.hip", "bloc
            "noalloc.hip", "seq_persist.hip", "apply_rows.hip", "q4.hip", "q4_apply_bf16.hip",
            "q4_apply_f16.hip", "gated.hip", "gated_gemm_bf16.hip", "gated_gemm_f16.hip",
            "gated_rows.hip", "adamw.hip", "linear.hip", "linear_rows.hip",
-           "linear_gemm_bf16.hip", "linear_gemm_f16.hip"]
+           "linear_gemm_bf16.hip", "linear_gemm_f16.hip", "moe_route.hip", "moe.hip"]
 ARCH = "gfx950"
 
 COMMON = [

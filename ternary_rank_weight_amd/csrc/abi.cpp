@@ -17,6 +17,7 @@
 #include "adamw.hpp"
 #include "kernels.hpp"
 #include "linear.hpp"
+#include "moe.hpp"
 
 namespace {
 
@@ -243,6 +244,75 @@ int check_linear(const externd::LinearArgs& a) {
   for (const void* p : {a.x, a.w, a.bias, a.residual, (const void*)a.y, a.dy, (const void*)a.dx, (const void*)a.dw, (const void*)a.db})
     if (!aligned_to(p, 2)) return fail(EXTERND_EINVAL, "pointers must be aligned to their type");
   if (!aligned_to(a.z, 4)) return fail(EXTERND_EINVAL, "z must be aligned to its type");
+  return EXTERND_OK;
+}
+
+// Sizes of a mixture-of-experts call; rows = 0: of the router alone.
+int check_moe_sizes(int64_t tokens, int64_t cols, int64_t rows, int64_t experts, int32_t top) {
+  if (tokens < 0 || bad_size(experts, cols) || (rows != 0 && bad_size(rows, cols)))
+    return fail(EXTERND_EINVAL, "bad number of tokens or shape of the weights");
+  if (top < 1 || top > experts) return fail(EXTERND_EINVAL, "top must be 1 to the number of experts");
+  if (experts > externd::kMoeExperts || top > externd::kMoeTop || cols > kMaxGated || rows > kMaxGated)
+    return fail(EXTERND_EUNSUPPORTED, "at most %d experts, %d of them for a token, and 2^21 rows and columns",
+                externd::kMoeExperts, externd::kMoeTop);
+  if (tokens > EXTERND_MOE_SLOTS / top) return fail(EXTERND_EUNSUPPORTED, "tokens * top must be at most %d", EXTERND_MOE_SLOTS);
+  return EXTERND_OK;
+}
+
+// A call of the whole layer (wr and w given), of the router (w null) or of the experts (wr null).
+int moe_call(externd::MoeArgs& a, const externd_moe_weights* w, int64_t experts, int64_t cols, void* stream, void* workspace,
+             size_t workspace_bytes) {
+  const bool router = a.ids_out != nullptr || a.weights_out != nullptr || a.wr != nullptr || !w;
+  if (bad_dtype(a.dtype)) return fail(EXTERND_EINVAL, "unknown dtype %d", a.dtype);
+  if (a.dtype == EXTERND_F32) return fail(EXTERND_EUNSUPPORTED, "the experts take bf16 or fp16");
+  if (w && bad_act(a.act)) return fail(EXTERND_EINVAL, "unknown activation %d", a.act);
+  if (router && a.wr_dtype != a.dtype && a.wr_dtype != EXTERND_F32) return fail(EXTERND_EINVAL, "the router must be of dtype or fp32");
+  if (w && w->rows < 1) return fail(EXTERND_EINVAL, "bad shape of the weights");
+  int st = check_moe_sizes(a.tokens, cols, w ? w->rows : 0, experts, a.top);
+  if (st != EXTERND_OK) return st;
+  if (bad_stride(a.ldx, cols) || (router && bad_stride(a.ldr, cols))) return fail(EXTERND_EINVAL, "row strides must be at least the columns");
+  if (w && (bad_stride(w->up_ld, cols) || bad_stride(w->down_ld, w->rows) || bad_stride(w->up_stride, 1) || bad_stride(w->down_stride, 1)))
+    return fail(EXTERND_EINVAL, "strides of the experts: rows at least as long as they are, experts at least 1");
+  if (a.tokens == 0) return EXTERND_OK;
+  if (!a.x || (router && (!a.wr || !a.ids_out || !a.weights_out)) || (!router && (!a.ids || !a.weights)) ||
+      (w && (!w->wg || !w->wu || !w->wd || !a.y)))
+    return fail(EXTERND_EINVAL, "null pointer");
+  if (!aligned_to(a.x, 2) || !aligned_to(a.wr, dtype_bytes(a.wr_dtype)) || !aligned_to(a.y, 2) || !aligned_to(a.ids, 4) ||
+      !aligned_to(a.weights, 4) || !aligned_to(a.ids_out, 4) || !aligned_to(a.weights_out, 4) ||
+      (w && (!aligned_to(w->wg, 2) || !aligned_to(w->wu, 2) || !aligned_to(w->wd, 2))))
+    return fail(EXTERND_EINVAL, "pointers must be aligned to their type");
+  a.cols = cols;
+  if (w) a.w = *w;
+  a.w.experts = experts;
+  const externd::MoeSpace size = externd::moe_space(nullptr, a.tokens, experts, a.top, w ? w->rows : 0, cols, router, w != nullptr);
+  const int64_t slots = a.slots(), wr_bytes = (int64_t)dtype_bytes(a.wr_dtype);
+  const Region none = packed(nullptr, 0, ""), ry = w ? packed(a.y, 2 * a.tokens * cols, "y") : none,
+               ri = packed(a.ids_out, 4 * slots, "ids"), rw = packed(a.weights_out, 4 * slots, "weights"),
+               rs = packed(workspace, (int64_t)size.bytes, "workspace");
+  // an expert's matrix as one stretch
+  auto matrices = [&](const void* p, int64_t rows, int64_t width, int64_t ld, int64_t stride, const char* name) {
+    return Region{p, experts, 2 * ((rows - 1) * ld + width), 2 * stride, name};
+  };
+  st = check_apart({ry, ri, rw, rs},
+                   {{a.x, a.tokens, 2 * cols, 2 * a.ldx, "x"},
+                    router ? Region{a.wr, experts, wr_bytes * cols, wr_bytes * a.ldr, "wr"} : none,
+                    router ? none : packed(a.ids, 4 * slots, "ids"), router ? none : packed(a.weights, 4 * slots, "weights"),
+                    w ? matrices(w->wg, w->rows, cols, w->up_ld, w->up_stride, "wg") : none,
+                    w ? matrices(w->wu, w->rows, cols, w->up_ld, w->up_stride, "wu") : none,
+                    w ? matrices(w->wd, cols, w->rows, w->down_ld, w->down_stride, "wd") : none});
+  if (st != EXTERND_OK) return st;
+  if ((st = check_device(&a.cus)) != EXTERND_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  Workspace ws;
+  if ((st = op_ws(ws, workspace, workspace_bytes, size.bytes, s)) != EXTERND_OK) return st;
+  const externd::MoeSpace space = externd::moe_space(ws.ptr, a.tokens, experts, a.top, w ? w->rows : 0, cols, router, w != nullptr);
+  if (router) {
+    a.ids = a.ids_out;
+    a.weights = a.weights_out;
+  }
+  hipError_t e = router ? externd::run_moe_route(a, space, w != nullptr, s) : externd::run_moe_plan(a, space, s);
+  if (e == hipSuccess && w) e = externd::run_moe_experts(a, space, s);
+  if (e != hipSuccess) return hip_fail(e, "mixture of experts");
   return EXTERND_OK;
 }
 
@@ -985,6 +1055,52 @@ int externd_linear_backward(const void* x, int64_t tokens, int64_t cols, int64_t
   hipError_t e = externd::run_linear_backward(a, ws.ptr, s);
   if (e != hipSuccess) return hip_fail(e, "linear backward");
   return EXTERND_OK;
+}
+
+size_t externd_moe_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int64_t experts, int32_t top) {
+  if (tokens < 1 || rows < 0 || check_moe_sizes(tokens, cols, rows, experts, top) != EXTERND_OK) return 0;
+  return externd::moe_space(nullptr, tokens, experts, top, rows, cols, true, rows > 0).bytes;
+}
+
+int externd_moe_route(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* wr, int64_t experts, int64_t ldr,
+                      int32_t wr_dtype, int32_t dtype, int32_t top, int32_t normalize, void* stream, int32_t* ids,
+                      float* weights, void* workspace, size_t workspace_bytes) {
+  externd::MoeArgs a = {};
+  a.x = x; a.wr = wr;
+  a.tokens = tokens; a.ldx = ldx; a.ldr = ldr;
+  a.wr_dtype = wr_dtype; a.dtype = dtype;
+  a.top = top; a.normalize = normalize != 0;
+  a.ids_out = ids; a.weights_out = weights;
+  return moe_call(a, nullptr, experts, cols, stream, workspace, workspace_bytes);
+}
+
+int externd_moe_experts(const void* x, int64_t tokens, int64_t ldx, const int32_t* ids, const float* weights, int32_t top,
+                        const externd_moe_weights* w, int32_t dtype, int32_t act, void* stream, void* y, void* workspace,
+                        size_t workspace_bytes) {
+  if (!w) return fail(EXTERND_EINVAL, "null weights");
+  externd::MoeArgs a = {};
+  a.x = x;
+  a.tokens = tokens; a.ldx = ldx;
+  a.dtype = dtype; a.act = act;
+  a.top = top;
+  a.ids = ids; a.weights = weights;
+  a.y = y;
+  return moe_call(a, w, w->experts, w->cols, stream, workspace, workspace_bytes);
+}
+
+int externd_moe(const void* x, int64_t tokens, int64_t ldx, const void* wr, int64_t ldr, int32_t wr_dtype, int32_t top,
+                int32_t normalize, const externd_moe_weights* w, int32_t dtype, int32_t act, void* stream, void* y,
+                int32_t* ids, float* weights, void* workspace, size_t workspace_bytes) {
+  if (!w) return fail(EXTERND_EINVAL, "null weights");
+  if (tokens > 0 && (!wr || !ids || !weights)) return fail(EXTERND_EINVAL, "null pointer");
+  externd::MoeArgs a = {};
+  a.x = x; a.wr = wr;
+  a.tokens = tokens; a.ldx = ldx; a.ldr = ldr;
+  a.wr_dtype = wr_dtype; a.dtype = dtype; a.act = act;
+  a.top = top; a.normalize = normalize != 0;
+  a.ids_out = ids; a.weights_out = weights;
+  a.y = y;
+  return moe_call(a, w, w->experts, w->cols, stream, workspace, workspace_bytes);
 }
 
 }  // extern "C"

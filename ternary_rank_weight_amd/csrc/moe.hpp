@@ -1,0 +1,56 @@
+// The mixture-of-experts layer for a few tokens: arguments and workspace shared by the C ABI, the
+// routing (moe_route.hip) and the experts' products (moe.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/externd.h"
+
+namespace externd {
+
+constexpr int kMoeExperts = 1024;   // most experts: a thread each when the slots are sorted
+constexpr int kMoeTop = 64;         // most experts of a token
+constexpr int kMoeGroup = 16;       // slots that go through an expert's weights together
+
+// A slot is one of a token's choices: slot = token top + choice.  A group is up to 16 slots of one expert.
+struct MoeGroup {
+  int expert, first, count, pad;    // its slots: plan.slots[first .. first + count - 1]
+};
+
+struct MoeArgs {
+  const void *x, *wr;
+  int64_t tokens, cols, ldx, ldr;   // ldr: rows of the router
+  int wr_dtype, dtype, act, top, normalize;
+  externd_moe_weights w;
+  const int32_t* ids;               // the choice, and its weights: read by the experts
+  const float* weights;
+  int32_t* ids_out;                 // written by the router
+  float* weights_out;
+  void* y;
+  int cus;
+  int64_t slots() const { return tokens * top; }
+};
+
+// Where things lie in the workspace.
+struct MoeSpace {
+  double* logits;      // tokens x experts
+  int32_t* groups_n;   // number of groups
+  MoeGroup* groups;
+  int32_t* sorted;     // slots by expert
+  uint32_t* tops;      // fp16: the largest magnitude of each slot's h, as bits of fp32
+  float* h;            // slots x ldh
+  float* part;         // slots x cols: what each slot's expert gives
+  int64_t ldh;
+  size_t bytes;
+};
+int64_t moe_most_groups(int64_t slots, int64_t experts);
+// experts_too: for the experts' products; without, for the router alone
+MoeSpace moe_space(void* base, int64_t tokens, int64_t experts, int64_t top, int64_t rows, int64_t cols, bool router, bool experts_too);
+
+// Logits, choice and weights; and, where plan is given, the groups.
+hipError_t run_moe_route(const MoeArgs& a, const MoeSpace& s, bool plan, hipStream_t stream);
+// The groups of a choice that was made elsewhere.
+hipError_t run_moe_plan(const MoeArgs& a, const MoeSpace& s, hipStream_t stream);
+hipError_t run_moe_experts(const MoeArgs& a, const MoeSpace& s, hipStream_t stream);
+
+}  // namespace externd

@@ -131,3 +131,52 @@ def test_linear_backward():
     assert bad(dx=H, z=None) and bad(dx=H, dy=None) and bad(dx=H, x=None) and bad(act=5, dx=H) and not bad(dx=H, z=None, act=3)
     assert linear_backward() == 0 and linear_backward(tokens=0, dx=H) == 0
     assert trw._linear_forward_ws(0, 64, 32, 1) == 0 and trw._linear_backward_ws(4, 64, 32, 7, 1) == 0
+
+
+H, I, J = (ctypes.c_void_p((k + 10) << 32) for k in range(3))
+
+
+def experts(**kw):
+    w = trw._MoeWeights(B, C, D, 6, 32, 64, 64, 2048, 32, 2048)
+    for k, v in kw.items():
+        setattr(w, k, v)
+    return w
+
+
+def moe(x=A, wr=F, y=G, ids=H, weights=I, top=2, tokens=4, dtype=1, wr_dtype=1, act=0, ws=None, wsb=0, ldx=64, ldr=64, **kw):
+    return trw._moe(x, tokens, ldx, wr, ldr, wr_dtype, top, 1, ctypes.byref(experts(**kw)), dtype, act, None, y, ids, weights, ws, wsb)
+
+
+def test_moe():
+    # 6 experts of 32 x 64: 24576 bytes of each matrix; y 512 bytes, ids and weights 32
+    assert not refused(moe()) and moe(tokens=0) == 0 and not refused(moe(wr_dtype=0)) and not refused(moe(wu=B.value))
+    for at, name in ((A, "x"), (F, "wr"), (B, "wg"), (C, "wu"), (D, "wd")):
+        assert refused(moe(y=at), "y", name) and refused(moe(ids=at), "ids", name) and refused(moe(weights=at), "weights", name)
+        if at is not A and at is not F:
+            assert refused(moe(y=off(at, 24574)), "y", name) and not refused(moe(y=off(at, 24576)))
+    assert refused(moe(ids=off(G, 508)), "ids", "y") and not refused(moe(ids=off(G, 512)))
+    assert refused(moe(weights=off(H, 28)), "weights", "ids")
+    # between two experts that lie apart
+    assert not refused(moe(y=off(B, 4096), up_stride=1 << 20)) and refused(moe(y=off(B, (1 << 21) + 2), up_stride=1 << 20))
+    need = trw._moe_ws(4, 64, 32, 6, 2)
+    assert refused(moe(ws=G, wsb=need), "workspace", "y") and refused(moe(ws=off(A, 256), wsb=need), "workspace", "x")
+    assert not refused(moe(ws=J, wsb=need)) and trw._moe_ws(4, 64, 0, 6, 2) < need
+    bad = lambda **kw: moe(**kw) == EINVAL
+    assert bad(x=None) and bad(wr=None) and bad(y=None) and bad(ids=None) and bad(weights=None) and bad(wg=None) and bad(wd=None)
+    assert bad(top=0) and bad(top=7) and bad(tokens=-1) and bad(act=3) and bad(dtype=5) and bad(wr_dtype=2) and bad(ldx=63) and bad(ldr=63)
+    assert bad(up_ld=63) and bad(down_ld=31) and bad(up_stride=0) and bad(down_stride=-1) and bad(rows=0) and bad(experts=0)
+    assert bad(x=off(A, 1)) and bad(ids=off(H, 2)) and bad(wu=C.value + 1) and bad(wr=off(F, 2), wr_dtype=0)
+    unsupported = lambda **kw: moe(**kw) == 4
+    assert unsupported(dtype=0) and unsupported(experts=1025) and unsupported(top=65, experts=100) and unsupported(tokens=4097)
+    assert unsupported(cols=(1 << 21) + 64, up_ld=1 << 22, ldx=1 << 22, ldr=1 << 22)
+    assert trw._moe_ws(0, 64, 32, 6, 2) == 0 and trw._moe_ws(4, 64, 32, 6, 7) == 0 and trw._moe_ws(4097, 64, 32, 6, 2) == 0
+
+
+def test_moe_parts():
+    route = lambda ids=H, weights=I, wr=F: trw._moe_route(A, 4, 64, 64, wr, 6, 64, 1, 1, 2, 1, None, ids, weights, None, 0)
+    assert not refused(route()) and refused(route(ids=A), "ids", "x") and refused(route(weights=off(F, 766)), "weights", "wr")
+    assert route(ids=None) == EINVAL and route(wr=None) == EINVAL
+    given = lambda y=G, ids=H, weights=I: trw._moe_experts(A, 4, 64, ids, weights, 2, ctypes.byref(experts()), 1, 0, None, y, None, 0)
+    assert not refused(given()) and not refused(given(ids=A)) and refused(given(y=H), "y", "ids") and refused(given(y=off(I, 30)), "y", "weights")
+    assert given(ids=None) == EINVAL and given(weights=None) == EINVAL and given(y=None) == EINVAL
+    assert trw._moe_experts(A, 4, 64, H, I, 2, None, 1, 0, None, G, None, 0) == EINVAL
