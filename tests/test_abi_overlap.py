@@ -174,7 +174,7 @@ def test_moe():
 
 def test_moe_parts():
     route = lambda ids=H, weights=I, wr=F: trw._moe_route(A, 4, 64, 64, wr, 6, 64, 1, 1, 2, 1, None, ids, weights, None, 0)
-    assert not refused(route()) and refused(route(ids=A), "ids", "x") and refused(route(weights=off(F, 766)), "weights", "wr")
+    assert not refused(route()) and refused(route(ids=A), "ids", "x") and refused(route(weights=off(F, 764)), "weights", "wr")
     assert route(ids=None) == EINVAL and route(wr=None) == EINVAL
     given = lambda y=G, ids=H, weights=I: trw._moe_experts(A, 4, 64, ids, weights, 2, ctypes.byref(experts()), 1, 0, None, y, None, 0)
     assert not refused(given()) and not refused(given(ids=A)) and refused(given(y=H), "y", "ids") and refused(given(y=off(I, 30)), "y", "weights")
