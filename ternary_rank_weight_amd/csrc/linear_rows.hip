@@ -23,7 +23,7 @@ struct LinearRows {
 template <bool BF, int NT, int WV, bool AL>
 __global__ __launch_bounds__(WV * kWave) void k_linear_rows(LinearRows a) {
   __shared__ float red[WV][256];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane & 15, p = lane >> 4;
   const int64_t row0 = tile_row0(blockIdx.x, a.apart_bits);
   if (row0 >= a.rows) return;
@@ -36,7 +36,7 @@ __global__ __launch_bounds__(WV * kWave) void k_linear_rows(LinearRows a) {
   f32x4 acc[1][NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) acc[0][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  rows_product<BF, 1, NT, WV, AL, 1, 4>(w, shift, a.cols, wave, x, acc);
+  rows_product<BF, 1, NT, WV, AL, 1>(w, shift, (int)a.cols, wave, x, acc);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     if (n) __syncthreads();

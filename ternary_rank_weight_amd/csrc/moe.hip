@@ -2,8 +2,9 @@
 //   h = act(Wg_e x) (Wu_e x) for every slot (a token and one of its experts e),
 //   y[t] = the sum over t's slots of weight * Wd_e h.
 // Bound by the weights of the experts that are chosen, which are read once for each group of up to 16 of an expert's
-// slots (rows_core.hpp).  h and each slot's result are fp32: the layer's output is rounded once.  h enters the second
-// product in two 16-bit parts; in fp16, whose range it may leave, multiplied by a power of two for each slot.
+// slots (rows_core.hpp).  Each slot's result is fp32, and h enters the second product in two 16-bit parts, the rounded
+// value and what the rounding took away: the layer's output is rounded once.  bf16's parts are written by the first
+// product; fp16's, whose range h may leave, in a pass of their own, multiplied by a power of two for each slot.
 #include <algorithm>
 
 #include "activation.hpp"
@@ -11,140 +12,264 @@
 #include "frag.hpp"
 #include "gated.hpp"
 #include "moe.hpp"
+#include "moe_choose.hpp"
 #include "rows_core.hpp"
 
 namespace externd {
 
 namespace {
 
+// A value as two of 16 bits: rounded, and what the rounding took away.
+template <bool BF>
+__device__ __forceinline__ void split16(float v, uint32_t& hi, uint32_t& lo) {
+  hi = f32_to_16<BF>(v);
+  const float rest = v - f32_from_16<BF>(hi);
+  lo = __builtin_isfinite(rest) ? f32_to_16<BF>(rest) : 0u;   // (infinite and NaN are in the first part)
+}
+
 struct UpArgs {
   const uint16_t *x, *w[2];
   int64_t cols, rows, ldx, ldw, stride;   // stride: from one expert to the next
   int top, apart_bits, act;
-  const int32_t* groups_n;
-  const MoeGroup* groups;
-  const int32_t* sorted;
+  MoeGroup* groups;
   uint32_t* tops;
-  float* h;
-  int64_t ldh;
+  float* h;          // fp16
+  uint16_t* parts;   // bf16
+  int64_t ldh, rest;
+  // one token, whose choice this kernel makes
+  const double* logits;
+  int experts, normalize;
+  int32_t* ids;
+  float* weights;
 };
 
-template <bool BF, int WV, bool AL, int NX>
-__global__ __launch_bounds__(WV * kWave) void k_moe_up(UpArgs a) {
-  __shared__ float red[WV][2][256];
-  if ((int)blockIdx.y >= *a.groups_n) return;
-  const MoeGroup g = a.groups[blockIdx.y];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int r = lane & 15, p = lane >> 4;
-  const int64_t row0 = tile_row0(blockIdx.x, a.apart_bits);
-  if (row0 >= a.rows) return;
-  const int64_t mine = row0 + ((int64_t)r << a.apart_bits), row = mine < a.rows ? mine : row0;   // (past the end: the first again)
-  const int64_t at_expert = g.expert * a.stride;
-  const uint16_t* const w[2] = {a.w[0] + at_expert + row * a.ldw, a.w[1] + at_expert + row * a.ldw};
-  const int shift[2] = {AL ? 0 : shift_of(a.w[0] + at_expert + row0 * a.ldw), AL ? 0 : shift_of(a.w[1] + at_expert + row0 * a.ldw)};
-  Rows16<1, AL> x;
-  x.row[0] = a.x + (int64_t)(a.sorted[g.first + min(r, g.count - 1)] / a.top) * a.ldx;   // (a missing slot: the last)
+// A workgroup of WV waves takes WV / SW tiles of 16 hidden units, SW waves each, of one group of slots.
+// ONE: a single token.  Every wave works the choice out from the logits, as far as the group's own; the
+// first workgroup, which does so to the end, writes it down.
+template <bool BF, int WV, int SW, bool AL, int NX, bool ONE>
+__global__ __launch_bounds__(WV * kWave, 4) void k_moe_up(UpArgs a) {
+  __shared__ float red[SW > 1 ? WV : 1][2][256];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r = lane & 15, p = lane >> 4, group = blockIdx.y;
+  int expert, count = 1, slot = group;   // slot: the lane's (a missing one: the last)
+  if constexpr (ONE) {
+    int chosen;
+    float weight;
+    const bool all = blockIdx.x == 0 && blockIdx.y == 0 && wave == 0;
+    expert = choose<4>(a.logits, a.experts, all ? a.top : group + 1, a.normalize, chosen, weight);
+    if (all) {
+      expert = __builtin_amdgcn_readlane(chosen, 0);
+      if (lane < a.top) {
+        a.ids[lane] = chosen;
+        a.weights[lane] = weight;
+        a.groups[lane].expert = chosen;
+        a.groups[lane].count = 1;
+        for (int k = 0; k < kMoeGroup; ++k) a.groups[lane].slot[k] = lane;
+      }
+    }
+  } else {
+    const MoeGroup& g = a.groups[group];
+    expert = g.expert;
+    count = g.count;
+    slot = g.slot[r];
+    if (expert < 0) return;
+  }
+  const int64_t tile = (int64_t)blockIdx.x * (WV / SW) + wave / SW, row0 = tile_row0(tile, a.apart_bits);
   f32x4 acc[2][1];
   acc[0][0] = acc[1][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-  rows_product<BF, 2, 1, WV, AL, NX, 3>(w, shift, a.cols, wave, x, acc);
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[wave][q][(4 * p + e) * 16 + r] = acc[q][0][e];
-  __syncthreads();
-  for (int o = threadIdx.x; o < 256; o += WV * kWave) {
-    const int64_t unit = row0 + ((int64_t)(o & 15) << a.apart_bits);
-    const bool in = (o >> 4) < g.count && unit < a.rows;
-    const int slot = a.sorted[g.first + min(o >> 4, g.count - 1)];
-    float v[2] = {0.f, 0.f};
+  if (row0 < a.rows) {
+    const int64_t mine = row0 + ((int64_t)r << a.apart_bits), row = mine < a.rows ? mine : row0;   // (past the end: the first again)
+    const uint16_t* const base[2] = {a.w[0] + expert * a.stride, a.w[1] + expert * a.stride};
+    const uint16_t* const w[2] = {base[0] + row * a.ldw, base[1] + row * a.ldw};
+    const int shift[2] = {AL ? 0 : shift_of(base[0] + row0 * a.ldw), AL ? 0 : shift_of(base[1] + row0 * a.ldw)};
+    Rows16<1, AL> x;
+    x.row[0] = a.x + (ONE ? 0 : (int64_t)(slot / a.top) * a.ldx);
+    rows_product<BF, 2, 1, SW, AL, NX>(w, shift, (int)a.cols, wave % SW, x, acc);
+  }
+  if constexpr (SW > 1) {
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int k = 0; k < WV; ++k) v[q] += red[k][q][o];
+      for (int e = 0; e < 4; ++e) red[wave][q][(4 * p + e) * 16 + r] = acc[q][0][e];
+    __syncthreads();
+  }
+  if (row0 >= a.rows) return;
+  // v: both projections of slot s of the group (ss: its number), unit k of the tile
+  auto put = [&](int s, int ss, int k, const float (&v)[2]) {
+    const int64_t unit = row0 + ((int64_t)k << a.apart_bits);
+    const bool in = s < count && unit < a.rows;
     const float h = act_value(a.act, v[0]) * v[1];
-    if (in) a.h[slot * a.ldh + unit] = h;
-    if constexpr (!BF) {
+    if constexpr (BF) {
+      if (in) {
+        uint32_t hi, lo;
+        split16<true>(h, hi, lo);
+        a.parts[ss * a.ldh + unit] = (uint16_t)hi;
+        a.parts[a.rest + ss * a.ldh + unit] = (uint16_t)lo;
+      }
+    } else {
+      if (in) a.h[ss * a.ldh + unit] = h;
       float size = in && __builtin_isfinite(h) ? fabsf(h) : 0.f;
 #pragma unroll
-      for (int k = 8; k > 0; k >>= 1) size = fmaxf(size, __shfl_xor(size, k, 16));
-      if (in && (o & 15) == 0) atomicMax(a.tops + slot, __float_as_uint(size));
+      for (int w = 8; w > 0; w >>= 1) size = fmaxf(size, __shfl_xor(size, w, 16));
+      if (s < count && k == 0) atomicMax(a.tops + ss, __float_as_uint(size));
     }
+  };
+  if constexpr (SW > 1) {
+    for (int o = wave % SW * kWave + lane; o < 256; o += SW * kWave) {
+      float v[2] = {0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int k = 0; k < SW; ++k) v[q] += red[wave / SW * SW + k][q][o];
+      put(o >> 4, ONE ? group : a.groups[group].slot[o >> 4], o & 15, v);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float v[2] = {acc[0][0][e], acc[1][0][e]};
+      put(4 * p + e, ONE ? group : a.groups[group].slot[4 * p + e], r, v);
+    }
+  }
+}
+
+// h of every slot in two parts, scaled so that its largest is in fp16's range.
+__global__ __launch_bounds__(256) void k_moe_split(const float* __restrict__ h, const uint32_t* __restrict__ tops, int64_t slots,
+                                                    int64_t ldh, uint16_t* __restrict__ parts) {
+  const int64_t count = slots * ldh;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < count; i += (int64_t)gridDim.x * 1024) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(h + i);
+    const float scale = scale_of(tops[i / ldh]);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split16<false>(v[j] * scale, hi[j], lo[j]);
+    *reinterpret_cast<uint2*>(parts + i) = uint2{hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16)};
+    *reinterpret_cast<uint2*>(parts + count + i) = uint2{lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16)};
   }
 }
 
 struct DownArgs {
-  const float* h;
+  const uint16_t* parts;
   const uint16_t* w;
-  int64_t cols, rows, ldh, ldw, stride;   // rows: of each expert's matrix, the layer's outputs
+  int64_t cols, rows, ldh, rest, ldw, stride;   // rows: of each expert's matrix, the layer's outputs
   int apart_bits;
-  const int32_t* groups_n;
   const MoeGroup* groups;
-  const int32_t* sorted;
   const uint32_t* tops;
   float* part;
 };
 
-template <bool BF, int WV, bool AL>
-__global__ __launch_bounds__(WV * kWave) void k_moe_down(DownArgs a) {
-  __shared__ float red[WV][256];
-  if ((int)blockIdx.y >= *a.groups_n) return;
-  const MoeGroup g = a.groups[blockIdx.y];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+// As k_moe_up, for tiles of 16 outputs.  RT > 1 (and SW = 1): a wave takes that many tiles at once, whose rows start
+// alike, so that h is read once for all of them.
+template <bool BF, int WV, int SW, int RT, bool AL>
+__global__ __launch_bounds__(WV * kWave, 4) void k_moe_down(DownArgs a) {
+  static_assert(RT == 1 || SW == 1, "a wave's own tiles");
+  __shared__ float red[SW > 1 ? WV : 1][256];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane & 15, p = lane >> 4;
-  const int64_t row0 = tile_row0(blockIdx.x, a.apart_bits);
-  if (row0 >= a.rows) return;
-  const int64_t mine = row0 + ((int64_t)r << a.apart_bits);
-  const uint16_t* const base = a.w + g.expert * a.stride;
-  const uint16_t* const w[1] = {base + (mine < a.rows ? mine : row0) * a.ldw};
-  const int shift[1] = {AL ? 0 : shift_of(base + row0 * a.ldw)};
-  const int slot = a.sorted[g.first + min(r, g.count - 1)];
-  Rows32<BF, 1> x;
-  x.row[0] = a.h + slot * a.ldh;
-  x.scale[0] = BF ? 1.f : scale_of(a.tops[slot]);
-  f32x4 acc[1][1];
-  acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-  rows_product<BF, 1, 1, WV, AL, 1, 4>(w, shift, a.cols, wave, x, acc);
+  const MoeGroup& g = a.groups[blockIdx.y];
+  const int expert = g.expert, count = g.count, slot = g.slot[r];
+  if (expert < 0) return;
+  const int64_t at = (int64_t)blockIdx.x * (WV / SW) + wave / SW;
+  // tiles 2^apart_bits apart
+  const int64_t tile = ((at >> a.apart_bits) * RT << a.apart_bits) + (at & (((int64_t)1 << a.apart_bits) - 1));
+  int64_t row0[RT];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) red[wave][(4 * p + e) * 16 + r] = acc[0][0][e];
-  __syncthreads();
-  for (int o = threadIdx.x; o < 256; o += WV * kWave) {
-    const int64_t row = row0 + ((int64_t)(o & 15) << a.apart_bits);
-    if ((o >> 4) >= g.count || row >= a.rows) continue;
-    const int64_t to = a.sorted[g.first + (o >> 4)];
-    float v = 0.f;
+  for (int q = 0; q < RT; ++q) row0[q] = tile_row0(tile + ((int64_t)q << a.apart_bits), a.apart_bits);
+  f32x4 acc[RT][1];
 #pragma unroll
-    for (int k = 0; k < WV; ++k) v += red[k][o];
+  for (int q = 0; q < RT; ++q) acc[q][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (row0[0] < a.rows) {
+    const uint16_t* const base = a.w + expert * a.stride;
+    const uint16_t* w[RT];
+    int shift[RT];
+#pragma unroll
+    for (int q = 0; q < RT; ++q) {
+      const int64_t mine = row0[q] + ((int64_t)r << a.apart_bits);
+      w[q] = base + (mine < a.rows ? mine : row0[0]) * a.ldw;   // (past the end: the first again)
+      shift[q] = AL ? 0 : shift_of(base + row0[0] * a.ldw);
+    }
+    RowsParts<AL> x;
+    x.part.row[0] = a.parts + slot * a.ldh;
+    x.part.row[1] = x.part.row[0] + a.rest;
+    rows_product<BF, RT, 1, SW, AL, 1>(w, shift, (int)a.cols, wave % SW, x, acc);
+  }
+  auto put = [&](int s, int64_t row, float v) {
+    if (s >= count || row >= a.rows) return;
+    const int64_t to = g.slot[s];
     a.part[to * a.rows + row] = BF ? v : v * unscale_of(a.tops[to]);
+  };
+  if constexpr (SW > 1) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[wave][(4 * p + e) * 16 + r] = acc[0][0][e];
+    __syncthreads();
+    for (int o = wave % SW * kWave + lane; o < 256; o += SW * kWave) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < SW; ++k) v += red[wave / SW * SW + k][o];
+      put(o >> 4, row0[0] + ((int64_t)(o & 15) << a.apart_bits), v);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < RT; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) put(4 * p + e, row0[q] + ((int64_t)r << a.apart_bits), acc[q][0][e]);
   }
 }
 
 // y[t] = the sum over t's choices of weight * part, in the order of the choices; a choice outside the experts
-// adds nothing.
+// adds nothing.  (Done instead by the workgroup of the second product that comes last to a column of outputs, it cost
+// more than this pass: each has to wait for its stores and for the count, 150 us against 108 and 7 for 32 tokens, 8 of 128
+// experts of 768 x 2560.)
 template <bool BF>
 __global__ __launch_bounds__(256) void k_moe_join(const float* __restrict__ part, const int32_t* __restrict__ ids,
-                                                   const float* __restrict__ weights, int64_t tokens, int64_t cols, int top,
-                                                   int experts, uint16_t* __restrict__ y) {
-  const int64_t count = tokens * cols;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / cols, c = i - t * cols;
-    float v = 0.f;
-    for (int j = 0; j < top; ++j) {
-      const int64_t slot = t * top + j;
-      const int e = ids[slot];
-      if (e >= 0 && e < experts) v = fmaf(weights[slot], part[slot * cols + c], v);
-    }
-    y[i] = (uint16_t)f32_to_16<BF>(v);
+                                                   const float* __restrict__ weights, int64_t cols, int top, int experts,
+                                                   uint16_t* __restrict__ y) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+  if (c >= cols) return;
+  float v = 0.f;
+#pragma unroll 8
+  for (int j = 0; j < top; ++j) {
+    const int64_t slot = t * top + j;
+    const int e = ids[slot];
+    if (e >= 0 && e < experts) v = fmaf(weights[slot], part[slot * cols + c], v);
   }
+  y[t * cols + c] = (uint16_t)f32_to_16<BF>(v);
 }
 
 bool pieces_aligned(const void* p, int64_t stride, int64_t ld, int64_t cols) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0 && ld % 8 == 0 && cols % 8 == 0;
 }
 
+// Waves that share a tile: as many as bring the launch to sixteen a compute unit.
+int waves_a_tile(int64_t tiles, int64_t groups, int cus, int least, int most) {
+  int sw = least;
+  while (sw < most && tiles * groups * sw < (int64_t)cus * 16) sw *= 2;
+  return sw;
+}
+
+template <bool BF, int SW, bool ONE>
+void launch_up(const UpArgs& u, bool al, bool alike, unsigned groups, hipStream_t s) {
+  constexpr int WV = SW > 8 ? SW : 8;
+  const int64_t tiles = rows_tiles(u.rows, u.apart_bits);
+  const dim3 grid((unsigned)((tiles + WV / SW - 1) / (WV / SW)), groups), block(WV * kWave);
+  if (al) hipLaunchKernelGGL((k_moe_up<BF, WV, SW, true, 1, ONE>), grid, block, 0, s, u);
+  else if (alike) hipLaunchKernelGGL((k_moe_up<BF, WV, SW, false, 1, ONE>), grid, block, 0, s, u);
+  else hipLaunchKernelGGL((k_moe_up<BF, WV, SW, false, 2, ONE>), grid, block, 0, s, u);
+}
+
+template <bool BF, int SW, int RT>
+void launch_down(const DownArgs& d, bool al, unsigned groups, hipStream_t s) {
+  constexpr int WV = SW > 8 ? SW : 8;
+  const int64_t row_groups = (d.rows + ((int64_t)16 << d.apart_bits) - 1) / ((int64_t)16 << d.apart_bits);
+  const int64_t units = (row_groups + RT - 1) / RT << d.apart_bits;   // of RT tiles
+  const dim3 grid((unsigned)((units + WV / SW - 1) / (WV / SW)), groups), block(WV * kWave);
+  if (al) hipLaunchKernelGGL((k_moe_down<BF, WV, SW, RT, true>), grid, block, 0, s, d);
+  else hipLaunchKernelGGL((k_moe_down<BF, WV, SW, RT, false>), grid, block, 0, s, d);
+}
+
 template <bool BF>
-hipError_t experts(const MoeArgs& a, const MoeSpace& s, hipStream_t stream) {
+hipError_t experts(const MoeArgs& a, const MoeSpace& s, bool one, hipStream_t stream) {
   const externd_moe_weights& w = a.w;
-  const unsigned groups = (unsigned)moe_most_groups(a.slots(), w.experts);
+  const int64_t groups = moe_most_groups(a.slots(), w.experts);
   UpArgs u = {};
   u.x = static_cast<const uint16_t*>(a.x);
   u.w[0] = static_cast<const uint16_t*>(w.wg);
@@ -157,24 +282,41 @@ hipError_t experts(const MoeArgs& a, const MoeSpace& s, hipStream_t stream) {
   u.top = a.top;
   u.apart_bits = rows_apart_bits(w.up_ld);
   u.act = a.act;
-  u.groups_n = s.groups_n;
   u.groups = s.groups;
-  u.sorted = s.sorted;
   u.tops = s.tops;
   u.h = s.h;
+  u.parts = s.parts;
   u.ldh = s.ldh;
-  constexpr int WV = 8;
-  const dim3 block(WV * kWave), up((unsigned)rows_tiles(w.rows, u.apart_bits), groups);
+  u.rest = a.slots() * s.ldh;
+  u.logits = s.logits;
+  u.experts = (int)w.experts;
+  u.normalize = a.normalize;
+  u.ids = a.ids_out;
+  u.weights = a.weights_out;
   const bool al = pieces_aligned(w.wg, w.up_stride, w.up_ld, a.cols) && pieces_aligned(w.wu, w.up_stride, w.up_ld, a.cols) &&
                   pieces_aligned(a.x, 0, a.ldx, a.cols);
   const bool alike = ((reinterpret_cast<uintptr_t>(w.wg) ^ reinterpret_cast<uintptr_t>(w.wu)) & 15) == 0;
-  if (al) hipLaunchKernelGGL((k_moe_up<BF, WV, true, 1>), up, block, 0, stream, u);
-  else if (alike) hipLaunchKernelGGL((k_moe_up<BF, WV, false, 1>), up, block, 0, stream, u);
-  else hipLaunchKernelGGL((k_moe_up<BF, WV, false, 2>), up, block, 0, stream, u);
+  const int up = waves_a_tile(rows_tiles(w.rows, u.apart_bits), groups, a.cus, 4, 16);
+  if (one) {
+    if (up == 4) launch_up<BF, 4, true>(u, al, alike, (unsigned)groups, stream);
+    else if (up == 8) launch_up<BF, 8, true>(u, al, alike, (unsigned)groups, stream);
+    else launch_up<BF, 16, true>(u, al, alike, (unsigned)groups, stream);
+  } else {
+    if (up == 4) launch_up<BF, 4, false>(u, al, alike, (unsigned)groups, stream);
+    else if (up == 8) launch_up<BF, 8, false>(u, al, alike, (unsigned)groups, stream);
+    else launch_up<BF, 16, false>(u, al, alike, (unsigned)groups, stream);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if constexpr (!BF) {
+    const int64_t quads = u.rest / 4;
+    hipLaunchKernelGGL(k_moe_split, dim3((unsigned)std::min<int64_t>((quads + 255) / 256, 4096)), dim3(256), 0, stream, s.h, s.tops,
+                       a.slots(), s.ldh, s.parts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   DownArgs d = {};
-  d.h = s.h;
+  d.parts = s.parts;
+  d.rest = u.rest;
   d.w = static_cast<const uint16_t*>(w.wd);
   d.cols = w.rows;
   d.rows = a.cols;
@@ -182,25 +324,28 @@ hipError_t experts(const MoeArgs& a, const MoeSpace& s, hipStream_t stream) {
   d.ldw = w.down_ld;
   d.stride = w.down_stride;
   d.apart_bits = rows_apart_bits(w.down_ld);
-  d.groups_n = s.groups_n;
   d.groups = s.groups;
-  d.sorted = s.sorted;
   d.tops = s.tops;
   d.part = s.part;
-  const dim3 down((unsigned)rows_tiles(a.cols, d.apart_bits), groups);
-  if (pieces_aligned(w.wd, w.down_stride, w.down_ld, w.rows)) hipLaunchKernelGGL((k_moe_down<BF, WV, true>), down, block, 0, stream, d);
-  else hipLaunchKernelGGL((k_moe_down<BF, WV, false>), down, block, 0, stream, d);
+  const bool dal = pieces_aligned(w.wd, w.down_stride, w.down_ld, w.rows);
+  const int64_t tiles = rows_tiles(a.cols, d.apart_bits);
+  const int down = waves_a_tile(tiles, groups, a.cus, 1, 16);
+  if (down == 1 && tiles * groups >= (int64_t)a.cus * 32) launch_down<BF, 1, 2>(d, dal, (unsigned)groups, stream);
+  else if (down == 1) launch_down<BF, 1, 1>(d, dal, (unsigned)groups, stream);
+  else if (down == 2) launch_down<BF, 2, 1>(d, dal, (unsigned)groups, stream);
+  else if (down == 4) launch_down<BF, 4, 1>(d, dal, (unsigned)groups, stream);
+  else if (down == 8) launch_down<BF, 8, 1>(d, dal, (unsigned)groups, stream);
+  else launch_down<BF, 16, 1>(d, dal, (unsigned)groups, stream);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const int64_t grid = std::min<int64_t>((a.tokens * a.cols + 255) / 256, 1 << 14);
-  hipLaunchKernelGGL(k_moe_join<BF>, dim3((unsigned)grid), dim3(256), 0, stream, s.part, a.ids, a.weights, a.tokens, a.cols, a.top,
-                     (int)w.experts, static_cast<uint16_t*>(a.y));
+  hipLaunchKernelGGL(k_moe_join<BF>, dim3((unsigned)((a.cols + 255) / 256), (unsigned)a.tokens), dim3(256), 0, stream, s.part, a.ids,
+                     a.weights, a.cols, a.top, (int)w.experts, static_cast<uint16_t*>(a.y));
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t run_moe_experts(const MoeArgs& a, const MoeSpace& s, hipStream_t stream) {
-  return a.dtype == EXTERND_BF16 ? experts<true>(a, s, stream) : experts<false>(a, s, stream);
+hipError_t run_moe_experts(const MoeArgs& a, const MoeSpace& s, bool one, hipStream_t stream) {
+  return a.dtype == EXTERND_BF16 ? experts<true>(a, s, one, stream) : experts<false>(a, s, one, stream);
 }
 
 }  // namespace externd

@@ -12,9 +12,11 @@ constexpr int kMoeExperts = 1024;   // most experts: a thread each when the slot
 constexpr int kMoeTop = 64;         // most experts of a token
 constexpr int kMoeGroup = 16;       // slots that go through an expert's weights together
 
-// A slot is one of a token's choices: slot = token top + choice.  A group is up to 16 slots of one expert.
+// A slot is one of a token's choices: slot = token top + choice.  A group is up to 16 slots of one expert; slots
+// past `count` repeat the last, and a group of expert -1 is not there.
 struct MoeGroup {
-  int expert, first, count, pad;    // its slots: plan.slots[first .. first + count - 1]
+  int expert, count, pad[2];
+  int slot[kMoeGroup];
 };
 
 struct MoeArgs {
@@ -34,11 +36,10 @@ struct MoeArgs {
 // Where things lie in the workspace.
 struct MoeSpace {
   double* logits;      // tokens x experts
-  int32_t* groups_n;   // number of groups
-  MoeGroup* groups;
-  int32_t* sorted;     // slots by expert
-  uint32_t* tops;      // fp16: the largest magnitude of each slot's h, as bits of fp32
-  float* h;            // slots x ldh
+  MoeGroup* groups;    // moe_most_groups of them
+  uint32_t* tops;      // fp16: the largest magnitude of each slot's h, as bits of fp32; cleared by a call's first kernel
+  float* h;            // fp16: slots x ldh
+  uint16_t* parts;     // h in two 16-bit parts, each slots x ldh
   float* part;         // slots x cols: what each slot's expert gives
   int64_t ldh;
   size_t bytes;
@@ -47,10 +48,13 @@ int64_t moe_most_groups(int64_t slots, int64_t experts);
 // experts_too: for the experts' products; without, for the router alone
 MoeSpace moe_space(void* base, int64_t tokens, int64_t experts, int64_t top, int64_t rows, int64_t cols, bool router, bool experts_too);
 
-// Logits, choice and weights; and, where plan is given, the groups.
-hipError_t run_moe_route(const MoeArgs& a, const MoeSpace& s, bool plan, hipStream_t stream);
-// The groups of a choice that was made elsewhere.
-hipError_t run_moe_plan(const MoeArgs& a, const MoeSpace& s, hipStream_t stream);
-hipError_t run_moe_experts(const MoeArgs& a, const MoeSpace& s, hipStream_t stream);
+// Whether the first product makes the choice itself (one token).
+inline bool moe_one(const MoeArgs& a) { return a.tokens == 1 && a.w.experts <= 256; }
+
+hipError_t run_moe_logits(const MoeArgs& a, const MoeSpace& s, hipStream_t stream);
+// Choice and weights from the logits, or a choice that was made elsewhere (router false); and, where plan is given, the groups.
+hipError_t run_moe_choose(const MoeArgs& a, const MoeSpace& s, bool router, bool plan, hipStream_t stream);
+// one: the choice is not made yet
+hipError_t run_moe_experts(const MoeArgs& a, const MoeSpace& s, bool one, hipStream_t stream);
 
 }  // namespace externd

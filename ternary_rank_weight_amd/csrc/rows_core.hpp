@@ -7,6 +7,8 @@
 // stride, so a workgroup takes sixteen of those, reads them from the multiple at or before their
 // start, and the vectors as many columns earlier.
 #pragma once
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "frag.hpp"
 
@@ -32,86 +34,131 @@ __device__ __forceinline__ int64_t tile_row0(int64_t tile, int apart_bits) {
 // Entries from the multiple of 16 bytes at or before p up to it.
 __device__ __forceinline__ int shift_of(const uint16_t* p) { return (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 7; }
 
-// The eight entries of a row from column c on, in a row of cols entries; those outside
-// are some entry of the row.
-template <typename T>
-__device__ __forceinline__ void load8_around(const T* row, int64_t c, int64_t cols, T (&v)[8]) {
+// Eight entries from a place of any alignment, as they are read: the dwords that hold them (as load8<false>).
+struct Any8 {
+  u32x4 v;
+  uint32_t w;
+  __device__ void load(const uint16_t* q) {
+    const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(q) >> 1) & 1u;
+    v = *reinterpret_cast<const u32x4_a4*>(q - odd);
+    w = *reinterpret_cast<const uint32_t*>(q - odd + (odd ? 8 : 6));
+  }
+  __device__ u32x4 get(const uint16_t* q) const {
+    const uint32_t sh = ((uint32_t)(reinterpret_cast<uintptr_t>(q) >> 1) & 1u) * 16u;
+    u32x4 r;
+    r.x = __builtin_amdgcn_alignbit(v.y, v.x, sh);
+    r.y = __builtin_amdgcn_alignbit(v.z, v.y, sh);
+    r.z = __builtin_amdgcn_alignbit(v.w, v.z, sh);
+    r.w = __builtin_amdgcn_alignbit(w, v.w, sh);
+    return r;
+  }
+};
+
+// The eight entries of a row from column c on, in a row of cols entries; those outside are 0.  They are read where
+// they are nearest and still inside, at column `at`, and what lies there before c or past its eight is masked: so two
+// edges of the same c and cols have the same entry of their row in each place.  AL: c and cols are multiples of 8.
+// A row of fewer than eight entries is read entry by entry.
+template <bool AL>
+struct Edge8 {
+  typename std::conditional<AL, u32x4, Any8>::type v;
+  __device__ static int nearest(int c, int cols) { return max(0, min(c, cols - 8)); }
+  __device__ void load(const uint16_t* row, int c, int cols) {
+    if constexpr (AL) {
+      v = load8<true>(row + nearest(c, cols));
+    } else if (cols >= 8) {
+      v.load(row + nearest(c, cols));
+    } else {
+      uint16_t e[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = row[max<int64_t>(0, min(c + j, cols - 1))];
-}
+      for (int j = 0; j < 8; ++j) e[j] = row[max(0, min(c + j, cols - 1))];
+      v.v = pack8(e, -c, cols - c);
+    }
+  }
+  __device__ u32x4 get(const uint16_t* row, int c, int cols) const {
+    const int at = nearest(c, cols), from = c - at, to = from + 8;   // entries of `at` that are wanted
+    if constexpr (AL) {
+      return from == 0 ? v : u32x4{0u, 0u, 0u, 0u};
+    } else {
+      if (cols < 8) return v.v;
+      u32x4 r = v.get(row + at);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        r[k] &= (2 * k >= from && 2 * k < to ? 0xffffu : 0u) | (2 * k + 1 >= from && 2 * k + 1 < to ? 0xffff0000u : 0u);
+      return r;
+    }
+  }
+};
 
 // Vectors of 16-bit entries.  AL: whole pieces of them start on 16 bytes.
 template <int NT, bool AL>
 struct Rows16 {
   static constexpr int kParts = 1;
   const uint16_t* row[NT];   // the lane's row of each tile
-  struct Raw {
-    uint16_t v[8];
+  struct Whole {
+    typename std::conditional<AL, u32x4, Any8>::type v;
   };
-  __device__ void whole(int n, int64_t c, u32x4 (&f)[1]) const { f[0] = load8<AL>(row[n] + c); }
-  __device__ void around(int n, int64_t c, int64_t cols, Raw& raw) const { load8_around(row[n], c, cols, raw.v); }
-  __device__ static void pack(const Raw& raw, int64_t from, int64_t to, u32x4 (&f)[1]) { f[0] = pack8(raw.v, from, to); }
+  struct Edge {
+    Edge8<AL> v;
+  };
+  __device__ void load(int n, int c, Whole& raw) const {
+    if constexpr (AL) raw.v = load8<true>(row[n] + c);
+    else raw.v.load(row[n] + c);
+  }
+  __device__ void finish(int n, int c, const Whole& raw, u32x4 (&f)[1]) const {
+    if constexpr (AL) f[0] = raw.v;
+    else f[0] = raw.v.get(row[n] + c);
+  }
+  __device__ void load_edge(int n, int c, int cols, Edge& raw) const { raw.v.load(row[n], c, cols); }
+  __device__ void finish_edge(int n, int c, int cols, const Edge& raw, u32x4 (&f)[1]) const { f[0] = raw.v.get(row[n], c, cols); }
 };
 
-// Vectors of fp32 entries, entered in two 16-bit parts: the rounded value and what the rounding
-// took away.  fp16: after a multiplication by `scale`, a power of two that brings the lane's row into its range.
-template <bool BF, int NT>
-struct Rows32 {
+// Vectors in two 16-bit parts.
+template <bool AL>
+struct RowsParts {
   static constexpr int kParts = 2;
-  const float* row[NT];
-  float scale[NT];
-  struct Raw {
-    float v[8];
-    float scale;
+  Rows16<2, AL> part;   // the lane's row of either part
+  struct Whole {
+    typename Rows16<2, AL>::Whole p[2];
   };
-  __device__ static void split(const float (&v)[8], float scale, u32x4 (&f)[2]) {
+  struct Edge {
+    Edge8<AL> p[2];
+  };
+  __device__ void load(int, int c, Whole& raw) const {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      uint32_t hi[2], lo[2];
+    for (int e = 0; e < 2; ++e) part.load(e, c, raw.p[e]);
+  }
+  __device__ void finish(int, int c, const Whole& raw, u32x4 (&f)[2]) const {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float x = BF ? v[j + e] : v[j + e] * scale;
-        hi[e] = f32_to_16<BF>(x);
-        const float rest = x - f32_from_16<BF>(hi[e]);
-        lo[e] = __builtin_isfinite(rest) ? f32_to_16<BF>(rest) : 0u;   // (infinite and NaN are in the first part)
-      }
-      f[0][j / 2] = hi[0] | (hi[1] << 16);
-      f[1][j / 2] = lo[0] | (lo[1] << 16);
+    for (int e = 0; e < 2; ++e) {
+      u32x4 v[1];
+      part.finish(e, c, raw.p[e], v);
+      f[e] = v[0];
     }
   }
-  __device__ void whole(int n, int64_t c, u32x4 (&f)[2]) const {
-    const u32x4_a4 a = *reinterpret_cast<const u32x4_a4*>(row[n] + c), b = *reinterpret_cast<const u32x4_a4*>(row[n] + c + 4);
-    float v[8];
+  __device__ void load_edge(int, int c, int cols, Edge& raw) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = __uint_as_float(a[j]);
-      v[4 + j] = __uint_as_float(b[j]);
-    }
-    split(v, scale[n], f);
+    for (int e = 0; e < 2; ++e) raw.p[e].load(part.row[e], c, cols);
   }
-  __device__ void around(int n, int64_t c, int64_t cols, Raw& raw) const {
-    load8_around(row[n], c, cols, raw.v);
-    raw.scale = scale[n];
-  }
-  __device__ static void pack(const Raw& raw, int64_t from, int64_t to, u32x4 (&f)[2]) {
-    float v[8];
+  __device__ void finish_edge(int, int c, int cols, const Edge& raw, u32x4 (&f)[2]) const {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j >= from && j < to ? raw.v[j] : 0.f;
-    split(v, raw.scale, f);
+    for (int e = 0; e < 2; ++e) f[e] = raw.p[e].get(part.row[e], c, cols);
   }
 };
 
 // acc[q][n] += the products of matrix q's 16 rows (w[q]: the lane's) with tile n's vectors, over the stretches
-// of 64 columns wave, wave + WV, ...; the waves' sums together are the whole product.  shift[q]: as
+// of 64 columns (one aligned matrix: 128) wave, wave + WV, ...; the waves' sums together are the whole product.  shift[q]: as
 // shift_of gives it for the matrix (0 with AL).  NX = 1: all matrices are shifted alike; MATS: each has its own
-// reading of the vectors.  DEPTH - 1 stretches are on their way ahead of the one that is worked on.
-template <bool BF, int MATS, int NT, int WV, bool AL, int NX, int DEPTH, typename X>
-__device__ __forceinline__ void rows_product(const uint16_t* const (&w)[MATS], const int (&shift)[MATS], int64_t cols, int wave,
+// reading of the vectors.  A stretch is on its way ahead of the one that is worked on.
+template <bool BF, int MATS, int NT, int WV, bool AL, int NX, typename X>
+__device__ __forceinline__ void rows_product(const uint16_t* const (&w)[MATS], const int (&shift)[MATS], int cols, int wave,
                                              const X& x, f32x4 (&acc)[MATS][NT]) {
-  constexpr int S = 2, P = X::kParts;   // 32-column slices per stretch
+  constexpr int S = AL && MATS == 1 ? 4 : 2, P = X::kParts;   // 32-column slices per stretch
   const int p = (threadIdx.x & (kWave - 1)) >> 4;
   struct Stage {
     u32x4 w[MATS][S];
+  };
+  struct Vectors {
+    typename X::Whole v[NT][NX][S];
   };
   int most = 0, least = 0;
   if constexpr (!AL) {
@@ -123,75 +170,115 @@ __device__ __forceinline__ void rows_product(const uint16_t* const (&w)[MATS], c
     }
   }
   auto shifted = [&](int q) -> int { return AL ? 0 : shift[q % NX]; };
-  const int64_t stretches = (cols + most + 32 * S - 1) / (32 * S);
+  const int stretches = (cols + most + 32 * S - 1) / (32 * S);
   // whole ones, first to full - 1: not the first where there is a shift, nor what reaches past the end
-  const int64_t first = most > 0 ? 1 : 0;
-  const int64_t full = max(first, (cols + least) / (32 * S));
-  auto fetch = [&](int64_t c, Stage& st) {
+  const int first = most > 0 ? 1 : 0;
+  const int full = max(first, (cols + least) / (32 * S));
+  auto fetch = [&](int c, Stage& st) {
 #pragma unroll
     for (int q = 0; q < MATS; ++q)
 #pragma unroll
-      for (int i = 0; i < S; ++i) st.w[q][i] = load8<true>(w[q] + 32 * (S * c + i) + 8 * p - shifted(q));
+      for (int i = 0; i < S; ++i) st.w[q][i] = load8<true>(w[q] + (32 * (S * c + i) + 8 * p - shifted(q)));
   };
-  auto work = [&](int64_t c, const Stage& st) {
+  // A stretch sets out while the one before it is worked on, the vectors' entries before the weights, and in the
+  // steady loop no load hangs on a condition: loads come back in order, and a wait for the vectors would otherwise be
+  // one for weights that were sent for later.  (Three stretches ahead instead of one: 13.8 against 12.8 us for one
+  // token at 2560 x 9728, no less anywhere.)
+  auto load_x = [&](int c, Vectors& xs) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      u32x4 f[NX][S][P];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int q = 0; q < NX; ++q)
 #pragma unroll
-        for (int i = 0; i < S; ++i) x.whole(n, 32 * (S * c + i) + 8 * p - shifted(q), f[q][i]);
+        for (int i = 0; i < S; ++i) x.load(n, 32 * (S * c + i) + 8 * p - shifted(q), xs.v[n][q][i]);
+  };
+  auto work = [&](int c, const Stage& st, const Vectors& xs) {
 #pragma unroll
-      for (int i = 0; i < S; ++i)
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        u32x4 f[NX][P];
+#pragma unroll
+        for (int q = 0; q < NX; ++q) x.finish(n, 32 * (S * c + i) + 8 * p - shifted(q), xs.v[n][q][i], f[q]);
 #pragma unroll
         for (int e = 0; e < P; ++e)
 #pragma unroll
-          for (int q = 0; q < MATS; ++q) acc[q][n] = mfma16<BF>(f[q % NX][i][e], st.w[q][i], acc[q][n]);
-    }
+          for (int q = 0; q < MATS; ++q) acc[q][n] = mfma16<BF>(f[q % NX][e], st.w[q][i], acc[q][n]);
+      }
   };
-  Stage st[DEPTH];
-  int64_t c = first + wave;
+  // The stretches that are not whole, three at most: a wave each, the last ones, which have the fewest others.
+  // Their loads and the first whole stretch's travel together.
+  const int odd = WV - 1 - wave, odds = first + stretches - full;
+  auto edges = [&](int odd) { return 32 * S * (odd < first ? 0 : full + odd - first) + 8 * p; };
+  Edge8<AL> we[MATS][2];   // two slices at a time
+  typename X::Edge xe[NX][NT][2];
+  auto load_edges = [&](int at) {
 #pragma unroll
-  for (int d = 0; d + 1 < DEPTH; ++d)
-    if (c + d * WV < full) fetch(c + d * WV, st[d]);
-  // The stretches that are not whole, three at most: a wave each, their narrow loads together.
-  for (int64_t odd = wave; odd < first + stretches - full; odd += WV) {
-    const int64_t e = odd < first ? 0 : full + odd - first;
-#pragma unroll 1
-    for (int i = 0; i < S; ++i) {
-      const int64_t col = 32 * (S * e + i) + 8 * p;
-      uint16_t wv[MATS][8];
-      typename X::Raw raw[NX][NT];
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-      for (int q = 0; q < MATS; ++q) load8_around(w[q], col - shifted(q), cols, wv[q]);
+      for (int q = 0; q < MATS; ++q) we[q][i].load(w[q], at + 32 * i - shifted(q), cols);
 #pragma unroll
       for (int q = 0; q < NX; ++q)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x.around(n, col - shifted(q), cols, raw[q][n]);
-      loads_made();
+        for (int n = 0; n < NT; ++n) x.load_edge(n, at + 32 * i - shifted(q), cols, xe[q][n][i]);
+    }
+    loads_made();
+  };
+  auto work_edges = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int q = 0; q < MATS; ++q) {
-        const int64_t from = shifted(q) - col, to = cols + from;
-        const u32x4 wf = pack8(wv[q], from, to);
+        const int c = at + 32 * i - shifted(q);
+        const u32x4 wf = we[q][i].get(w[q], c, cols);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           u32x4 f[P];
-          X::pack(raw[q % NX][n], from, to, f);
+          x.finish_edge(n, c, cols, xe[q % NX][n][i], f);
 #pragma unroll
-          for (int e = 0; e < P; ++e) acc[q][n] = mfma16<BF>(f[e], wf, acc[q][n]);
+          for (int k = 0; k < P; ++k) acc[q][n] = mfma16<BF>(f[k], wf, acc[q][n]);
         }
       }
+  };
+  Stage st[2];
+  Vectors xs[2];
+  int c = first + wave;
+  const bool any = full > first;   // (a wave without whole stretches reads the last one)
+  auto begin = [&] {
+    load_x(min(c, full - 1), xs[0]);
+    fetch(min(c, full - 1), st[0]);
+  };
+  // (one branch: were the edges' loads and their use in two, the loop would wait for loads in every round)
+  if (odd < odds) {
+    load_edges(edges(odd));
+    if (any) begin();
+    work_edges(edges(odd));
+    for (int i = 1; i < ((odds - odd + WV - 1) / WV) * (S / 2); ++i) {   // (more slices, or fewer waves than such stretches)
+      const int at = edges(odd + i / (S / 2) * WV) + i % (S / 2) * 64;
+      load_edges(at);
+      work_edges(at);
+    }
+  } else if (any) {
+    begin();
+  }
+  if (!any) return;
+  for (; c + 2 * WV < full; c += 2 * WV) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      load_x(c + (u + 1) * WV, xs[1 - u]);
+      fetch(c + (u + 1) * WV, st[1 - u]);
+      __builtin_amdgcn_sched_barrier(0);
+      work(c + u * WV, st[u], xs[u]);
     }
   }
-  while (c < full) {
-#pragma unroll
-    for (int u = 0; u < DEPTH; ++u) {
-      if (c < full) {
-        if (c + (DEPTH - 1) * WV < full) fetch(c + (DEPTH - 1) * WV, st[(u + DEPTH - 1) % DEPTH]);
-        work(c, st[u]);
-        c += WV;
-      }
-    }
+  if (c >= full) return;
+  if (c + WV < full) {   // two left, or one
+    load_x(c + WV, xs[1]);
+    fetch(c + WV, st[1]);
+    work(c, st[0], xs[0]);
+    work(c + WV, st[1], xs[1]);
+  } else {
+    work(c, st[0], xs[0]);
   }
 }
 
