@@ -902,6 +902,7 @@ def gated(x, Wg, Wu, act="silu"):
 # ---- linear layer ----
 
 _LINEAR_ACT = {None: 3, **_ACT}
+_LINEAR_ROWS = 32   # most tokens of the few-token kernel, which needs no workspace
 
 
 def _linear_act(act):
@@ -953,37 +954,49 @@ def linear_forward(x, W, bias=None, act=None, residual=None, save=False, out=Non
     x W^T + bias (tokens, rows) in float32, which linear_backward takes, or None without an activation, whose
     gradients need none.  Rows of x, W and residual may be strided.  linear() is the differentiable form: asking for a
     gradient of this one raises an error (with save, its result carries none)."""
-    code = _linear_act(act)
-    given = [t for t in (x, W, bias, residual) if t is not None]
-    record = not save and any(t.requires_grad for t in given) and _records(out)
-    index = _op_device(*given)
-    wanted = x, W, bias, residual
+    code = _LINEAR_ACT.get(act)
+    if code is None:
+        _linear_act(act)
+    record = not save and (x.requires_grad or W.requires_grad or bias is not None and bias.requires_grad or
+                           residual is not None and residual.requires_grad) and _records(out)
+    index = x.get_device()
+    if index < 0 or W.get_device() != index or index != _current_device() or \
+            bias is not None and bias.get_device() != index or residual is not None and residual.get_device() != index:
+        _op_device(*(t for t in (x, W, bias, residual) if t is not None))
+    given = x, W, bias, residual
     W, ldw, dtype = _linear_weights(x, W)
     rows, cols = W.shape
     shape = (*x.shape[:-1], rows)
+    bp = rp = zp = None
     if bias is not None:
         _need(bias, x.dtype, "bias")
         if tuple(bias.shape) != (rows,):
             raise ValueError(f"bias must have shape {(rows,)}")
+        bp = bias.data_ptr()
     ldr = rows
     if residual is not None:
-        if residual.dtype != x.dtype or tuple(residual.shape) != shape:
+        if residual.dtype != x.dtype or residual.shape != shape:
             raise ValueError(f"residual must be {x.dtype} of shape {shape}")
         residual, ldr = _rows_of(residual, rows, "residual")
+        rp = residual.data_ptr()
     y = x.new_empty(shape) if out is None else _out_or_new(out, shape, x.dtype, x.device)
     x, ldx = _rows_of(x, cols, "x")
     tokens = x.shape[0]
-    z = torch.empty((tokens, rows), dtype=torch.float32, device=x.device) if save and act is not None else None
+    z = None
+    if save and act is not None:
+        z = torch.empty((tokens, rows), dtype=torch.float32, device=x.device)
+        zp = z.data_ptr()
     xp, wp = x.data_ptr(), W.data_ptr()
-    aligned = (xp | wp) & 15 == 0 and (ldx | ldw | cols) & 7 == 0 and max(ldx, ldw) < 1 << 22
-    ws, wsb, keep = _linear_scratch(workspace, lambda al: _linear_forward_ws(tokens, cols, rows, al), x, aligned)
-    status = _linear_forward(xp, tokens, cols, ldx, wp, rows, ldw, None if bias is None else bias.data_ptr(),
-                             None if residual is None else residual.data_ptr(), ldr, dtype, code, _raw_stream(index),
-                             y.data_ptr(), None if z is None else z.data_ptr(), ws, wsb)
+    ws, wsb = None, 0
+    if workspace is not None or tokens > _LINEAR_ROWS:
+        aligned = (xp | wp) & 15 == 0 and (ldx | ldw | cols) & 7 == 0 and max(ldx, ldw) < 1 << 22
+        ws, wsb, keep = _linear_scratch(workspace, lambda al: _linear_forward_ws(tokens, cols, rows, al), x, aligned)
+    status = _linear_forward(xp, tokens, cols, ldx, wp, rows, ldw, bp, rp, ldr, dtype, code, _raw_stream(index), y.data_ptr(), zp,
+                             ws, wsb)
     if status:
         _check(status)
     if record:
-        return _NoGradient.apply("linear_forward has no gradient; linear has", y, *wanted)
+        return _NoGradient.apply("linear_forward has no gradient; linear has", y, *given)
     return (y, z) if save else y
 
 
@@ -1080,22 +1093,27 @@ def _moe_router(x, Wr):
 
 def _moe_weights(x, Wg, Wu, Wd):
     """The experts' matrices as the C structure."""
+    dtype, shape = x.dtype, Wg.shape
     for w, name in ((Wg, "Wg"), (Wu, "Wu"), (Wd, "Wd")):
-        if w.dtype != x.dtype:
-            raise TypeError(f"{name} must be {x.dtype} like x, got {w.dtype}")
+        if w.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype} like x, got {w.dtype}")
         if w.dim() != 3:
             raise ValueError(f"{name} must be 3-D")
-    experts, rows, cols = Wg.shape
-    if Wu.shape != Wg.shape or tuple(Wd.shape) != (experts, cols, rows):
+    experts, rows, cols = shape
+    if Wu.shape != shape or Wd.shape != (experts, cols, rows):
         raise ValueError(f"Wg and Wu must be of one shape (experts, rows, cols) and Wd (experts, cols, rows), got "
-                         f"{tuple(Wg.shape)}, {tuple(Wu.shape)}, {tuple(Wd.shape)}")
+                         f"{tuple(shape)}, {tuple(Wu.shape)}, {tuple(Wd.shape)}")
     (gs, gl, g1), (us, ul, u1), (ds, dl, d1) = Wg.stride(), Wu.stride(), Wd.stride()
     # (a dimension of one entry may have any stride)
-    gl, ul = (gl, ul) if rows > 1 else (cols, cols)
-    dl = dl if cols > 1 else rows
-    gs, us, ds = (gs, us, ds) if experts > 1 else (rows * cols,) * 3
-    if g1 != 1 and cols > 1 or u1 != 1 and cols > 1 or d1 != 1 and rows > 1 or gs != us or gl != ul or \
-            gl < cols or dl < rows or gs < 1 or ds < 1:
+    if rows <= 1:
+        gl = ul = cols
+        d1 = 1
+    if cols <= 1:
+        dl = rows
+        g1 = u1 = 1
+    if experts <= 1:
+        gs = us = ds = rows * cols
+    if g1 != 1 or u1 != 1 or d1 != 1 or gs != us or gl != ul or gl < cols or dl < rows or gs < 1 or ds < 1:
         raise ValueError("each expert's rows must be contiguous, and Wg and Wu strided alike")
     return _MoeWeights(Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), experts, rows, cols, gl, gs, dl, ds)
 
@@ -1148,21 +1166,24 @@ def moe_experts(x, ids, weights, Wg, Wu, Wd, act="silu", out=None, workspace=Non
 def moe(x, Wr, Wg, Wu, Wd, top, act="silu", normalize=True, routing=False, out=None, workspace=None):
     """A mixture-of-experts layer for a few tokens: moe_experts with the choice that moe_route makes, in one call.  With
     routing, returns (y, ids, weights)."""
+    record = (x.requires_grad or Wr.requires_grad or Wg.requires_grad or Wu.requires_grad or Wd.requires_grad) and _records(out)
     given = x, Wr, Wg, Wu, Wd
-    record = any(t.requires_grad for t in given) and _records(out)
-    index = _op_device(*given)
+    index = _op_device(x, Wr, Wg, Wu, Wd)
     w = _moe_weights(x, Wg, Wu, Wd)
     Wr, ldr, kind = _moe_router(x, Wr)
-    if tuple(Wr.shape) != (w.experts, w.cols):
-        raise ValueError(f"Wr must have shape {(w.experts, w.cols)}")
+    experts, cols = w.experts, w.cols
+    if Wr.shape != (experts, cols):
+        raise ValueError(f"Wr must have shape {(experts, cols)}")
     shape = (*x.shape[:-1], top)
     y = x.new_empty(x.shape) if out is None else _out_or_new(out, x.shape, x.dtype, x.device)
-    x, ldx, dtype = _moe_input(x, w.cols)
-    ids = torch.empty(shape, dtype=torch.int32, device=x.device)
-    weights = torch.empty(shape, dtype=torch.float32, device=x.device)
-    ws, wsb, keep = _moe_scratch(workspace, x, w.rows, w.experts, top)
-    _check(_moe(x.data_ptr(), x.shape[0], ldx, Wr.data_ptr(), ldr, kind, top, normalize, w, dtype, _act_code(act),
-                _raw_stream(index), y.data_ptr(), ids.data_ptr(), weights.data_ptr(), ws, wsb))
+    x, ldx, dtype = _moe_input(x, cols)
+    ids = x.new_empty(shape, dtype=torch.int32)
+    weights = x.new_empty(shape, dtype=torch.float32)
+    ws, wsb, keep = _moe_scratch(workspace, x, w.rows, experts, top)
+    status = _moe(x.data_ptr(), x.shape[0], ldx, Wr.data_ptr(), ldr, kind, top, normalize, w, dtype, _act_code(act),
+                  _raw_stream(index), y.data_ptr(), ids.data_ptr(), weights.data_ptr(), ws, wsb)
+    if status:
+        _check(status)
     if record:
         y = _NoGradient.apply("moe has no gradient", y, *given)
     return (y, ids, weights) if routing else y
@@ -1252,6 +1273,9 @@ class AdamW:
                 t.m_exp, t.v_exp = (s.data_ptr() + total + at // ADAMW_BLOCK for s in (self._m, self._v))
             if master and p.dtype != torch.float32:
                 t.master = self._master.data_ptr() + 4 * at
+        self._entries = [(t, p, p.numel()) for t, p in zip(self._table, self._params)]
+        self._at = [p.data_ptr() for p in self._params]   # what the table holds
+        self._inference = any(p.is_inference() for p in self._params)
         self._opts = _AdamOpts(0.0, betas[0], betas[1], eps, None, None, 1.0, bits, self._step.data_ptr())
 
     @property
@@ -1263,40 +1287,51 @@ class AdamW:
         """Applies one gradient per tensor (by default their .grad; a tensor whose gradient is None stays as it is).
         lr (by default the attribute lr) and grad_scale, which every gradient is multiplied by first, are numbers or
         float32 tensors of one element on the device, which a captured step reads in each replay."""
-        params, table, opts = self._params, self._table, self._opts
+        params, opts = self._params, self._opts
         if grads is None:
             grads = [p.grad for p in params]
         if len(grads) != len(params):
             raise ValueError(f"{len(grads)} gradients for {len(params)} tensors")
-        if self._index != _current_device():
+        index = self._index
+        if index != _current_device():
             _op_device(*params)
-        keep, changed = [], []
-        for t, p, g in zip(table, params, grads):
+        keep, changed = [], params
+        for k, (t, p, n) in enumerate(self._entries):
+            g = grads[k]
             if g is None:
                 t.n = 0
+                if changed is params:
+                    changed = params[:k]
                 continue
-            if g.shape != p.shape or g.get_device() != self._index:
-                raise ValueError(f"a gradient must have its tensor's shape {tuple(p.shape)} and device")
             code = _DTYPE.get(g.dtype)
             if code is None:
                 _dtype_code(g.dtype, "a gradient")
+            if g.shape != p.shape or g.get_device() != index:
+                raise ValueError(f"a gradient must have its tensor's shape {tuple(p.shape)} and device")
             if not g.is_contiguous():
                 g = g.contiguous()
                 keep.append(g)
-            if p.data_ptr() != t.param:
+            at = p.data_ptr()
+            if at != self._at[k]:
                 # (another storage of the same kind, as after p.data = ...)
                 _need(p, p.dtype, "a parameter")
-                if p.get_device() != self._index or _DTYPE.get(p.dtype) != t.param_dtype:
-                    raise ValueError("a parameter's type or device has changed")
-                t.param = p.data_ptr()
-            t.grad, t.grad_dtype, t.n = g.data_ptr(), code, p.numel()
-            changed.append(p)
-        opts.lr, opts.lr_device = _one_float(self.lr if lr is None else lr, "lr", self._device)
-        opts.grad_scale, opts.grad_scale_device = _one_float(grad_scale, "grad_scale", self._device)
-        _check(_adamw_step(table, len(params), opts, _raw_stream(self._index)))
-        for p in changed:   # so that autograd sees a saved parameter's change
-            if not p.is_inference():
-                torch.autograd.graph.increment_version(p)
+                if p.get_device() != index or _DTYPE.get(p.dtype) != t.param_dtype or p.numel() != n:
+                    raise ValueError("a parameter's type, size or device has changed")
+                t.param = self._at[k] = at
+            t.grad, t.grad_dtype, t.n = g.data_ptr(), code, n
+            if changed is not params:
+                changed.append(p)
+        if lr is None:
+            lr = self.lr
+        opts.lr, opts.lr_device = (lr, None) if type(lr) is float else _one_float(lr, "lr", self._device)
+        opts.grad_scale, opts.grad_scale_device = (grad_scale, None) if type(grad_scale) is float else \
+            _one_float(grad_scale, "grad_scale", self._device)
+        status = _adamw_step(self._table, len(params), opts, _raw_stream(index))
+        if status:
+            _check(status)
+        if self._inference:
+            changed = [p for p in changed if not p.is_inference()]
+        torch.autograd.graph.increment_version(changed)   # so that autograd sees a saved parameter's change
 
     def moments(self):
         """(m, v) in float32, in the state's order; piece() takes a tensor's entries out of them."""

@@ -54,7 +54,7 @@ hipError_t operands(const GatedArgs& a, uint16_t* ws, Operands* o, hipStream_t s
   *o = {static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.wg), static_cast<const uint16_t*>(a.wu),
         a.ldx, a.ldw, a.cols};
   if (!needs_copies(a)) return hipSuccess;
-  PadArgs q;
+  PadArgs q = {};
   const int64_t ldp = padded(a.cols, kBK);
   q.src[0] = o->x; q.src[1] = o->wg; q.src[2] = o->wu;
   q.rows[0] = a.tokens; q.rows[1] = q.rows[2] = a.rows;

@@ -15,6 +15,8 @@ namespace externd {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) uint16_t* lds16;
@@ -430,10 +432,10 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   // ---- outputs: a lane holds row m, columns n .. n + 3 of each fragment ----
   const int r = lane & 15, p = lane >> 4;
   constexpr int NO = MODE == kFwd ? NI / 2 : NI;   // output fragments per fragment row
-  // whole: the fragment's four entries exist and may be stored at once
+  // whole: the fragment's four entries exist and are stored at once, wherever their row starts
   auto put16 = [&](uint16_t* q, int64_t left, bool whole, uint2 w) {
     if (whole) {
-      *reinterpret_cast<uint2*>(q) = w;
+      *reinterpret_cast<u32x2_a2*>(q) = u32x2_a2{w.x, w.y};
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -442,7 +444,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   };
   auto put32 = [&](float* q, int64_t left, bool whole, f32x4 v) {
     if (whole) {
-      *reinterpret_cast<f32x4*>(q) = v;
+      *reinterpret_cast<f32x4_a4*>(q) = v;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -465,9 +467,6 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
       }
   };
   const int64_t n_lane = wn * NO * 16 + 4 * p, m_lane = wm * MI * 16 + r;
-  const bool aligned = g.ldo % 4 == 0 &&
-                       ((reinterpret_cast<uintptr_t>(g.out[0]) | reinterpret_cast<uintptr_t>(g.out[1])) & 7) == 0 &&
-                       ((reinterpret_cast<uintptr_t>(g.save[0]) | reinterpret_cast<uintptr_t>(g.save[1])) & 15) == 0;
   auto round_outputs = [&] {
     if constexpr (MODE == kFwd) {
       if (g.act == EXTERND_ACT_SILU) activate(std::integral_constant<int, EXTERND_ACT_SILU>());
@@ -484,7 +483,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
         for (int j = 0; j < NO; ++j) packed[i][j] = pack(BF ? acc[i][j] : acc[i][j] * back[i]);
     }
   };
-  auto put_outputs = [&](auto inside) {   // inside: the whole tile is, and its rows are aligned
+  auto put_outputs = [&](auto inside) {   // inside: the whole tile is
     constexpr bool IN = decltype(inside)::value;
     constexpr int OUTS = outs_of(MODE);
 #pragma unroll
@@ -495,7 +494,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
       for (int j = 0; j < NO; ++j) {
         const int64_t left = g.ldo - (u.n0 + n_lane + j * 16);
         if (!IN && left <= 0) continue;
-        const bool whole = IN || (aligned && left >= 4);
+        const bool whole = IN || left >= 4;
         if constexpr (SPLIT) {
           float* q = g.part + ((int64_t)u.split * OUTS + u.outsel) * g.mo * g.ldo + at + j * 16;
           put32(q, left, whole, acc[i][j]);
@@ -512,7 +511,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   };
   // Linear forward, a row of fragments at a time: z = acc + bias, y = act(z) + residual.  A row's
   // residual is on its way while the row before it is put out.
-  auto put_linear = [&](auto inside) {   // inside: as above, and the residual's rows are read 8 bytes at a time
+  auto put_linear = [&](auto inside) {   // inside: as above
     constexpr bool IN = decltype(inside)::value;
     f32x4 bias[NO];
 #pragma unroll
@@ -529,8 +528,9 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
 #pragma unroll
       for (int j = 0; j < NO; ++j) {
         const int64_t n = u.n0 + n_lane + j * 16;
-        if constexpr (IN) {
-          res[i & 1][j] = *reinterpret_cast<const uint2*>(row + n);
+        if (IN || n + 4 <= g.ldo) {
+          const u32x2_a2 v = *reinterpret_cast<const u32x2_a2*>(row + n);
+          res[i & 1][j] = uint2{v.x, v.y};
         } else {
           uint32_t v[4];
 #pragma unroll
@@ -550,7 +550,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
         y[j] = acc[i][j] + bias[j];
         const int64_t left = g.ldo - (u.n0 + n_lane + j * 16);
         if (g.save[0] && (IN || (m < g.mo && left > 0)))
-          put32(g.save[0] + at + j * 16, left, IN || (aligned && left >= 4), y[j]);
+          put32(g.save[0] + at + j * 16, left, IN || left >= 4, y[j]);
       }
       if (g.act != EXTERND_ACT_NONE)
         with_act(g.act, [&](auto act) {
@@ -568,7 +568,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
         }
         const int64_t left = g.ldo - (u.n0 + n_lane + j * 16);
         if (IN || (m < g.mo && left > 0))
-          put16(g.out[0] + at + j * 16, left, IN || (aligned && left >= 4), pack(y[j]));
+          put16(g.out[0] + at + j * 16, left, IN || left >= 4, pack(y[j]));
       }
     }
   };
@@ -595,11 +595,11 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
     const bool more = at < units;
     const Unit next = locate(more ? at : blockIdx.x);
     if (more) begin(next);
-    const bool inside = aligned && u.m0 + BM <= g.mo && u.n0 + BNO <= g.ldo;
+    const bool inside = u.m0 + BM <= g.mo && u.n0 + BNO <= g.ldo;
     if constexpr (!SPLIT) round_outputs();
     wait_vm<0, 0>();
     if constexpr (MODE == kLin && !SPLIT) {
-      if (inside && g.ldr % 4 == 0 && (reinterpret_cast<uintptr_t>(g.residual) & 7) == 0) put_linear(std::true_type());
+      if (inside) put_linear(std::true_type());
       else put_linear(std::false_type());
     } else if (inside) put_outputs(std::true_type());
     else put_outputs(std::false_type());

@@ -21,29 +21,32 @@ namespace externd {
 
 namespace {
 
-// db: sums over the tokens of dz in fp32, in an order that does not depend on timing.  A workgroup takes
-// 64 columns, a wave every sixteenth token; the waves' sums are joined in wave order.
+// db: sums over the tokens of dz in fp32, in an order that does not depend on timing.  A workgroup takes COLS
+// columns, a wave's lanes 64 / COLS tokens of them at a time; the lanes' and the waves' sums are joined in order.  16
+// columns where 64 would leave most compute units without any (777 tokens at 1001 rows: 15 us with 64).
 constexpr int kSumWaves = 16;
-template <bool BF>
+template <bool BF, int COLS>
 __global__ __launch_bounds__(kSumWaves * kWave) void k_bias_sums(const uint16_t* __restrict__ dy, int64_t lddy,
                                                                   const float* __restrict__ z, int act, int64_t tokens,
                                                                   int64_t rows, uint16_t* __restrict__ db) {
-  __shared__ float red[kSumWaves][kWave];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int64_t c = (int64_t)blockIdx.x * kWave + lane, at = min(c, rows - 1);
-  constexpr int U = 4;   // tokens on their way
-  float sum[U] = {};
+  constexpr int LINES = kSumWaves * kWave / COLS;   // tokens that the workgroup takes at once
+  constexpr int U = 8;                              // times that on their way
+  __shared__ float red[LINES][COLS];
+  const int col = threadIdx.x % COLS, line = threadIdx.x / COLS;
+  const int64_t c = (int64_t)blockIdx.x * COLS + col, at = min(c, rows - 1);
+  float sum[2] = {};
   auto add = [&](auto slope) {
-    for (int64_t t0 = wave; t0 < tokens; t0 += U * kSumWaves) {
-      float d[U];
+    for (int64_t t0 = line; t0 < tokens; t0 += U * LINES) {
+      float d[U], v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t t = t0 + u * kSumWaves;
-        d[u] = t < tokens ? f32_from_16<BF>(dy[t * lddy + at]) : 0.f;
-        if (z) d[u] = t < tokens ? d[u] * slope(z[t * rows + at]) : 0.f;
+        const int64_t t = min(t0 + u * LINES, tokens - 1);
+        d[u] = f32_from_16<BF>(dy[t * lddy + at]);
+        v[u] = z ? z[t * rows + at] : 0.f;
       }
+      loads_made();
 #pragma unroll
-      for (int u = 0; u < U; ++u) sum[u] += d[u];
+      for (int u = 0; u < U; ++u) sum[u & 1] += t0 + u * LINES < tokens ? (z ? d[u] * slope(v[u]) : d[u]) : 0.f;
     }
   };
   if (z)
@@ -55,14 +58,24 @@ __global__ __launch_bounds__(kSumWaves * kWave) void k_bias_sums(const uint16_t*
       });
     });
   else add([](float) { return 1.f; });
-  red[wave][lane] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  red[line][col] = sum[0] + sum[1];
   __syncthreads();
-  if (wave == 0 && c < rows) {
-    float v = 0.f;
-#pragma unroll
-    for (int q = 0; q < kSumWaves; ++q) v += red[q][lane];
-    db[c] = (uint16_t)f32_to_16<BF>(v);
+  for (int n = LINES / 2; n > 0; n /= 2) {
+    if (line < n) red[line][col] += red[line + n][col];
+    __syncthreads();
   }
+  if (line == 0 && c < rows) db[c] = (uint16_t)f32_to_16<BF>(red[0][col]);
+}
+
+template <bool BF>
+void launch_bias_sums(const LinearArgs& a, const float* z, hipStream_t s) {
+  const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
+  uint16_t* db = static_cast<uint16_t*>(a.db);
+  const dim3 block(kSumWaves * kWave);
+  if (a.rows >= (int64_t)64 * a.cus)
+    hipLaunchKernelGGL((k_bias_sums<BF, 64>), dim3((unsigned)ceil_div64(a.rows, 64)), block, 0, s, dy, a.lddy, z, a.act, a.tokens, a.rows, db);
+  else
+    hipLaunchKernelGGL((k_bias_sums<BF, 16>), dim3((unsigned)ceil_div64(a.rows, 16)), block, 0, s, dy, a.lddy, z, a.act, a.tokens, a.rows, db);
 }
 
 hipError_t product(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, bool bf, int cus,
@@ -77,8 +90,9 @@ struct Operands {
 };
 int64_t copy_entries(int64_t tokens, int64_t cols, int64_t rows) { return (tokens + rows) * padded(cols, kBK); }
 
-// ws: room for the copies of x and W, then of dy; `forward`: dy is not looked at.
-hipError_t operands(const LinearArgs& a, bool copy_xw, bool copy_dy, uint16_t* ws, Operands* o, hipStream_t s) {
+// ws: room for the copies of x and W, then of dy.  zeros: words to clear on the way, or null.
+hipError_t operands(const LinearArgs& a, bool copy_xw, bool copy_dy, uint16_t* ws, uint32_t* zeros, int64_t zeros_n, Operands* o,
+                    hipStream_t s) {
   *o = {static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.w), static_cast<const uint16_t*>(a.dy),
         a.ldx, a.ldw, a.lddy, a.cols};
   PadArgs q = {};
@@ -103,7 +117,13 @@ hipError_t operands(const LinearArgs& a, bool copy_xw, bool copy_dy, uint16_t* w
     o->cols = padded(a.cols, kBK);
   }
   if (copy_dy) copy(o->dy, o->lddy, a.tokens, a.rows);
-  if (n == 0) return hipSuccess;
+  if (n == 0) {
+    if (!zeros) return hipSuccess;
+    hipLaunchKernelGGL(k_fill_zero<uint32_t>, dim3(64), dim3(256), 0, s, zeros, zeros_n);
+    return hipGetLastError();
+  }
+  q.zeros = zeros;
+  q.zeros_n = zeros_n;
   hipLaunchKernelGGL(k_pad_rows, dim3(blocks(most), n), dim3(256), 0, s, q);
   return hipGetLastError();
 }
@@ -126,7 +146,7 @@ hipError_t run_linear_forward(const LinearArgs& a, void* ws, hipStream_t s) {
   if (linear_takes_rows(a.tokens, a.cols, a.rows, al, a.cus)) return run_linear_rows(a, s);
   char* w = static_cast<char*>(ws);
   Operands o;
-  const hipError_t e = operands(a, !al, false, reinterpret_cast<uint16_t*>(w), &o, s);
+  const hipError_t e = operands(a, !al, false, reinterpret_cast<uint16_t*>(w), nullptr, 0, &o, s);
   if (e != hipSuccess) return e;
   if (!al) w += region(2 * (size_t)copy_entries(a.tokens, a.cols, a.rows));
   GatedGemm g = {};
@@ -146,12 +166,12 @@ hipError_t run_linear_forward(const LinearArgs& a, void* ws, hipStream_t s) {
   return product(kLin, g, p, reinterpret_cast<float*>(w), a.dtype == EXTERND_BF16, a.cus, s);
 }
 
-// Workspace: dz in two parts and its largest magnitudes where there is an activation, padded copies, the
-// split sums.
+// Workspace: dz in two parts (fp16: with two scales) and its largest magnitudes where there is an activation,
+// padded copies, the split sums.
 size_t linear_backward_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, int act, bool aligned, bool reads_dy, int cus) {
   const bool parts = act != EXTERND_ACT_NONE;
   const GatedPlan px = plan_linear_dx(tokens, cols, rows, parts, cus), pw = plan_linear_dw(tokens, cols, rows, parts, cus);
-  return (parts ? region(2 * (size_t)(2 * tokens * padded(rows, 8))) + region(4 * (size_t)(tokens + padded(rows, 8))) : 0) +
+  return (parts ? region(2 * (size_t)(4 * tokens * padded(rows, 8))) + region(4 * (size_t)(tokens + padded(rows, 8))) : 0) +
          region(2 * (size_t)((aligned ? 0 : copy_entries(tokens, cols, rows)) + (parts || reads_dy ? 0 : tokens * padded(rows, kBK)))) +
          region(4 * (size_t)std::max(part_floats(kDx, tokens, cols, px), part_floats(kLinDw, rows, cols, pw)));
 }
@@ -169,51 +189,47 @@ hipError_t run_linear_backward(const LinearArgs& a, void* ws, hipStream_t s) {
     return hipSuccess;
   }
   if (a.db) {
-    const dim3 grid((unsigned)ceil_div64(a.rows, kWave)), block(kSumWaves * kWave);
-    const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
-    const float* z = parts ? a.z : nullptr;
-    if (bf) hipLaunchKernelGGL(k_bias_sums<true>, grid, block, 0, s, dy, a.lddy, z, a.act, a.tokens, a.rows, static_cast<uint16_t*>(a.db));
-    else hipLaunchKernelGGL(k_bias_sums<false>, grid, block, 0, s, dy, a.lddy, z, a.act, a.tokens, a.rows, static_cast<uint16_t*>(a.db));
+    if (bf) launch_bias_sums<true>(a, parts ? a.z : nullptr, s);
+    else launch_bias_sums<false>(a, parts ? a.z : nullptr, s);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (!a.dx && !a.dw) return hipSuccess;
   char* w = static_cast<char*>(ws);
-  // dz and its rest
+  // dz and its rest; fp16: scaled by token for dx, and again by row of W for dW
   const int64_t ldd = padded(a.rows, 8), part_len = a.tokens * ldd;
-  uint16_t* dz = reinterpret_cast<uint16_t*>(w);
+  uint16_t *dz = reinterpret_cast<uint16_t*>(w), *dz_by_unit = bf ? dz : dz + 2 * part_len;
   uint32_t *by_unit = nullptr, *by_token = nullptr;
   const SlopeArgs sa = {a.z, nullptr, static_cast<const uint16_t*>(a.dy), a.tokens, a.rows, a.lddy};
   if (parts) {
-    w += region(2 * (size_t)(2 * part_len));
+    w += region(2 * (size_t)(4 * part_len));
     by_unit = reinterpret_cast<uint32_t*>(w);
     by_token = by_unit + ldd;
     w += region(4 * (size_t)(a.tokens + ldd));
-    if (!bf) {
+  }
+  const bool al = linear_is_aligned(a), reads_dy = linear_reads_dy(a), scaled = parts && !bf;
+  Operands o;
+  e = operands(a, !al, !parts && !reads_dy, reinterpret_cast<uint16_t*>(w), scaled ? by_unit : nullptr, a.tokens + ldd, &o, s);
+  if (e != hipSuccess) return e;
+  w += region(2 * (size_t)((al ? 0 : copy_entries(a.tokens, a.cols, a.rows)) + (parts || reads_dy ? 0 : a.tokens * padded(a.rows, kBK))));
+  if (parts) {
+    const dim3 grid(blocks(a.tokens * (ldd / 8))), block(256);
+    if (bf) {
+      hipLaunchKernelGGL((k_gated_slopes<true, false>), grid, block, 0, s, sa, ldd, a.act, part_len, nullptr, nullptr, dz, nullptr);
+    } else {
       const int64_t strips = ceil_div64(a.rows, 256);
       const int strip = ceil_div64(a.tokens, 64) * strips >= 2 * a.cus ? 64 : 16;
-      hipLaunchKernelGGL(k_fill_zero<uint32_t>, dim3(64), dim3(256), 0, s, by_unit, a.tokens + ldd);
       hipLaunchKernelGGL(k_gated_tops<false>, dim3((unsigned)(ceil_div64(a.tokens, strip) * strips)), dim3(256), 0, s, sa, ldd,
                          a.act, strip, by_token, by_unit);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
+      hipLaunchKernelGGL((k_gated_slopes<false, false>), grid, block, 0, s, sa, ldd, a.act, part_len, a.dx ? by_token : nullptr,
+                         a.dw ? by_unit : nullptr, dz, dz_by_unit);
     }
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  // fp16: for dx scaled by token, for dW by row of W
-  auto slopes = [&](const uint32_t* token, const uint32_t* unit) {
-    const dim3 grid(blocks(a.tokens * (ldd / 8))), block(256);
-    if (bf) hipLaunchKernelGGL((k_gated_slopes<true, false>), grid, block, 0, s, sa, ldd, a.act, part_len, token, unit, dz, nullptr);
-    else hipLaunchKernelGGL((k_gated_slopes<false, false>), grid, block, 0, s, sa, ldd, a.act, part_len, token, unit, dz, nullptr);
-    return hipGetLastError();
-  };
-  const bool al = linear_is_aligned(a), reads_dy = linear_reads_dy(a);
-  Operands o;
-  if ((e = operands(a, !al, !parts && !reads_dy, reinterpret_cast<uint16_t*>(w), &o, s)) != hipSuccess) return e;
-  w += region(2 * (size_t)((al ? 0 : copy_entries(a.tokens, a.cols, a.rows)) + (parts || reads_dy ? 0 : a.tokens * padded(a.rows, kBK))));
   float* part = reinterpret_cast<float*>(w);
   const int64_t cols8 = padded(a.cols, 8);
   const uint16_t* d = parts ? dz : o.dy;
   const int64_t ld = parts ? ldd : o.lddy;
   if (a.dx) {
-    if (parts && (e = slopes(by_token, nullptr)) != hipSuccess) return e;
     const GatedPlan px = plan_linear_dx(a.tokens, a.cols, a.rows, parts, a.cus);
     GatedGemm g = {};
     g.a = {{d, d}, ld, px.stacked * a.tokens};
@@ -228,9 +244,9 @@ hipError_t run_linear_backward(const LinearArgs& a, void* ws, hipStream_t s) {
     if ((e = product(kDx, g, px, part, bf, a.cus, s)) != hipSuccess) return e;
   }
   if (a.dw) {
-    if (parts && (!bf || !a.dx) && (e = slopes(nullptr, by_unit)) != hipSuccess) return e;
     GatedGemm g = {};
-    g.a = {{d, d}, ld, ldd};
+    const uint16_t* const du = parts ? dz_by_unit : d;
+    g.a = {{du, du}, ld, ldd};
     g.b = {{o.x, o.x}, o.ldx, cols8};
     g.segs = parts ? 2 : 1;
     g.rest = part_len;

@@ -23,7 +23,7 @@ inline GatedPlan plan_linear(int mode, int64_t m, int64_t n, int64_t steps, int 
       const double per = (double)ceil_div64(std::max<int64_t>(steps, 1), splits);
       const double rounds = (double)ceil_div64(units, (int64_t)cus * (kind == kPair ? 2 : 1));
       double us = kind == kBig    ? rounds * (per * 1.4 + 6.0)
-                  : kind == kMid  ? rounds * (per * 1.05 + 6.0)
+                  : kind == kMid  ? rounds * (per * 1.2 + 6.0)
                   : kind == kPair ? rounds * (per * 0.95 + 4.0)
                                   : per * 0.45 + 8.0;
       if (splits > 1) us += 4.0 + (double)m * (double)n * 4.0 * (double)(splits * 2) / 4e6;

@@ -215,6 +215,45 @@ __global__ __launch_bounds__(WV * kWave, 4) void k_moe_down(DownArgs a) {
   }
 }
 
+// One token's outputs: a workgroup of sixteen waves takes a tile of all its experts, SL waves each (with more than sixteen
+// experts, a wave several), and writes y: no results of slots, no join.  One token through 4 of 64 experts of 1024 x
+// 2560: MEASURED.
+template <bool BF, int SL, bool AL>
+__global__ __launch_bounds__(16 * kWave) void k_moe_down_one(DownArgs a, const int32_t* __restrict__ ids,
+                                                              const float* __restrict__ weights, int top, int experts,
+                                                              uint16_t* __restrict__ y) {
+  __shared__ float red[16][16];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r = lane & 15;
+  const int64_t row0 = tile_row0(blockIdx.x, a.apart_bits);
+  if (row0 >= a.rows) return;
+  const int64_t mine = row0 + ((int64_t)r << a.apart_bits), row = mine < a.rows ? mine : row0;   // (past the end: the first again)
+  float sum = 0.f;
+  for (int slot = wave / SL; slot < top; slot += 16 / SL) {
+    const int expert = ids[slot];
+    if (expert < 0 || expert >= experts) continue;
+    const uint16_t* const base = a.w + expert * a.stride;
+    const uint16_t* const w[1] = {base + row * a.ldw};
+    const int shift[1] = {AL ? 0 : shift_of(base + row0 * a.ldw)};
+    RowsParts<AL> x;
+    x.part.row[0] = a.parts + slot * a.ldh;
+    x.part.row[1] = x.part.row[0] + a.rest;
+    f32x4 acc[1][1];
+    acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    rows_product<BF, 1, 1, SL, AL, 1>(w, shift, (int)a.cols, wave % SL, x, acc);
+    const float v = BF ? acc[0][0][0] : acc[0][0][0] * unscale_of(a.tops[slot]);   // (every row of the product is the token)
+    sum = fmaf(weights[slot], v, sum);
+  }
+  if (lane < 16) red[wave][lane] = sum;
+  __syncthreads();
+  if (threadIdx.x < 16 && mine < a.rows) {
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) v += red[q][threadIdx.x];
+    y[mine] = (uint16_t)f32_to_16<BF>(v);
+  }
+}
+
 // y[t] = the sum over t's choices of weight * part, in the order of the choices; a choice outside the experts
 // adds nothing.  (Done instead by the workgroup of the second product that comes last to a column of outputs, it cost
 // more than this pass: each has to wait for its stores and for the count, 150 us against 108 and 7 for 32 tokens, 8 of 128
@@ -264,6 +303,15 @@ void launch_down(const DownArgs& d, bool al, unsigned groups, hipStream_t s) {
   const dim3 grid((unsigned)((units + WV / SW - 1) / (WV / SW)), groups), block(WV * kWave);
   if (al) hipLaunchKernelGGL((k_moe_down<BF, WV, SW, RT, true>), grid, block, 0, s, d);
   else hipLaunchKernelGGL((k_moe_down<BF, WV, SW, RT, false>), grid, block, 0, s, d);
+}
+
+template <bool BF, int SL>
+void launch_one(const DownArgs& d, bool al, const MoeArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)rows_tiles(d.rows, d.apart_bits)), block(16 * kWave);
+  uint16_t* const y = static_cast<uint16_t*>(a.y);
+  const int experts = (int)a.w.experts;
+  if (al) hipLaunchKernelGGL((k_moe_down_one<BF, SL, true>), grid, block, 0, s, d, a.ids, a.weights, a.top, experts, y);
+  else hipLaunchKernelGGL((k_moe_down_one<BF, SL, false>), grid, block, 0, s, d, a.ids, a.weights, a.top, experts, y);
 }
 
 template <bool BF>
@@ -328,6 +376,14 @@ hipError_t experts(const MoeArgs& a, const MoeSpace& s, bool one, hipStream_t st
   d.tops = s.tops;
   d.part = s.part;
   const bool dal = pieces_aligned(w.wd, w.down_stride, w.down_ld, w.rows);
+  if (a.tokens == 1) {
+    if (a.top == 1) launch_one<BF, 16>(d, dal, a, stream);
+    else if (a.top == 2) launch_one<BF, 8>(d, dal, a, stream);
+    else if (a.top <= 4) launch_one<BF, 4>(d, dal, a, stream);
+    else if (a.top <= 8) launch_one<BF, 2>(d, dal, a, stream);
+    else launch_one<BF, 1>(d, dal, a, stream);
+    return hipGetLastError();
+  }
   const int64_t tiles = rows_tiles(a.cols, d.apart_bits);
   const int down = waves_a_tile(tiles, groups, a.cus, 1, 16);
   if (down == 1 && tiles * groups >= (int64_t)a.cus * 32) launch_down<BF, 1, 2>(d, dal, (unsigned)groups, stream);

@@ -26,9 +26,13 @@ struct PadArgs {
   const uint16_t* src[3];
   uint16_t* dst[3];
   int64_t rows[3], ld[3], cols[3], ldp[3];
+  uint32_t* zeros;   // words to clear besides, or null
+  int64_t zeros_n;
 };
 __global__ __launch_bounds__(256) void k_pad_rows(PadArgs a) {
   const int w = blockIdx.y;
+  if (a.zeros && w == 0)
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.zeros_n; i += (int64_t)gridDim.x * 256) a.zeros[i] = 0u;
   const int64_t ldp = a.ldp[w], per = ldp / 8, total = a.rows[w] * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / per, c = (i - row * per) * 8, left = a.cols[w] - c;

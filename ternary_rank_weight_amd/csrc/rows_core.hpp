@@ -146,13 +146,13 @@ struct RowsParts {
 };
 
 // acc[q][n] += the products of matrix q's 16 rows (w[q]: the lane's) with tile n's vectors, over the stretches
-// of 64 columns (one aligned matrix: 128) wave, wave + WV, ...; the waves' sums together are the whole product.  shift[q]: as
+// of 64 columns wave, wave + WV, ...; the waves' sums together are the whole product.  shift[q]: as
 // shift_of gives it for the matrix (0 with AL).  NX = 1: all matrices are shifted alike; MATS: each has its own
 // reading of the vectors.  A stretch is on its way ahead of the one that is worked on.
 template <bool BF, int MATS, int NT, int WV, bool AL, int NX, typename X>
 __device__ __forceinline__ void rows_product(const uint16_t* const (&w)[MATS], const int (&shift)[MATS], int cols, int wave,
                                              const X& x, f32x4 (&acc)[MATS][NT]) {
-  constexpr int S = AL && MATS == 1 ? 4 : 2, P = X::kParts;   // 32-column slices per stretch
+  constexpr int S = 2, P = X::kParts;   // 32-column slices per stretch
   const int p = (threadIdx.x & (kWave - 1)) >> 4;
   struct Stage {
     u32x4 w[MATS][S];
@@ -210,11 +210,11 @@ __device__ __forceinline__ void rows_product(const uint16_t* const (&w)[MATS], c
   // Their loads and the first whole stretch's travel together.
   const int odd = WV - 1 - wave, odds = first + stretches - full;
   auto edges = [&](int odd) { return 32 * S * (odd < first ? 0 : full + odd - first) + 8 * p; };
-  Edge8<AL> we[MATS][2];   // two slices at a time
-  typename X::Edge xe[NX][NT][2];
+  Edge8<AL> we[MATS][S];
+  typename X::Edge xe[NX][NT][S];
   auto load_edges = [&](int at) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < S; ++i) {
 #pragma unroll
       for (int q = 0; q < MATS; ++q) we[q][i].load(w[q], at + 32 * i - shifted(q), cols);
 #pragma unroll
@@ -226,7 +226,7 @@ __device__ __forceinline__ void rows_product(const uint16_t* const (&w)[MATS], c
   };
   auto work_edges = [&](int at) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < S; ++i)
 #pragma unroll
       for (int q = 0; q < MATS; ++q) {
         const int c = at + 32 * i - shifted(q);
@@ -253,10 +253,9 @@ __device__ __forceinline__ void rows_product(const uint16_t* const (&w)[MATS], c
     load_edges(edges(odd));
     if (any) begin();
     work_edges(edges(odd));
-    for (int i = 1; i < ((odds - odd + WV - 1) / WV) * (S / 2); ++i) {   // (more slices, or fewer waves than such stretches)
-      const int at = edges(odd + i / (S / 2) * WV) + i % (S / 2) * 64;
-      load_edges(at);
-      work_edges(at);
+    for (int more = odd + WV; more < odds; more += WV) {   // (fewer waves than such stretches)
+      load_edges(edges(more));
+      work_edges(edges(more));
     }
   } else if (any) {
     begin();

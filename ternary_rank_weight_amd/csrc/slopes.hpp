@@ -123,7 +123,8 @@ __global__ __launch_bounds__(256) void k_gated_tops(SlopeArgs a, int64_t ldd, in
 // what the rounding took away.  Bound by HBM: reads 4 + 4 + 2 bytes, writes
 // 4 + 4 per hidden unit and token; 62 us for 2048 x 9728 (5.8 TB/s: part of what
 // it writes stays in the last-level cache).  fp16: scaled by the power of two that
-// k_gated_tops' bits give for the token, or for the hidden unit of dg and of du (the other null).
+// k_gated_tops' bits give for the token, or for the hidden unit of dg and of du (the other null).  Not GATED: dg alone,
+// in fp16 scaled by token into dg's place and by hidden unit into du's, each where its bits are given.
 template <bool BF, bool GATED = true>
 __global__ __launch_bounds__(256) void k_gated_slopes(SlopeArgs a, int64_t ldd, int act, int64_t rest,
                                                        const uint32_t* __restrict__ by_token,
@@ -137,8 +138,8 @@ __global__ __launch_bounds__(256) void k_gated_slopes(SlopeArgs a, int64_t ldd, 
       slopes_at<BF, decltype(kind)::value, BF, GATED>(a, t, c, vg, vu);
       if constexpr (!BF) {
         const float all = by_token ? scale_of(by_token[t]) : 0.f;
-        u32x4 tg[2], tu[2];
-        if (!by_token) {
+        u32x4 tg[2] = {}, tu[2] = {};
+        if (GATED ? !by_token : by_unit != nullptr) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             tg[h] = *reinterpret_cast<const u32x4*>(by_unit + c + 4 * h);
@@ -147,6 +148,11 @@ __global__ __launch_bounds__(256) void k_gated_slopes(SlopeArgs a, int64_t ldd, 
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
+          if constexpr (!GATED) {
+            vu[e] = vg[e] * scale_of(tg[e / 4][e & 3]);
+            vg[e] *= all;
+            continue;
+          }
           vg[e] *= by_token ? all : scale_of(tg[e / 4][e & 3]);
           if constexpr (GATED) vu[e] *= by_token ? all : scale_of(tu[e / 4][e & 3]);
         }
@@ -168,10 +174,11 @@ __global__ __launch_bounds__(256) void k_gated_slopes(SlopeArgs a, int64_t ldd, 
         rg[e / 2] = lg[0] | (lg[1] << 16);
         ru[e / 2] = lu[0] | (lu[1] << 16);
       }
-      *reinterpret_cast<u32x4*>(dg + t * ldd + c) = og;
-      if constexpr (GATED) *reinterpret_cast<u32x4*>(du + t * ldd + c) = ou;
-      *reinterpret_cast<u32x4*>(dg + rest + t * ldd + c) = rg;
-      if constexpr (GATED) *reinterpret_cast<u32x4*>(du + rest + t * ldd + c) = ru;
+      const bool first = GATED || BF || by_token, second = GATED || (!BF && by_unit);
+      if (first) *reinterpret_cast<u32x4*>(dg + t * ldd + c) = og;
+      if (second) *reinterpret_cast<u32x4*>(du + t * ldd + c) = ou;
+      if (first) *reinterpret_cast<u32x4*>(dg + rest + t * ldd + c) = rg;
+      if (second) *reinterpret_cast<u32x4*>(du + rest + t * ldd + c) = ru;
     }
   });
 }
