@@ -902,7 +902,7 @@ def gated(x, Wg, Wu, act="silu"):
 # ---- linear layer ----
 
 _LINEAR_ACT = {None: 3, **_ACT}
-_LINEAR_ROWS = 32   # most tokens of the few-token kernel, which needs no workspace
+_LINEAR_ROWS = 3, 32   # tokens that need no workspace: of any operands, of such as are not aligned
 
 
 def _linear_act(act):
@@ -988,8 +988,8 @@ def linear_forward(x, W, bias=None, act=None, residual=None, save=False, out=Non
         zp = z.data_ptr()
     xp, wp = x.data_ptr(), W.data_ptr()
     ws, wsb = None, 0
-    if workspace is not None or tokens > _LINEAR_ROWS:
-        aligned = (xp | wp) & 15 == 0 and (ldx | ldw | cols) & 7 == 0 and max(ldx, ldw) < 1 << 22
+    aligned = (xp | wp) & 15 == 0 and (ldx | ldw | cols) & 7 == 0 and max(ldx, ldw) < 1 << 22
+    if workspace is not None or tokens > _LINEAR_ROWS[not aligned]:
         ws, wsb, keep = _linear_scratch(workspace, lambda al: _linear_forward_ws(tokens, cols, rows, al), x, aligned)
     status = _linear_forward(xp, tokens, cols, ldx, wp, rows, ldw, bp, rp, ldr, dtype, code, _raw_stream(index), y.data_ptr(), zp,
                              ws, wsb)

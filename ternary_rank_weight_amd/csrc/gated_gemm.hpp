@@ -217,7 +217,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   // an end: rows are padded to 8 entries (with zeros, where they were padded here).
   // A thread's loads are in flight together; a slot past an end loads the operand's first.
   auto stage_operand = [&](auto n, lds16 image, const uint16_t* inside, auto source) {
-    constexpr int PER = NA == 4 ? 4 : BM == 128 ? 2 : 1;   // (what each kind has registers for)
+    constexpr int ALL = decltype(n)::value / NTHR, PER = std::min(ALL, NA == 4 ? 4 : BM == 128 ? 2 : 1);   // (what each kind has registers for)
     static_assert(decltype(n)::value % (PER * NTHR) == 0);
 #pragma unroll 1
     for (int slot = tid; slot < decltype(n)::value; slot += PER * NTHR) {
@@ -659,8 +659,9 @@ __global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ pa
 // Persistent workgroups: as many as are resident together.
 template <bool BF, int MODE, GatedKind KIND, bool SPLIT>
 hipError_t launch_tile(GatedGemm g, int cus, hipStream_t s) {
-  constexpr int B = KIND == kBig || KIND == kMid ? 256 : 128, BN = KIND == kMid ? 192 : B, WN = B == 256 ? 4 : 2;
-  constexpr int NA = KIND == kDeep ? 4 : 3, NB = KIND == kDeep ? 4 : 2;
+  constexpr int B = KIND == kBig || KIND == kMid ? 256 : 128, BN = KIND == kMid ? 192 : KIND == kSlim ? 64 : B, WN = B == 256 ? 4 : 2;
+  constexpr bool FAR = KIND == kDeep || KIND == kSlim;   // loads three steps ahead
+  constexpr int NA = FAR ? 4 : 3, NB = FAR ? 4 : 2;
   g.mt = MODE == kDw ? 2 * ceil_div64(g.a.outer, B) : ceil_div64(g.a.outer, B);
   g.nt = ceil_div64(g.b.outer, MODE == kFwd ? B / 2 : BN);
   const int64_t resident = (int64_t)cus * (KIND == kPair ? 2 : 1);
@@ -676,16 +677,20 @@ hipError_t product(GatedGemm g, const GatedPlan& plan, float* part, int cus, hip
   const int64_t whole = std::max<int64_t>(1, g.segs * g.full);
   g.split_steps = ceil_div64(whole, plan.splits);
   g.splits = ceil_div64(whole, g.split_steps);   // none without steps
-  if constexpr (WIDE)
+  if constexpr (WIDE) {
     if (plan.splits == 1 && plan.kind == kMid) return launch_tile<BF, MODE, kMid, false>(g, cus, s);
+    if (plan.splits == 1 && plan.stacked == 1 && plan.kind == kSlim) return launch_tile<BF, MODE, kSlim, false>(g, cus, s);
+  }
   if (plan.splits == 1 && plan.stacked == 1)
     return plan.kind == kBig    ? launch_tile<BF, MODE, kBig, false>(g, cus, s)
            : plan.kind == kPair ? launch_tile<BF, MODE, kPair, false>(g, cus, s)
                                 : launch_tile<BF, MODE, kDeep, false>(g, cus, s);
   g.part = part;
   hipError_t e = hipSuccess;
-  if constexpr (WIDE)
+  if constexpr (WIDE) {
     if (plan.kind == kMid) e = launch_tile<BF, MODE, kMid, true>(g, cus, s);
+    if (plan.kind == kSlim) e = launch_tile<BF, MODE, kSlim, true>(g, cus, s);
+  }
   if constexpr (MODE == kDx || WIDE)
     if (plan.kind == kBig) e = launch_tile<BF, MODE, kBig, true>(g, cus, s);
   if (plan.kind == kDeep) e = launch_tile<BF, MODE, kDeep, true>(g, cus, s);

@@ -13,8 +13,8 @@ constexpr int kBK = 64;   // contraction entries per step: two 16x16x32 products
 
 // How a product is run: 256 x 256 tiles, 128 x 128 tiles two to a CU, or one to a CU
 // with loads three steps ahead; and the splits of its contraction.  The linear layer's also
-// in 256 x 192 tiles.
-enum GatedKind { kBig, kPair, kDeep, kMid };
+// in 256 x 192 tiles, and in 128 x 64 with loads three steps ahead.
+enum GatedKind { kBig, kPair, kDeep, kMid, kSlim };
 struct GatedPlan {
   GatedKind kind;
   int64_t splits;

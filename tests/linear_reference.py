@@ -10,8 +10,6 @@ smallest step is the type's subnormal one, for fp16 after the scaling that bring
 import numpy as np
 import torch
 
-from oracle import linear as ol
-
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 TINY = {torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -25}
 E = 2.0 ** -24
@@ -27,7 +25,19 @@ def inputs(tokens, cols, rows, dtype, seed, bias=True, residual=True):
 
 
 def _act(act, z):
-    return (torch.from_numpy(v).cuda() for v in ol.act(act, z.cpu().numpy()))
+    """act(z) and act'(z) in fp64 on the device (oracle/linear.py's formulas)."""
+    if act is None:
+        return z, torch.ones_like(z)
+    if act == "silu":
+        s = torch.special.expit(z)
+        return z * s, s + z * s * (1 - s)
+    if act == "gelu":
+        phi = 0.5 * torch.special.erfc(-z / np.sqrt(2))
+        return z * phi, phi + z * torch.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+    c = 2 * np.sqrt(2 / np.pi)
+    a = c * (z + 0.044715 * z ** 3)
+    s = torch.special.expit(a)
+    return z * s, s + z * s * torch.special.expit(-a) * c * (1 + 3 * 0.044715 * z * z)
 
 
 def _z(x, W, bias):
