@@ -310,10 +310,10 @@ int moe_call(externd::MoeArgs& a, const externd_moe_weights* w, int64_t experts,
     a.ids = a.ids_out;
     a.weights = a.weights_out;
   }
-  const bool one = router && w && externd::moe_one(a);
+  const bool few = router && w && externd::moe_few(a);
   hipError_t e = router ? externd::run_moe_logits(a, space, s) : hipSuccess;
-  if (e == hipSuccess && !one) e = externd::run_moe_choose(a, space, router, w != nullptr, s);
-  if (e == hipSuccess && w) e = externd::run_moe_experts(a, space, one, s);
+  if (e == hipSuccess && !few) e = externd::run_moe_choose(a, space, router, w != nullptr, s);
+  if (e == hipSuccess && w) e = externd::run_moe_experts(a, space, few, s);
   if (e != hipSuccess) return hip_fail(e, "mixture of experts");
   return EXTERND_OK;
 }

@@ -39,7 +39,7 @@ struct MoeSpace {
   MoeGroup* groups;    // moe_most_groups of them
   uint32_t* tops;      // fp16: the largest magnitude of each slot's h, as bits of fp32; cleared by a call's first kernel
   float* h;            // fp16: slots x ldh
-  uint16_t* parts;     // h in two 16-bit parts, each slots x ldh
+  uint16_t* parts;     // bf16: h in two 16-bit parts, each slots x ldh; the same place
   float* part;         // slots x cols: what each slot's expert gives
   int64_t ldh;
   size_t bytes;
@@ -48,13 +48,14 @@ int64_t moe_most_groups(int64_t slots, int64_t experts);
 // experts_too: for the experts' products; without, for the router alone
 MoeSpace moe_space(void* base, int64_t tokens, int64_t experts, int64_t top, int64_t rows, int64_t cols, bool router, bool experts_too);
 
-// Whether the first product makes the choice itself (one token).
-inline bool moe_one(const MoeArgs& a) { return a.tokens == 1 && a.w.experts <= 256; }
+// Whether the first product makes the choice itself: a wave a token of its workgroups' eight, a lane a slot.
+constexpr int kMoeFewSlots = 64;
+inline bool moe_few(const MoeArgs& a) { return a.tokens <= 8 && a.slots() <= kMoeFewSlots && a.w.experts <= 256; }
 
 hipError_t run_moe_logits(const MoeArgs& a, const MoeSpace& s, hipStream_t stream);
 // Choice and weights from the logits, or a choice that was made elsewhere (router false); and, where plan is given, the groups.
 hipError_t run_moe_choose(const MoeArgs& a, const MoeSpace& s, bool router, bool plan, hipStream_t stream);
-// one: the choice is not made yet
-hipError_t run_moe_experts(const MoeArgs& a, const MoeSpace& s, bool one, hipStream_t stream);
+// few: the choice is not made yet
+hipError_t run_moe_experts(const MoeArgs& a, const MoeSpace& s, bool few, hipStream_t stream);
 
 }  // namespace externd

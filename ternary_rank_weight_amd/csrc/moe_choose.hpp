@@ -13,11 +13,10 @@ __device__ __forceinline__ uint64_t order_of(double v) {
   return b < 0 ? ~(uint64_t)b : (uint64_t)b | 0x8000000000000000ull;
 }
 
-// One token's first `upto` choices by a wave: lane l holds the logits of experts l C .. l C + C - 1.
-// Returns the last of them.  With upto = top, lane j < top has choice j in `chosen`, and in `weight`
-// exp(logit - the largest) over the sum of those of the chosen (normalize), or of all.
+// One token's choices by a wave: lane l holds the logits of experts l C .. l C + C - 1.  Lane j < top has choice j in
+// `chosen`, and in `weight` exp(logit - the largest) over the sum of those of the chosen (normalize), or of all (weighted; else 0).
 template <int C>
-__device__ int choose(const double* __restrict__ logits, int experts, int upto, bool normalize, int& chosen, float& weight) {
+__device__ void choose(const double* __restrict__ logits, int experts, int top, bool normalize, bool weighted, int& chosen, float& weight) {
   const int lane = threadIdx.x & (kWave - 1);
   double v[C];
   uint64_t key[C];   // 0 and taken: past the end, or chosen before
@@ -30,9 +29,8 @@ __device__ int choose(const double* __restrict__ logits, int experts, int upto, 
     key[c] = order_of(v[c] + 0.0);   // (-0 is 0)
   }
   double largest = 0.0, mine = 0.0;   // mine: the logit of this lane's choice
-  int last = 0;
   chosen = 0;
-  for (int j = 0; j < upto; ++j) {
+  for (int j = 0; j < top; ++j) {
     // the lane's largest, the first of equal ones; lanes without one are out
     int at = -1;
     uint64_t best = 0;
@@ -59,9 +57,10 @@ __device__ int choose(const double* __restrict__ logits, int experts, int upto, 
     expert = __builtin_amdgcn_readlane(expert, who);
     if (j == 0) largest = got;
     if (lane == j) { mine = got; chosen = expert; }
-    last = expert;
   }
-  const double e = lane < upto ? exp(mine - largest) : 0.0;
+  weight = 0.f;
+  if (!weighted) return;
+  const double e = lane < top ? exp(mine - largest) : 0.0;
   double part = e;
   if (!normalize) {
     part = 0.0;
@@ -70,7 +69,6 @@ __device__ int choose(const double* __restrict__ logits, int experts, int upto, 
       if (lane * C + c < experts) part += exp(v[c] - largest);
   }
   weight = (float)(e / lane63(wave_sum_to63(part)));
-  return last;
 }
 
 }  // namespace

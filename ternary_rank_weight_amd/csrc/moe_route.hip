@@ -73,7 +73,7 @@ __global__ __launch_bounds__(1024) void k_moe_choose(MoeArgs a, const double* __
     for (int64_t t = wave; t < a.tokens; t += 16) {
       int chosen;
       float weight;
-      choose<C>(logits + t * experts, experts, a.top, a.normalize, chosen, weight);
+      choose<C>(logits + t * experts, experts, a.top, a.normalize, true, chosen, weight);
       if (lane < a.top) {
         ids[t * a.top + lane] = chosen;
         a.ids_out[t * a.top + lane] = chosen;
@@ -160,8 +160,8 @@ MoeSpace moe_space(void* base, int64_t tokens, int64_t experts, int64_t top, int
     s.ldh = (rows + 7) / 8 * 8;
     s.groups = static_cast<MoeGroup*>(take(sizeof(MoeGroup) * (size_t)moe_most_groups(slots, experts)));
     s.tops = static_cast<uint32_t*>(take(4 * (size_t)slots));
-    s.h = static_cast<float*>(take(4 * (size_t)(slots * s.ldh)));   // (of no use to bf16)
-    s.parts = static_cast<uint16_t*>(take(4 * (size_t)(slots * s.ldh)));
+    s.h = static_cast<float*>(take(4 * (size_t)(slots * s.ldh)));
+    s.parts = reinterpret_cast<uint16_t*>(s.h);
     s.part = static_cast<float*>(take(4 * (size_t)(slots * cols)));
   }
   s.bytes = at;

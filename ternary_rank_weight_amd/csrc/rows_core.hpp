@@ -27,6 +27,14 @@ inline int64_t rows_tiles(int64_t rows, int apart_bits) {
 
 namespace {
 
+// A value as two of 16 bits: rounded, and what the rounding took away.
+template <bool BF>
+__device__ __forceinline__ void split16(float v, uint32_t& hi, uint32_t& lo) {
+  hi = f32_to_16<BF>(v);
+  const float rest = v - f32_from_16<BF>(hi);
+  lo = __builtin_isfinite(rest) ? f32_to_16<BF>(rest) : 0u;   // (infinite and NaN are in the first part)
+}
+
 // First row of a tile; its row i is first + (i << apart_bits).  (It may lie past the end.)
 __device__ __forceinline__ int64_t tile_row0(int64_t tile, int apart_bits) {
   return ((tile >> apart_bits) << (4 + apart_bits)) + (tile & (((int64_t)1 << apart_bits) - 1));
@@ -142,6 +150,56 @@ struct RowsParts {
   __device__ void finish_edge(int, int c, int cols, const Edge& raw, u32x4 (&f)[2]) const {
 #pragma unroll
     for (int e = 0; e < 2; ++e) f[e] = raw.p[e].get(part.row[e], c, cols);
+  }
+};
+
+// Vectors of fp32 entries, entered in two 16-bit parts after a multiplication by `scale`, a power of two that
+// brings the lane's row into fp16's range: the rounded value, and what the rounding took away.
+struct RowsScaled {
+  static constexpr int kParts = 2;
+  const float* row;
+  float scale;
+  struct Whole {
+    u32x4 a, b;
+  };
+  struct Edge {
+    float v[8];
+  };
+  __device__ void split(const float (&v)[8], u32x4 (&f)[2]) const {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) split16<false>(v[j + e] * scale, hi[e], lo[e]);
+      f[0][j / 2] = hi[0] | (hi[1] << 16);
+      f[1][j / 2] = lo[0] | (lo[1] << 16);
+    }
+  }
+  __device__ void load(int, int c, Whole& raw) const {
+    raw.a = *reinterpret_cast<const u32x4_a4*>(row + c);
+    raw.b = *reinterpret_cast<const u32x4_a4*>(row + c + 4);
+  }
+  __device__ void finish(int, int, const Whole& raw, u32x4 (&f)[2]) const {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = __uint_as_float(raw.a[j]);
+      v[4 + j] = __uint_as_float(raw.b[j]);
+    }
+    split(v, f);
+  }
+  // (the entries of Edge8's places: those of a row of eight and more that lie nearest)
+  __device__ void load_edge(int, int c, int cols, Edge& raw) const {
+    const int at = cols >= 8 ? max(0, min(c, cols - 8)) : c;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) raw.v[j] = row[max(0, min(at + j, cols - 1))];
+  }
+  __device__ void finish_edge(int, int c, int cols, const Edge& raw, u32x4 (&f)[2]) const {
+    const int at = cols >= 8 ? max(0, min(c, cols - 8)) : c;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = at + j >= max(c, 0) && at + j < min(c + 8, cols) ? raw.v[j] : 0.f;
+    split(v, f);
   }
 };
 
