@@ -1036,6 +1036,8 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, bias, act, residual):
         ctx.act = act
+        if not any(ctx.needs_input_grad[:3]):   # the residual's alone, which is dy
+            return linear_forward(x.detach(), W.detach(), None if bias is None else bias.detach(), act, residual.detach())
         y, z = linear_forward(x, W, bias, act, residual, save=True)
         ctx.save_for_backward(x, W, z)
         return y
@@ -1043,10 +1045,10 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        x, W, z = ctx.saved_tensors
         need_dx, need_dw, need_db, _, need_dr = ctx.needs_input_grad
         dx = dw = db = None
         if need_dx or need_dw or need_db:
+            x, W, z = ctx.saved_tensors
             dx, dw, db = linear_backward(x, W, z, dy, ctx.act, need_dx, need_dw, need_db)
         return dx, dw, db, None, dy if need_dr else None
 

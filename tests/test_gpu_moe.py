@@ -90,6 +90,37 @@ def test_layer(lib, dtype, tokens, cols, rows, experts, top):
     _check(lib, ops, top, ("silu", "gelu", "gelu_tanh")[(cols + rows) % 3], normalize=tokens % 2 == 0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("tokens,cols,rows,experts,top", [
+    (8, 72, 40, 256, 8), (8, 72, 40, 257, 8), (8, 200, 33, 9, 8), (9, 72, 40, 256, 7), (8, 72, 40, 255, 9), (7, 71, 39, 256, 9),
+    (2, 136, 48, 64, 32), (2, 136, 48, 64, 33), (1, 64, 40, 64, 64), (1, 64, 40, 65, 64), (1, 1000, 72, 1024, 64),
+    (8, 64, 24, 2, 2), (8, 64, 24, 1, 1), (4, 8, 8, 16, 16), (4, 8, 8, 17, 17)])
+def test_where_the_choices_are_made(lib, dtype, tokens, cols, rows, experts, top):
+    # up to 8 tokens, 64 slots and 256 experts the first product makes them, past that a kernel of its own
+    ops = _inputs(tokens, cols, rows, experts, dtype, tokens + experts)
+    for normalize in (False, True):
+        _check(lib, ops, top, "silu", normalize)
+
+
+def test_few_tokens_that_choose_alike(lib):
+    # all slots of a group: fewer experts than there may be groups; and every token its own experts
+    x, Wr, Wg, Wu, Wd = _inputs(8, 64, 40, 32, BF16, 12)
+    x = x.abs()
+    for chosen in ([5, 9, 31], [0, 1, 2]):
+        Wr[:] = -1
+        for k, e in enumerate(chosen):
+            Wr[e] = 2.0 ** -k
+        ids = _check(lib, (x, Wr, Wg, Wu, Wd), 3)[1]
+        assert bool((ids == torch.tensor(chosen, device="cuda", dtype=torch.int32)).all())
+    Wr[:] = 0
+    x[:] = 0
+    for t in range(8):
+        x[t, t] = 1
+        Wr[4 * t:4 * t + 4, t] = torch.tensor([1.0, 2.0, 3.0, 4.0], device="cuda").bfloat16()
+    ids = _check(lib, (x, Wr, Wg, Wu, Wd), 4)[1]
+    assert torch.equal(ids, (4 * torch.arange(8, device="cuda")[:, None] + torch.arange(3, -1, -1, device="cuda")).int())
+
+
 @pytest.mark.parametrize("normalize", [False, True])
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 def test_kinds_and_fp32_routers(lib, act, normalize):
