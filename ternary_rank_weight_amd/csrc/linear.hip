@@ -22,18 +22,27 @@ namespace externd {
 namespace {
 
 // db: sums over the tokens of dz in fp32, in an order that does not depend on timing.  A workgroup takes COLS
-// columns, a wave's lanes 64 / COLS tokens of them at a time; the lanes' and the waves' sums are joined in order.  16
-// columns where 64 would leave most compute units without any (777 tokens at 1001 rows: 15 us with 64).
+// columns, a wave's lanes 64 / COLS tokens of them at a time; the lanes' and the waves' sums are joined in order.
+// Fewer columns where more would leave compute units without any (777 tokens at 1001 rows: 15 us with 64, 7 with 16),
+// but whole lines of z where there are enough (2048 tokens at 9728 rows, with dz: 74 us with 16, 55 with 32).
 constexpr int kSumWaves = 16;
+struct BiasArgs {
+  const uint16_t* dy;
+  const float* z;   // null: without an activation
+  uint16_t* db;
+  int64_t lddy, tokens, rows;
+  int act;
+};
 template <bool BF, int COLS>
-__global__ __launch_bounds__(kSumWaves * kWave) void k_bias_sums(const uint16_t* __restrict__ dy, int64_t lddy,
-                                                                  const float* __restrict__ z, int act, int64_t tokens,
-                                                                  int64_t rows, uint16_t* __restrict__ db) {
+__device__ __forceinline__ void sum_bias(const BiasArgs& a, int64_t block) {
+  const uint16_t* __restrict__ const dy = a.dy;
+  const float* __restrict__ const z = a.z;
+  const int64_t tokens = a.tokens, rows = a.rows, lddy = a.lddy;
   constexpr int LINES = kSumWaves * kWave / COLS;   // tokens that the workgroup takes at once
   constexpr int U = 8;                              // times that on their way
   __shared__ float red[LINES][COLS];
   const int col = threadIdx.x % COLS, line = threadIdx.x / COLS;
-  const int64_t c = (int64_t)blockIdx.x * COLS + col, at = min(c, rows - 1);
+  const int64_t c = block * COLS + col, at = min(c, rows - 1);
   float sum[2] = {};
   auto add = [&](auto slope) {
     for (int64_t t0 = line; t0 < tokens; t0 += U * LINES) {
@@ -50,10 +59,10 @@ __global__ __launch_bounds__(kSumWaves * kWave) void k_bias_sums(const uint16_t*
     }
   };
   if (z)
-    with_act(act, [&](auto kind) {
+    with_act(a.act, [&](auto kind) {
       add([](float v) {
-        float a, s;
-        act_both_fast<decltype(kind)::value>(v, a, s);
+        float h, s;
+        act_both_fast<decltype(kind)::value>(v, h, s);
         return s;
       });
     });
@@ -64,18 +73,52 @@ __global__ __launch_bounds__(kSumWaves * kWave) void k_bias_sums(const uint16_t*
     if (line < n) red[line][col] += red[line + n][col];
     __syncthreads();
   }
-  if (line == 0 && c < rows) db[c] = (uint16_t)f32_to_16<BF>(red[0][col]);
+  if (line == 0 && c < rows) a.db[c] = (uint16_t)f32_to_16<BF>(red[0][col]);
 }
 
-template <bool BF>
-void launch_bias_sums(const LinearArgs& a, const float* z, hipStream_t s) {
-  const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
-  uint16_t* db = static_cast<uint16_t*>(a.db);
-  const dim3 block(kSumWaves * kWave);
-  if (a.rows >= (int64_t)64 * a.cus)
-    hipLaunchKernelGGL((k_bias_sums<BF, 64>), dim3((unsigned)ceil_div64(a.rows, 64)), block, 0, s, dy, a.lddy, z, a.act, a.tokens, a.rows, db);
+template <bool BF, int COLS>
+__global__ __launch_bounds__(kSumWaves * kWave) void k_bias_sums(BiasArgs a) { sum_bias<BF, COLS>(a, blockIdx.x); }
+
+// dz in parts, and db by the first workgroups, which are its slowest: together in the time of the longer, and one
+// launch.  777 tokens x 1001, fp16: 9.8 us, apart 6.5 and 6.0.  Bound by HBM with many: 2048 x 9728, bf16, 55 us for
+// 320 MB, of which dy and z come twice (apart, with 16 columns: 51 and 31).
+struct PartsArgs {
+  SlopeArgs s;
+  int64_t ldd, rest;
+  const uint32_t *by_token, *by_unit;
+  uint16_t *dz, *dz_by_unit;
+  BiasArgs b;
+  int bias_blocks;
+};
+template <bool BF, int COLS>
+__global__ __launch_bounds__(kSumWaves * kWave) void k_linear_parts(PartsArgs a) {
+  if ((int)blockIdx.x < a.bias_blocks) sum_bias<BF, COLS>(a.b, blockIdx.x);
   else
-    hipLaunchKernelGGL((k_bias_sums<BF, 16>), dim3((unsigned)ceil_div64(a.rows, 16)), block, 0, s, dy, a.lddy, z, a.act, a.tokens, a.rows, db);
+    put_slopes<BF, false>(a.s, a.ldd, a.b.act, a.rest, a.by_token, a.by_unit, a.dz, a.dz_by_unit,
+                          (int64_t)(blockIdx.x - a.bias_blocks) * blockDim.x + threadIdx.x,
+                          (int64_t)(gridDim.x - a.bias_blocks) * blockDim.x);
+}
+
+// Columns of db a workgroup takes.
+int bias_cols(const LinearArgs& a) { return a.rows >= (int64_t)64 * a.cus ? 64 : a.rows >= (int64_t)32 * a.cus ? 32 : 16; }
+
+hipError_t launch_bias_sums(const LinearArgs& a, const BiasArgs& b, hipStream_t s) {
+  const int cols = bias_cols(a);
+  const auto kernel = a.dtype == EXTERND_BF16 ? (cols == 64 ? k_bias_sums<true, 64> : cols == 32 ? k_bias_sums<true, 32> : k_bias_sums<true, 16>)
+                                              : (cols == 64 ? k_bias_sums<false, 64> : cols == 32 ? k_bias_sums<false, 32> : k_bias_sums<false, 16>);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)ceil_div64(a.rows, cols)), dim3(kSumWaves * kWave), 0, s, b);
+  return hipGetLastError();
+}
+
+hipError_t launch_parts(const LinearArgs& a, PartsArgs q, hipStream_t s) {
+  const int cols = bias_cols(a);
+  constexpr int THREADS = kSumWaves * kWave;
+  q.bias_blocks = a.db ? (int)ceil_div64(a.rows, cols) : 0;
+  const int64_t most = std::min<int64_t>(ceil_div64(a.tokens * (q.ldd / 8), THREADS), 1 << 15);
+  const auto kernel = a.dtype == EXTERND_BF16 ? (cols == 64 ? k_linear_parts<true, 64> : cols == 32 ? k_linear_parts<true, 32> : k_linear_parts<true, 16>)
+                                              : (cols == 64 ? k_linear_parts<false, 64> : cols == 32 ? k_linear_parts<false, 32> : k_linear_parts<false, 16>);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(q.bias_blocks + most)), dim3(THREADS), 0, s, q);
+  return hipGetLastError();
 }
 
 hipError_t product(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, bool bf, int cus,
@@ -188,12 +231,10 @@ hipError_t run_linear_backward(const LinearArgs& a, void* ws, hipStream_t s) {
     }
     return hipSuccess;
   }
-  if (a.db) {
-    if (bf) launch_bias_sums<true>(a, parts ? a.z : nullptr, s);
-    else launch_bias_sums<false>(a, parts ? a.z : nullptr, s);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  if (!a.dx && !a.dw) return hipSuccess;
+  const BiasArgs bias = {static_cast<const uint16_t*>(a.dy), parts ? a.z : nullptr, static_cast<uint16_t*>(a.db), a.lddy, a.tokens, a.rows, a.act};
+  const bool products = a.dx || a.dw;
+  if (a.db && !(parts && products) && (e = launch_bias_sums(a, bias, s)) != hipSuccess) return e;
+  if (!products) return hipSuccess;
   char* w = static_cast<char*>(ws);
   // dz and its rest; fp16: scaled by token for dx, and again by row of W for dW
   const int64_t ldd = padded(a.rows, 8), part_len = a.tokens * ldd;
@@ -212,18 +253,15 @@ hipError_t run_linear_backward(const LinearArgs& a, void* ws, hipStream_t s) {
   if (e != hipSuccess) return e;
   w += region(2 * (size_t)((al ? 0 : copy_entries(a.tokens, a.cols, a.rows)) + (parts || reads_dy ? 0 : a.tokens * padded(a.rows, kBK))));
   if (parts) {
-    const dim3 grid(blocks(a.tokens * (ldd / 8))), block(256);
-    if (bf) {
-      hipLaunchKernelGGL((k_gated_slopes<true, false>), grid, block, 0, s, sa, ldd, a.act, part_len, nullptr, nullptr, dz, nullptr);
-    } else {
+    if (!bf) {
       const int64_t strips = ceil_div64(a.rows, 256);
       const int strip = ceil_div64(a.tokens, 64) * strips >= 2 * a.cus ? 64 : 16;
       hipLaunchKernelGGL(k_gated_tops<false>, dim3((unsigned)(ceil_div64(a.tokens, strip) * strips)), dim3(256), 0, s, sa, ldd,
                          a.act, strip, by_token, by_unit);
-      hipLaunchKernelGGL((k_gated_slopes<false, false>), grid, block, 0, s, sa, ldd, a.act, part_len, a.dx ? by_token : nullptr,
-                         a.dw ? by_unit : nullptr, dz, dz_by_unit);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const PartsArgs q = {sa, ldd, part_len, !bf && a.dx ? by_token : nullptr, !bf && a.dw ? by_unit : nullptr, dz, dz_by_unit, bias, 0};
+    if ((e = launch_parts(a, q, s)) != hipSuccess) return e;
   }
   float* part = reinterpret_cast<float*>(w);
   const int64_t cols8 = padded(a.cols, 8);

@@ -125,14 +125,14 @@ __global__ __launch_bounds__(256) void k_gated_tops(SlopeArgs a, int64_t ldd, in
 // it writes stays in the last-level cache).  fp16: scaled by the power of two that
 // k_gated_tops' bits give for the token, or for the hidden unit of dg and of du (the other null).  Not GATED: dg alone,
 // in fp16 scaled by token into dg's place and by hidden unit into du's, each where its bits are given.
-template <bool BF, bool GATED = true>
-__global__ __launch_bounds__(256) void k_gated_slopes(SlopeArgs a, int64_t ldd, int act, int64_t rest,
-                                                       const uint32_t* __restrict__ by_token,
-                                                       const uint32_t* __restrict__ by_unit,
-                                                       uint16_t* __restrict__ dg, uint16_t* __restrict__ du) {
+// This is one thread's part, `id` of `threads`.
+template <bool BF, bool GATED>
+__device__ __forceinline__ void put_slopes(const SlopeArgs& a, int64_t ldd, int act, int64_t rest, const uint32_t* __restrict__ by_token,
+                                           const uint32_t* __restrict__ by_unit, uint16_t* __restrict__ dg, uint16_t* __restrict__ du,
+                                           int64_t id, int64_t threads) {
   const int64_t per = ldd / 8, total = a.tokens * per;
   with_act(act, [&](auto kind) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = id; i < total; i += threads) {
       const int64_t t = i / per, c = (i - t * per) * 8;
       float vg[8], vu[8];
       slopes_at<BF, decltype(kind)::value, BF, GATED>(a, t, c, vg, vu);
@@ -181,6 +181,14 @@ __global__ __launch_bounds__(256) void k_gated_slopes(SlopeArgs a, int64_t ldd, 
       if (second) *reinterpret_cast<u32x4*>(du + rest + t * ldd + c) = ru;
     }
   });
+}
+
+template <bool BF>
+__global__ __launch_bounds__(256) void k_gated_slopes(SlopeArgs a, int64_t ldd, int act, int64_t rest,
+                                                       const uint32_t* __restrict__ by_token,
+                                                       const uint32_t* __restrict__ by_unit,
+                                                       uint16_t* __restrict__ dg, uint16_t* __restrict__ du) {
+  put_slopes<BF, true>(a, ldd, act, rest, by_token, by_unit, dg, du, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 }  // namespace

@@ -47,7 +47,7 @@ def test_parts_of_the_epilogue(lib, act, bias, residual):
 
 
 @pytest.mark.parametrize("tokens,cols,rows", [(4096, 136, 2320), (4100, 192, 2304), (2000, 4160, 40), (70, 200, 9000),
-                                              (2048, 2560, 1024), (300, 9728, 640)])
+                                              (2048, 2560, 1024), (300, 9728, 640), (70, 40, 16401)])
 def test_more_tiles_than_units_resident_and_splits(lib, tokens, cols, rows):
     _check(lib, *inputs(tokens, cols, rows, BF16, tokens), None)
     _check(lib, *inputs(tokens, cols, rows, F16, tokens), "gelu")
