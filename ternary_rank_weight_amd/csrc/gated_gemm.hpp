@@ -109,21 +109,21 @@ __device__ __forceinline__ void for_constants(F&& f) {
 // kept 234 us; dx, both parts of dg and du, 337 us and its join 16; dW, both parts, 333 us
 // (1.23 PFLOP/s).  What is lost is the end of a tile (6 of 62 us a tile of 40 steps) and
 // the last round of tiles.
+// `block` of `grid` workgroups.  The images are separate objects: the compiler then sees that a read of one need not
+// wait for the loads into another.
+struct Images {
+  lds16 a[4], b[4];
+};
 template <bool BF, int MODE, int BM, int BN, int WM, int WN, int NA, int NB, bool SPLIT>
-__global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void k_gated_gemm(GatedGemm g) {
+__device__ __forceinline__ void gated_gemm(const GatedGemm& g, const Images& images, uint32_t block, uint32_t grid) {
   constexpr int NTHR = WM * WN * kWave;
   constexpr bool ACOLS = MODE == kDw || MODE == kLinDw, BCOLS = MODE != kFwd && MODE != kLin;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   using TA = Tile<ACOLS, BM>;
   using TB = Tile<BCOLS, BN>;
   constexpr int SA = TA::kSlots / NTHR, SB = TB::kSlots / NTHR;
-  // separate objects: the compiler then sees that a read of one image need not
-  // wait for the loads into another
-  constexpr int A3 = NA > 3 ? BM * kBK : 8, B2 = NB > 2 ? BN * kBK : 8;
-  __shared__ __align__(16) uint16_t sa0[BM * kBK], sa1[BM * kBK], sa2[BM * kBK], sa3[A3];
-  __shared__ __align__(16) uint16_t sb0[BN * kBK], sb1[BN * kBK], sb2[B2], sb3[B2];
-  const lds16 la0 = (lds16)sa0, la1 = (lds16)sa1, la2 = (lds16)sa2, la3 = (lds16)sa3;
-  const lds16 lb0 = (lds16)sb0, lb1 = (lds16)sb1, lb2 = (lds16)sb2, lb3 = (lds16)sb3;
+  const lds16 la0 = images.a[0], la1 = images.a[1], la2 = images.a[2], la3 = images.a[3];
+  const lds16 lb0 = images.b[0], lb1 = images.b[1], lb2 = images.b[2], lb3 = images.b[3];
   auto image_a = [&](auto index) {
     constexpr int I = decltype(index)::value % NA;
     if constexpr (I == 0) return la0;
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
     q.last = q.split == g.splits - 1;
     return q;
   };
-  Unit u = locate(blockIdx.x);
+  Unit u = locate(block);
 
   f32x4 acc[MI][NI];
   auto clear = [&] {
@@ -575,7 +575,7 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   begin(u);
   wait_vm<0, 0>();
 #pragma unroll 1
-  for (uint32_t at = blockIdx.x;;) {
+  for (uint32_t at = block;;) {
     clear();
     block_barrier();   // every wave has waited for its first loads
     contract();
@@ -591,9 +591,9 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
     // The next unit's first loads travel while this one's outputs are worked out,
     // and have arrived before the first output is stored: the stores then drain
     // behind the next unit's products.
-    at += gridDim.x;
+    at += grid;
     const bool more = at < units;
-    const Unit next = locate(more ? at : blockIdx.x);
+    const Unit next = locate(more ? at : block);
     if (more) begin(next);
     const bool inside = u.m0 + BM <= g.mo && u.n0 + BNO <= g.ldo;
     if constexpr (!SPLIT) round_outputs();
@@ -606,6 +606,26 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
     if (!more) break;
     u = next;
   }
+}
+
+template <bool BF, int MODE, int BM, int BN, int WM, int WN, int NA, int NB, bool SPLIT>
+__global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void k_gated_gemm(GatedGemm g) {
+  constexpr int A3 = NA > 3 ? BM * kBK : 8, B2 = NB > 2 ? BN * kBK : 8;
+  __shared__ __align__(16) uint16_t sa0[BM * kBK], sa1[BM * kBK], sa2[BM * kBK], sa3[A3];
+  __shared__ __align__(16) uint16_t sb0[BN * kBK], sb1[BN * kBK], sb2[B2], sb3[B2];
+  const Images images = {{(lds16)sa0, (lds16)sa1, (lds16)sa2, (lds16)sa3}, {(lds16)sb0, (lds16)sb1, (lds16)sb2, (lds16)sb3}};
+  gated_gemm<BF, MODE, BM, BN, WM, WN, NA, NB, SPLIT>(g, images, blockIdx.x, gridDim.x);
+}
+
+// The linear layer's dx and dW in one launch, `first` workgroups for dx: both in 128 x 64 tiles with loads two steps ahead, two
+// workgroups to a CU, where each alone would leave CUs without any.  777 tokens at 1001 x 1237, fp16, 140 and 160
+// tiles: 27 us, one after the other with loads three steps ahead 20 + 17.
+template <bool BF>
+__global__ __launch_bounds__(4 * kWave, 2) void k_linear_gradients(GatedGemm dx, GatedGemm dw, uint32_t first) {
+  __shared__ __align__(16) uint16_t sa0[128 * kBK], sa1[128 * kBK], sa2[128 * kBK], sb0[64 * kBK], sb1[64 * kBK], sb2[64 * kBK];
+  const Images images = {{(lds16)sa0, (lds16)sa1, (lds16)sa2, (lds16)sa0}, {(lds16)sb0, (lds16)sb1, (lds16)sb2, (lds16)sb0}};
+  if (blockIdx.x < first) gated_gemm<BF, kDx, 128, 64, 2, 2, 3, 3, false>(dx, images, blockIdx.x, first);
+  else gated_gemm<BF, kLinDw, 128, 64, 2, 2, 3, 3, false>(dw, images, blockIdx.x - first, gridDim.x - first);
 }
 
 // Outputs of a product, and of a join.
@@ -715,6 +735,22 @@ hipError_t any_linear(GatedProduct mode, const GatedGemm& g, const GatedPlan& pl
   if (mode == kLin) return product<BF, kLin, true>(g, plan, part, cus, s);
   if (mode == kDx) return product<BF, kDx, true>(g, plan, part, cus, s);
   return product<BF, kLinDw, true>(g, plan, part, cus, s);
+}
+
+template <bool BF>
+hipError_t both_gradients(GatedGemm dx, GatedGemm dw, hipStream_t s) {
+  int64_t tiles[2];
+  int n = 0;
+  for (GatedGemm* g : {&dx, &dw}) {
+    g->full = g->inner / kBK;
+    g->split_steps = std::max<int64_t>(1, g->segs * g->full);
+    g->splits = 1;
+    g->mt = ceil_div64(g->a.outer, 128);
+    g->nt = ceil_div64(g->b.outer, 64);
+    tiles[n++] = g->mt * g->nt;
+  }
+  hipLaunchKernelGGL(k_linear_gradients<BF>, dim3((unsigned)(tiles[0] + tiles[1])), dim3(4 * kWave), 0, s, dx, dw, (uint32_t)tiles[0]);
+  return hipGetLastError();
 }
 
 }  // namespace

@@ -267,34 +267,30 @@ hipError_t run_linear_backward(const LinearArgs& a, void* ws, hipStream_t s) {
   const int64_t cols8 = padded(a.cols, 8);
   const uint16_t* d = parts ? dz : o.dy;
   const int64_t ld = parts ? ldd : o.lddy;
-  if (a.dx) {
-    const GatedPlan px = plan_linear_dx(a.tokens, a.cols, a.rows, parts, a.cus);
-    GatedGemm g = {};
-    g.a = {{d, d}, ld, px.stacked * a.tokens};
-    g.b = {{o.w, o.w}, o.ldw, cols8};
-    g.segs = parts && px.stacked == 1 ? 2 : 1;   // stacked: a segment's rows are both parts
-    g.rest = part_len;
-    g.tops = parts && !bf ? by_token : nullptr;
-    g.inner = a.rows;
-    g.out[0] = static_cast<uint16_t*>(a.dx);
-    g.mo = px.stacked * a.tokens;
-    g.ldo = a.cols;
-    if ((e = product(kDx, g, px, part, bf, a.cus, s)) != hipSuccess) return e;
-  }
-  if (a.dw) {
-    GatedGemm g = {};
-    const uint16_t* const du = parts ? dz_by_unit : d;
-    g.a = {{du, du}, ld, ldd};
-    g.b = {{o.x, o.x}, o.ldx, cols8};
-    g.segs = parts ? 2 : 1;
-    g.rest = part_len;
-    g.tops = parts && !bf ? by_unit : nullptr;
-    g.inner = a.tokens;
-    g.out[0] = static_cast<uint16_t*>(a.dw);
-    g.mo = a.rows;
-    g.ldo = a.cols;
-    if ((e = product(kLinDw, g, plan_linear_dw(a.tokens, a.cols, a.rows, parts, a.cus), part, bf, a.cus, s)) != hipSuccess) return e;
-  }
+  const GatedPlan px = plan_linear_dx(a.tokens, a.cols, a.rows, parts, a.cus), pw = plan_linear_dw(a.tokens, a.cols, a.rows, parts, a.cus);
+  GatedGemm x = {}, y = {};   // dx and dW
+  x.a = {{d, d}, ld, px.stacked * a.tokens};
+  x.b = {{o.w, o.w}, o.ldw, cols8};
+  x.segs = parts && px.stacked == 1 ? 2 : 1;   // stacked: a segment's rows are both parts
+  x.rest = part_len;
+  x.tops = parts && !bf ? by_token : nullptr;
+  x.inner = a.rows;
+  x.out[0] = static_cast<uint16_t*>(a.dx);
+  x.mo = px.stacked * a.tokens;
+  x.ldo = a.cols;
+  const uint16_t* const du = parts ? dz_by_unit : d;
+  y.a = {{du, du}, ld, ldd};
+  y.b = {{o.x, o.x}, o.ldx, cols8};
+  y.segs = parts ? 2 : 1;
+  y.rest = part_len;
+  y.tops = parts && !bf ? by_unit : nullptr;
+  y.inner = a.tokens;
+  y.out[0] = static_cast<uint16_t*>(a.dw);
+  y.mo = a.rows;
+  y.ldo = a.cols;
+  if (a.dx && a.dw && linear_joins(px, pw)) return bf ? linear_gradients_bf16(x, y, s) : linear_gradients_f16(x, y, s);
+  if (a.dx && (e = product(kDx, x, px, part, bf, a.cus, s)) != hipSuccess) return e;
+  if (a.dw && (e = product(kLinDw, y, pw, part, bf, a.cus, s)) != hipSuccess) return e;
   return hipSuccess;
 }
 

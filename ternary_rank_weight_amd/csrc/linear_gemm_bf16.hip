@@ -7,5 +7,6 @@ hipError_t linear_product_bf16(GatedProduct mode, const GatedGemm& g, const Gate
                               hipStream_t s) {
   return any_linear<true>(mode, g, plan, part, cus, s);
 }
+hipError_t linear_gradients_bf16(const GatedGemm& dx, const GatedGemm& dw, hipStream_t s) { return both_gradients<true>(dx, dw, s); }
 
 }  // namespace externd

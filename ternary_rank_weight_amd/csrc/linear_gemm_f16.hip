@@ -7,5 +7,6 @@ hipError_t linear_product_f16(GatedProduct mode, const GatedGemm& g, const Gated
                               hipStream_t s) {
   return any_linear<false>(mode, g, plan, part, cus, s);
 }
+hipError_t linear_gradients_f16(const GatedGemm& dx, const GatedGemm& dw, hipStream_t s) { return both_gradients<false>(dx, dw, s); }
 
 }  // namespace externd

@@ -67,4 +67,9 @@ inline GatedPlan plan_linear_dw(int64_t tokens, int64_t cols, int64_t rows, bool
   return plan_linear(kLinDw, rows, cols, (parts ? 2 : 1) * steps_of(tokens), cus);
 }
 
+// dx and dW in one launch: both in whole 128 x 64 tiles, of which each has no more than CUs.
+inline bool linear_joins(const GatedPlan& dx, const GatedPlan& dw) {
+  return dx.kind == kSlim && dw.kind == kSlim && dx.splits == 1 && dw.splits == 1 && dx.stacked == 1;
+}
+
 }  // namespace externd

@@ -21,7 +21,12 @@ def test_form(lib, dtype, tokens, cols, rows, act):
     x, W, b, r, dy = inputs(tokens, cols, rows, dtype, tokens + cols + rows)
     y, z = lib.linear_forward(x, W, b, act, r, save=True)
     assert torch.equal(lib.linear_forward(x, W, b, act, r), y)
-    got = (z, y, *lib.linear_backward(x, W, z, dy, act))
+    grads = lib.linear_backward(x, W, z, dy, act)
+    # dx and dW may be made by one launch: each alone is the same
+    assert torch.equal(lib.linear_backward(x, W, z, dy, act, need_dw=False)[0], grads[0])
+    assert torch.equal(lib.linear_backward(x, W, z, dy, act, need_dx=False, need_db=False)[1], grads[1])
+    assert torch.equal(lib.linear_backward(x, W, z, dy, act, need_dx=False, need_dw=False)[2], grads[2])
+    got = (z, y, *grads)
     for have, (name, want, tol) in zip(got, forward_checks(x, W, b, act, r) + gradient_checks(x, W, b, dy, act)):
         if have is None:
             continue

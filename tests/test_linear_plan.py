@@ -24,7 +24,7 @@ int main() {
     printf("%d %lld %lld %lld  ", x.kind, (long long)x.splits, (long long)x.stacked,
            (long long)((parts && x.stacked == 1 ? 2 : 1) * steps_of(r)));
     printf("%d %lld 1 %lld  ", w.kind, (long long)w.splits, (long long)((parts ? 2 : 1) * steps_of(t)));
-    printf("%d %d\n", linear_takes_rows(t, c, r, true, cus), linear_takes_rows(t, c, r, false, cus));
+    printf("%d %d %d\n", linear_takes_rows(t, c, r, true, cus), linear_takes_rows(t, c, r, false, cus), linear_joins(x, w));
   }
 }
 """
@@ -36,7 +36,7 @@ FAR = (DEEP, SLIM)
 @pytest.fixture(scope="module")
 def plans(tmp_path_factory):
     """plans(shapes) -> per shape ([(kind, splits, stacked, steps) of the forward, dx and dW], few-token kernel when
-    aligned, and when not)."""
+    aligned, and when not, dx and dW in one launch)."""
     gxx = shutil.which("g++")
     if not gxx:
         pytest.skip("no host compiler")
@@ -49,7 +49,7 @@ def plans(tmp_path_factory):
         text = "".join(f"{t} {c} {r} {int(parts)} {cus}\n" for t, c, r, parts in shapes)
         out = subprocess.run([str(where / "plan")], input=text, capture_output=True, text=True, check=True).stdout
         rows = [list(map(int, line.split())) for line in out.splitlines()]
-        return [([tuple(row[i:i + 4]) for i in (0, 4, 8)], bool(row[12]), bool(row[13])) for row in rows]
+        return [([tuple(row[i:i + 4]) for i in (0, 4, 8)], bool(row[12]), bool(row[13]), bool(row[14])) for row in rows]
     return run
 
 
@@ -63,7 +63,7 @@ def counts(splits, steps):
 
 def forms(entry):
     """(product, kind, split, steps modulo what its images repeat after) of units of eight steps and more."""
-    products, rows, _ = entry
+    products, rows = entry[:2]
     for product, (kind, splits, stacked, steps) in enumerate(products):
         used, ns = counts(splits, steps)
         if product == 0 and rows:
@@ -82,14 +82,22 @@ def test_shapes_reach_every_form(plans):
     assert not WANT - seen
 
 
+def test_shapes_reach_every_number_of_steps_of_joined_gradients(plans):
+    seen = {(product, steps % 3) for products, _, _, joined in plans(SHAPES) if joined for product in (1, 2)
+            for steps in products[product][3:] if steps >= 8}
+    assert seen == {(product, n) for product in (1, 2) for n in range(3)}
+
+
 def test_plans_keep_what_the_kernels_assume(plans):
     shapes = [(t, c, r, parts) for t in (1, 16, 33, 64, 65, 200, 777, 4096, 100000) for c in (1, 63, 64, 520, 2560, 9728, 40000)
               for r in (1, 65, 640, 4100, 9728, 1 << 21) for parts in (False, True)]
     for cus in (256, 304, 32):
-        for (t, c, r, parts), (products, rows, unaligned_rows) in zip(shapes, plans(shapes, cus)):
+        for (t, c, r, parts), (products, rows, unaligned_rows, joined) in zip(shapes, plans(shapes, cus)):
             assert unaligned_rows == (t <= 32) and not (rows and t > 32) and (rows or t > 3)
             for product, (kind, splits, stacked, steps) in enumerate(products):
                 assert 1 <= splits <= 16 and (splits == 1 or steps >= 4 * splits) and not (splits > 1 and kind == PAIR)
+                if joined and product:
+                    assert (kind, splits, stacked) == (SLIM, 1, 1)
                 assert stacked == 1 or (product == 1 and kind in FAR and t <= 64 and parts)
                 if kind in FAR:
                     m, n = ((t, r), (stacked * t, c), (r, c))[product]
