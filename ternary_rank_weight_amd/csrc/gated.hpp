@@ -58,8 +58,8 @@ hipError_t linear_product_bf16(GatedProduct mode, const GatedGemm& g, const Gate
                                hipStream_t s);
 hipError_t linear_product_f16(GatedProduct mode, const GatedGemm& g, const GatedPlan& plan, float* part, int cus,
                               hipStream_t s);
-// dx and dW together, of plans that linear_joins takes.
-hipError_t linear_gradients_bf16(const GatedGemm& dx, const GatedGemm& dw, hipStream_t s);
-hipError_t linear_gradients_f16(const GatedGemm& dx, const GatedGemm& dw, hipStream_t s);
+// dx and dW together, in the numbers of workgroups and tiles that linear_join says.
+hipError_t linear_gradients_bf16(const GatedGemm& dx, const GatedGemm& dw, int64_t first, int64_t rest, GatedKind kind, hipStream_t s);
+hipError_t linear_gradients_f16(const GatedGemm& dx, const GatedGemm& dw, int64_t first, int64_t rest, GatedKind kind, hipStream_t s);
 
 }  // namespace externd

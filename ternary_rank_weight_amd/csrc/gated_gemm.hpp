@@ -617,15 +617,17 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
   gated_gemm<BF, MODE, BM, BN, WM, WN, NA, NB, SPLIT>(g, images, blockIdx.x, gridDim.x);
 }
 
-// The linear layer's dx and dW in one launch, `first` workgroups for dx: both in 128 x 64 tiles with loads two steps ahead, two
-// workgroups to a CU, where each alone would leave CUs without any.  777 tokens at 1001 x 1237, fp16, 140 and 160
-// tiles: 27 us, one after the other with loads three steps ahead 20 + 17.
-template <bool BF>
-__global__ __launch_bounds__(4 * kWave, 2) void k_linear_gradients(GatedGemm dx, GatedGemm dw, uint32_t first) {
-  __shared__ __align__(16) uint16_t sa0[128 * kBK], sa1[128 * kBK], sa2[128 * kBK], sb0[64 * kBK], sb1[64 * kBK], sb2[64 * kBK];
+// The linear layer's dx and dW in one launch, `first` workgroups for dx.  128 x 64 tiles with loads two steps ahead, two
+// workgroups to a CU, where each product alone would leave CUs without any: 777 tokens at 1001 x 1237, fp16, 140 and 160
+// tiles: 27 us, one after the other with loads three steps ahead 20 + 17.  256 x 192 tiles, one workgroup to a CU: see
+// linear_join.
+template <bool BF, int BM, int BN, int WM, int WN, int NB>
+__global__ __launch_bounds__(WM * WN * kWave, 2) void k_linear_gradients(GatedGemm dx, GatedGemm dw, uint32_t first) {
+  constexpr int B2 = NB > 2 ? BN * kBK : 8;
+  __shared__ __align__(16) uint16_t sa0[BM * kBK], sa1[BM * kBK], sa2[BM * kBK], sb0[BN * kBK], sb1[BN * kBK], sb2[B2];
   const Images images = {{(lds16)sa0, (lds16)sa1, (lds16)sa2, (lds16)sa0}, {(lds16)sb0, (lds16)sb1, (lds16)sb2, (lds16)sb0}};
-  if (blockIdx.x < first) gated_gemm<BF, kDx, 128, 64, 2, 2, 3, 3, false>(dx, images, blockIdx.x, first);
-  else gated_gemm<BF, kLinDw, 128, 64, 2, 2, 3, 3, false>(dw, images, blockIdx.x - first, gridDim.x - first);
+  if (blockIdx.x < first) gated_gemm<BF, kDx, BM, BN, WM, WN, 3, NB, false>(dx, images, blockIdx.x, first);
+  else gated_gemm<BF, kLinDw, BM, BN, WM, WN, 3, NB, false>(dw, images, blockIdx.x - first, gridDim.x - first);
 }
 
 // Outputs of a product, and of a join.
@@ -738,18 +740,20 @@ hipError_t any_linear(GatedProduct mode, const GatedGemm& g, const GatedPlan& pl
 }
 
 template <bool BF>
-hipError_t both_gradients(GatedGemm dx, GatedGemm dw, hipStream_t s) {
-  int64_t tiles[2];
-  int n = 0;
+hipError_t both_gradients(GatedGemm dx, GatedGemm dw, int64_t first, int64_t rest, GatedKind kind, hipStream_t s) {
+  const int64_t bm = kind == kSlim ? 128 : 256, bn = kind == kSlim ? 64 : 192;
   for (GatedGemm* g : {&dx, &dw}) {
     g->full = g->inner / kBK;
     g->split_steps = std::max<int64_t>(1, g->segs * g->full);
     g->splits = 1;
-    g->mt = ceil_div64(g->a.outer, 128);
-    g->nt = ceil_div64(g->b.outer, 64);
-    tiles[n++] = g->mt * g->nt;
+    g->mt = ceil_div64(g->a.outer, bm);
+    g->nt = ceil_div64(g->b.outer, bn);
   }
-  hipLaunchKernelGGL(k_linear_gradients<BF>, dim3((unsigned)(tiles[0] + tiles[1])), dim3(4 * kWave), 0, s, dx, dw, (uint32_t)tiles[0]);
+  const dim3 grid((unsigned)(first + rest));
+  if (kind == kSlim)
+    hipLaunchKernelGGL((k_linear_gradients<BF, 128, 64, 2, 2, 3>), grid, dim3(4 * kWave), 0, s, dx, dw, (uint32_t)first);
+  else
+    hipLaunchKernelGGL((k_linear_gradients<BF, 256, 192, 2, 4, 2>), grid, dim3(8 * kWave), 0, s, dx, dw, (uint32_t)first);
   return hipGetLastError();
 }
 

@@ -288,7 +288,8 @@ hipError_t run_linear_backward(const LinearArgs& a, void* ws, hipStream_t s) {
   y.out[0] = static_cast<uint16_t*>(a.dw);
   y.mo = a.rows;
   y.ldo = a.cols;
-  if (a.dx && a.dw && linear_joins(px, pw)) return bf ? linear_gradients_bf16(x, y, s) : linear_gradients_f16(x, y, s);
+  const LinearJoin j = linear_join(a.tokens, a.cols, a.rows, parts, a.cus);
+  if (a.dx && a.dw && j.dx > 0) return (bf ? linear_gradients_bf16 : linear_gradients_f16)(x, y, j.dx, j.dw, j.kind, s);
   if (a.dx && (e = product(kDx, x, px, part, bf, a.cus, s)) != hipSuccess) return e;
   if (a.dw && (e = product(kLinDw, y, pw, part, bf, a.cus, s)) != hipSuccess) return e;
   return hipSuccess;

@@ -25,7 +25,7 @@ inline bool linear_takes_rows(int64_t tokens, int64_t cols, int64_t rows, bool a
 
 // The least of an estimate in microseconds, as plan_of; a tile of 256 x 192 (mid) and one of 256 x 256
 // may be split in every product.
-inline GatedPlan plan_linear(int mode, int64_t m, int64_t n, int64_t steps, int cus) {
+inline GatedPlan plan_linear(int mode, int64_t m, int64_t n, int64_t steps, int cus, double* estimate = nullptr) {
   GatedPlan best = {kPair, 1};
   double least = 1e300;
   for (const GatedKind kind : {kBig, kMid, kPair, kDeep, kSlim}) {
@@ -49,27 +49,51 @@ inline GatedPlan plan_linear(int mode, int64_t m, int64_t n, int64_t steps, int 
       }
     }
   }
+  if (estimate) *estimate = least;
   return best;
 }
 
 // dx from dz in one part or two.  For few tokens the two are stacked as twice the rows, as in the
 // gated block.
-inline GatedPlan plan_linear_dx(int64_t tokens, int64_t cols, int64_t rows, bool parts, int cus) {
+inline GatedPlan plan_linear_dx(int64_t tokens, int64_t cols, int64_t rows, bool parts, int cus, double* estimate = nullptr) {
   const bool stack = parts && tokens <= 64 && tiles_of(kDx, 2 * tokens, cols, false) <= cus;
-  GatedPlan p = plan_linear(kDx, stack ? 2 * tokens : tokens, cols, (parts && !stack ? 2 : 1) * steps_of(rows), cus);
+  GatedPlan p = plan_linear(kDx, stack ? 2 * tokens : tokens, cols, (parts && !stack ? 2 : 1) * steps_of(rows), cus, estimate);
   if (stack) {
     if (p.kind != kDeep && p.kind != kSlim) p = {kDeep, 1};
     p.stacked = 2;
   }
   return p;
 }
-inline GatedPlan plan_linear_dw(int64_t tokens, int64_t cols, int64_t rows, bool parts, int cus) {
-  return plan_linear(kLinDw, rows, cols, (parts ? 2 : 1) * steps_of(tokens), cus);
+inline GatedPlan plan_linear_dw(int64_t tokens, int64_t cols, int64_t rows, bool parts, int cus, double* estimate = nullptr) {
+  return plan_linear(kLinDw, rows, cols, (parts ? 2 : 1) * steps_of(tokens), cus, estimate);
 }
 
-// dx and dW in one launch: both in whole 128 x 64 tiles, of which each has no more than CUs.
-inline bool linear_joins(const GatedPlan& dx, const GatedPlan& dw) {
-  return dx.kind == kSlim && dw.kind == kSlim && dx.splits == 1 && dw.splits == 1 && dx.stacked == 1;
+// dx and dW in one launch, the first `dx` workgroups for dx and `dw` for dW; dx = 0: in two.  Either both in whole 128 x 64
+// tiles, where each has no more of them than CUs; or both in 256 x 192 tiles, where the product of fewer tiles has a
+// workgroup for each and the other takes the rest of the CUs, if the longer of them is estimated to end before
+// one after the other would.  bf16, tokens, cols x rows, dx and dW apart and in one launch, us:
+//   2264, 2296 x 2872: 55 + 42, 64    2656, 1880 x 2488: 48 + 43, 55    2206, 2968 x 1704: 34 + 37, 50
+//   2048, 2560 x 9728: 125 + 103, 222   512, 9728 x 2560: 38 + 41, 71   1106, 1872 x 912: 14.5 + 13, 28
+struct LinearJoin {
+  int64_t dx, dw;
+  GatedKind kind;
+};
+inline LinearJoin linear_join(int64_t tokens, int64_t cols, int64_t rows, bool parts, int cus) {
+  double ux, uw;
+  const GatedPlan px = plan_linear_dx(tokens, cols, rows, parts, cus, &ux), pw = plan_linear_dw(tokens, cols, rows, parts, cus, &uw);
+  const LinearJoin none = {0, 0, kSlim};
+  if (px.stacked != 1) return none;
+  auto tiles = [&](int64_t m, int64_t bm, int64_t bn) { return ceil_div64(m, bm) * ceil_div64(cols, bn); };
+  if (px.kind == kSlim && pw.kind == kSlim && px.splits == 1 && pw.splits == 1)
+    return {tiles(tokens, 128, 64), tiles(rows, 128, 64), kSlim};
+  const int64_t x = tiles(tokens, 256, 192), w = tiles(rows, 256, 192), least = std::min(x, w), rest = (cus - least) / 8 * 8;
+  if (rest <= 0) return none;
+  auto time = [&](int64_t t, int64_t inner) {   // of a product of t tiles
+    return (t == least ? 1.0 : (double)ceil_div64(t, rest)) * ((double)((parts ? 2 : 1) * steps_of(inner)) * 1.2 + 6.0);
+  };
+  if (std::max(time(x, rows), time(w, tokens)) > 0.95 * (ux + uw)) return none;
+  const int64_t most = std::min(std::max(x, w), rest);
+  return x <= w ? LinearJoin{x, most, kMid} : LinearJoin{most, w, kMid};
 }
 
 }  // namespace externd

@@ -1,6 +1,6 @@
 """(tokens, cols, rows, with an activation) that together run every form of the linear layer's tiled product (each product by
 each kind of tiles, with its contraction whole and split) for every number of steps, modulo the steps after which
-a kind's images repeat; and dx and dW by one launch too; eight steps and more, so that its steady loop runs.  tests/test_linear_plan.py holds them to that."""
+a kind's images repeat; and dx and dW by one launch too, in either kind of tiles; eight steps and more, so that its steady loop runs.  tests/test_linear_plan.py holds them to that."""
 
 SHAPES = [
     (1368, 1856, 264, True), (1224, 512, 1256, True), (288, 2792, 1808, True), (263, 1360, 1024, True),
@@ -16,4 +16,5 @@ SHAPES = [
     (391, 8304, 1360, True), (2446, 648, 3208, False), (4234, 976, 3544, True), (1350, 8184, 3136, False),
     (2055, 720, 3881, True), (2206, 776, 3611, False), (1305, 832, 5936, False), (4902, 648, 2328, True),
     (2107, 704, 5630, False), (2756, 7664, 1576, False), (2565, 784, 4441, True), (4957, 848, 2320, False),
-    (837, 8320, 4736, False), (600, 1000, 776, True), (777, 1237, 1001, True), (700, 904, 971, False)]
+    (837, 8320, 4736, False), (600, 1000, 776, True), (777, 1237, 1001, True), (700, 904, 971, False),
+    (1150, 2168, 1324, False), (1106, 1872, 913, False)]

@@ -22,12 +22,12 @@ def test_form(lib, dtype, tokens, cols, rows, act):
     y, z = lib.linear_forward(x, W, b, act, r, save=True)
     assert torch.equal(lib.linear_forward(x, W, b, act, r), y)
     grads = lib.linear_backward(x, W, z, dy, act)
-    # dx and dW may be made by one launch: each alone is the same
-    assert torch.equal(lib.linear_backward(x, W, z, dy, act, need_dw=False)[0], grads[0])
-    assert torch.equal(lib.linear_backward(x, W, z, dy, act, need_dx=False, need_db=False)[1], grads[1])
-    assert torch.equal(lib.linear_backward(x, W, z, dy, act, need_dx=False, need_dw=False)[2], grads[2])
-    got = (z, y, *grads)
-    for have, (name, want, tol) in zip(got, forward_checks(x, W, b, act, r) + gradient_checks(x, W, b, dy, act)):
+    # dx and dW may be made by one launch: each alone too
+    alone = [lib.linear_backward(x, W, z, dy, act, *(i == k for i in range(3)))[k] for k in range(3)]
+    assert torch.equal(alone[2], grads[2])
+    got = (z, y, *grads, *alone[:2])
+    checks = gradient_checks(x, W, b, dy, act)
+    for have, (name, want, tol) in zip(got, forward_checks(x, W, b, act, r) + checks + checks[:2]):
         if have is None:
             continue
         err = (have.double() - want).abs()

@@ -24,7 +24,9 @@ int main() {
     printf("%d %lld %lld %lld  ", x.kind, (long long)x.splits, (long long)x.stacked,
            (long long)((parts && x.stacked == 1 ? 2 : 1) * steps_of(r)));
     printf("%d %lld 1 %lld  ", w.kind, (long long)w.splits, (long long)((parts ? 2 : 1) * steps_of(t)));
-    printf("%d %d %d\n", linear_takes_rows(t, c, r, true, cus), linear_takes_rows(t, c, r, false, cus), linear_joins(x, w));
+    const LinearJoin j = linear_join(t, c, r, parts, cus);
+    printf("%d %d %lld %lld %d\n", linear_takes_rows(t, c, r, true, cus), linear_takes_rows(t, c, r, false, cus), (long long)j.dx,
+           (long long)j.dw, j.kind);
   }
 }
 """
@@ -36,7 +38,7 @@ FAR = (DEEP, SLIM)
 @pytest.fixture(scope="module")
 def plans(tmp_path_factory):
     """plans(shapes) -> per shape ([(kind, splits, stacked, steps) of the forward, dx and dW], few-token kernel when
-    aligned, and when not, dx and dW in one launch)."""
+    aligned, and when not, workgroups of dx and dW in one launch and their tiles)."""
     gxx = shutil.which("g++")
     if not gxx:
         pytest.skip("no host compiler")
@@ -49,7 +51,7 @@ def plans(tmp_path_factory):
         text = "".join(f"{t} {c} {r} {int(parts)} {cus}\n" for t, c, r, parts in shapes)
         out = subprocess.run([str(where / "plan")], input=text, capture_output=True, text=True, check=True).stdout
         rows = [list(map(int, line.split())) for line in out.splitlines()]
-        return [([tuple(row[i:i + 4]) for i in (0, 4, 8)], bool(row[12]), bool(row[13]), bool(row[14])) for row in rows]
+        return [([tuple(row[i:i + 4]) for i in (0, 4, 8)], bool(row[12]), bool(row[13]), tuple(row[14:17])) for row in rows]
     return run
 
 
@@ -82,10 +84,12 @@ def test_shapes_reach_every_form(plans):
     assert not WANT - seen
 
 
-def test_shapes_reach_every_number_of_steps_of_joined_gradients(plans):
-    seen = {(product, steps % 3) for products, _, _, joined in plans(SHAPES) if joined for product in (1, 2)
-            for steps in products[product][3:] if steps >= 8}
-    assert seen == {(product, n) for product in (1, 2) for n in range(3)}
+def test_shapes_reach_every_form_of_joined_gradients(plans):
+    seen = {(product, joined[2], steps % (3 if joined[2] == SLIM else 6))
+            for (t, c, r, parts), (products, _, _, joined) in zip(SHAPES, plans(SHAPES)) if joined[0]
+            for product, steps in ((1, (2 if parts else 1) * (r // 64)), (2, (2 if parts else 1) * (t // 64))) if steps >= 8}
+    want = {(product, kind, n) for product in (1, 2) for kind in (SLIM, MID) for n in range(3 if kind == SLIM else 6)}
+    assert not want - seen
 
 
 def test_plans_keep_what_the_kernels_assume(plans):
@@ -94,10 +98,15 @@ def test_plans_keep_what_the_kernels_assume(plans):
     for cus in (256, 304, 32):
         for (t, c, r, parts), (products, rows, unaligned_rows, joined) in zip(shapes, plans(shapes, cus)):
             assert unaligned_rows == (t <= 32) and not (rows and t > 32) and (rows or t > 3)
+            dx, dw, tiles = joined
+            if dx:
+                # as many workgroups as are resident, none without a tile
+                tm, tn = TILES[tiles]
+                most = [-(-m // tm) * -(-c // tn) for m in (t, r)]
+                assert tiles in (SLIM, MID) and products[1][2] == 1 and 0 < dx <= most[0] and 0 < dw <= most[1]
+                assert dx + dw <= (2 if tiles == SLIM else 1) * cus
             for product, (kind, splits, stacked, steps) in enumerate(products):
                 assert 1 <= splits <= 16 and (splits == 1 or steps >= 4 * splits) and not (splits > 1 and kind == PAIR)
-                if joined and product:
-                    assert (kind, splits, stacked) == (SLIM, 1, 1)
                 assert stacked == 1 or (product == 1 and kind in FAR and t <= 64 and parts)
                 if kind in FAR:
                     m, n = ((t, r), (stacked * t, c), (r, c))[product]
