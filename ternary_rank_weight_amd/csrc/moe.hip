@@ -5,6 +5,8 @@
 // slots (rows_core.hpp).  Each slot's result is fp32, and h enters the second product in two 16-bit parts, the rounded
 // value and what the rounding took away: the layer's output is rounded once.  bf16's parts are written by the first
 // product; fp16's, whose range h may leave, are made where they are read, multiplied by a power of two for each slot.
+// bf16, us of both products: one token through 4 of 64 experts of 1024 x 2560 11.4 + 7.4 (63 MB), 32 tokens through
+// 8 of 128 of 768 x 2560 157 + 95 (4.9 and 4.1 TB/s); fp16, unaligned, 7 tokens, 3 of 13 of 701 x 1237 20.5 + 9.6.
 #include <algorithm>
 
 #include "activation.hpp"
