@@ -1055,7 +1055,8 @@ class _Linear(torch.autograd.Function):
 
 def linear(x, W, bias=None, act=None, residual=None):
     """linear_forward as a differentiable torch operation (gradients of x, W, bias and residual; z is kept in float32
-    only where a gradient of an activation is needed)."""
+    only where a gradient of an activation is needed).  A captured step asks for its gradients by torch.autograd.grad:
+    backward() into leaves that an eager graph still holds cannot be captured."""
     if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, W, bias, residual))):
         return linear_forward(x, W, bias, act, residual)
     return _Linear.apply(x, W, bias, act, residual)
@@ -1216,8 +1217,9 @@ class AdamW:
 
     state, as the property of that name returns it, takes the place of new zeros (its tensors are used, not
     copied): "step" float64 (4,): steps taken, beta1 and beta2 to that power, 0; "m", "v" and "master" (or
-    None) have every tensor's entries filled up with zeros to a multiple of 256, one tensor after the other; m
-    and v are float32, or with bits = 8 uint8: the codes of all, then the blocks' exponent bytes.
+    None; a float32 parameter's part of it is not used) have every tensor's entries filled up with zeros to a
+    multiple of 256, one tensor after the other; m and v are float32, or with bits = 8 uint8: the codes of all,
+    then the blocks' exponent bytes.
 
     Calls of one object belong on one stream, or in an order."""
 

@@ -153,9 +153,6 @@ __global__ __launch_bounds__(kWaves * kWave) void k_adamw(AdamArgs a) {
   const float b1 = (float)a.b1, c1 = (float)(1.0 - a.b1), b2 = (float)a.b2, c2 = (float)(1.0 - a.b2);
   const float rate = (float)(lr / (1.0 - q1)), root = (float)(1.0 / sqrt(1.0 - q2)), eps = (float)a.eps;
 
-  // Each workgroup counts itself once it has read the old step, and the last to do so writes the new one. (Counted
-  // here, 12 ns each, the workgroups do not wait for one another at the end.)
-  uint32_t before = 0u;
   int i = 0;
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     while (i + 1 < a.count && c >= a.t[i + 1].first) ++i;
@@ -236,7 +233,8 @@ __global__ __launch_bounds__(kWaves * kWave) void k_adamw(AdamArgs a) {
     else work(std::false_type());
   }
 
-  // The last workgroup to get here counts the step: every other has read the old one.
+  // The last workgroup to get here counts the step: every other has read the old one.  (Counting at the start, past that
+  // read, was slower: a wave's loads return behind its atomic.)
   if (a.advance) {
     __syncthreads();
     if (threadIdx.x == 0) {
