@@ -93,13 +93,17 @@ __device__ __forceinline__ void for_constants(F&& f) {
   }
 }
 
-// The images are separate objects: the compiler then sees that a read of one need not wait for the loads into another.
-struct Images {
-  lds16 a[4], b[4];
-};
+// An image of N entries.  Images are separate objects: the compiler then sees that a read of one need not wait for the
+// loads into another.
+template <int N, int WHICH>
+__device__ __forceinline__ lds16 image_of() {
+  __shared__ __align__(16) uint16_t image[N];
+  return (lds16)image;
+}
 
 // out tile = sum over k of A[m][k] B[n][k], by `block` of `grid` workgroups.  BM x BN outputs per workgroup of
-// WM x WN waves.  The products take b's fragment as first and a's as second
+// WM x WN waves.  (g is a copy: by reference the 256 x 256 tiles of dx and dW lack registers, 394 and 362 us against
+// 344 and 340.)  The products take b's fragment as first and a's as second
 // operand, so that a lane holds four neighbouring output columns of one row.
 //
 // Whole steps go from memory to LDS without passing through registers (so every
@@ -117,15 +121,16 @@ struct Images {
 // The linear layer's: z and y of 4096 tokens, 2560 x 9728, 197 us (1.04 PFLOP/s; the library's product alone 182); of
 // 2048 tokens at 9728 x 2560 forward 92 + 26 for the join of three splits, dx 117, dW 96 (library 107, 110, 98).
 template <bool BF, int MODE, int BM, int BN, int WM, int WN, int NA, int NB, bool SPLIT>
-__device__ __forceinline__ void gated_gemm(const GatedGemm& g, const Images& images, uint32_t block, uint32_t grid) {
+__device__ __forceinline__ void gated_gemm(GatedGemm g, uint32_t block, uint32_t grid) {
   constexpr int NTHR = WM * WN * kWave;
   constexpr bool ACOLS = MODE == kDw || MODE == kLinDw, BCOLS = MODE != kFwd && MODE != kLin;
   constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
   using TA = Tile<ACOLS, BM>;
   using TB = Tile<BCOLS, BN>;
   constexpr int SA = TA::kSlots / NTHR, SB = TB::kSlots / NTHR;
-  const lds16 la0 = images.a[0], la1 = images.a[1], la2 = images.a[2], la3 = images.a[3];
-  const lds16 lb0 = images.b[0], lb1 = images.b[1], lb2 = images.b[2], lb3 = images.b[3];
+  constexpr int A = BM * kBK, B = BN * kBK;
+  const lds16 la0 = image_of<A, 0>(), la1 = image_of<A, 1>(), la2 = image_of<A, 2>(), la3 = image_of<(NA > 3 ? A : 8), 3>();
+  const lds16 lb0 = image_of<B, 4>(), lb1 = image_of<B, 5>(), lb2 = image_of<(NB > 2 ? B : 8), 6>(), lb3 = image_of<(NB > 3 ? B : 8), 7>();
   auto image_a = [&](auto index) {
     constexpr int I = decltype(index)::value % NA;
     if constexpr (I == 0) return la0;
@@ -612,11 +617,7 @@ __device__ __forceinline__ void gated_gemm(const GatedGemm& g, const Images& ima
 
 template <bool BF, int MODE, int BM, int BN, int WM, int WN, int NA, int NB, bool SPLIT>
 __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void k_gated_gemm(GatedGemm g) {
-  constexpr int A3 = NA > 3 ? BM * kBK : 8, B2 = NB > 2 ? BN * kBK : 8;
-  __shared__ __align__(16) uint16_t sa0[BM * kBK], sa1[BM * kBK], sa2[BM * kBK], sa3[A3];
-  __shared__ __align__(16) uint16_t sb0[BN * kBK], sb1[BN * kBK], sb2[B2], sb3[B2];
-  const Images images = {{(lds16)sa0, (lds16)sa1, (lds16)sa2, (lds16)sa3}, {(lds16)sb0, (lds16)sb1, (lds16)sb2, (lds16)sb3}};
-  gated_gemm<BF, MODE, BM, BN, WM, WN, NA, NB, SPLIT>(g, images, blockIdx.x, gridDim.x);
+  gated_gemm<BF, MODE, BM, BN, WM, WN, NA, NB, SPLIT>(g, blockIdx.x, gridDim.x);
 }
 
 // The linear layer's dx and dW in one launch, `first` workgroups for dx.  128 x 64 tiles with loads two steps ahead, two
@@ -625,11 +626,8 @@ __global__ __launch_bounds__(WM * WN * kWave, BM == 256 || NB == 2 ? 2 : 1) void
 // linear_join.
 template <bool BF, int BM, int BN, int WM, int WN, int NB>
 __global__ __launch_bounds__(WM * WN * kWave, 2) void k_linear_gradients(GatedGemm dx, GatedGemm dw, uint32_t first) {
-  constexpr int B2 = NB > 2 ? BN * kBK : 8;
-  __shared__ __align__(16) uint16_t sa0[BM * kBK], sa1[BM * kBK], sa2[BM * kBK], sb0[BN * kBK], sb1[BN * kBK], sb2[B2];
-  const Images images = {{(lds16)sa0, (lds16)sa1, (lds16)sa2, (lds16)sa0}, {(lds16)sb0, (lds16)sb1, (lds16)sb2, (lds16)sb0}};
-  if (blockIdx.x < first) gated_gemm<BF, kDx, BM, BN, WM, WN, 3, NB, false>(dx, images, blockIdx.x, first);
-  else gated_gemm<BF, kLinDw, BM, BN, WM, WN, 3, NB, false>(dw, images, blockIdx.x - first, gridDim.x - first);
+  if (blockIdx.x < first) gated_gemm<BF, kDx, BM, BN, WM, WN, 3, NB, false>(dx, blockIdx.x, first);
+  else gated_gemm<BF, kLinDw, BM, BN, WM, WN, 3, NB, false>(dw, blockIdx.x - first, gridDim.x - first);
 }
 
 // Outputs of a product, and of a join.

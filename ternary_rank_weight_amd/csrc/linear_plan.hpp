@@ -72,8 +72,9 @@ inline GatedPlan plan_linear_dw(int64_t tokens, int64_t cols, int64_t rows, bool
 // tiles, where each has no more of them than CUs; or both in 256 x 192 tiles, where the product of fewer tiles has a
 // workgroup for each and the other takes the rest of the CUs, if the longer of them is estimated to end before
 // one after the other would.  bf16, tokens, cols x rows, dx and dW apart and in one launch, us:
-//   2264, 2296 x 2872: 55 + 42, 64    2656, 1880 x 2488: 48 + 43, 55    2206, 2968 x 1704: 34 + 37, 50
-//   2048, 2560 x 9728: 125 + 103, 222   512, 9728 x 2560: 38 + 41, 71   1106, 1872 x 912: 14.5 + 13, 28
+//   2264, 2296 x 2872: 52 + 40, 62    2656, 1880 x 2488: 47 + 43, 55    2206, 2968 x 1704: 34 + 37, 50
+//   2048, 2560 x 9728: 109 + 105, 221   512, 9728 x 2560: 38 + 37, 68   1106, 1872 x 912: 14 + 12, 27
+// (the first of the lower row, and the last, the estimate takes wrongly, by 3 in 100).
 struct LinearJoin {
   int64_t dx, dw;
   GatedKind kind;
