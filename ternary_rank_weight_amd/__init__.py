@@ -1074,7 +1074,8 @@ def _moe_scratch(workspace, x, rows, experts, top):
         need = _moe_ws(x.shape[0], x.shape[1], rows, experts, top) if x.shape[0] else 0
         if need == 0:   # the call refuses the sizes
             return None, 0, None
-        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+        workspace = x.new_empty((need,), dtype=torch.uint8)
+        return workspace.data_ptr(), need, workspace
     return (*_scratch(workspace, x.get_device()), workspace)
 
 
@@ -1096,16 +1097,16 @@ def _moe_router(x, Wr):
 
 def _moe_weights(x, Wg, Wu, Wd):
     """The experts' matrices as the C structure."""
-    dtype, shape = x.dtype, Wg.shape
-    for w, name in ((Wg, "Wg"), (Wu, "Wu"), (Wd, "Wd")):
-        if w.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype} like x, got {w.dtype}")
-        if w.dim() != 3:
-            raise ValueError(f"{name} must be 3-D")
+    dtype, shape, back = x.dtype, Wg.shape, Wd.shape
+    if Wg.dtype is not dtype or Wu.dtype is not dtype or Wd.dtype is not dtype or len(shape) != 3:
+        for w, name in ((Wg, "Wg"), (Wu, "Wu"), (Wd, "Wd")):
+            if w.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype} like x, got {w.dtype}")
+        raise ValueError("Wg must be 3-D")
     experts, rows, cols = shape
-    if Wu.shape != shape or Wd.shape != (experts, cols, rows):
+    if Wu.shape != shape or len(back) != 3 or back[0] != experts or back[1] != cols or back[2] != rows:
         raise ValueError(f"Wg and Wu must be of one shape (experts, rows, cols) and Wd (experts, cols, rows), got "
-                         f"{tuple(shape)}, {tuple(Wu.shape)}, {tuple(Wd.shape)}")
+                         f"{tuple(shape)}, {tuple(Wu.shape)}, {tuple(back)}")
     (gs, gl, g1), (us, ul, u1), (ds, dl, d1) = Wg.stride(), Wu.stride(), Wd.stride()
     # (a dimension of one entry may have any stride)
     if rows <= 1:
@@ -1171,18 +1172,21 @@ def moe(x, Wr, Wg, Wu, Wd, top, act="silu", normalize=True, routing=False, out=N
     routing, returns (y, ids, weights)."""
     record = (x.requires_grad or Wr.requires_grad or Wg.requires_grad or Wu.requires_grad or Wd.requires_grad) and _records(out)
     given = x, Wr, Wg, Wu, Wd
-    index = _op_device(x, Wr, Wg, Wu, Wd)
+    index = x.get_device()
+    if index < 0 or Wr.get_device() != index or Wg.get_device() != index or Wu.get_device() != index or \
+            Wd.get_device() != index or index != _current_device():
+        _op_device(*given)
     w = _moe_weights(x, Wg, Wu, Wd)
     Wr, ldr, kind = _moe_router(x, Wr)
-    experts, cols = w.experts, w.cols
-    if Wr.shape != (experts, cols):
+    experts, rows, cols = Wg.shape
+    if Wr.shape[0] != experts or Wr.shape[1] != cols:
         raise ValueError(f"Wr must have shape {(experts, cols)}")
     shape = (*x.shape[:-1], top)
     y = x.new_empty(x.shape) if out is None else _out_or_new(out, x.shape, x.dtype, x.device)
     x, ldx, dtype = _moe_input(x, cols)
     ids = x.new_empty(shape, dtype=torch.int32)
     weights = x.new_empty(shape, dtype=torch.float32)
-    ws, wsb, keep = _moe_scratch(workspace, x, w.rows, experts, top)
+    ws, wsb, keep = _moe_scratch(workspace, x, rows, experts, top)
     status = _moe(x.data_ptr(), x.shape[0], ldx, Wr.data_ptr(), ldr, kind, top, normalize, w, dtype, _act_code(act),
                   _raw_stream(index), y.data_ptr(), ids.data_ptr(), weights.data_ptr(), ws, wsb)
     if status:
