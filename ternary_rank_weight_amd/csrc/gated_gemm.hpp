@@ -115,11 +115,11 @@ __device__ __forceinline__ lds16 image_of() {
 // PFLOP/s (a large library product without the activation: 1.43).  K = 2560, F = 9728,
 // bf16: forward of 4096 tokens 330 us (1.24 PFLOP/s; the same two products by the
 // library, without activation and product: 428 us); of 2048 tokens with g and u
-// kept 234 us; dx, both parts of dg and du, 337 us and its join 16; dW, both parts, 333 us
+// kept 234 us; dx, both parts of dg and du, 337 us and its join 12; dW, both parts, 333 us
 // (1.23 PFLOP/s).  What is lost is the end of a tile (6 of 62 us a tile of 40 steps) and
 // the last round of tiles.
 // The linear layer's: z and y of 4096 tokens, 2560 x 9728, 197 us (1.04 PFLOP/s; the library's product alone 182); of
-// 2048 tokens at 9728 x 2560 forward 92 + 26 for the join of three splits, dx 117, dW 96 (library 107, 110, 98).
+// 2048 tokens at 9728 x 2560 forward 92 + 16 for the join of three splits, dx 117, dW 96 (library 107, 110, 98).
 template <bool BF, int MODE, int BM, int BN, int WM, int WN, int NA, int NB, bool SPLIT>
 __device__ __forceinline__ void gated_gemm(GatedGemm g, uint32_t block, uint32_t grid) {
   constexpr int NTHR = WM * WN * kWave;
@@ -640,13 +640,41 @@ struct JoinEnd {
 // What the split contractions left: the splits' sums in their order, then the
 // outputs as the unsplit kernel makes them.  part: (split, outs, count) fp32, rows of ldo;
 // tops: as in GatedGemm.
-// Forward: both projections, the activation and the product.  Bound by HBM: 16 us for
-// three splits of 2048 x 2560 (4.3 TB/s).
+// Forward: both projections, the activation and the product.  Bound by HBM, where rows are multiples of four: three splits
+// of 2048 x 2560, linear with a residual, 15.6 us (5.4 TB/s, in part from the last-level cache; an output a thread: 27).
 template <bool BF, int MODE>
 __global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ part, int64_t count, int64_t splits,
                                                      uint16_t* __restrict__ out0, uint16_t* __restrict__ out1,
                                                      float* __restrict__ g, float* __restrict__ u, int act, JoinEnd z) {
   constexpr int OUTS = outs_of(MODE);
+  if constexpr (OUTS == 1)
+    if (z.ldo % 4 == 0) {   // four neighbouring outputs of a row
+      for (int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < count; i += (int64_t)gridDim.x * 1024) {
+        f32x4 s = *reinterpret_cast<const f32x4_a4*>(part + i);
+#pragma unroll 4
+        for (int64_t q = 1; q < splits; ++q) s += *reinterpret_cast<const f32x4_a4*>(part + q * count + i);
+        const int64_t row = i / z.ldo, col = i - row * z.ldo;
+        uint32_t w[4];
+        if constexpr (MODE == kLin) {
+          u32x2_a2 r = {0u, 0u};
+          if (z.residual) r = *reinterpret_cast<const u32x2_a2*>(z.residual + row * z.ldr + col);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (z.bias) s[e] += f32_from_16<BF>(z.bias[col + e]);
+            float y = act == EXTERND_ACT_NONE ? s[e] : act_value(act, s[e]);
+            if (z.residual) y += f32_from_16<BF>((r[e / 2] >> (16 * (e & 1))) & 0xffffu);
+            w[e] = f32_to_16<BF>(y);
+          }
+          if (g) *reinterpret_cast<f32x4_a4*>(g + i) = s;
+        } else {
+          const float back = !BF && z.tops ? unscale_of(z.tops[row]) : 1.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = f32_to_16<BF>(BF ? s[e] : s[e] * back);
+        }
+        *reinterpret_cast<u32x2_a2*>(out0 + i) = u32x2_a2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
+      }
+      return;
+    }
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
     float s[OUTS];
 #pragma unroll
@@ -718,7 +746,8 @@ hipError_t product(GatedGemm g, const GatedPlan& plan, float* part, int cus, hip
   if (plan.kind == kDeep) e = launch_tile<BF, MODE, kDeep, true>(g, cus, s);
   if (e != hipSuccess) return e;
   const int64_t count = g.mo / plan.stacked * g.ldo;   // (a half is as good as a split)
-  const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(ceil_div64(count, 256), 1 << 15))), block(256);
+  const int64_t per = outs_of(MODE) == 1 && g.ldo % 4 == 0 ? 1024 : 256;   // outputs of a workgroup
+  const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(ceil_div64(count, per), 1 << 15))), block(256);
   hipLaunchKernelGGL((k_gated_join<BF, MODE>), grid, block, 0, s, part, count, g.splits * plan.stacked, g.out[0], g.out[1], g.save[0],
                      g.save[1], g.act, JoinEnd{g.ldo, g.tops_of_up, g.ldr, g.tops, g.bias, g.residual});
   return hipGetLastError();
