@@ -506,8 +506,8 @@ size_t externd_linear_backward_workspace_bytes(int64_t tokens, int64_t cols, int
  *
  * Each token goes through `top` of the experts, gated blocks with a projection back:
  *   y[t] = sum over j of weights[t][j] * Wd_e (act(Wg_e x[t]) * (Wu_e x[t])),  e = ids[t][j].
- * Sums, activations and what lies between the products are fp32 or more, and y is rounded once.  dtype of x, the
- * experts and y: EXTERND_BF16 or EXTERND_F16.  tokens * top at most EXTERND_MOE_SLOTS, experts at most 1024, top at
+ * Sums, activations and what lies between the products are fp32 or more (fp16: each slot's hidden values to 2^-39 of its
+ * largest), and y is rounded once.  dtype of x, the experts and y: EXTERND_BF16 or EXTERND_F16.  tokens * top at most EXTERND_MOE_SLOTS, experts at most 1024, top at
  * most 64 and at most the experts, rows and cols at most 2^21 (EXTERND_EUNSUPPORTED beyond). */
 #define EXTERND_MOE_SLOTS 8192
 

@@ -2,11 +2,12 @@
 //   h = act(Wg_e x) (Wu_e x) for every slot (a token and one of its experts e),
 //   y[t] = the sum over t's slots of weight * Wd_e h.
 // Bound by the weights of the experts that are chosen, which are read once for each group of up to 16 of an expert's
-// slots (rows_core.hpp).  Each slot's result is fp32, and h enters the second product in two 16-bit parts, the rounded
-// value and what the rounding took away: the layer's output is rounded once.  bf16's parts are written by the first
-// product; fp16's, whose range h may leave, are made where they are read, multiplied by a power of two for each slot.
-// bf16, us of both products: one token through 4 of 64 experts of 1024 x 2560 11.4 + 7.4 (63 MB), 32 tokens through
-// 8 of 128 of 768 x 2560 157 + 95 (4.9 and 4.1 TB/s); fp16, unaligned, 7 tokens, 3 of 13 of 701 x 1237 20.5 + 9.6.
+// slots (rows_core.hpp).  h and each slot's result are fp32; h enters the second product in three 16-bit parts that are
+// made where it is read and whose sum it is (fp16: multiplied by a power of two for each slot, to 2^-39 of the slot's
+// largest), so y is rounded once.  (In two parts, which 17 bits of bf16 and 22 of fp16 fill, outputs that cancel were off;
+// one token 21.9 us then, 23 now, 7 tokens 35 and 36, 32 tokens the same.)
+// bf16, us of both products: one token through 4 of 64 experts of 1024 x 2560 11.8 + 9.0 (63 MB), 32 tokens through
+// 8 of 128 of 768 x 2560 157 + 94 (4.9 and 4.2 TB/s); fp16, unaligned, 7 tokens, 3 of 13 of 701 x 1237 21 + 10.4.
 #include <algorithm>
 
 #include "activation.hpp"
@@ -27,9 +28,8 @@ struct UpArgs {
   int top, apart_bits, act;
   MoeGroup* groups;
   uint32_t* tops;
-  float* h;          // fp16
-  uint16_t* parts;   // bf16
-  int64_t ldh, rest;
+  float* h;
+  int64_t ldh;
   // few tokens, whose choices this kernel makes
   const double* logits;
   int tokens, experts, normalize;
@@ -120,15 +120,8 @@ __global__ __launch_bounds__(WV * kWave, 4) void k_moe_up(UpArgs a) {
     const int64_t unit = row0 + ((int64_t)k << a.apart_bits);
     const bool in = s < count && unit < a.rows;
     const float h = act_value(a.act, v[0]) * v[1];
-    if constexpr (BF) {
-      if (in) {
-        uint32_t hi, lo;
-        split16<true>(h, hi, lo);
-        a.parts[ss * a.ldh + unit] = (uint16_t)hi;
-        a.parts[a.rest + ss * a.ldh + unit] = (uint16_t)lo;
-      }
-    } else {
-      if (in) a.h[ss * a.ldh + unit] = h;
+    if (in) a.h[ss * a.ldh + unit] = h;
+    if constexpr (!BF) {
       float size = in && __builtin_isfinite(h) ? fabsf(h) : 0.f;
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) size = fmaxf(size, __shfl_xor(size, w, 16));
@@ -146,10 +139,9 @@ __global__ __launch_bounds__(WV * kWave, 4) void k_moe_up(UpArgs a) {
 }
 
 struct DownArgs {
-  const uint16_t* parts;   // bf16
-  const float* h;          // fp16
+  const float* h;
   const uint16_t* w;
-  int64_t cols, rows, ldh, rest, ldw, stride;   // rows: of each expert's matrix, the layer's outputs
+  int64_t cols, rows, ldh, ldw, stride;   // rows: of each expert's matrix, the layer's outputs
   int apart_bits;
   const MoeGroup* groups;
   const uint32_t* tops;
@@ -157,16 +149,9 @@ struct DownArgs {
 };
 
 // The lane's slot of h as the second product's vectors.
-template <bool BF, bool AL>
-__device__ __forceinline__ auto hidden_of(const DownArgs& a, int slot) {
-  if constexpr (BF) {
-    RowsParts<AL> x;
-    x.part.row[0] = a.parts + slot * a.ldh;
-    x.part.row[1] = x.part.row[0] + a.rest;
-    return x;
-  } else {
-    return RowsScaled{a.h + slot * a.ldh, scale_of(a.tops[slot])};
-  }
+template <bool BF>
+__device__ __forceinline__ RowsSplit<BF> hidden_of(const DownArgs& a, int slot) {
+  return {a.h + slot * a.ldh, BF ? 1.f : scale_of(a.tops[slot])};
 }
 
 // As k_moe_up, for tiles of 16 outputs.  RT > 1 (and SW = 1): a wave takes that many tiles at once, whose rows start
@@ -199,7 +184,7 @@ __global__ __launch_bounds__(WV * kWave, 4) void k_moe_down(DownArgs a) {
       w[q] = base + (mine < a.rows ? mine : row0[0]) * a.ldw;   // (past the end: the first again)
       shift[q] = AL ? 0 : shift_of(base + row0[0] * a.ldw);
     }
-    rows_product<BF, RT, 1, SW, AL, 1>(w, shift, (int)a.cols, wave % SW, hidden_of<BF, AL>(a, slot), acc);
+    rows_product<BF, RT, 1, SW, AL, 1>(w, shift, (int)a.cols, wave % SW, hidden_of<BF>(a, slot), acc);
   }
   auto put = [&](int s, int64_t row, float v) {
     if (s >= count || row >= a.rows) return;
@@ -226,7 +211,7 @@ __global__ __launch_bounds__(WV * kWave, 4) void k_moe_down(DownArgs a) {
 
 // One token's outputs: a workgroup of sixteen waves takes a tile of all its experts, SL waves each (with more than sixteen
 // experts, a wave several), and writes y: no results of slots, no join.  One token through 4 of 64 experts of 1024 x
-// 2560: 7.1 us against 6.6 + 2.4 for the second product and the join; layer 28 -> 22 us.
+// 2560, h in two parts: 7.1 us against 6.6 + 2.4 for the second product and the join; layer 28 -> 22 us.
 template <bool BF, int SL, bool AL>
 __global__ __launch_bounds__(16 * kWave) void k_moe_down_one(DownArgs a, const int32_t* __restrict__ ids,
                                                               const float* __restrict__ weights, int top, int experts,
@@ -246,7 +231,7 @@ __global__ __launch_bounds__(16 * kWave) void k_moe_down_one(DownArgs a, const i
     const int shift[1] = {AL ? 0 : shift_of(base + row0 * a.ldw)};
     f32x4 acc[1][1];
     acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-    rows_product<BF, 1, 1, SL, AL, 1>(w, shift, (int)a.cols, wave % SL, hidden_of<BF, AL>(a, slot), acc);
+    rows_product<BF, 1, 1, SL, AL, 1>(w, shift, (int)a.cols, wave % SL, hidden_of<BF>(a, slot), acc);
     const float v = BF ? acc[0][0][0] : acc[0][0][0] * unscale_of(a.tops[slot]);   // (every row of the product is the token)
     sum = fmaf(weights[slot], v, sum);
   }
@@ -339,9 +324,7 @@ hipError_t experts(const MoeArgs& a, const MoeSpace& s, bool few, hipStream_t st
   u.groups = s.groups;
   u.tops = s.tops;
   u.h = s.h;
-  u.parts = s.parts;
   u.ldh = s.ldh;
-  u.rest = a.slots() * s.ldh;
   u.logits = s.logits;
   u.tokens = (int)a.tokens;
   u.experts = (int)w.experts;
@@ -364,9 +347,7 @@ hipError_t experts(const MoeArgs& a, const MoeSpace& s, bool few, hipStream_t st
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   DownArgs d = {};
-  d.parts = s.parts;
   d.h = s.h;
-  d.rest = u.rest;
   d.w = static_cast<const uint16_t*>(w.wd);
   d.cols = w.rows;
   d.rows = a.cols;

@@ -38,8 +38,7 @@ struct MoeSpace {
   double* logits;      // tokens x experts
   MoeGroup* groups;    // moe_most_groups of them
   uint32_t* tops;      // fp16: the largest magnitude of each slot's h, as bits of fp32; cleared by a call's first kernel
-  float* h;            // fp16: slots x ldh
-  uint16_t* parts;     // bf16: h in two 16-bit parts, each slots x ldh; the same place
+  float* h;            // slots x ldh
   float* part;         // slots x cols: what each slot's expert gives
   int64_t ldh;
   size_t bytes;

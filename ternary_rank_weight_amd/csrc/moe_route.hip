@@ -163,7 +163,6 @@ MoeSpace moe_space(void* base, int64_t tokens, int64_t experts, int64_t top, int
     s.groups = static_cast<MoeGroup*>(take(sizeof(MoeGroup) * (size_t)moe_most_groups(slots, experts)));
     s.tops = static_cast<uint32_t*>(take(4 * (size_t)slots));
     s.h = static_cast<float*>(take(4 * (size_t)(slots * s.ldh)));
-    s.parts = reinterpret_cast<uint16_t*>(s.h);
     s.part = static_cast<float*>(take(4 * (size_t)(slots * cols)));
   }
   s.bytes = at;

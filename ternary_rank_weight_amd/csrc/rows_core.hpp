@@ -27,12 +27,16 @@ inline int64_t rows_tiles(int64_t rows, int apart_bits) {
 
 namespace {
 
-// A value as two of 16 bits: rounded, and what the rounding took away.
+// A value as three of 16 bits whose sum it is: 24 bits of fp32, as 3 x 8 of bf16 (cut off: a rounding up might leave the
+// range) or 3 x 11 of fp16.  Infinite and NaN are in the first; fp16 ends at its smallest step, 2^-24.
 template <bool BF>
-__device__ __forceinline__ void split16(float v, uint32_t& hi, uint32_t& lo) {
-  hi = f32_to_16<BF>(v);
-  const float rest = v - f32_from_16<BF>(hi);
-  lo = __builtin_isfinite(rest) ? f32_to_16<BF>(rest) : 0u;   // (infinite and NaN are in the first part)
+__device__ __forceinline__ void split16(float v, uint32_t (&part)[3]) {
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    part[e] = BF ? __float_as_uint(v) >> 16 : f32_to_16<BF>(v);
+    v -= f32_from_16<BF>(part[e]);
+    if (e == 0 && !__builtin_isfinite(v)) v = 0.f;
+  }
 }
 
 // First row of a tile; its row i is first + (i << apart_bits).  (It may lie past the end.)
@@ -120,66 +124,34 @@ struct Rows16 {
   __device__ void finish_edge(int n, int c, int cols, const Edge& raw, u32x4 (&f)[1]) const { f[0] = raw.v.get(row[n], c, cols); }
 };
 
-// Vectors in two 16-bit parts.
-template <bool AL>
-struct RowsParts {
-  static constexpr int kParts = 2;
-  Rows16<2, AL> part;   // the lane's row of either part
-  struct Whole {
-    typename Rows16<2, AL>::Whole p[2];
-  };
-  struct Edge {
-    Edge8<AL> p[2];
-  };
-  __device__ void load(int, int c, Whole& raw) const {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) part.load(e, c, raw.p[e]);
-  }
-  __device__ void finish(int, int c, const Whole& raw, u32x4 (&f)[2]) const {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      u32x4 v[1];
-      part.finish(e, c, raw.p[e], v);
-      f[e] = v[0];
-    }
-  }
-  __device__ void load_edge(int, int c, int cols, Edge& raw) const {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) raw.p[e].load(part.row[e], c, cols);
-  }
-  __device__ void finish_edge(int, int c, int cols, const Edge& raw, u32x4 (&f)[2]) const {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) f[e] = raw.p[e].get(part.row[e], c, cols);
-  }
-};
-
-// Vectors of fp32 entries, entered in two 16-bit parts after a multiplication by `scale`, a power of two that
-// brings the lane's row into fp16's range: the rounded value, and what the rounding took away.
-struct RowsScaled {
-  static constexpr int kParts = 2;
+// Vectors of fp32 entries, entered in three 16-bit parts; fp16 after a multiplication by `scale`, a power of two
+// that brings the lane's row into its range.
+template <bool BF>
+struct RowsSplit {
+  static constexpr int kParts = 3;
   const float* row;
-  float scale;
+  float scale;   // fp16
   struct Whole {
     u32x4 a, b;
   };
   struct Edge {
     float v[8];
   };
-  __device__ void split(const float (&v)[8], u32x4 (&f)[2]) const {
+  __device__ void split(const float (&v)[8], u32x4 (&f)[kParts]) const {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      uint32_t hi[2], lo[2];
+      uint32_t part[2][kParts];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) split16<false>(v[j + e] * scale, hi[e], lo[e]);
-      f[0][j / 2] = hi[0] | (hi[1] << 16);
-      f[1][j / 2] = lo[0] | (lo[1] << 16);
+      for (int e = 0; e < 2; ++e) split16<BF>(BF ? v[j + e] : v[j + e] * scale, part[e]);
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) f[k][j / 2] = part[0][k] | (part[1][k] << 16);
     }
   }
   __device__ void load(int, int c, Whole& raw) const {
     raw.a = *reinterpret_cast<const u32x4_a4*>(row + c);
     raw.b = *reinterpret_cast<const u32x4_a4*>(row + c + 4);
   }
-  __device__ void finish(int, int, const Whole& raw, u32x4 (&f)[2]) const {
+  __device__ void finish(int, int, const Whole& raw, u32x4 (&f)[kParts]) const {
     float v[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -194,7 +166,7 @@ struct RowsScaled {
 #pragma unroll
     for (int j = 0; j < 8; ++j) raw.v[j] = row[max(0, min(at + j, cols - 1))];
   }
-  __device__ void finish_edge(int, int c, int cols, const Edge& raw, u32x4 (&f)[2]) const {
+  __device__ void finish_edge(int, int c, int cols, const Edge& raw, u32x4 (&f)[kParts]) const {
     const int at = cols >= 8 ? max(0, min(c, cols - 8)) : c;
     float v[8];
 #pragma unroll
