@@ -1275,14 +1275,13 @@ class AdamW:
         step = 4 if bits == 32 else 1
         self._table = (_AdamTensor * len(self._params))()
         for t, p, at, d in zip(self._table, self._params, self._starts, decay):
-            t.param, t.n, t.decay, t.param_dtype = p.data_ptr(), p.numel(), d, _DTYPE[p.dtype]
+            t.decay, t.param_dtype = d, _DTYPE[p.dtype]
             t.m, t.v = self._m.data_ptr() + at * step, self._v.data_ptr() + at * step
             if bits == 8:
                 t.m_exp, t.v_exp = (s.data_ptr() + total + at // ADAMW_BLOCK for s in (self._m, self._v))
             if master and p.dtype != torch.float32:
                 t.master = self._master.data_ptr() + 4 * at
-        self._entries = [(t, p, p.numel()) for t, p in zip(self._table, self._params)]
-        self._at = [p.data_ptr() for p in self._params]   # what the table holds
+        self._entries = [(t, p, p.numel(), p.shape, p.dtype) for t, p in zip(self._table, self._params)]
         self._inference = any(p.is_inference() for p in self._params)
         self._opts = _AdamOpts(0.0, betas[0], betas[1], eps, None, None, 1.0, bits, self._step.data_ptr())
 
@@ -1304,7 +1303,7 @@ class AdamW:
         if index != _current_device():
             _op_device(*params)
         keep, changed = [], params
-        for k, (t, p, n) in enumerate(self._entries):
+        for k, (t, p, n, shape, dtype) in enumerate(self._entries):
             g = grads[k]
             if g is None:
                 t.n = 0
@@ -1314,19 +1313,19 @@ class AdamW:
             code = _DTYPE.get(g.dtype)
             if code is None:
                 _dtype_code(g.dtype, "a gradient")
-            if g.shape != p.shape or g.get_device() != index:
-                raise ValueError(f"a gradient must have its tensor's shape {tuple(p.shape)} and device")
+            now = p.shape
+            if g.shape != now or g.get_device() != index:
+                raise ValueError(f"a gradient must have its tensor's shape {tuple(now)} and device")
             if not g.is_contiguous():
                 g = g.contiguous()
                 keep.append(g)
+            # (p.data may have been given anything since the last step, at the same address too)
             at = p.data_ptr()
-            if at != self._at[k]:
-                # (another storage of the same kind, as after p.data = ...)
-                _need(p, p.dtype, "a parameter")
-                if p.get_device() != index or _DTYPE.get(p.dtype) != t.param_dtype or p.numel() != n:
-                    raise ValueError("a parameter's type, size or device has changed")
-                t.param = self._at[k] = at
-            t.grad, t.grad_dtype, t.n = g.data_ptr(), code, n
+            if now != shape and p.numel() != n or p.dtype is not dtype or not p.is_contiguous() or \
+                    at != t.param and p.get_device() != index:
+                _need(p, dtype, "a parameter")
+                raise ValueError("a parameter's size or device has changed")
+            t.param, t.grad, t.grad_dtype, t.n = at, g.data_ptr(), code, n
             if changed is not params:
                 changed.append(p)
         if lr is None:
