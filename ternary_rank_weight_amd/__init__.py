@@ -1169,7 +1169,7 @@ def moe_experts(x, ids, weights, Wg, Wu, Wd, act="silu", out=None, workspace=Non
 
 def moe(x, Wr, Wg, Wu, Wd, top, act="silu", normalize=True, routing=False, out=None, workspace=None):
     """A mixture-of-experts layer for a few tokens: moe_experts with the choice that moe_route makes, in one call.  With
-    routing, returns (y, ids, weights)."""
+    routing, returns (y, ids, weights).  There is no gradient: asking for one, of y or of weights, raises an error."""
     record = (x.requires_grad or Wr.requires_grad or Wg.requires_grad or Wu.requires_grad or Wd.requires_grad) and _records(out)
     given = x, Wr, Wg, Wu, Wd
     index = x.get_device()
@@ -1193,6 +1193,8 @@ def moe(x, Wr, Wg, Wu, Wd, top, act="silu", normalize=True, routing=False, out=N
         _check(status)
     if record:
         y = _NoGradient.apply("moe has no gradient", y, *given)
+        if routing:
+            weights = _NoGradient.apply("moe has no gradient", weights, *given[:2])
     return (y, ids, weights) if routing else y
 
 
