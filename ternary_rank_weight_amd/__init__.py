@@ -611,6 +611,18 @@ def _records(out):
     return True
 
 
+_forward_ad = torch.autograd.forward_ad
+
+
+def _no_tangents(name, *tensors):
+    """An error where a tensor carries a forward-mode tangent: the kernels have no derivative to pass it on by.  (A dual
+    tensor does not require a gradient.)"""
+    if getattr(_forward_ad, "_current_level", 0) < 0:   # (outside every level, where a look at each would cost a call's time)
+        return
+    if any(t is not None and _forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise RuntimeError(f"{name} has no forward-mode derivative")
+
+
 def _q4_part(t, dtype, count, codes, name):
     if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         _need(t, dtype, name)
@@ -742,6 +754,7 @@ def q4_apply(q, x, out=None, workspace=None):
     if x.get_device() != index or index != _current_device():
         _op_device(x, q._codes)
     record = x.requires_grad and _records(out)
+    _no_tangents("q4_apply", x)
     given = x
     y = x.new_empty((*x.shape[:-1], q._rows)) if out is None else \
         _out_or_new(out, (*x.shape[:-1], q._rows), x.dtype, x.device)
@@ -763,6 +776,7 @@ def q4_gated(qg, qu, x, act="silu", out=None, workspace=None):
     if x.get_device() != index or qu._index != index or index != _current_device():
         _op_device(x, qg._codes, qu._codes)
     record = x.requires_grad and _records(out)
+    _no_tangents("q4_gated", x)
     given = x
     h = x.new_empty((*x.shape[:-1], qg._rows)) if out is None else \
         _out_or_new(out, (*x.shape[:-1], qg._rows), x.dtype, x.device)
@@ -825,6 +839,8 @@ def gated_forward(x, Wg, Wu, act="silu", save=False, out=None, workspace=None):
     of this one raises an error (with save, its result carries none)."""
     act = _act_code(act)
     record = not save and (x.requires_grad or Wg.requires_grad or Wu.requires_grad) and _records(out)
+    if not save:
+        _no_tangents("the gated block", x, Wg, Wu)
     given = x, Wg, Wu
     index = _op_device(x, Wg, Wu)
     Wg, Wu, ldw, dtype = _gated_weights(x, Wg, Wu)
@@ -959,6 +975,8 @@ def linear_forward(x, W, bias=None, act=None, residual=None, save=False, out=Non
         _linear_act(act)
     record = not save and (x.requires_grad or W.requires_grad or bias is not None and bias.requires_grad or
                            residual is not None and residual.requires_grad) and _records(out)
+    if not save:
+        _no_tangents("the linear layer", x, W, bias, residual)
     index = x.get_device()
     if index < 0 or W.get_device() != index or index != _current_device() or \
             bias is not None and bias.get_device() != index or residual is not None and residual.get_device() != index:
@@ -1130,6 +1148,7 @@ def moe_route(x, Wr, top, normalize=True, workspace=None):
     gradient: asking for one raises an error."""
     given = x, Wr
     record = (x.requires_grad or Wr.requires_grad) and _records(None)
+    _no_tangents("moe_route", x, Wr)
     index = _op_device(x, Wr)
     Wr, ldr, kind = _moe_router(x, Wr)
     experts, cols = Wr.shape
@@ -1152,6 +1171,7 @@ def moe_experts(x, ids, weights, Wg, Wu, Wd, act="silu", out=None, workspace=Non
     For a few tokens: at most 8192 ids.  There is no gradient: asking for one raises an error."""
     given = x, weights, Wg, Wu, Wd
     record = any(t.requires_grad for t in given) and _records(out)
+    _no_tangents("moe_experts", *given)
     index = _op_device(ids, *given)
     w = _moe_weights(x, Wg, Wu, Wd)
     if ids.dim() == 0 or ids.shape[:-1] != x.shape[:-1] or ids.shape != weights.shape:
@@ -1171,6 +1191,7 @@ def moe(x, Wr, Wg, Wu, Wd, top, act="silu", normalize=True, routing=False, out=N
     """A mixture-of-experts layer for a few tokens: moe_experts with the choice that moe_route makes, in one call.  With
     routing, returns (y, ids, weights).  There is no gradient: asking for one, of y or of weights, raises an error."""
     record = (x.requires_grad or Wr.requires_grad or Wg.requires_grad or Wu.requires_grad or Wd.requires_grad) and _records(out)
+    _no_tangents("moe", x, Wr, Wg, Wu, Wd)
     given = x, Wr, Wg, Wu, Wd
     index = x.get_device()
     if index < 0 or Wr.get_device() != index or Wg.get_device() != index or Wu.get_device() != index or \
