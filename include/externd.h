@@ -546,8 +546,9 @@ size_t externd_moe_workspace_bytes(int64_t tokens, int64_t cols, int64_t rows, i
  * Per entry, steps in fp32:
  *   g1 = g grad_scale, m1 = beta1 m + (1 - beta1) g1, v1 = beta2 v + (1 - beta2) (g1 g1),
  *   w1 = (1 - lr decay) w - lr / (1 - beta1^t) * m1 / (sqrt(v1) / sqrt(1 - beta2^t) + eps)
- * with t the number of this step.  w is the tensor's master weight where it has one, and
- * the parameter becomes its rounding; else the parameter.
+ * with t the number of this step: one count for all tensors, also for those that earlier steps left
+ * out.  w is the tensor's master weight where it has one, and the parameter becomes its rounding; else
+ * the parameter.
  *
  * Moments are kept for whole blocks of EXTERND_ADAMW_BLOCK entries (as is the master weight),
  * 0 past the tensor's end.  bits = 32: fp32.  bits = 8: a byte per entry, and a byte b per
