@@ -141,8 +141,9 @@ __device__ __forceinline__ uint32_t encode_v(const float (&v)[4], int b) {
   return w;
 }
 
-// Bound by HBM: 74.7 million bf16 parameters with master weights, 417 us with 32-bit moments (28 bytes an
-// entry, 5.0 TB/s), 230 to 250 with 8-bit ones (16 bytes, 4.8 to 5.2).
+// Bound by HBM: 74.7 million bf16 parameters and gradients with master weights, 417 us with 32-bit moments (28 bytes
+// an entry, 5.0 TB/s), 230 to 250 with 8-bit ones (16 bytes, 4.8 to 5.2); with fp32 gradients 442 and 277 (30 and 18 bytes,
+// 5.1 and 4.9 TB/s).
 template <bool EIGHT, int PT, int GT, bool MASTER>
 __global__ __launch_bounds__(kWaves * kWave) void k_adamw(AdamArgs a) {
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -264,29 +265,41 @@ __global__ __launch_bounds__(256) void k_adamw_moments(const uint8_t* __restrict
   }
 }
 
+// Few workgroups of many waves: each counts itself at the end, 12 ns one after the other (11 million entries in 8
+// bits: 42 us with eight of four waves a compute unit, 33 with four of eight).  With 32 bits no more than are resident
+// together, as the kernel's registers allow: three where gradients are fp32 and the weights are too or have masters, whose
+// fourth would begin when another ends (74.7 million entries, 16-bit parameters with masters 453 -> 442 us, fp32 415 -> 411; held to
+// the registers of four 458 and 421).  With 8 bits a fourth that waits costs nothing (277, 279 with three).
 template <bool EIGHT, int PT, int GT, bool MASTER>
-hipError_t launch(const AdamArgs& a, unsigned grid, hipStream_t s) {
-  hipLaunchKernelGGL((k_adamw<EIGHT, PT, GT, MASTER>), dim3(grid), dim3(kWaves * kWave), 0, s, a);
+hipError_t launch(const AdamArgs& a, int cus, hipStream_t s) {
+  const auto kernel = k_adamw<EIGHT, PT, GT, MASTER>;
+  static const int resident = [&] {
+    int n = 0;
+    if (EIGHT || hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kWaves * kWave, 0) != hipSuccess) n = 4;
+    return std::clamp(n, 1, 4);
+  }();
+  const unsigned grid = std::max(1u, std::min(a.chunks, (uint32_t)(cus * resident)));
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(kWaves * kWave), 0, s, a);
   return hipGetLastError();
 }
 
 template <bool EIGHT, int PT, bool MASTER>
-hipError_t pick_grad(const AdamArgs& a, int grad, unsigned grid, hipStream_t s) {
-  if (grad == EXTERND_F32) return launch<EIGHT, PT, EXTERND_F32, MASTER>(a, grid, s);
-  if (grad == EXTERND_BF16) return launch<EIGHT, PT, EXTERND_BF16, MASTER>(a, grid, s);
-  return launch<EIGHT, PT, EXTERND_F16, MASTER>(a, grid, s);
+hipError_t pick_grad(const AdamArgs& a, int grad, int cus, hipStream_t s) {
+  if (grad == EXTERND_F32) return launch<EIGHT, PT, EXTERND_F32, MASTER>(a, cus, s);
+  if (grad == EXTERND_BF16) return launch<EIGHT, PT, EXTERND_BF16, MASTER>(a, cus, s);
+  return launch<EIGHT, PT, EXTERND_F16, MASTER>(a, cus, s);
 }
 
 template <bool EIGHT>
-hipError_t pick(const AdamArgs& a, int kind, unsigned grid, hipStream_t s) {
+hipError_t pick(const AdamArgs& a, int kind, int cus, hipStream_t s) {
   const int grad = kind % 3, param = kind / 3 % 3;
   const bool master = kind >= 9;
-  if (param == EXTERND_F32) return pick_grad<EIGHT, EXTERND_F32, false>(a, grad, grid, s);
+  if (param == EXTERND_F32) return pick_grad<EIGHT, EXTERND_F32, false>(a, grad, cus, s);
   if (param == EXTERND_BF16)
-    return master ? pick_grad<EIGHT, EXTERND_BF16, true>(a, grad, grid, s)
-                  : pick_grad<EIGHT, EXTERND_BF16, false>(a, grad, grid, s);
-  return master ? pick_grad<EIGHT, EXTERND_F16, true>(a, grad, grid, s)
-                : pick_grad<EIGHT, EXTERND_F16, false>(a, grad, grid, s);
+    return master ? pick_grad<EIGHT, EXTERND_BF16, true>(a, grad, cus, s)
+                  : pick_grad<EIGHT, EXTERND_BF16, false>(a, grad, cus, s);
+  return master ? pick_grad<EIGHT, EXTERND_F16, true>(a, grad, cus, s)
+                : pick_grad<EIGHT, EXTERND_F16, false>(a, grad, cus, s);
 }
 
 // Tensors of one kind go through one kernel.
@@ -311,10 +324,7 @@ hipError_t run_adamw(const externd_adamw_tensor* tensors, int64_t count, const e
     if (tensors[i].n > 0 && left[kind_of(tensors[i])]++ == 0) kinds[used++] = kind_of(tensors[i]);
   auto run = [&](int kind, bool last) {
     a.advance = last;
-    // No more workgroups than are resident together, and few of many waves: each counts itself at the end, 12 ns
-    // one after the other (11 million entries in 8 bits: 42 us with eight of four waves a compute unit, 33 with four of eight).
-    const unsigned grid = std::max(1u, std::min(a.chunks, (uint32_t)cus * 4u));
-    const hipError_t e = o.bits == 8 ? pick<true>(a, kind, grid, s) : pick<false>(a, kind, grid, s);
+    const hipError_t e = o.bits == 8 ? pick<true>(a, kind, cus, s) : pick<false>(a, kind, cus, s);
     a.count = 0;
     a.chunks = 0;
     return e;
