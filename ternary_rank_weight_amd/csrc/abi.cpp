@@ -310,7 +310,7 @@ int moe_call(externd::MoeArgs& a, const externd_moe_weights* w, int64_t experts,
     a.ids = a.ids_out;
     a.weights = a.weights_out;
   }
-  const bool few = router && w && externd::moe_few(a);
+  const bool few = router && w && externd::moe_few(a.tokens, a.top, a.w.experts);
   hipError_t e = router ? externd::run_moe_logits(a, space, s) : hipSuccess;
   if (e == hipSuccess && !few) e = externd::run_moe_choose(a, space, router, w != nullptr, s);
   if (e == hipSuccess && w) e = externd::run_moe_experts(a, space, few, s);

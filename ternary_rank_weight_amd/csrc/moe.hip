@@ -269,13 +269,6 @@ bool pieces_aligned(const void* p, int64_t stride, int64_t ld, int64_t cols) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0 && ld % 8 == 0 && cols % 8 == 0;
 }
 
-// Waves that share a tile: as many as bring the launch to sixteen a compute unit.
-int waves_a_tile(int64_t tiles, int64_t groups, int cus, int least, int most) {
-  int sw = least;
-  while (sw < most && tiles * groups * sw < (int64_t)cus * 16) sw *= 2;
-  return sw;
-}
-
 template <bool BF, int SW, bool FEW>
 void launch_up(const UpArgs& u, bool al, bool alike, unsigned groups, hipStream_t s) {
   constexpr int WV = SW > 8 ? SW : 8;
@@ -334,14 +327,14 @@ hipError_t experts(const MoeArgs& a, const MoeSpace& s, bool few, hipStream_t st
   const bool al = pieces_aligned(w.wg, w.up_stride, w.up_ld, a.cols) && pieces_aligned(w.wu, w.up_stride, w.up_ld, a.cols) &&
                   pieces_aligned(a.x, 0, a.ldx, a.cols);
   const bool alike = ((reinterpret_cast<uintptr_t>(w.wg) ^ reinterpret_cast<uintptr_t>(w.wu)) & 15) == 0;
-  const int up = waves_a_tile(rows_tiles(w.rows, u.apart_bits), groups, a.cus, 4, 16);
+  const MoeForms f = moe_forms(a.tokens, a.top, w.experts, w.rows, a.cols, w.up_ld, w.down_ld, a.cus);
   if (few) {
-    if (up == 4) launch_up<BF, 4, true>(u, al, alike, (unsigned)groups, stream);
-    else if (up == 8) launch_up<BF, 8, true>(u, al, alike, (unsigned)groups, stream);
+    if (f.up == 4) launch_up<BF, 4, true>(u, al, alike, (unsigned)groups, stream);
+    else if (f.up == 8) launch_up<BF, 8, true>(u, al, alike, (unsigned)groups, stream);
     else launch_up<BF, 16, true>(u, al, alike, (unsigned)groups, stream);
   } else {
-    if (up == 4) launch_up<BF, 4, false>(u, al, alike, (unsigned)groups, stream);
-    else if (up == 8) launch_up<BF, 8, false>(u, al, alike, (unsigned)groups, stream);
+    if (f.up == 4) launch_up<BF, 4, false>(u, al, alike, (unsigned)groups, stream);
+    else if (f.up == 8) launch_up<BF, 8, false>(u, al, alike, (unsigned)groups, stream);
     else launch_up<BF, 16, false>(u, al, alike, (unsigned)groups, stream);
   }
   hipError_t e = hipGetLastError();
@@ -360,20 +353,18 @@ hipError_t experts(const MoeArgs& a, const MoeSpace& s, bool few, hipStream_t st
   d.part = s.part;
   const bool dal = pieces_aligned(w.wd, w.down_stride, w.down_ld, w.rows);
   if (a.tokens == 1) {
-    if (a.top == 1) launch_one<BF, 16>(d, dal, a, stream);
-    else if (a.top == 2) launch_one<BF, 8>(d, dal, a, stream);
-    else if (a.top <= 4) launch_one<BF, 4>(d, dal, a, stream);
-    else if (a.top <= 8) launch_one<BF, 2>(d, dal, a, stream);
+    if (f.one == 16) launch_one<BF, 16>(d, dal, a, stream);
+    else if (f.one == 8) launch_one<BF, 8>(d, dal, a, stream);
+    else if (f.one == 4) launch_one<BF, 4>(d, dal, a, stream);
+    else if (f.one == 2) launch_one<BF, 2>(d, dal, a, stream);
     else launch_one<BF, 1>(d, dal, a, stream);
     return hipGetLastError();
   }
-  const int64_t tiles = rows_tiles(a.cols, d.apart_bits);
-  const int down = waves_a_tile(tiles, groups, a.cus, 1, 16);
-  if (down == 1 && tiles * groups >= (int64_t)a.cus * 32) launch_down<BF, 1, 2>(d, dal, (unsigned)groups, stream);
-  else if (down == 1) launch_down<BF, 1, 1>(d, dal, (unsigned)groups, stream);
-  else if (down == 2) launch_down<BF, 2, 1>(d, dal, (unsigned)groups, stream);
-  else if (down == 4) launch_down<BF, 4, 1>(d, dal, (unsigned)groups, stream);
-  else if (down == 8) launch_down<BF, 8, 1>(d, dal, (unsigned)groups, stream);
+  if (f.down_tiles == 2) launch_down<BF, 1, 2>(d, dal, (unsigned)groups, stream);
+  else if (f.down == 1) launch_down<BF, 1, 1>(d, dal, (unsigned)groups, stream);
+  else if (f.down == 2) launch_down<BF, 2, 1>(d, dal, (unsigned)groups, stream);
+  else if (f.down == 4) launch_down<BF, 4, 1>(d, dal, (unsigned)groups, stream);
+  else if (f.down == 8) launch_down<BF, 8, 1>(d, dal, (unsigned)groups, stream);
   else launch_down<BF, 16, 1>(d, dal, (unsigned)groups, stream);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(k_moe_join<BF>, dim3((unsigned)((a.cols + 255) / 256), (unsigned)a.tokens), dim3(256), 0, stream, s.part, a.ids,

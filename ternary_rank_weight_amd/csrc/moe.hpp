@@ -5,12 +5,12 @@
 #include <stdint.h>
 
 #include "../../include/externd.h"
+#include "moe_plan.hpp"
 
 namespace externd {
 
 constexpr int kMoeExperts = 1024;   // most experts: a thread each when the slots are sorted
 constexpr int kMoeTop = 64;         // most experts of a token
-constexpr int kMoeGroup = 16;       // slots that go through an expert's weights together
 
 // A slot is one of a token's choices: slot = token top + choice.  A group is up to 16 slots of one expert; slots
 // past `count` repeat the last, and a group of expert -1 is not there.
@@ -43,13 +43,8 @@ struct MoeSpace {
   int64_t ldh;
   size_t bytes;
 };
-int64_t moe_most_groups(int64_t slots, int64_t experts);
 // experts_too: for the experts' products; without, for the router alone
 MoeSpace moe_space(void* base, int64_t tokens, int64_t experts, int64_t top, int64_t rows, int64_t cols, bool router, bool experts_too);
-
-// Whether the first product makes the choice itself: a wave a token of its workgroups' eight, a lane a slot.
-constexpr int kMoeFewSlots = 64;
-inline bool moe_few(const MoeArgs& a) { return a.tokens <= 8 && a.slots() <= kMoeFewSlots && a.w.experts <= 256; }
 
 hipError_t run_moe_logits(const MoeArgs& a, const MoeSpace& s, hipStream_t stream);
 // Choice and weights from the logits, or a choice that was made elsewhere (router false); and, where plan is given, the groups.

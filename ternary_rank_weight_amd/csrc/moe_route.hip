@@ -143,10 +143,6 @@ void launch_logits(const MoeArgs& a, const MoeSpace& s, hipStream_t stream) {
 
 }  // namespace
 
-int64_t moe_most_groups(int64_t slots, int64_t experts) {
-  return std::min(slots, std::min(slots, experts) + slots / kMoeGroup);
-}
-
 MoeSpace moe_space(void* base, int64_t tokens, int64_t experts, int64_t top, int64_t rows, int64_t cols, bool router, bool experts_too) {
   MoeSpace s = {};
   char* const begin = static_cast<char*>(base);
