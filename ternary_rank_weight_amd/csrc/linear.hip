@@ -5,7 +5,9 @@
 //   db = the sum of dz over the tokens    (one pass)
 // for T tokens, K columns and F rows of W.  The products are the tiled kernel of the gated block
 // (gated_gemm.hpp) in forms of one weight matrix; with an activation dz is held in two 16-bit
-// parts as dg and du are there, so that each gradient is rounded once.
+// parts as dg and du are there, so that each gradient is rounded once.  That doubles dx and dW: bf16, 2048 tokens at 2560 x
+// 9728, silu, the whole backward pass 372 us in two parts and 200 in one, whose dx and dW are off by 2.35e-3 of their
+// size instead of 1.66e-3, which rounding them leaves (fp16: 400 and 206 us, 2.9e-4 and 2.1e-4).
 #include <algorithm>
 
 #include "activation.hpp"

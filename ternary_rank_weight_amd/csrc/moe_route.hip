@@ -60,8 +60,8 @@ __global__ __launch_bounds__(kSplit * kWave) void k_moe_logits(MoeArgs a, double
 
 constexpr int kMostGroups = kMoeExperts + EXTERND_MOE_SLOTS / kMoeGroup;
 
-// Choice of every token (logits given), and the groups (given): one workgroup, since the groups need every token's choice.
-// Bound by latency, a chain of reductions over a wave for each choice: 12 us for 32 tokens, 8 of 128.
+// Choice of every token (logits given), and the groups (given): one workgroup, since the groups need every token's choice
+// (routing alone, which makes none, runs it too).  Bound by latency, a chain of reductions over a wave for each choice: 12 us for 32 tokens, 8 of 128.
 template <int C>
 __global__ __launch_bounds__(1024) void k_moe_choose(MoeArgs a, const double* __restrict__ logits, MoeGroup* __restrict__ groups,
                                                       int most, uint32_t* __restrict__ tops) {
