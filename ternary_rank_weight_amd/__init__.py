@@ -1241,9 +1241,9 @@ class AdamW:
     moments of a byte per entry and a byte per 256 (include/externd.h has the formulas and the codes).  master:
     float32 weights behind the 16-bit parameters, which become their rounding.  weight_decay: a number, or one per
     tensor.  The step is counted on the device, so that a captured step counts in each replay of its graph: one count for
-    all tensors, with which each is corrected.  A tensor that gets its first gradient at a late step t is corrected for t
-    steps that it did not have (its first update is (1 - beta1) / sqrt(1 - beta2) of lr in the end, 3.2 by default, not 1), and a step
-    without any gradient counts; tensors that start later belong in an object of their own.
+    all tensors, with which each is corrected.  A tensor that gets its first gradient at a late step is corrected
+    for steps that it did not have (its first update tends to (1 - beta1) / sqrt(1 - beta2) times lr, 3.2 by default), and a
+    step without any gradient counts; tensors that start later belong in an object of their own.
 
     state, as the property of that name returns it, takes the place of new zeros (its tensors are used, not
     copied): "step" float64 (4,): steps taken, beta1 and beta2 to that power, 0; "m", "v" and "master" (or
