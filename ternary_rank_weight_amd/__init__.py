@@ -1308,6 +1308,7 @@ class AdamW:
             if master and p.dtype != torch.float32:
                 t.master = self._master.data_ptr() + 4 * at
         self._entries = [(t, p, p.numel(), p.shape, p.dtype) for t, p in zip(self._table, self._params)]
+        self._held = [None] * len(self._params)   # (address, gradient's type) as the table has them; None: left out
         self._inference = any(p.is_inference() for p in self._params)
         self._opts = _AdamOpts(0.0, betas[0], betas[1], eps, None, None, 1.0, bits, self._step.data_ptr())
 
@@ -1328,11 +1329,11 @@ class AdamW:
         index = self._index
         if index != _current_device():
             _op_device(*params)
-        keep, changed = [], params
+        keep, changed, held = [], params, self._held
         for k, (t, p, n, shape, dtype) in enumerate(self._entries):
             g = grads[k]
             if g is None:
-                t.n = 0
+                t.n, held[k] = 0, None
                 if changed is params:
                     changed = params[:k]
                 continue
@@ -1347,11 +1348,14 @@ class AdamW:
                 keep.append(g)
             # (p.data may have been given anything since the last step, at the same address too)
             at = p.data_ptr()
-            if now != shape and p.numel() != n or p.dtype is not dtype or not p.is_contiguous() or \
-                    at != t.param and p.get_device() != index:
+            if now != shape and p.numel() != n or p.dtype is not dtype or not p.is_contiguous():
                 _need(p, dtype, "a parameter")
-                raise ValueError("a parameter's size or device has changed")
-            t.param, t.grad, t.grad_dtype, t.n = at, g.data_ptr(), code, n
+                raise ValueError("a parameter's size has changed")
+            t.grad = g.data_ptr()
+            if held[k] != (at, code):
+                if p.get_device() != index:
+                    raise ValueError("a parameter's device has changed")
+                t.param, t.grad_dtype, t.n, held[k] = at, code, n, (at, code)
             if changed is not params:
                 changed.append(p)
         if lr is None:
